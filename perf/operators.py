@@ -199,7 +199,7 @@ def prepare(case, seed):
         from bit_recurrent_state_lores_b200 import lores as L
         st["L"] = L
         st["cfg"] = L.make_scan_config(N, T, H, dk, dv, heads_qk=hq, delta=case["delta"],
-                                       dtype=dt)
+                                       dtype=dt, max_len=st["longest"])
         size = L.lores_scan_workspace(st["cfg"], backward=case["kind"] == "grad")
         st["work"] = torch.empty(size, dtype=torch.uint8, device="cuda")
     return st
