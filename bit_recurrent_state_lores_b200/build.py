@@ -5,7 +5,8 @@
 csrc/lores.cu (host side, loader, dequantizer) and 45 compilations of csrc/lores_inst.cu
 (one decode-step kernel family per key width x single/multi-token x storage family --
 plain; dense and per-lane; per-lane only --, one two-rows-per-lane family per key width x
-single/multi-token, and one key-axis family per key width) build in parallel, one nvcc
+single/multi-token, and one key-axis family per key width) and of the state scan
+(csrc/lores_scan.cu and one csrc/lores_scan_inst.cu per key width and number of input planes) build in parallel, one nvcc
 process per CPU core, then link.
 
 --checked builds liblores_checked.so instead: the same sources compiled with
@@ -27,9 +28,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRC = os.path.join(CSRC, "lores.cu")
 INST = os.path.join(CSRC, "lores_inst.cu")
+SCAN = os.path.join(CSRC, "lores_scan.cu")
+SCAN_INST = os.path.join(CSRC, "lores_scan_inst.cu")
 DEPS = [SRC, INST, os.path.join(CSRC, "lores_step.cuh"), os.path.join(CSRC, "lores_device.cuh"),
         os.path.join(CSRC, "lores_key.cuh"), os.path.join(CSRC, "lores_pair.cuh"),
-        os.path.join(CSRC, "lores_mma.cuh"),
+        os.path.join(CSRC, "lores_mma.cuh"), os.path.join(CSRC, "lores_host.h"),
+        os.path.join(CSRC, "lores_pool.cuh"),
+        os.path.join(CSRC, "lores_scan.cu"), os.path.join(CSRC, "lores_scan_inst.cu"),
+        os.path.join(CSRC, "lores_scan.cuh"),
         os.path.join(ROOT, "include", "lores.h")]
 LIB = os.path.join(PKG, "liblores.so")
 LIB_CHECKED = os.path.join(PKG, "liblores_checked.so")
@@ -38,6 +44,7 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std
          "-fmad=false", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 KEY_WIDTHS = (16, 32, 64, 128, 256)
 MMA_WIDTHS = (16, 32, 64, 128)       # key widths of the tensor-core kernel
+SCAN_WIDTHS = (16, 32, 64, 128)      # key widths of the state scan's chunk kernels
 
 
 def units():
@@ -57,6 +64,11 @@ def units():
         out.append((INST, [f"-DLORES_DK={dk}", "-DLORES_MMA=1"], f"lores_mma_{dk}.o"))
     for dk in KEY_WIDTHS:
         out.append((INST, [f"-DLORES_DK={dk}", "-DLORES_KEY=1"], f"lores_key_{dk}.o"))
+    for np_ in (2, 1):
+        for dk in reversed(SCAN_WIDTHS):
+            out.append((SCAN_INST, [f"-DLORES_DK={dk}", f"-DLORES_NP={np_}"],
+                        f"lores_scan_{dk}_{np_}.o"))
+    out.append((SCAN, [], "lores_scan.o"))
     out.append((SRC, [], "lores.o"))
     return out
 

@@ -28,6 +28,8 @@
 #include "lores_key.cuh"
 #include "lores_pair.cuh"
 #include "lores_mma.cuh"
+#include "lores_host.h"
+#include "lores_pool.cuh"
 
 namespace lores {
 
@@ -286,6 +288,17 @@ static DequantFn dequant_kernel_for(int dk) {
   return nullptr;
 }
 
+static PoolFn pool_kernel_for(int dk, bool write) {
+  switch (dk) {
+    case 16: return write ? write_states_kernel<16> : read_states_kernel<16>;
+    case 32: return write ? write_states_kernel<32> : read_states_kernel<32>;
+    case 64: return write ? write_states_kernel<64> : read_states_kernel<64>;
+    case 128: return write ? write_states_kernel<128> : read_states_kernel<128>;
+    case 256: return write ? write_states_kernel<256> : read_states_kernel<256>;
+  }
+  return nullptr;
+}
+
 }  // namespace lores
 
 using namespace lores;
@@ -339,29 +352,6 @@ struct lores_handle {
 };
 
 namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-lores_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return LORES_OK;
-  if (e == cudaErrorMemoryAllocation) {
-    (void)cudaGetLastError();
-    return LORES_ERR_OOM;
-  }
-  return LORES_ERR_CUDA;
-}
 
 void free_all(lores_handle *h) {
   if (h->codes) cudaFree(h->codes - kGuardBytes);
@@ -1060,6 +1050,65 @@ lores_status lores_load_state(lores_handle *h, const float *S, uint64_t step, vo
   const int blocks = (int)((warps + kWarps - 1) / kWarps);
   load_kernel_for(h->cfg.d_k)<<<blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cuda_status(cudaGetLastError());
+}
+
+// The write and read of chosen slots: one launch over n entries.
+static lores_status move_states(lores_handle *h, int32_t n, const int32_t *slots, const void *src,
+                                void *dst, bool write, int32_t dtype, uint64_t step, void *stream) {
+  const void *buf = write ? src : dst;
+  if (!h || n < 0 || n > h->cfg.batch || dtype < LORES_F32 || dtype > LORES_F16 ||
+      (n > 0 && (!buf || !aligned16(buf))) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return LORES_ERR_INVALID_ARG;
+  if (write && h->axis) return LORES_ERR_UNSUPPORTED;
+  const lores_config &c = h->cfg;
+  const int rows = kPoolThreads / (c.d_k / 16);
+  const long long blocks = ((long long)c.heads * c.d_v + rows - 1) / rows;
+  if ((long long)c.heads * c.d_v > 0x7FFFFFFFll || blocks * n > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
+  if (n == 0) return LORES_OK;
+  DeviceGuard guard(c.device);
+  if (!guard.ok) return LORES_ERR_CUDA;
+  PoolParams p{};
+  p.codes = h->codes;
+  p.scales = h->scales;
+  p.fmt = h->d_fmt;
+  p.head_off = h->d_head_off;
+  p.seq_bytes = h->seq_bytes;
+  p.H = c.heads;
+  p.d_v = c.d_v;
+  p.ng = h->ng;
+  p.G = h->G;
+  p.axis = h->axis;
+  p.batch = c.batch;
+  p.n = n;
+  p.blocks = (int)blocks;
+  p.slots = slots;
+  p.src = src;
+  p.dst = dst;
+  p.dtype = dtype;
+  p.wide = (reinterpret_cast<uintptr_t>(buf) & 31u) == 0;
+  p.step_key = step_key_of(c.seed, step);
+  p.stochastic = c.stochastic;
+  p.flag = h->flag;
+#ifdef LORES_INDEX_CHECKS
+  p.rg = ranges_of(h, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 1);
+  const unsigned long long bytes =
+      (unsigned long long)n * c.heads * c.d_v * c.d_k * (dtype == LORES_F32 ? 4 : 2);
+  p.rg.base[kRgS] = buf;
+  p.rg.bytes[kRgS] = bytes > h->trim[kRgS] ? bytes - h->trim[kRgS] : 0;
+#endif
+  pool_kernel_for(c.d_k, write)<<<(unsigned)(blocks * n), kPoolThreads, 0,
+                                 static_cast<cudaStream_t>(stream)>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+lores_status lores_write_states(lores_handle *h, int32_t n, const int32_t *slots, const void *S,
+                                int32_t dtype, uint64_t step, void *stream) {
+  return move_states(h, n, slots, S, nullptr, true, dtype, step, stream);
+}
+
+lores_status lores_read_states(lores_handle *h, int32_t n, const int32_t *slots, void *out,
+                               int32_t dtype, void *stream) {
+  return move_states(h, n, slots, nullptr, out, false, dtype, 0, stream);
 }
 
 lores_status lores_export_codes(lores_handle *h, void *codes, float *scales, void *stream) {

@@ -1,0 +1,416 @@
+// lores_scan.cu -- C entry points of the state scan and its backward pass: checks, workspace
+// layout, launches.  The kernels and the mathematics are in lores_scan.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "lores.h"
+#include "lores_host.h"
+#include "lores_scan.cuh"
+
+namespace lores {
+namespace scan {
+
+void scan_kernels_16_1(ScanKernels &t);
+void scan_kernels_16_2(ScanKernels &t);
+void scan_kernels_32_1(ScanKernels &t);
+void scan_kernels_32_2(ScanKernels &t);
+void scan_kernels_64_1(ScanKernels &t);
+void scan_kernels_64_2(ScanKernels &t);
+void scan_kernels_128_1(ScanKernels &t);
+void scan_kernels_128_2(ScanKernels &t);
+
+}  // namespace scan
+}  // namespace lores
+
+using namespace lores;
+using namespace lores::scan;
+
+namespace {
+
+// Sequences up to this many tokens go token by token: the chunk kernels always pay for 64.
+constexpr int kRecurrentMost = 16;
+constexpr int kMaxDevices = 64;
+
+struct Kernels {
+  ScanKernels by_width[4];             // 16, 32, 64, 128
+  ScanFn recurrent[5][2];              // 16 .. 256, delta
+  Kernels() {
+    scan_kernels_16_1(by_width[0]); scan_kernels_16_2(by_width[0]);
+    scan_kernels_32_1(by_width[1]); scan_kernels_32_2(by_width[1]);
+    scan_kernels_64_1(by_width[2]); scan_kernels_64_2(by_width[2]);
+    scan_kernels_128_1(by_width[3]); scan_kernels_128_2(by_width[3]);
+    recurrent[0][0] = scan_recurrent_kernel<16, false>;  recurrent[0][1] = scan_recurrent_kernel<16, true>;
+    recurrent[1][0] = scan_recurrent_kernel<32, false>;  recurrent[1][1] = scan_recurrent_kernel<32, true>;
+    recurrent[2][0] = scan_recurrent_kernel<64, false>;  recurrent[2][1] = scan_recurrent_kernel<64, true>;
+    recurrent[3][0] = scan_recurrent_kernel<128, false>; recurrent[3][1] = scan_recurrent_kernel<128, true>;
+    recurrent[4][0] = scan_recurrent_kernel<256, false>; recurrent[4][1] = scan_recurrent_kernel<256, true>;
+  }
+};
+const Kernels &kernels() {
+  static const Kernels k;
+  return k;
+}
+
+int width_index(int dk) {
+  return dk == 16 ? 0 : dk == 32 ? 1 : dk == 64 ? 2 : dk == 128 ? 3 : dk == 256 ? 4 : -1;
+}
+
+// A configuration with its defaults filled in.
+struct Shape {
+  lores_scan_config c;
+  int np, dvp, n_slots, rec_width;
+  bool recurrent;
+  bool raw[3];                         // q, k, v (and d_o like v) need planes of their own
+  bool raw_do;
+};
+
+lores_status shape_of(const lores_scan_config *cfg, bool backward, Shape &s) {
+  if (!cfg) return LORES_ERR_INVALID_ARG;
+  lores_scan_config &c = s.c;
+  c = *cfg;
+  if (c.n_seq < 1 || c.total < 0 || c.total > 0x7FFFFFFFll || c.max_len < 0 || c.heads < 1 ||
+      c.heads > 65535 || c.heads_qk < 0 || c.d_v < 4 || c.d_v > 4096 || c.d_v % 4 || width_index(c.d_k) < 0 ||
+      c.delta < 0 || c.delta > 1 || c.dtype < LORES_F32 || c.dtype > LORES_F16 || c.device < 0)
+    return LORES_ERR_INVALID_ARG;
+  if (c.heads_qk == 0) c.heads_qk = c.heads;
+  if (c.heads % c.heads_qk) return LORES_ERR_INVALID_ARG;
+  if (c.max_len == 0 || c.max_len > c.total) c.max_len = c.total;
+  if ((long long)c.n_seq * c.heads > 0x7FFFFFFFll || c.total / kChunk + c.n_seq > 0x7FFFFFFFll)
+    return LORES_ERR_INVALID_ARG;
+  const long long wq = (long long)c.heads_qk * c.d_k, wv = (long long)c.heads * c.d_v;
+  int64_t *st[4] = {&c.q_stride, &c.k_stride, &c.v_stride, &c.o_stride};
+  for (int i = 0; i < 4; ++i) {
+    const long long width = i < 2 ? wq : wv;
+    if (*st[i] == 0) *st[i] = width;
+    if (*st[i] < width || *st[i] % 4 || *st[i] > (1ll << 40)) return LORES_ERR_INVALID_ARG;
+  }
+  if (backward && c.d_k == 256) return LORES_ERR_UNSUPPORTED;
+  s.np = c.dtype == LORES_BF16 ? 1 : 2;
+  s.dvp = (c.d_v + 15) / 16 * 16;
+  s.n_slots = (int)(c.total / kChunk + c.n_seq);
+  s.recurrent = !backward && (c.max_len <= kRecurrentMost || c.d_k == 256);
+  for (int i = 0; i < 3; ++i)
+    s.raw[i] = s.np == 2 || *st[i] % 8 || (i == 2 && c.d_v % 8);
+  s.raw_do = s.np == 2 || c.o_stride % 8 || c.d_v % 8;
+  return LORES_OK;
+}
+
+// Hands out the workspace's parts in one order, for sizing and for use.
+struct Carver {
+  uint8_t *base;
+  unsigned long long at = 256;         // the first 256 bytes hold the error word
+  template <class T>
+  T *take(unsigned long long count) {
+    T *r = base ? reinterpret_cast<T *>(base + at) : nullptr;
+    at += (count * sizeof(T) + 255) / 256 * 256;
+    return r;
+  }
+};
+
+void planes_of(Carver &w, const Shape &s, bool raw, const void *src, long long stride, int heads, int dim,
+               Planes &out, Raw &r) {
+  r.src = nullptr;
+  if (!raw) {
+    out = {static_cast<const __nv_bfloat16 *>(src), nullptr, stride, dim};
+    return;
+  }
+  const int dimp = (dim + 15) / 16 * 16;
+  const unsigned long long n = (unsigned long long)s.c.total * heads * dimp;
+  r = {src, stride, heads, dim, dimp, w.take<__nv_bfloat16>(n), nullptr};
+  if (s.np == 2) r.lo = w.take<__nv_bfloat16>(n);
+  out = {r.hi, r.lo, (long long)heads * dimp, dimp};
+}
+
+// Fills the parameters and returns the bytes of workspace.
+unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, const void *q, const void *k,
+                          const void *v, const void *d_o, ScanParams &p) {
+  const lores_scan_config &c = s.c;
+  Carver w{ws};
+  p.flag = reinterpret_cast<unsigned *>(ws);
+  if (s.recurrent) return w.at;
+  planes_of(w, s, s.raw[0], q, c.q_stride, c.heads_qk, c.d_k, p.q, p.raw[0]);
+  planes_of(w, s, s.raw[1], k, c.k_stride, c.heads_qk, c.d_k, p.k, p.raw[1]);
+  planes_of(w, s, s.raw[2], v, c.v_stride, c.heads, c.d_v, p.v, p.raw[2]);
+  if (backward) planes_of(w, s, s.raw_do, d_o, c.o_stride, c.heads, c.d_v, p.dO, p.raw[3]);
+  const unsigned long long recs = (unsigned long long)s.n_slots * c.heads, sq = 2 * kChunk * kChunk,
+                           tile = 2ull * kChunk * c.d_k;
+  p.gates = w.take<float>(recs * kGateFloats);
+  p.pp = w.take<__nv_bfloat16>(recs * sq);
+  if (c.delta) {
+    p.tm = w.take<__nv_bfloat16>(recs * sq);
+    p.kt = w.take<__nv_bfloat16>(recs * tile);
+  }
+  if (!backward) return w.at;
+  if (c.delta) {
+    p.z = w.take<__nv_bfloat16>(recs * sq);
+    p.kb = w.take<__nv_bfloat16>(recs * tile);
+  }
+  p.s0 = w.take<__nv_bfloat16>(recs * 2 * s.dvp * c.d_k);
+  p.dd = w.take<__nv_bfloat16>(recs * 2 * s.dvp * c.d_k);
+  p.et = w.take<__nv_bfloat16>(recs * 2 * s.dvp * kChunk);
+  p.rt = w.take<__nv_bfloat16>(recs * 2 * s.dvp * kChunk);
+  if (c.heads != c.heads_qk) {
+    const unsigned long long n = (unsigned long long)c.total * c.heads * c.d_k;
+    p.dq = w.take<float>(n);
+    p.dk = w.take<float>(n);
+  }
+  return w.at;
+}
+
+ScanParams params_of(const Shape &s) {
+  const lores_scan_config &c = s.c;
+  ScanParams p{};
+  p.n_seq = c.n_seq;
+  p.H = c.heads;
+  p.share = c.heads / c.heads_qk;
+  p.d_v = c.d_v;
+  p.dvp = s.dvp;
+  p.dtype = c.dtype;
+  p.n_slots = s.n_slots;
+  p.max_len = (int)c.max_len;
+  p.total = c.total;
+  p.o_stride = c.o_stride;
+  p.stages = 2;
+  return p;
+}
+
+constexpr int kMaxShared = 232448;     // dynamic shared memory of one CTA
+
+// A kernel's dynamic shared memory differs from call to call; its limit is raised once per device.
+cudaError_t launch(ScanFn fn, dim3 grid, int threads, int smem, cudaStream_t s, int device, const ScanParams &p,
+                   std::atomic<unsigned long long> &raised) {
+  if (smem > 48 * 1024) {
+    const unsigned long long bit = device < kMaxDevices ? 1ull << device : 0;
+    if (!bit || !(raised.load(std::memory_order_acquire) & bit)) {
+      const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+      if (e != cudaSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  fn<<<grid, threads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+int sm_count(int device) {
+  static std::atomic<int> known[kMaxDevices];
+  if (device < kMaxDevices) {
+    const int n = known[device].load(std::memory_order_relaxed);
+    if (n) return n;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 148;
+  if (device < kMaxDevices) known[device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+lores_status device_ok(int device) {
+  static std::atomic<int> known[kMaxDevices];
+  if (device < kMaxDevices && known[device].load(std::memory_order_relaxed) == 1) return LORES_OK;
+  int major = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return LORES_ERR_CUDA;
+  }
+  if (major != 10) return LORES_ERR_UNSUPPORTED;
+  if (device < kMaxDevices) known[device].store(1, std::memory_order_relaxed);
+  return LORES_OK;
+}
+
+// Compute warps (16 value rows each) per CTA of the chunk walks: as many as share one fetch
+// of a chunk's tiles, but few enough that the CTAs fill the SMs.
+int walk_warps(const Shape &s) {
+  const long long walks = (long long)s.c.n_seq * s.c.heads;
+  const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
+  int w = 4;
+  while (w > 1 && (blocks < w || walks * ((blocks + w - 1) / w) < sms * 3 / 4)) w >>= 1;
+  return w;
+}
+
+bool aligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3u) == 0; }
+bool given16(const void *x, bool needed) { return aligned16(x) && (x || !needed); }
+
+// Planes and per-chunk matrices.
+cudaError_t run_prep(const Shape &s, bool backward, const ScanParams &p, cudaStream_t st) {
+  const lores_scan_config &c = s.c;
+  long long most = 0;
+  for (const Raw &r : p.raw)
+    if (r.src) most = std::max<long long>(most, c.total * r.heads * (r.dimp / 4));
+  if (most) {
+    const unsigned blocks = (unsigned)std::min<long long>((most + 255) / 256, 16ll * sm_count(c.device));
+    scan_planes_kernel<<<dim3(blocks, backward ? 4 : 3), 256, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  static std::atomic<unsigned long long> raised[4][2][2][2];
+  const int wi = width_index(c.d_k), ld = c.d_k + 8;
+  const int smem = 2 * s.np * kChunk * ld * 2 + kChunk * kLdF * 4 * 2 + kChunk * 8 + kChunk * 4 * 4;
+  return launch(kernels().by_width[wi].prep[s.np - 1][c.delta][backward], dim3(s.n_slots, c.heads), kPrepThreads,
+                smem, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
+}
+
+cudaError_t run_chain(const Shape &s, bool save, ScanParams p, cudaStream_t st) {
+  const lores_scan_config &c = s.c;
+  static std::atomic<unsigned long long> raised[4][2][2][2];
+  const int wi = width_index(c.d_k), w = walk_warps(s);
+  const int stage = chain_layout(c.d_k, s.np, w, c.delta, !save).bytes;
+  p.stages = 2 * stage <= kMaxShared ? 2 : 1;
+  return launch(kernels().by_width[wi].chain[s.np - 1][c.delta][save],
+                dim3(c.n_seq * c.heads, (s.dvp / 16 + w - 1) / w), 32 * (w + kLoadWarps), p.stages * stage, st,
+                c.device, p, raised[wi][s.np - 1][c.delta][save]);
+}
+
+cudaError_t run_reverse(const Shape &s, ScanParams p, cudaStream_t st) {
+  const lores_scan_config &c = s.c;
+  static std::atomic<unsigned long long> raised[4][2][2];
+  const int wi = width_index(c.d_k), w = walk_warps(s);
+  const int stage = reverse_layout(c.d_k, s.np, w, c.delta).bytes;
+  p.stages = 2 * stage <= kMaxShared ? 2 : 1;
+  return launch(kernels().by_width[wi].reverse[s.np - 1][c.delta],
+                dim3(c.n_seq * c.heads, (s.dvp / 16 + w - 1) / w), 32 * (w + kLoadWarps), p.stages * stage, st,
+                c.device, p, raised[wi][s.np - 1][c.delta]);
+}
+
+cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
+  const lores_scan_config &c = s.c;
+  static std::atomic<unsigned long long> raised[4][2][2];
+  const int wi = width_index(c.d_k);
+  const GradLayout l = grad_layout(c.d_k, s.np);
+  p.stages = l.stage + 2 * l.stage_bytes <= kMaxShared ? 2 : 1;
+  return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3(s.n_slots, c.heads), kGradThreads,
+                l.stage + p.stages * l.stage_bytes, st, c.device, p, raised[wi][s.np - 1][c.delta]);
+}
+
+lores_status check_inputs(const Shape &s, const void *q, const void *k, const void *v, const float *log_alpha,
+                          const float *beta, const int32_t *offsets, const float *state_in, const void *workspace) {
+  const bool any = s.c.total > 0;
+  if (!given16(q, any) || !given16(k, any) || !given16(v, any) || !aligned4(log_alpha) || !aligned4(beta) ||
+      (any && (!log_alpha || !beta)) || !aligned4(offsets) || !given16(state_in, false) ||
+      !given16(workspace, true))
+    return LORES_ERR_INVALID_ARG;
+  if (!offsets && s.c.total % s.c.n_seq) return LORES_ERR_INVALID_ARG;
+  return LORES_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward, uint64_t *bytes) {
+  if (!bytes || backward < 0 || backward > 1) return LORES_ERR_INVALID_ARG;
+  Shape s;
+  const lores_status st = shape_of(cfg, backward != 0, s);
+  if (st != LORES_OK) return st;
+  ScanParams p = params_of(s);
+  *bytes = layout(s, backward != 0, nullptr, nullptr, nullptr, nullptr, nullptr, p);
+  return LORES_OK;
+}
+
+lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, const void *k, const void *v,
+                                const float *log_alpha, const float *beta, const int32_t *offsets,
+                                const float *state_in, void *o, float *state_out, void *workspace,
+                                uint64_t workspace_bytes, void *stream) {
+  Shape s;
+  lores_status st = shape_of(cfg, false, s);
+  if (st == LORES_OK) st = check_inputs(s, q, k, v, log_alpha, beta, offsets, state_in, workspace);
+  if (st != LORES_OK) return st;
+  if (!given16(o, s.c.total > 0) || !given16(state_out, false)) return LORES_ERR_INVALID_ARG;
+  ScanParams p = params_of(s);
+  if (layout(s, false, static_cast<uint8_t *>(workspace), q, k, v, nullptr, p) > workspace_bytes)
+    return LORES_ERR_INVALID_ARG;
+  const lores_scan_config &c = s.c;
+  if ((st = device_ok(c.device)) != LORES_OK) return st;
+  DeviceGuard guard(c.device);
+  if (!guard.ok) return LORES_ERR_CUDA;
+  p.offsets = offsets;
+  p.log_alpha = log_alpha;
+  p.beta = beta;
+  p.state_in = state_in;
+  p.state_out = state_out;
+  p.o = o;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (s.recurrent) {
+    p.uq = q; p.uk = k; p.uv = v;
+    p.uq_stride = c.q_stride; p.uk_stride = c.k_stride; p.uv_stride = c.v_stride;
+    const long long lanes = (long long)c.n_seq * c.heads * (c.d_v / kRecRows) * (c.d_k / 16);
+    const long long blocks = (lanes + kRecThreads - 1) / kRecThreads;
+    if (blocks > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
+    kernels().recurrent[width_index(c.d_k)][c.delta]<<<(unsigned)blocks, kRecThreads, 0, cs>>>(p);
+    return cuda_status(cudaGetLastError());
+  }
+  cudaError_t e = run_prep(s, false, p, cs);
+  if (e == cudaSuccess) e = run_chain(s, false, p, cs);
+  return cuda_status(e);
+}
+
+lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, const void *k, const void *v,
+                                 const float *log_alpha, const float *beta, const int32_t *offsets,
+                                 const float *state_in, const void *d_o, const float *d_state_out, void *dq,
+                                 void *dk, void *dv, float *dlog_alpha, float *dbeta, float *d_state_in,
+                                 void *workspace, uint64_t workspace_bytes, void *stream) {
+  Shape s;
+  lores_status st = shape_of(cfg, true, s);
+  if (st == LORES_OK) st = check_inputs(s, q, k, v, log_alpha, beta, offsets, state_in, workspace);
+  if (st != LORES_OK) return st;
+  const bool any = s.c.total > 0;
+  if (!given16(d_o, any) || !given16(d_state_out, false) || !given16(dq, any) || !given16(dk, any) ||
+      !given16(dv, any) || !aligned4(dlog_alpha) || !aligned4(dbeta) || (any && (!dlog_alpha || !dbeta)) ||
+      !given16(d_state_in, false))
+    return LORES_ERR_INVALID_ARG;
+  ScanParams p = params_of(s);
+  if (layout(s, true, static_cast<uint8_t *>(workspace), q, k, v, d_o, p) > workspace_bytes)
+    return LORES_ERR_INVALID_ARG;
+  const lores_scan_config &c = s.c;
+  if ((st = device_ok(c.device)) != LORES_OK) return st;
+  DeviceGuard guard(c.device);
+  if (!guard.ok) return LORES_ERR_CUDA;
+  p.offsets = offsets;
+  p.log_alpha = log_alpha;
+  p.beta = beta;
+  p.state_in = state_in;
+  p.d_state_out = d_state_out;
+  p.d_state_in = d_state_in;
+  p.o = dv;
+  p.o_stride = c.v_stride;
+  p.dlog_alpha = dlog_alpha;
+  p.dbeta = dbeta;
+  p.parts = c.heads != c.heads_qk;
+  const float *parts_q = static_cast<const float *>(p.dq), *parts_k = static_cast<const float *>(p.dk);
+  if (!p.parts) {
+    p.dq = dq;
+    p.dk = dk;
+  }
+  p.dq_stride = c.q_stride;
+  p.dk_stride = c.k_stride;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = run_prep(s, true, p, cs);
+  if (e == cudaSuccess) e = run_chain(s, true, p, cs);
+  if (e == cudaSuccess) e = run_reverse(s, p, cs);
+  if (e == cudaSuccess) e = run_grads(s, p, cs);
+  if (e == cudaSuccess && p.parts && any) {
+    p.dq = dq;
+    p.dk = dk;
+    const long long n = c.total * c.heads_qk * (c.d_k / 4) * 2;
+    const unsigned blocks = (unsigned)std::min<long long>((n + 255) / 256, 32ll * sm_count(c.device));
+    scan_shared_kernel<<<blocks, 256, 0, cs>>>(p, parts_q, parts_k, c.d_k);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e);
+}
+
+lores_status lores_scan_check_errors(const lores_scan_config *cfg, const void *workspace, void *stream) {
+  if (!cfg || !workspace || cfg->device < 0) return LORES_ERR_INVALID_ARG;
+  DeviceGuard guard(cfg->device);
+  if (!guard.ok) return LORES_ERR_CUDA;
+  unsigned f = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&f, workspace, sizeof f, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_status(e);
+  return f ? LORES_ERR_INVALID_ARG : LORES_OK;
+}
+
+}  // extern "C"

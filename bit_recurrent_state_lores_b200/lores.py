@@ -25,6 +25,11 @@ LORES_ERR_CORRUPT = 7
 LORES_ERR_INDEX = 8
 
 
+LORES_F32 = 0
+LORES_BF16 = 1
+LORES_F16 = 2
+
+
 class LoresError(RuntimeError):
     def __init__(self, status, where):
         self.status = int(status)
@@ -46,6 +51,14 @@ class lores_layout(C.Structure):
                 ("units_per_step", C.c_int32), ("grid", C.c_int32), ("smem_bytes", C.c_int32),
                 ("codes_dev", C.c_void_p), ("scales_dev", C.c_void_p),
                 ("step_kernel", C.c_int32)]
+
+
+class lores_scan_config(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("total", C.c_int64), ("max_len", C.c_int64),
+                ("heads", C.c_int32), ("heads_qk", C.c_int32), ("d_k", C.c_int32),
+                ("d_v", C.c_int32), ("delta", C.c_int32), ("dtype", C.c_int32),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("o_stride", C.c_int64), ("device", C.c_int32)]
 
 
 def load_library(path=LIB_PATH):
@@ -70,6 +83,12 @@ def load_library(path=LIB_PATH):
                                             P, P]),
         "lores_dequant_state": (I32, [P, P, P]),
         "lores_load_state": (I32, [P, P, U64, P]),
+        "lores_write_states": (I32, [P, I32, P, P, I32, U64, P]),
+        "lores_read_states": (I32, [P, I32, P, P, I32, P]),
+        "lores_scan_workspace": (I32, [C.POINTER(lores_scan_config), I32, C.POINTER(U64)]),
+        "lores_scan_forward": (I32, [C.POINTER(lores_scan_config)] + [P] * 10 + [U64, P]),
+        "lores_scan_backward": (I32, [C.POINTER(lores_scan_config)] + [P] * 16 + [U64, P]),
+        "lores_scan_check_errors": (I32, [C.POINTER(lores_scan_config), P, P]),
         "lores_export_codes": (I32, [P, P, P, P]),
         "lores_load_codes": (I32, [P, P, P, P]),
         "lores_get_layout": (I32, [P, C.POINTER(lores_layout), P]),
@@ -209,6 +228,83 @@ def lores_dequant_state(h, out, stream=None):
 def lores_load_state(h, S, step, stream=None):
     _check(_lib.lores_load_state(h, _ptr(S), step & (2**64 - 1), _stream(stream)),
            "lores_load_state")
+
+
+def _dtype(x):
+    """A lores_dtype from an int, a torch dtype, or a tensor of one."""
+    if isinstance(x, int):
+        return x
+    name = str(getattr(x, "dtype", x)).replace("torch.", "")
+    try:
+        return {"float32": LORES_F32, "bfloat16": LORES_BF16, "float16": LORES_F16}[name]
+    except KeyError:
+        raise TypeError(f"no lores_dtype for {x}") from None
+
+
+def lores_write_states(h, n, slots, S, step, dtype=None, stream=None):
+    """Quantize S [n, H, d_v, d_k] into slots (int32 tensor [n] on the device, or None).
+    dtype: of S; taken from the tensor where it is one."""
+    _check(_lib.lores_write_states(h, int(n), _ptr(slots), _ptr(S),
+                                   _dtype(S if dtype is None else dtype), step & (2**64 - 1),
+                                   _stream(stream)), "lores_write_states")
+
+
+def lores_read_states(h, n, slots, out, dtype=None, stream=None):
+    """Dequantize slots into out [n, H, d_v, d_k]; dtype as for lores_write_states."""
+    _check(_lib.lores_read_states(h, int(n), _ptr(slots), _ptr(out),
+                                  _dtype(out if dtype is None else dtype), _stream(stream)),
+           "lores_read_states")
+
+
+def make_scan_config(n_seq, total, heads, d_k, d_v, heads_qk=0, delta=1, dtype=LORES_F32,
+                     max_len=0, q_stride=0, k_stride=0, v_stride=0, o_stride=0, device=0):
+    """A lores_scan_config; dtype may be a torch dtype."""
+    return lores_scan_config(n_seq, total, max_len, heads, heads_qk, d_k, d_v, delta,
+                             _dtype(dtype), q_stride, k_stride, v_stride, o_stride, device)
+
+
+def lores_scan_workspace(cfg, backward=False):
+    """Bytes of device workspace of a call with this configuration."""
+    n = C.c_uint64()
+    _check(_lib.lores_scan_workspace(C.byref(cfg), int(bool(backward)), C.byref(n)),
+           "lores_scan_workspace")
+    return n.value
+
+
+def _work(workspace, nbytes):
+    if nbytes is None:
+        nbytes = workspace.numel() * workspace.element_size()
+    return _ptr(workspace), int(nbytes)
+
+
+def lores_scan_forward(cfg, q, k, v, log_alpha, beta, offsets, state_in, o, state_out, workspace,
+                       workspace_bytes=None, stream=None):
+    """The state scan.  workspace: a device tensor of lores_scan_workspace(cfg) bytes (or a
+    pointer and workspace_bytes)."""
+    _check(_lib.lores_scan_forward(C.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                                   _ptr(beta), _ptr(offsets), _ptr(state_in), _ptr(o),
+                                   _ptr(state_out), *_work(workspace, workspace_bytes),
+                                   _stream(stream)), "lores_scan_forward")
+
+
+def lores_scan_backward(cfg, q, k, v, log_alpha, beta, offsets, state_in, d_o, d_state_out, dq, dk,
+                        dv, dlog_alpha, dbeta, d_state_in, workspace, workspace_bytes=None,
+                        stream=None):
+    """Gradients of the state scan.  workspace: lores_scan_workspace(cfg, backward=True) bytes."""
+    _check(_lib.lores_scan_backward(C.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                                    _ptr(beta), _ptr(offsets), _ptr(state_in), _ptr(d_o),
+                                    _ptr(d_state_out), _ptr(dq), _ptr(dk), _ptr(dv),
+                                    _ptr(dlog_alpha), _ptr(dbeta), _ptr(d_state_in),
+                                    *_work(workspace, workspace_bytes), _stream(stream)),
+           "lores_scan_backward")
+
+
+def lores_scan_check_errors(cfg, workspace, stream=None):
+    """LORES_OK, or LORES_ERR_INVALID_ARG if the last call found offsets that do not fit."""
+    st = _lib.lores_scan_check_errors(C.byref(cfg), _ptr(workspace), _stream(stream))
+    if st not in (LORES_OK, LORES_ERR_INVALID_ARG):
+        raise LoresError(st, "lores_scan_check_errors")
+    return st
 
 
 def lores_export_codes(h, codes, scales, stream=None):

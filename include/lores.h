@@ -55,6 +55,9 @@ typedef enum {
     LORES_ERR_INDEX = 8          /* index-checked build: an access fell outside its buffer */
 } lores_status;
 
+/* Element types of the calls that take more than fp32. */
+typedef enum { LORES_F32 = 0, LORES_BF16 = 1, LORES_F16 = 2 } lores_dtype;
+
 typedef struct lores_handle lores_handle;
 
 /* Create-time description of one recurrent layer's state for a batch. */
@@ -248,6 +251,25 @@ lores_status lores_dequant_state(lores_handle *h, float *out, void *stream);
  * (fp32 heads copy S).  Used to start from a warmed-up fp32 state.  Asynchronous. */
 lores_status lores_load_state(lores_handle *h, const float *S, uint64_t step, void *stream);
 
+/* The same for chosen sequences: entry i of a list of n (0 .. B) is the state of sequence
+ * (slot) slots[i] of the handle, [H, d_v, d_k] of dtype (a lores_dtype).  A serving engine moves single
+ * sequences in and out of a running batch with them (a prompt's last state in, a paused
+ * sequence out and in again), and carries states through lores_scan_forward.
+ *   slots   device int32 [n], or NULL for slots 0 .. n-1.  An entry whose slot is outside
+ *           0 .. B-1 (-1, say) is skipped: nothing is written for it, neither to the pool nor
+ *           to `out`.
+ * lores_write_states quantizes with the step's quantizer and the dither of `step` (the slot's
+ * result is that of lores_load_state, bit for bit); where a slot is named twice the later
+ * entry counts; a row that holds inf, NaN or a magnitude above 2^100 is stored as zero and
+ * raises the sticky NONFINITE flag (fp32 heads copy it).  lores_read_states writes code * scale,
+ * rounded to dtype.  The other slots are untouched.  Asynchronous, allocation-free, capturable.
+ * Errors: INVALID_ARG (NULL or misaligned pointers, n outside 0 .. B, dtype); UNSUPPORTED
+ * (lores_write_states on a key-axis handle); CUDA. */
+lores_status lores_write_states(lores_handle *h, int32_t n, const int32_t *slots, const void *S,
+                                int32_t dtype, uint64_t step, void *stream);
+lores_status lores_read_states(lores_handle *h, int32_t n, const int32_t *slots, void *out,
+                               int32_t dtype, void *stream);
+
 /* Copy the raw state out: codes (layout_.code_bytes bytes; per sequence the heads'
  * tiles back to back in head order; a tile is row-major [d_v][d_k] bytes of 5- to
  * 8-bit codes (two's complement), or [d_v][d_k/2] bytes of 4-bit codes with the even
@@ -325,6 +347,97 @@ lores_status lores_debug_last_flags(lores_handle *h, uint32_t *flags);
  * [0, 1] or bits outside 4..8 and 32. */
 lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, float frac_high,
                                         int32_t bits_high, int32_t bits_low, int32_t *out_bits);
+
+/* ---------------------------------------------------------------------------------------
+ * The state scan: the recurrence over whole runs of tokens, and its backward pass
+ * ---------------------------------------------------------------------------------------
+ * lores_scan_forward applies the decode step's recurrence (General recurrence form) to runs
+ * of tokens of many sequences, with an fp32 state and no quantizer between tokens: what a
+ * model does over a prompt before decoding, over a few drafted tokens, or in training.  With
+ * lores_read_states and lores_write_states it carries the states of a handle over a prompt:
+ * read slots -> scan -> write slots -> decode steps.
+ *
+ *   S'_t = a_t S_{t-1};   S_t = S'_t + beta_t (v_t - delta S'_t k_t) k_t^T;   o_t = S_t q_t,
+ *   a_t = exp(log_alpha_t)
+ *
+ * Sequences are packed one after another: sequence i holds tokens offsets[i] ..
+ * offsets[i+1] - 1 of `total`.  Decay is one scalar per head and token, given as its natural
+ * logarithm: 0 keeps the state, -infinity drops it (a_t = 0).  A handle's alpha is
+ * exp(log_alpha).
+ *
+ * There is no handle: the caller owns every buffer, and the calls allocate nothing, so they
+ * may be captured into a CUDA graph.  Two calls may share a workspace only if they are ordered
+ * on the GPU.
+ *
+ * Accuracy.  Products run on the tensor cores on operands of 16 bits of significand (two bf16 parts;
+ * bf16 inputs are exact), sums and the state are fp32: outputs are within 1e-5 (relative
+ * L2) of the recurrence in exact arithmetic, before their rounding to `dtype`, while
+ * |k_t|^2 beta_t < 2 holds (the domain of the recurrence).  An infinity or NaN in a token's
+ * inputs may turn the outputs of the whole 64-token chunk that holds it (counted from the
+ * sequence's start), and what follows, to NaN; other sequences are not touched. */
+typedef struct {
+    int32_t n_seq;      /* sequences, >= 1                                                   */
+    int64_t total;      /* tokens of all of them, 0 .. 2^31 - 1                              */
+    int64_t max_len;    /* no sequence is longer than this (0: total).  At most 16 (or        */
+                        /* d_k = 256) selects the token-by-token kernel                      */
+    int32_t heads;      /* H: heads of v, o, the gates and the states                        */
+    int32_t heads_qk;   /* heads of q and k; divides H (0: H).  Head h reads head            */
+                        /* h / (H / heads_qk); dq and dk are summed over such heads           */
+    int32_t d_k;        /* 16, 32, 64, 128; the forward pass also 256                        */
+    int32_t d_v;        /* multiple of 4, 4..4096                                            */
+    int32_t delta;      /* 1: delta rule; 0: none                                            */
+    int32_t dtype;      /* lores_dtype of q, k, v, o and of their gradients                  */
+    int64_t q_stride;   /* elements from token to token (0: heads * width); a multiple of 4,  */
+    int64_t k_stride;   /* at least heads * width.  A token's heads lie back to back.         */
+    int64_t v_stride;   /* dq, dk, dv, d_o have the strides of q, k, v, o                    */
+    int64_t o_stride;
+    int32_t device;     /* CUDA device ordinal                                               */
+} lores_scan_config;
+
+/* Bytes of workspace that a call with this configuration needs (backward: 0 or 1), at least
+ * 256.  Host only.  Errors: INVALID_ARG, UNSUPPORTED (d_k = 256 with backward = 1). */
+lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward, uint64_t *bytes);
+
+/*   q, k       [total, heads_qk, d_k] of dtype, strides as in cfg, k of unit norm (not
+ *              renormalised here)
+ *   v          [total, H, d_v] of dtype
+ *   log_alpha  [total, H] fp32, <= 0;   beta [total, H] fp32
+ *   offsets    device int32 [n_seq + 1], or NULL: n_seq sequences of total / n_seq tokens.
+ *              A sequence that does not satisfy 0 <= offsets[i] <= offsets[i+1] <= total with
+ *              at most max_len tokens is taken as empty and reported by
+ *              lores_scan_check_errors; sequences must not overlap.
+ *   state_in   [n_seq, H, d_v, d_k] fp32, or NULL for zero states
+ *   o          [total, H, d_v] of dtype; rows of tokens in no sequence are left as they were
+ *   state_out  as state_in, may be the same buffer; NULL: not wanted.  An empty sequence's
+ *              state is copied.
+ *   workspace  workspace_bytes >= lores_scan_workspace(cfg, 0) of device memory
+ * All pointers 16-byte aligned (gates and offsets 4-byte).  Asynchronous on `stream`.
+ * Errors: INVALID_ARG (shapes, strides, NULL or misaligned pointers, workspace too small, NULL
+ * offsets where n_seq does not divide total), UNSUPPORTED (device without sm_100), CUDA. */
+lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, const void *k,
+                                const void *v, const float *log_alpha, const float *beta,
+                                const int32_t *offsets, const float *state_in, void *o,
+                                float *state_out, void *workspace, uint64_t workspace_bytes,
+                                void *stream);
+
+/* Gradients of the same call.  d_o [total, H, d_v] of dtype and d_state_out (fp32, NULL: zero)
+ * are the gradients of o and state_out; dq, dk, dv (dtype), dlog_alpha, dbeta [total, H] fp32
+ * and d_state_in (fp32, may be NULL, may be d_state_out's buffer) receive those of the inputs.
+ * The forward pass is recomputed from the inputs; nothing of an earlier call is used.  Every
+ * sum has a fixed order, so equal calls give equal bits.  Where log_alpha is below -1000 its
+ * gradient is zero.  Rows of tokens in no sequence are left as they were.  Errors as above;
+ * UNSUPPORTED for d_k = 256. */
+lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, const void *k,
+                                 const void *v, const float *log_alpha, const float *beta,
+                                 const int32_t *offsets, const float *state_in, const void *d_o,
+                                 const float *d_state_out, void *dq, void *dk, void *dv,
+                                 float *dlog_alpha, float *dbeta, float *d_state_in,
+                                 void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Wait for `stream` and report what the last call on this workspace found: INVALID_ARG if a
+ * sequence's offsets did not fit, else OK. */
+lores_status lores_scan_check_errors(const lores_scan_config *cfg, const void *workspace,
+                                     void *stream);
 
 /* Static English name of a status code. */
 const char *lores_status_string(lores_status s);
