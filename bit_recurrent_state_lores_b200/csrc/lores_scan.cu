@@ -61,10 +61,8 @@ int width_index(int dk) {
 // A configuration with its defaults filled in.
 struct Shape {
   lores_scan_config c;
-  int np, dvp, n_slots, rec_width;
+  int np, dvp, n_slots;
   bool recurrent;
-  bool raw[3];                         // q, k, v (and d_o like v) need planes of their own
-  bool raw_do;
 };
 
 lores_status shape_of(const lores_scan_config *cfg, bool backward, Shape &s) {
@@ -88,13 +86,10 @@ lores_status shape_of(const lores_scan_config *cfg, bool backward, Shape &s) {
     if (*st[i] < width || *st[i] % 4 || *st[i] > (1ll << 40)) return LORES_ERR_INVALID_ARG;
   }
   if (backward && c.d_k == 256) return LORES_ERR_UNSUPPORTED;
-  s.np = c.dtype == LORES_BF16 ? 1 : 2;
+  s.np = c.dtype == LORES_F32 ? 2 : 1;           // fp16 planes that hold the inputs
   s.dvp = (c.d_v + 15) / 16 * 16;
   s.n_slots = (int)(c.total / kChunk + c.n_seq);
   s.recurrent = !backward && (c.max_len <= kRecurrentMost || c.d_k == 256);
-  for (int i = 0; i < 3; ++i)
-    s.raw[i] = s.np == 2 || *st[i] % 8 || (i == 2 && c.d_v % 8);
-  s.raw_do = s.np == 2 || c.o_stride % 8 || c.d_v % 8;
   return LORES_OK;
 }
 
@@ -110,48 +105,33 @@ struct Carver {
   }
 };
 
-void planes_of(Carver &w, const Shape &s, bool raw, const void *src, long long stride, int heads, int dim,
-               Planes &out, Raw &r) {
-  r.src = nullptr;
-  if (!raw) {
-    out = {static_cast<const __nv_bfloat16 *>(src), nullptr, stride, dim};
-    return;
-  }
-  const int dimp = (dim + 15) / 16 * 16;
-  const unsigned long long n = (unsigned long long)s.c.total * heads * dimp;
-  r = {src, stride, heads, dim, dimp, w.take<__nv_bfloat16>(n), nullptr};
-  if (s.np == 2) r.lo = w.take<__nv_bfloat16>(n);
-  out = {r.hi, r.lo, (long long)heads * dimp, dimp};
-}
-
-// Fills the parameters and returns the bytes of workspace.
-unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, const void *q, const void *k,
-                          const void *v, const void *d_o, ScanParams &p) {
+// Lays the workspace out for the call and returns its bytes.
+unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, ScanParams &p) {
   const lores_scan_config &c = s.c;
   Carver w{ws};
   p.flag = reinterpret_cast<unsigned *>(ws);
   if (s.recurrent) return w.at;
-  planes_of(w, s, s.raw[0], q, c.q_stride, c.heads_qk, c.d_k, p.q, p.raw[0]);
-  planes_of(w, s, s.raw[1], k, c.k_stride, c.heads_qk, c.d_k, p.k, p.raw[1]);
-  planes_of(w, s, s.raw[2], v, c.v_stride, c.heads, c.d_v, p.v, p.raw[2]);
-  if (backward) planes_of(w, s, s.raw_do, d_o, c.o_stride, c.heads, c.d_v, p.dO, p.raw[3]);
   const unsigned long long recs = (unsigned long long)s.n_slots * c.heads, sq = 2 * kChunk * kChunk,
-                           tile = 2ull * kChunk * c.d_k;
+                           tile = 2ull * kChunk * c.d_k, rows = (unsigned long long)s.dvp;
+  p.khat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
+  p.qhat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
   p.gates = w.take<float>(recs * kGateFloats);
-  p.pp = w.take<__nv_bfloat16>(recs * sq);
+  if (!backward || !c.delta) p.pp = w.take<__half>(recs * sq);
   if (c.delta) {
-    p.tm = w.take<__nv_bfloat16>(recs * sq);
-    p.kt = w.take<__nv_bfloat16>(recs * tile);
+    p.tm = w.take<__half>(recs * sq);
+    p.kt = w.take<__half>(recs * tile);
   }
   if (!backward) return w.at;
   if (c.delta) {
-    p.z = w.take<__nv_bfloat16>(recs * sq);
-    p.kb = w.take<__nv_bfloat16>(recs * tile);
+    p.z = w.take<__half>(recs * sq);
+    p.kb = w.take<__half>(recs * tile);
   }
-  p.s0 = w.take<__nv_bfloat16>(recs * 2 * s.dvp * c.d_k);
-  p.dd = w.take<__nv_bfloat16>(recs * 2 * s.dvp * c.d_k);
-  p.et = w.take<__nv_bfloat16>(recs * 2 * s.dvp * kChunk);
-  p.rt = w.take<__nv_bfloat16>(recs * 2 * s.dvp * kChunk);
+  p.s0 = w.take<__half>(recs * 2 * rows * c.d_k);
+  p.dd = w.take<__half>(recs * 2 * rows * c.d_k);
+  p.et = w.take<__half>(recs * 2 * rows * kChunk);
+  p.rt = w.take<__half>(recs * 2 * rows * kChunk);
+  p.fscale = w.take<float>(recs * (rows / 16));
+  p.bscale = w.take<float>(recs * (rows / 16));
   if (c.heads != c.heads_qk) {
     const unsigned long long n = (unsigned long long)c.total * c.heads * c.d_k;
     p.dq = w.take<float>(n);
@@ -172,7 +152,14 @@ ScanParams params_of(const Shape &s) {
   p.n_slots = s.n_slots;
   p.max_len = (int)c.max_len;
   p.total = c.total;
+  p.q_stride = c.q_stride;
+  p.k_stride = c.k_stride;
+  p.v_stride = c.v_stride;
   p.o_stride = c.o_stride;
+  // rows of a 16-bit type are 16-byte aligned where strides and widths are multiples of 8
+  p.qk16 = c.dtype == LORES_F32 || (c.q_stride % 8 == 0 && c.k_stride % 8 == 0);
+  p.v16 = c.dtype == LORES_F32 || (c.v_stride % 8 == 0 && c.d_v % 8 == 0);
+  p.o16 = c.dtype == LORES_F32 || (c.o_stride % 8 == 0 && c.d_v % 8 == 0);
   p.stages = 2;
   return p;
 }
@@ -220,58 +207,46 @@ lores_status device_ok(int device) {
   return LORES_OK;
 }
 
-// Compute warps (16 value rows each) per CTA of the chunk walks: as many as share one fetch
-// of a chunk's tiles, but few enough that the CTAs fill the SMs.
-int walk_warps(const Shape &s) {
+// How a walk over the chunks is cut: 16-row blocks per CTA (rb) and warps per block (nh).  The chain
+// from chunk to chunk bounds it while there are fewer blocks than SM quarters, so two
+// warps then share a block; beyond that a warp per block needs no exchange.
+struct Walk {
+  int rb, nh;
+};
+Walk walk_of(const Shape &s) {
   const long long walks = (long long)s.c.n_seq * s.c.heads;
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
-  int w = 4;
-  while (w > 1 && (blocks < w || walks * ((blocks + w - 1) / w) < sms * 3 / 4)) w >>= 1;
+  Walk w{kWalkWarps, 1};
+  if (s.c.d_k >= 32 && walks * blocks <= 4ll * sms) w = {kWalkWarps / 2, 2};
+  while (w.rb > 1 && (blocks < w.rb || walks * ((blocks + w.rb - 1) / w.rb) < sms * 3 / 4)) w.rb >>= 1;
   return w;
 }
 
 bool aligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3u) == 0; }
 bool given16(const void *x, bool needed) { return aligned16(x) && (x || !needed); }
 
-// Planes and per-chunk matrices.
 cudaError_t run_prep(const Shape &s, bool backward, const ScanParams &p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
-  long long most = 0;
-  for (const Raw &r : p.raw)
-    if (r.src) most = std::max<long long>(most, c.total * r.heads * (r.dimp / 4));
-  if (most) {
-    const unsigned blocks = (unsigned)std::min<long long>((most + 255) / 256, 16ll * sm_count(c.device));
-    scan_planes_kernel<<<dim3(blocks, backward ? 4 : 3), 256, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
   static std::atomic<unsigned long long> raised[4][2][2][2];
-  const int wi = width_index(c.d_k), ld = c.d_k + 8;
-  const int smem = 2 * s.np * kChunk * ld * 2 + kChunk * kLdF * 4 * 2 + kChunk * 8 + kChunk * 4 * 4;
+  const int wi = width_index(c.d_k);
   return launch(kernels().by_width[wi].prep[s.np - 1][c.delta][backward], dim3(s.n_slots, c.heads), kPrepThreads,
-                smem, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
+                prep_layout(c.d_k, s.np).bytes, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
 }
 
-cudaError_t run_chain(const Shape &s, bool save, ScanParams p, cudaStream_t st) {
+// what = 0: forward, 1: the backward pass's recomputation, 2: reverse
+cudaError_t run_walk(const Shape &s, int what, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
-  static std::atomic<unsigned long long> raised[4][2][2][2];
-  const int wi = width_index(c.d_k), w = walk_warps(s);
-  const int stage = chain_layout(c.d_k, s.np, w, c.delta, !save).bytes;
-  p.stages = 2 * stage <= kMaxShared ? 2 : 1;
-  return launch(kernels().by_width[wi].chain[s.np - 1][c.delta][save],
-                dim3(c.n_seq * c.heads, (s.dvp / 16 + w - 1) / w), 32 * (w + kLoadWarps), p.stages * stage, st,
-                c.device, p, raised[wi][s.np - 1][c.delta][save]);
-}
-
-cudaError_t run_reverse(const Shape &s, ScanParams p, cudaStream_t st) {
-  const lores_scan_config &c = s.c;
-  static std::atomic<unsigned long long> raised[4][2][2];
-  const int wi = width_index(c.d_k), w = walk_warps(s);
-  const int stage = reverse_layout(c.d_k, s.np, w, c.delta).bytes;
-  p.stages = 2 * stage <= kMaxShared ? 2 : 1;
-  return launch(kernels().by_width[wi].reverse[s.np - 1][c.delta],
-                dim3(c.n_seq * c.heads, (s.dvp / 16 + w - 1) / w), 32 * (w + kLoadWarps), p.stages * stage, st,
-                c.device, p, raised[wi][s.np - 1][c.delta]);
+  static std::atomic<unsigned long long> raised[4][2][2][3][2];
+  const int wi = width_index(c.d_k);
+  const Walk w = walk_of(s);
+  const WalkLayout l = walk_layout(c.d_k, s.np, w.rb, w.nh, c.delta, what);
+  const int tail = l.part + 64;
+  p.rb = w.rb;
+  p.stages = 2 * l.bytes + tail <= kMaxShared ? 2 : 1;
+  const ScanKernels &k = kernels().by_width[wi];
+  const ScanFn fn = what == 2 ? k.reverse[s.np - 1][c.delta][w.nh - 1] : k.chain[s.np - 1][c.delta][what][w.nh - 1];
+  return launch(fn, dim3(c.n_seq * c.heads, (s.dvp / 16 + w.rb - 1) / w.rb), 32 * (w.rb * w.nh + kLoadWarps),
+                p.stages * l.bytes + tail, st, c.device, p, raised[wi][s.np - 1][c.delta][what][w.nh - 1]);
 }
 
 cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
@@ -305,7 +280,7 @@ lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward
   const lores_status st = shape_of(cfg, backward != 0, s);
   if (st != LORES_OK) return st;
   ScanParams p = params_of(s);
-  *bytes = layout(s, backward != 0, nullptr, nullptr, nullptr, nullptr, nullptr, p);
+  *bytes = layout(s, backward != 0, nullptr, p);
   return LORES_OK;
 }
 
@@ -319,12 +294,15 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
   if (st != LORES_OK) return st;
   if (!given16(o, s.c.total > 0) || !given16(state_out, false)) return LORES_ERR_INVALID_ARG;
   ScanParams p = params_of(s);
-  if (layout(s, false, static_cast<uint8_t *>(workspace), q, k, v, nullptr, p) > workspace_bytes)
+  if (layout(s, false, static_cast<uint8_t *>(workspace), p) > workspace_bytes)
     return LORES_ERR_INVALID_ARG;
   const lores_scan_config &c = s.c;
   if ((st = device_ok(c.device)) != LORES_OK) return st;
   DeviceGuard guard(c.device);
   if (!guard.ok) return LORES_ERR_CUDA;
+  p.q = q;
+  p.k = k;
+  p.v = v;
   p.offsets = offsets;
   p.log_alpha = log_alpha;
   p.beta = beta;
@@ -333,8 +311,6 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
   p.o = o;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (s.recurrent) {
-    p.uq = q; p.uk = k; p.uv = v;
-    p.uq_stride = c.q_stride; p.uk_stride = c.k_stride; p.uv_stride = c.v_stride;
     const long long lanes = (long long)c.n_seq * c.heads * (c.d_v / kRecRows) * (c.d_k / 16);
     const long long blocks = (lanes + kRecThreads - 1) / kRecThreads;
     if (blocks > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
@@ -342,7 +318,7 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
     return cuda_status(cudaGetLastError());
   }
   cudaError_t e = run_prep(s, false, p, cs);
-  if (e == cudaSuccess) e = run_chain(s, false, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, 0, p, cs);
   return cuda_status(e);
 }
 
@@ -361,20 +337,23 @@ lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, co
       !given16(d_state_in, false))
     return LORES_ERR_INVALID_ARG;
   ScanParams p = params_of(s);
-  if (layout(s, true, static_cast<uint8_t *>(workspace), q, k, v, d_o, p) > workspace_bytes)
+  if (layout(s, true, static_cast<uint8_t *>(workspace), p) > workspace_bytes)
     return LORES_ERR_INVALID_ARG;
   const lores_scan_config &c = s.c;
   if ((st = device_ok(c.device)) != LORES_OK) return st;
   DeviceGuard guard(c.device);
   if (!guard.ok) return LORES_ERR_CUDA;
+  p.q = q;
+  p.k = k;
+  p.v = v;
   p.offsets = offsets;
   p.log_alpha = log_alpha;
   p.beta = beta;
   p.state_in = state_in;
   p.d_state_out = d_state_out;
   p.d_state_in = d_state_in;
-  p.o = dv;
-  p.o_stride = c.v_stride;
+  p.o = const_cast<void *>(d_o);
+  p.dv = dv;
   p.dlog_alpha = dlog_alpha;
   p.dbeta = dbeta;
   p.parts = c.heads != c.heads_qk;
@@ -383,12 +362,10 @@ lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, co
     p.dq = dq;
     p.dk = dk;
   }
-  p.dq_stride = c.q_stride;
-  p.dk_stride = c.k_stride;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = run_prep(s, true, p, cs);
-  if (e == cudaSuccess) e = run_chain(s, true, p, cs);
-  if (e == cudaSuccess) e = run_reverse(s, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, 1, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, 2, p, cs);
   if (e == cudaSuccess) e = run_grads(s, p, cs);
   if (e == cudaSuccess && p.parts && any) {
     p.dq = dq;

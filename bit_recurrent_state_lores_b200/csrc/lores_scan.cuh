@@ -8,24 +8,28 @@
 //   L_ts = dec_ts k_t.k_s (s < t)      P_ts = dec_ts q_t.k_s b_s (s <= t)
 //   Tm   = (I + d L diag(b))^-1        E = Tm (V - d diag(e^G) K S0^T)
 //   O    = diag(e^G) Q S0^T + P E      S_C = e^{G_C} S0 + (diag(w) E)^T K,  w = b e^{G_C - G}
-// Only S0 -> S_C is sequential, so the work is split in three:
-//   scan_planes   inputs that are not aligned bf16 rows -> one or two bf16 planes (below)
+// Only S0 -> S_C is sequential, so the work is split in two:
 //   scan_prep     all chunks at once: gates, Tm, P, Kt = -d Tm diag(e^G) K (and, for the
 //                 backward pass, Z = P Tm and Kb = Tm^T diag(w) K)
 //   scan_chain    per (sequence, head, block of value rows): E^T = S0 Kt^T + (Tm V)^T, O^T and
 //                 S_C, chunk after chunk.  Value rows are independent (as in the decode
-//                 step), so a warp owns 16 of them, keeps S [16][d_k] in its accumulators and
-//                 feeds it back as the next product's left operand without leaving registers.
+//                 step), so one or two warps own 16 of them, keep S [16][d_k] in their
+//                 accumulators and feed it back as the next product's left operand
+//                 without leaving registers.
 // Backward, D = dL/dS_C:
 //   R   = Z^T dO + Kb D^T (= dV)       D0 = e^{G_C} D + (diag(e^G) dO)^T Q - d (diag(e^G) R)^T K
 //   scan_reverse  the same walk backwards over R and D;
 //   scan_grads    all chunks at once: dQ, dK and the gates' gradients from S0, D, E, R.
 //
-// Precision.  The tensor cores multiply bf16 and add fp32.  Every fp32 operand x is given as two
-// bf16 planes, hi = bf16(x) and lo = bf16(x - hi) (16 bits of significand, 2^-18 at worst), and a product is
-// hi hi + hi lo + lo hi; a bf16 input is exact as one plane.  So states, gates' gradients and
-// everything between two products keep an error near 1e-6, which one bf16 product (2^-9)
-// could not.  The state itself and every sum stay in fp32.
+// Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
+// as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
+// 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi; 16-bit inputs are
+// exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
+// K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
+// operands by one scale per 16 value rows and chunk (largest entry of S0 and V, or of D and
+// dO, in [2^6, 2^7)).  The error of states and gradients stays near 1e-7; two bf16
+// planes would leave 3e-6 to 1e-5, one fp16 plane 2e-4.  Products that only reach a 16-bit
+// output (Q S0^T and P E) use one plane.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -36,59 +40,45 @@ namespace lores {
 namespace scan {
 
 constexpr int kChunk = 64;
-constexpr int kLdC = kChunk + 8;       // row stride of a [64][64] plane (16-byte rows apart: no
-                                       // bank conflict of the 8 rows that ldmatrix reads)
+constexpr int kLdC = kChunk + 8;       // row stride of a [64][64] plane in shared memory (rows 16
+                                       // bytes apart modulo 128: the 8 rows that ldmatrix
+                                       // reads fall into different banks)
 constexpr int kPrepThreads = 128;
 constexpr int kGradThreads = 256;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
 
-// bf16 planes of a token-major tensor: element (token, head, i) at token * stride +
-// head * hstride + i.  lo is null for one plane.
-struct Planes {
-  const __nv_bfloat16 *hi, *lo;
-  long long stride;
-  int hstride;
-};
-
-// A user's tensor that scan_planes turns into planes.
-struct Raw {
-  const void *src;
-  long long stride;                    // elements between tokens
-  int heads, dim, dimp;                // dimp: dim rounded up to 16 (zeros behind dim)
-  __nv_bfloat16 *hi, *lo;              // [total][heads][dimp]
-};
-
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
+  int rb;                              // walks: blocks of 16 value rows per CTA
+  int qk16, v16, o16;                  // 16-byte accesses to q and k, v (and dv), o (or d_o) rows
   long long total;
   const int *offsets;
-  Planes q, k, v, dO;
-  Raw raw[4];
+  const void *q, *k, *v;               // the caller's tensors
+  long long q_stride, k_stride, v_stride, o_stride;
   const float *log_alpha, *beta;       // [total][H]
   const float *state_in;               // [n_seq][H][d_v][d_k] or null
   float *state_out;                    // likewise or null
-  void *o;                             // forward: o; backward: dv
-  long long o_stride;
+  void *o;                             // forward: o; backward: d_o (read)
   unsigned *flag;
-  // workspace, records of one (slot, head)
-  float *gates;                        // [64] e^G, w, b, e^(G_C - G); [64] G (double)
-  __nv_bfloat16 *kt, *kb;              // [2][64][d_k]
-  __nv_bfloat16 *tm, *pp, *z;          // [2][64][64]
-  __nv_bfloat16 *s0, *dd;              // [2][dvp][d_k]
-  __nv_bfloat16 *et, *rt;              // [2][dvp][64]
+  // workspace, records of one (slot, head); khat, qhat of one (slot, q/k head)
+  float *gates;                        // kGateFloats
+  __half *khat, *qhat;                 // [NP][64][d_k], divided by their scales
+  __half *kt, *kb;                     // [2][64][d_k]
+  __half *tm, *pp, *z;                 // [2][64][64]
+  __half *s0, *dd;                     // [2][dvp][d_k]
+  __half *et, *rt;                     // [2][dvp][64]
+  float *fscale, *bscale;              // [dvp/16]: scales of s0 and et, of dd and rt
   // backward
   const float *d_state_out;
   float *d_state_in;
-  void *dq, *dk;                       // user's gradients, or fp32 parts [total][H][d_k]
-  long long dq_stride, dk_stride;
-  int parts;                           // dq, dk are fp32 parts of each head
+  void *dv, *dq, *dk;                  // dq, dk: the caller's, or fp32 parts [total][H][d_k]
+  int parts;                           // dq, dk are parts
   float *dlog_alpha, *dbeta;
-  // recurrent form: the user's tensors as they are
-  const void *uq, *uk, *uv;
-  long long uq_stride, uk_stride, uv_stride;
 };
 
-constexpr int kGateFloats = 4 * kChunk + 2 * kChunk;
+// Record of a chunk and head: e^G, w, b, e^(G_C - G) [64] each, G [64] (double), scales of K and Q
+constexpr int kGateFloats = 4 * kChunk + 2 * kChunk + 4;
+constexpr int kGateScales = 6 * kChunk;
 
 // -------------------------------------------------------------------------------------
 // sequences and chunk slots
@@ -115,7 +105,7 @@ __device__ __forceinline__ bool seq_range(const ScanParams &p, int i, long long 
 // the sequences is needed.
 __device__ __forceinline__ int slot_base(long long start, int i) { return (int)(start / kChunk) + i; }
 
-// The sequence and first token of a slot's chunk and its tokens (0: the slot is not used).
+// The first token of a slot's chunk and its number of tokens (0: the slot is not used).
 __device__ __forceinline__ int slot_tokens(const ScanParams &p, int slot, long long &token0) {
   int lo = 0, hi = p.n_seq - 1;
   if (!p.offsets) {
@@ -171,41 +161,42 @@ __device__ __forceinline__ void check_offsets(const ScanParams &p) {
 __device__ __forceinline__ uint32_t smem_addr(const void *x) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(x));
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const __nv_bfloat16 *row) {
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *row) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_addr(row)));
 }
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const __nv_bfloat16 *row) {
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void *row) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_addr(row)));
+}
+__device__ __forceinline__ void stsm4t(void *row, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_addr(row)),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 // Fragment loads of 16x16 blocks from row-major shared memory with row stride ld.
 //   right operand, two column tiles (r[0], r[1]: columns n0..n0+7; r[2], r[3]: n0+8..):
 //     b_rows:  stored [n][k]      b_cols: stored [k][n]
 //   left operand:
 //     a_rows:  stored [m][k]      a_cols: stored [k][m]
-__device__ __forceinline__ void b_rows(uint32_t (&r)[4], const __nv_bfloat16 *x, int ld, int n0,
-                                       int k0, int lane) {
+__device__ __forceinline__ void b_rows(uint32_t (&r)[4], const __half *x, int ld, int n0, int k0, int lane) {
   ldsm4(r, x + (n0 + ((lane >> 4) << 3) + (lane & 7)) * ld + k0 + (((lane >> 3) & 1) << 3));
 }
-__device__ __forceinline__ void b_cols(uint32_t (&r)[4], const __nv_bfloat16 *x, int ld, int k0,
-                                       int n0, int lane) {
+__device__ __forceinline__ void b_cols(uint32_t (&r)[4], const __half *x, int ld, int k0, int n0, int lane) {
   ldsm4t(r, x + (k0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + n0 + ((lane >> 4) << 3));
 }
-__device__ __forceinline__ void a_rows(uint32_t (&r)[4], const __nv_bfloat16 *x, int ld, int m0,
-                                       int k0, int lane) {
+__device__ __forceinline__ void a_rows(uint32_t (&r)[4], const __half *x, int ld, int m0, int k0, int lane) {
   ldsm4(r, x + (m0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + k0 + ((lane >> 4) << 3));
 }
-__device__ __forceinline__ void a_cols(uint32_t (&r)[4], const __nv_bfloat16 *x, int ld, int k0,
-                                       int m0, int lane) {
+__device__ __forceinline__ void a_cols(uint32_t (&r)[4], const __half *x, int ld, int k0, int m0, int lane) {
   ldsm4t(r, x + (k0 + ((lane >> 4) << 3) + (lane & 7)) * ld + m0 + (((lane >> 3) & 1) << 3));
 }
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -217,31 +208,71 @@ __device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint3
   mma(c1, a, b[2], b[3]);
 }
 
-// x, y -> packed bf16 (x low) and the packed rest.
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
-  const float rx = __fsub_rn(x, __uint_as_float(hi << 16));
-  const float ry = __fsub_rn(y, __uint_as_float(hi & 0xFFFF0000u));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(ry), "f"(rx));
+// x, y -> packed fp16 (x low).
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
+// ... and the packed rest: hi - x in one mixed-precision subtraction, rounded with its sign turned.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  hi = pack2(x, y);
+  float rx, ry;
+  asm("{\n\t.reg .f16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "sub.rn.f32.f16 %0, l, %3;\n\t"
+      "sub.rn.f32.f16 %1, h, %4;\n\t}"
+      : "=f"(rx), "=f"(ry)
+      : "r"(hi), "f"(x), "f"(y));
+  lo = pack2(-rx, -ry);
+}
+__device__ __forceinline__ float2 half2_of(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 bf162_of(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
+// A packed pair of the caller's 16-bit type.
+__device__ __forceinline__ float2 pair_of(uint32_t w, int dtype) {
+  return dtype == 1 ? bf162_of(w) : half2_of(w);
+}
 // Accumulator tiles 2j, 2j+1 (16 columns) as a left operand's planes: the layouts agree.
-__device__ __forceinline__ void split_tiles(const float (&c0)[4], const float (&c1)[4],
-                                            uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ void split_tiles(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4],
+                                            uint32_t (&lo)[4]) {
   split2(c0[0], c0[1], hi[0], lo[0]);
   split2(c0[2], c0[3], hi[1], lo[1]);
   split2(c1[0], c1[1], hi[2], lo[2]);
   split2(c1[2], c1[3], hi[3], lo[3]);
 }
+__device__ __forceinline__ void split_tiles(const float (&c0)[4], const float (&c1)[4], float by,
+                                            uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split2(c0[0] * by, c0[1] * by, hi[0], lo[0]);
+  split2(c0[2] * by, c0[3] * by, hi[1], lo[1]);
+  split2(c1[0] * by, c1[1] * by, hi[2], lo[2]);
+  split2(c1[2] * by, c1[3] * by, hi[3], lo[3]);
+}
+
+// Scales: the power of two c with m / c in [2^up, 2^(up+1)) for the magnitude m with the given
+// bits (1 for zero, limits at the ends of the range), and its inverse.
+__device__ __forceinline__ float scale_of(unsigned bits, int up, float &inv) {
+  int e = (int)(bits >> 23) - up;
+  e = bits == 0u ? 127 : max(1, min(253, e));
+  inv = __uint_as_float((unsigned)(254 - e) << 23);
+  return __uint_as_float((unsigned)e << 23);
+}
+__device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // -------------------------------------------------------------------------------------
-// asynchronous copies
+// copies
 // -------------------------------------------------------------------------------------
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool there) {
   const int n = there ? 16 : 0;        // 0: sixteen zero bytes
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp8(void *dst, const void *src, bool there) {
+  const int n = there ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -250,16 +281,34 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// rows x cols elements of bf16 -> shared rows of ld elements; rows >= there and columns >=
-// have are zeros.  cols and have are multiples of 8.
-__device__ __forceinline__ void copy_tile(__nv_bfloat16 *dst, int ld, const __nv_bfloat16 *src,
-                                          long long stride, int rows, int cols, int there, int have,
-                                          int tid, int threads) {
-  const int per = cols >> 3;
-  for (int i = tid; i < rows * per; i += threads) {
-    const int r = i / per, c = (i % per) << 3;
-    const bool in = r < there && c < have;
-    cp16(dst + r * ld + c, in ? src + r * stride + c : src, in);
+// A [ROWS][COLS] plane of a record (dense rows) into shared rows of LD elements.
+template <int ROWS, int COLS, int LD>
+__device__ __forceinline__ void copy_plane(__half *dst, const __half *src, int tid, int threads) {
+  constexpr int per = COLS / 8;
+#pragma unroll 4
+  for (int i = tid; i < ROWS * per; i += threads)
+    cp16(dst + (i / per) * LD + (i % per) * 8, src + i * 8, true);
+}
+// The lower triangle of a [64][64] plane, by 16x16 blocks (the others are not read).
+__device__ __forceinline__ void copy_lower(__half *dst, const __half *src, int tid, int threads) {
+#pragma unroll 4
+  for (int i = tid; i < kChunk * 8; i += threads) {
+    const int r = i >> 3, c = i & 7;
+    if ((c >> 1) <= (r >> 4)) cp16(dst + r * kLdC + c * 8, src + r * kChunk + c * 8, true);
+  }
+}
+// `cols` columns (a multiple of 16) of 64 token rows of the caller's tensor: rows >= n and
+// columns >= have (a multiple of 4) are zeros.  ld in elements.
+template <int SIZE>
+__device__ __forceinline__ void copy_tokens(uint8_t *dst, int ld, const uint8_t *src, long long stride, int cols,
+                                            int n, int have, bool by16, int tid, int threads) {
+  const int step = by16 ? 16 / SIZE : 8 / SIZE, per = cols / step;
+  for (int i = tid; i < kChunk * per; i += threads) {
+    const int r = i / per, c = (i % per) * step;
+    const bool in = r < n && c < have;
+    const uint8_t *s = in ? src + (r * stride + c) * SIZE : src;
+    if (by16) cp16(dst + (r * ld + c) * SIZE, s, in);
+    else cp8(dst + (r * ld + c) * SIZE, s, in);
   }
 }
 
@@ -268,18 +317,17 @@ __device__ __forceinline__ void store_as(void *base, int dtype, long long i, flo
   else if (dtype == 1) static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(x);
   else static_cast<__half *>(base)[i] = __float2half_rn(x);
 }
+// Two values of a 16-bit type, x low.
+__device__ __forceinline__ uint32_t pack_as(int dtype, float x, float y) {
+  if (dtype != 1) return pack2(x, y);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
 __device__ __forceinline__ void store_pair(void *base, int dtype, long long i, float x, float y) {
   if (dtype == 0) *reinterpret_cast<float2 *>(static_cast<float *>(base) + i) = make_float2(x, y);
-  else if (dtype == 1)
-    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(base) + i) = __floats2bfloat162_rn(x, y);
-  else *reinterpret_cast<__half2 *>(static_cast<__half *>(base) + i) = __floats2half2_rn(x, y);
+  else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + i) = pack_as(dtype, x, y);
 }
-
-// -------------------------------------------------------------------------------------
-// scan_planes: inputs -> bf16 planes
-// -------------------------------------------------------------------------------------
-// Grid (blocks over 4-element groups, tensor).  fp32 and fp16 give two planes (fp16's 11 bits
-// fit in them exactly), bf16 rows that are not 16-byte aligned one.
 __device__ __forceinline__ void load4(const void *src, int dtype, long long i, float (&x)[4]) {
   if (dtype == 0) {
     const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(src) + i));
@@ -287,34 +335,28 @@ __device__ __forceinline__ void load4(const void *src, int dtype, long long i, f
     return;
   }
   const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(src) + i));
-  if (dtype == 1) {
-    const float2 a = unpack2(w.x), b = unpack2(w.y);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  } else {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  }
+  const float2 a = pair_of(w.x, dtype), b = pair_of(w.y, dtype);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
-
-static __global__ void __launch_bounds__(256) scan_planes_kernel(const ScanParams p) {
-  const Raw r = p.raw[blockIdx.y];
-  if (!r.src) return;
-  const int per = r.dimp >> 2;
-  const long long n = p.total * r.heads * per;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const int c = (int)(i % per) << 2;
-    const long long th = i / per;
-    const int h = (int)(th % r.heads);
-    const long long t = th / r.heads;
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < r.dim) load4(r.src, p.dtype, t * r.stride + (long long)h * r.dim + c, x);
-    uint2 hi, lo;
-    split2(x[0], x[1], hi.x, lo.x);
-    split2(x[2], x[3], hi.y, lo.y);
-    const long long at = th * r.dimp + c;
-    *reinterpret_cast<uint2 *>(r.hi + at) = hi;
-    if (r.lo) *reinterpret_cast<uint2 *>(r.lo + at) = lo;
+// 8 entries of a row of the caller's tensor.
+__device__ __forceinline__ void load8(const void *src, int dtype, long long i, bool by16, float (&x)[8]) {
+  if (dtype != 0 && by16) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + i));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = pair_of(u[e], dtype);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+    load4(src, dtype, i + 4 * h, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * h + e] = y[e];
   }
 }
 
@@ -322,62 +364,110 @@ static __global__ void __launch_bounds__(256) scan_planes_kernel(const ScanParam
 // scan_prep
 // -------------------------------------------------------------------------------------
 // Grid (slot, head), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.] result, and only
-// blocks on and below the diagonal are formed.  Tm is inverted in fp32: the four diagonal
-// 16x16 blocks by forward substitution (one lane per column), then pairs of blocks joined as
-// [[A,0],[B,C]]^-1 = [[A',0],[-C'BA',C']], twice.
+// blocks on and below the diagonal are formed.  Tm = (I + A)^-1, A = L diag(b), by 16x16 blocks:
+// the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
+// forms block column j downwards, X_ij = -X_ii sum_{j <= k < i} A_ik X_kj, as
+// X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
+// product's left operand in place.
 constexpr int kLdF = kChunk + 2;       // row stride of the fp32 matrix in shared memory
+constexpr int kLdX = 24;               // row stride of a [16][16] plane
 
-template <int DK, int NP>
-constexpr int prep_smem() {
-  return (2 * NP * kChunk * (DK + 8)) * 2 + kChunk * kLdF * 4 * 2 + kChunk * 8 + kChunk * 4 * 4;
+struct PrepLayout {
+  int k, q, x, xd, f, bytes;           // q: also the planes of A (48 rows) once Q is used
+};
+__host__ __device__ constexpr PrepLayout prep_layout(int dk, int np) {
+  PrepLayout l{};
+  const int tile = np * kChunk * (dk + 8) * 2, planes = 2 * 48 * kLdC * 2;
+  l.k = 0;
+  l.q = tile;
+  l.x = l.q + (tile > planes ? tile : planes);
+  l.xd = l.x + kChunk * kLdF * 4;
+  l.f = l.xd + 4 * 2 * 16 * kLdX * 2;
+  l.bytes = l.f + (4 * kChunk + 2 * kChunk + 16) * 4;
+  return l;
 }
 
-__device__ __forceinline__ void inverse_join(float *X, float *Y, int n, int tid, int threads) {
-  // X holds, on the diagonal, inverted n x n blocks and below every second one the block B.
-  // Y is scratch of the same layout.
-  const int pairs = kChunk / (2 * n), per = n * n;
-  for (int i = tid; i < pairs * per; i += threads) {         // Y = C' B
-    const int b = i / per, r = (i % per) / n, c = i % n, o = b * 2 * n;
-    float s = 0.0f;
-    for (int m = 0; m <= r; ++m) s = fmaf(X[(o + n + r) * kLdF + o + n + m], X[(o + n + m) * kLdF + o + c], s);
-    Y[(o + n + r) * kLdF + o + c] = s;
+// Rows of K or Q of a chunk: their scale (left in *scale), planes in shared memory, and in the
+// workspace where `out` is given.
+template <int DK, int NP>
+__device__ __forceinline__ float stage_rows(const ScanParams &p, const void *src, long long stride, long long token0,
+                                            int qh, int n, __half *dst, __half *out, unsigned *red, int tid) {
+  constexpr int LD = DK + 8, PER = DK / 8;
+  unsigned m = 0;
+  for (int i = tid; i < kChunk * PER; i += kPrepThreads) {
+    const int r = i / PER, c = (i % PER) * 8;
+    if (r < n) {
+      float x[8];
+      load8(src, p.dtype, (token0 + r) * stride + (long long)qh * DK + c, p.qk16, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
+    }
   }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((tid & 31) == 0) red[tid >> 5] = m;
   __syncthreads();
-  for (int i = tid; i < pairs * per; i += threads) {         // X = -Y A'
-    const int b = i / per, r = (i % per) / n, c = i % n, o = b * 2 * n;
-    float s = 0.0f;
-    for (int m = c; m < n; ++m) s = fmaf(Y[(o + n + r) * kLdF + o + m], X[(o + m) * kLdF + o + c], s);
-    X[(o + n + r) * kLdF + o + c] = -s;
+  m = max(max(red[0], red[1]), max(red[2], red[3]));
+  float inv;
+  const float scale = scale_of(m, 0, inv);
+  for (int i = tid; i < kChunk * PER; i += kPrepThreads) {
+    const int r = i / PER, c = (i % PER) * 8;
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r < n) load8(src, p.dtype, (token0 + r) * stride + (long long)qh * DK + c, p.qk16, x);
+    uint4 hi, lo;
+    split2(x[0] * inv, x[1] * inv, hi.x, lo.x);
+    split2(x[2] * inv, x[3] * inv, hi.y, lo.y);
+    split2(x[4] * inv, x[5] * inv, hi.z, lo.z);
+    split2(x[6] * inv, x[7] * inv, hi.w, lo.w);
+    *reinterpret_cast<uint4 *>(dst + r * LD + c) = hi;
+    if (NP == 2) *reinterpret_cast<uint4 *>(dst + kChunk * LD + r * LD + c) = lo;
+    if (out) {
+      *reinterpret_cast<uint4 *>(out + r * DK + c) = hi;
+      if (NP == 2) *reinterpret_cast<uint4 *>(out + kChunk * DK + r * DK + c) = lo;
+    }
   }
-  __syncthreads();
+  return scale;
+}
+
+// Accumulators of 16 rows [m0 ..] x COLS as planes of a record with row length COLS.
+template <int TILES>
+__device__ __forceinline__ void store_planes(__half *dst, long long plane, int cols, int m0, const float (&c)[TILES][4],
+                                             int tiles, int lane) {
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+  for (int i = 0; i < TILES; ++i)
+    if (i < tiles)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t hi, lo;
+        split2(c[i][2 * h], c[i][2 * h + 1], hi, lo);
+        const long long at = (long long)(m0 + g + 8 * h) * cols + 8 * i + t2;
+        *reinterpret_cast<uint32_t *>(dst + at) = hi;
+        *reinterpret_cast<uint32_t *>(dst + plane + at) = lo;
+      }
 }
 
 template <int DK, int NP, bool DELTA, bool BWD>
-__global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) scan_prep_kernel(const ScanParams p) {
   constexpr int LD = DK + 8;
+  constexpr PrepLayout l = prep_layout(DK, NP);
   extern __shared__ __align__(16) uint8_t smem[];
-  __nv_bfloat16 *K = reinterpret_cast<__nv_bfloat16 *>(smem);       // NP planes
-  __nv_bfloat16 *Q = K + NP * kChunk * LD;
-  float *X = reinterpret_cast<float *>(Q + NP * kChunk * LD);       // Tm
-  float *Y = X + kChunk * kLdF;
-  double *G = reinterpret_cast<double *>(Y + kChunk * kLdF);
-  float *eG = reinterpret_cast<float *>(G + kChunk), *w = eG + kChunk, *be = w + kChunk,
-        *eC = be + kChunk;
+  __half *K = reinterpret_cast<__half *>(smem + l.k), *Q = reinterpret_cast<__half *>(smem + l.q);
+  __half *A16 = Q;                                                  // [2][48][kLdC]: rows 16..63 of A
+  float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then Tm
+  __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][kLdX]: X_ii
+  double *G = reinterpret_cast<double *>(smem + l.f);
+  float *eG = reinterpret_cast<float *>(G + kChunk), *w = eG + kChunk, *be = w + kChunk;
+  unsigned *red = reinterpret_cast<unsigned *>(be + 2 * kChunk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head = blockIdx.y;
   if (slot == 0 && head == 0) check_offsets(p);
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
   if (n == 0) return;
-  const int qh = head / p.share;
-#pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    copy_tile(K + c * kChunk * LD, LD, (c ? p.k.lo : p.k.hi) + token0 * p.k.stride + qh * p.k.hstride,
-              p.k.stride, kChunk, DK, n, DK, tid, kPrepThreads);
-    copy_tile(Q + c * kChunk * LD, LD, (c ? p.q.lo : p.q.hi) + token0 * p.q.stride + qh * p.q.hstride,
-              p.q.stride, kChunk, DK, n, DK, tid, kPrepThreads);
-  }
-  cp_commit();
+  const int qh = head / p.share, hq = p.H / p.share;
+  const long long rec = (long long)slot * p.H + head, qrec = (long long)slot * hq + qh;
+  const bool mine = head % p.share == 0;           // the first of the heads that share K and Q keeps them
+  float *gates = p.gates + rec * kGateFloats;
   if (warp == 0) {
     // Sums of log_alpha in 64 bits, so that the differences below keep their digits behind a
     // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
@@ -400,111 +490,198 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
     }
     const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
     const double Gt[2] = {run - a[1], run};
-    float *rec = p.gates + ((long long)slot * p.H + head) * kGateFloats;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i]));
       G[t] = Gt[i];
-      eG[t] = e; be[t] = b[i]; eC[t] = c; w[t] = b[i] * c;
-      rec[t] = e; rec[kChunk + t] = b[i] * c; rec[2 * kChunk + t] = b[i]; rec[3 * kChunk + t] = c;
-      reinterpret_cast<double *>(rec + 4 * kChunk)[t] = Gt[i];
+      eG[t] = e; be[t] = b[i]; w[t] = b[i] * c;
+      gates[t] = e; gates[kChunk + t] = b[i] * c; gates[2 * kChunk + t] = b[i]; gates[3 * kChunk + t] = c;
+      reinterpret_cast<double *>(gates + 4 * kChunk)[t] = Gt[i];
     }
   }
-  cp_wait<0>();
+  const float sk = stage_rows<DK, NP>(p, p.k, p.k_stride, token0, qh, n, K,
+                                      mine ? p.khat + qrec * (NP * kChunk * DK) : nullptr, red, tid);
+  const float sq = stage_rows<DK, NP>(p, p.q, p.q_stride, token0, qh, n, Q,
+                                      mine ? p.qhat + qrec * (NP * kChunk * DK) : nullptr, red + 4, tid);
+  if (tid == 0) {
+    gates[kGateScales] = sk;
+    gates[kGateScales + 1] = sq;
+  }
   __syncthreads();
 
-  const long long rec = (long long)slot * p.H + head;
   const int m0 = warp * 16;
-  float P[8][4], A[8][4];
+  float P[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) P[i][j] = A[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) P[i][j] = 0.0f;
+  {
+    float A[8][4];
 #pragma unroll
-  for (int ks = 0; ks < DK / 16; ++ks) {
-    uint32_t ak[NP][4], aq[NP][4];
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int c = 0; c < NP; ++c) {
-      if (DELTA) a_rows(ak[c], K + c * kChunk * LD, LD, m0, ks * 16, lane);
-      a_rows(aq[c], Q + c * kChunk * LD, LD, m0, ks * 16, lane);
-    }
+      for (int j = 0; j < 4; ++j) A[i][j] = 0.0f;
+#pragma unroll 2
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      if (np <= warp) {
-        uint32_t b[4];
-        b_rows(b, K, LD, np * 16, ks * 16, lane);
+      for (int c = 0; c < NP; ++c) {
+        if (DELTA) a_rows(ak[c], K + c * kChunk * LD, LD, m0, ks * 16, lane);
+        a_rows(aq[c], Q + c * kChunk * LD, LD, m0, ks * 16, lane);
+      }
 #pragma unroll
-        for (int c = 0; c < NP; ++c) {
-          if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], b);
-          mma2(P[2 * np], P[2 * np + 1], aq[c], b);
+      for (int np = 0; np < 4; ++np) {
+        if (np <= warp) {
+          uint32_t b[4];
+          b_rows(b, K, LD, np * 16, ks * 16, lane);
+#pragma unroll
+          for (int c = 0; c < NP; ++c) {
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], b);
+            mma2(P[2 * np], P[2 * np + 1], aq[c], b);
+          }
+          if (NP == 2) {
+            b_rows(b, K + kChunk * LD, LD, np * 16, ks * 16, lane);
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], b);
+            mma2(P[2 * np], P[2 * np + 1], aq[0], b);
+          }
         }
-        if (NP == 2) {
-          b_rows(b, K + kChunk * LD, LD, np * 16, ks * 16, lane);
-          if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], b);
-          mma2(P[2 * np], P[2 * np + 1], aq[0], b);
+      }
+    }
+    __syncthreads();                   // Q's tile becomes A's planes
+    // P (over the scale of Q) and, strictly below the diagonal, A
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i / 2 <= warp) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = m0 + g + 8 * h, s = 8 * i + t2;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float dec = s + j <= t ? expf((float)(G[t] - G[s + j])) * be[s + j] * sk : 0.0f;
+            P[i][2 * h + j] = s + j <= t ? P[i][2 * h + j] * dec : 0.0f;
+            if (DELTA) A[i][2 * h + j] = s + j < t ? A[i][2 * h + j] * dec * sk : 0.0f;
+          }
+          if (DELTA) {
+            if (i / 2 == warp) {
+              X[t * kLdF + s] = A[i][2 * h];
+              X[t * kLdF + s + 1] = A[i][2 * h + 1];
+            } else {
+              uint32_t hi, lo;
+              split2(A[i][2 * h], A[i][2 * h + 1], hi, lo);
+              *reinterpret_cast<uint32_t *>(A16 + (t - 16) * kLdC + s) = hi;
+              *reinterpret_cast<uint32_t *>(A16 + 48 * kLdC + (t - 16) * kLdC + s) = lo;
+            }
+          }
         }
       }
     }
   }
-  // decays; A below the diagonal to shared memory, P to its planes
-  __nv_bfloat16 *pp = p.pp + rec * (2 * kChunk * kChunk);
+  if (!BWD || !DELTA) {
+    // 16-bit outputs need one plane of P
+    __half *pp = p.pp + rec * (2 * kChunk * kChunk);
+    if (NP == 2 || BWD) store_planes<8>(pp, kChunk * kChunk, kChunk, m0, P, 2 * warp + 2, lane);
+    else
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i / 2 <= warp) {
+      for (int i = 0; i < 8; ++i)
+        if (i / 2 <= warp)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = m0 + g + 8 * h, s = 8 * i + t2;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float dec = s + j <= t ? expf((float)(G[t] - G[s + j])) * be[s + j] : 0.0f;
-          P[i][2 * h + j] = s + j <= t ? P[i][2 * h + j] * dec : 0.0f;
-          if (DELTA) X[t * kLdF + s + j] = s + j < t ? A[i][2 * h + j] * dec : 0.0f;
-        }
-        uint32_t hi, lo;
-        split2(P[i][2 * h], P[i][2 * h + 1], hi, lo);
-        *reinterpret_cast<uint32_t *>(pp + t * kChunk + s) = hi;
-        *reinterpret_cast<uint32_t *>(pp + kChunk * kChunk + t * kChunk + s) = lo;
-      }
-    }
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint32_t *>(pp + (m0 + g + 8 * h) * kChunk + 8 * i + t2) = pack2(P[i][2 * h], P[i][2 * h + 1]);
   }
   if (!DELTA) return;
-  __syncthreads();
-  if (lane < 16) {                     // this warp's diagonal block, column `lane`
+  __syncwarp();
+  {
+    // this warp's diagonal block: lanes c and c + 16 hold column c of its inverse
+    const int c = lane & 15;
     float x[16];
     float *B = X + m0 * kLdF + m0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float s0 = r == lane ? 1.0f : 0.0f, s1 = 0.0f;
+    for (int r = 0; r < 16; ++r) x[r] = r == c ? 1.0f : 0.0f;
 #pragma unroll
-      for (int m = 0; m < r; ++m) {
-        if (m & 1) s1 = fmaf(-B[r * kLdF + m], x[m], s1);
-        else s0 = fmaf(-B[r * kLdF + m], x[m], s0);
+    for (int r = 0; r < 15; ++r)
+#pragma unroll
+      for (int i = r + 1; i < 16; ++i) x[i] = fmaf(-B[i * kLdF + r], x[r], x[i]);
+    __syncwarp();
+    if (lane < 16) {
+      __half *d = XD + warp * (2 * 16 * kLdX);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        B[r * kLdF + c] = x[r];
+        const __half hi = __float2half_rn(x[r]);
+        d[r * kLdX + c] = hi;
+        d[16 * kLdX + r * kLdX + c] = __float2half_rn(x[r] - __half2float(hi));
       }
-      x[r] = s0 + s1;
     }
-    __syncwarp(0x0000FFFFu);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) B[r * kLdF + lane] = x[r];
   }
   __syncthreads();
-  inverse_join(X, Y, 16, tid, kPrepThreads);
-  inverse_join(X, Y, 32, tid, kPrepThreads);
-
-  // planes of Tm
-  __nv_bfloat16 *tm = p.tm + rec * (2 * kChunk * kChunk);
-  for (int i = tid; i < kChunk * kChunk / 2; i += kPrepThreads) {
-    const int r = i / (kChunk / 2), c = (i % (kChunk / 2)) * 2;
-    uint32_t hi = 0, lo = 0;
-    if ((c >> 4) <= (r >> 4)) split2(X[r * kLdF + c], X[r * kLdF + c + 1], hi, lo);
-    *reinterpret_cast<uint32_t *>(tm + r * kChunk + c) = hi;
-    *reinterpret_cast<uint32_t *>(tm + kChunk * kChunk + r * kChunk + c) = lo;
-  }
-  // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own
   {
-    float acc[DK / 8][4];
+    // block column `warp`: yh, yl[k] = planes of X_kj^T
+    uint32_t yh[4][4], yl[4][4];
+    {
+      // X_jj^T as a left operand: element (m, k) = X_jj[k][m], read transposed
+      const __half *d = XD + warp * (2 * 16 * kLdX);
+      a_cols(yh[0], d, kLdX, 0, 0, lane);
+      a_cols(yl[0], d + 16 * kLdX, kLdX, 0, 0, lane);
+    }
 #pragma unroll
-    for (int i = 0; i < DK / 8; ++i)
+    for (int di = 1; di < 4; ++di) {
+      const int i = warp + di;
+      if (i < 4) {
+        float z0[4] = {0, 0, 0, 0}, z1[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int dk = 0; dk < di; ++dk) {
+          uint32_t b[4];
+          b_rows(b, A16, kLdC, 16 * i - 16, 16 * (warp + dk), lane);
+          mma2(z0, z1, yh[dk], b);
+          mma2(z0, z1, yl[dk], b);
+          b_rows(b, A16 + 48 * kLdC, kLdC, 16 * i - 16, 16 * (warp + dk), lane);
+          mma2(z0, z1, yh[dk], b);
+        }
+        uint32_t zh[4], zl[4], b[4];
+        split_tiles(z0, z1, -1.0f, zh, zl);
+        float y0[4] = {0, 0, 0, 0}, y1[4] = {0, 0, 0, 0};
+        const __half *d = XD + i * (2 * 16 * kLdX);
+        b_rows(b, d, kLdX, 0, 0, lane);
+        mma2(y0, y1, zh, b);
+        mma2(y0, y1, zl, b);
+        b_rows(b, d + 16 * kLdX, kLdX, 0, 0, lane);
+        mma2(y0, y1, zh, b);
+        split_tiles(y0, y1, yh[di & 3], yl[di & 3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // y[c][r] -> X[16 i + r][16 warp + c]
+          const int c = g + 8 * (j >> 1), r = t2 + (j & 1);
+          X[(16 * i + r) * kLdF + m0 + c] = y0[j];
+          X[(16 * i + 8 + r) * kLdF + m0 + c] = y1[j];
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // planes of Tm (blocks on and below the diagonal)
+  __half *tm = p.tm + rec * (2 * kChunk * kChunk);
+  for (int i = tid; i < kChunk * 8; i += kPrepThreads) {
+    const int r = i >> 3, c = (i & 7) * 8;
+    if ((c >> 4) <= (r >> 4)) {
+      uint4 hi, lo;
+      const float *x = X + r * kLdF + c;
+      split2(x[0], x[1], hi.x, lo.x);
+      split2(x[2], x[3], hi.y, lo.y);
+      split2(x[4], x[5], hi.z, lo.z);
+      split2(x[6], x[7], hi.w, lo.w);
+      *reinterpret_cast<uint4 *>(tm + r * kChunk + c) = hi;
+      *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + r * kChunk + c) = lo;
+    }
+  }
+  // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own.  Two halves of the columns, so
+  // that the accumulators leave room for four CTAs per SM.
+  constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
+#pragma unroll 1
+  for (int half = 0; half < HALVES; ++half) {
+    float acc[HT][4];
+#pragma unroll
+    for (int i = 0; i < HT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
@@ -514,38 +691,30 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int t = m0 + g + 8 * (q & 1), s = ks * 16 + t2 + 8 * (q >> 1);
-          split2(-X[t * kLdF + s] * eG[s], -X[t * kLdF + s + 1] * eG[s + 1], ah[q], al[q]);
+          split2(-X[t * kLdF + s] * eG[s] * sk, -X[t * kLdF + s + 1] * eG[s + 1] * sk, ah[q], al[q]);
         }
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b, K, LD, ks * 16, np * 16, lane);
+        for (int np = 0; np < HT / 2; ++np) {
+          const int c0 = half * (DK / HALVES) + np * 16;
+          b_cols(b, K, LD, ks * 16, c0, lane);
           mma2(acc[2 * np], acc[2 * np + 1], ah, b);
           mma2(acc[2 * np], acc[2 * np + 1], al, b);
           if (NP == 2) {
-            b_cols(b, K + kChunk * LD, LD, ks * 16, np * 16, lane);
+            b_cols(b, K + kChunk * LD, LD, ks * 16, c0, lane);
             mma2(acc[2 * np], acc[2 * np + 1], ah, b);
           }
         }
       }
     }
-    __nv_bfloat16 *kt = p.kt + rec * (2 * kChunk * DK);
-#pragma unroll
-    for (int i = 0; i < DK / 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t hi, lo;
-        split2(acc[i][2 * h], acc[i][2 * h + 1], hi, lo);
-        const int at = (m0 + g + 8 * h) * DK + 8 * i + t2;
-        *reinterpret_cast<uint32_t *>(kt + at) = hi;
-        *reinterpret_cast<uint32_t *>(kt + kChunk * DK + at) = lo;
-      }
+    store_planes<HT>(p.kt + rec * (2 * kChunk * DK) + half * (DK / HALVES), kChunk * DK, DK, m0, acc, HT, lane);
   }
   if (!BWD) return;
   // Kb = Tm^T diag(w) K: rows s of this warp, t blocks from its own on
-  {
-    float acc[DK / 8][4];
+#pragma unroll 1
+  for (int half = 0; half < HALVES; ++half) {
+    float acc[HT][4];
 #pragma unroll
-    for (int i = 0; i < DK / 8; ++i)
+    for (int i = 0; i < HT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
@@ -555,33 +724,24 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int s = m0 + g + 8 * (q & 1), t = ks * 16 + t2 + 8 * (q >> 1);
-          split2(X[t * kLdF + s] * w[t], X[(t + 1) * kLdF + s] * w[t + 1], ah[q], al[q]);
+          split2(X[t * kLdF + s] * w[t] * sk, X[(t + 1) * kLdF + s] * w[t + 1] * sk, ah[q], al[q]);
         }
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b, K, LD, ks * 16, np * 16, lane);
+        for (int np = 0; np < HT / 2; ++np) {
+          const int c0 = half * (DK / HALVES) + np * 16;
+          b_cols(b, K, LD, ks * 16, c0, lane);
           mma2(acc[2 * np], acc[2 * np + 1], ah, b);
           mma2(acc[2 * np], acc[2 * np + 1], al, b);
           if (NP == 2) {
-            b_cols(b, K + kChunk * LD, LD, ks * 16, np * 16, lane);
+            b_cols(b, K + kChunk * LD, LD, ks * 16, c0, lane);
             mma2(acc[2 * np], acc[2 * np + 1], ah, b);
           }
         }
       }
     }
-    __nv_bfloat16 *kb = p.kb + rec * (2 * kChunk * DK);
-#pragma unroll
-    for (int i = 0; i < DK / 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t hi, lo;
-        split2(acc[i][2 * h], acc[i][2 * h + 1], hi, lo);
-        const int at = (m0 + g + 8 * h) * DK + 8 * i + t2;
-        *reinterpret_cast<uint32_t *>(kb + at) = hi;
-        *reinterpret_cast<uint32_t *>(kb + kChunk * DK + at) = lo;
-      }
+    store_planes<HT>(p.kb + rec * (2 * kChunk * DK) + half * (DK / HALVES), kChunk * DK, DK, m0, acc, HT, lane);
   }
-  // Z = P Tm: rows t of this warp; block (r, s) of Tm is zero for s > r
+  // Z = P Tm (over the scale of Q): rows t of this warp; block (r, s) of Tm is zero for s > r
   {
     float acc[8][4];
 #pragma unroll
@@ -605,561 +765,706 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
         }
       }
     }
-    __nv_bfloat16 *z = p.z + rec * (2 * kChunk * kChunk);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i / 2 <= warp)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi, lo;
-          split2(acc[i][2 * h], acc[i][2 * h + 1], hi, lo);
-          const int at = (m0 + g + 8 * h) * kChunk + 8 * i + t2;
-          *reinterpret_cast<uint32_t *>(z + at) = hi;
-          *reinterpret_cast<uint32_t *>(z + kChunk * kChunk + at) = lo;
-        }
+    store_planes<8>(p.z + rec * (2 * kChunk * kChunk), kChunk * kChunk, kChunk, m0, acc, 2 * warp + 2, lane);
   }
 }
 
 // -------------------------------------------------------------------------------------
 // scan_chain
 // -------------------------------------------------------------------------------------
-// Grid (sequence * H + head, block of 16 W value rows); W compute warps of 16 rows each and
-// two warps that fetch the next chunk's tiles meanwhile (two stages where they fit).
-// SAVE: the backward pass's recomputation, which keeps S0 and E of every chunk; otherwise
-// o and the last state are written.
+// Grid (sequence * H + head, group of p.rb blocks of 16 value rows).  NH warps share a block: warp h
+// holds the state's columns [h d_k/NH, (h+1) d_k/NH) and forms, over its columns, a part of S0 Kt^T
+// and S0 Q^T for all 64 tokens; the parts are added through shared memory, one barrier of the
+// NH warps per chunk; then each warp finishes O for its own 64/NH tokens and S for its own
+// columns.  (NH = 2 halves the chain from chunk to chunk where there are few blocks.)  Two more
+// warps fetch the next chunk's tiles meanwhile (two stages where they fit).
+// SAVE: the backward pass's recomputation, which keeps the planes of S0 and E of every chunk;
+// otherwise o and the last state are written.
 constexpr int kLoadWarps = 2;
+constexpr int kWalkWarps = 4;          // compute warps of a CTA, at most
 
-struct ChainLayout {                   // byte offsets inside one stage
-  int kt, k, q, tm, pp, v, gates, bytes;
+struct WalkLayout {                    // byte offsets inside one stage; `part` after the stages
+  int kt, k, q, tm, pp, v, gates, bytes, part;
 };
-__host__ __device__ inline ChainLayout chain_layout(int dk, int np, int w, bool delta, bool out) {
-  const int ld = dk + 8, tile = kChunk * ld * 2, sq = kChunk * kLdC * 2;
-  ChainLayout l{};
+// elements of a token row of the V (or dO) tile
+__host__ __device__ constexpr int tile_ld(int np, int rb) { return 16 * rb + (np == 2 ? 4 : 8); }
+
+// what = 0: forward, 1: recomputation, 2: reverse
+__host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh, bool delta, int what) {
+  const int tile = kChunk * (dk + 8) * 2, sq = kChunk * kLdC * 2;
+  WalkLayout l{};
   int at = 0;
-  l.kt = at; at += delta ? 2 * tile : 0;
+  l.kt = at; at += delta ? 2 * tile : 0;                       // Kt or Kb
   l.k = at; at += np * tile;
-  l.q = at; at += out ? np * tile : 0;
-  l.tm = at; at += delta ? 2 * sq : 0;
-  l.pp = at; at += out ? 2 * sq : 0;
-  l.v = at; at += np * kChunk * (16 * w + 8) * 2;
-  l.gates = at; at += 2 * kChunk * 4;
-  l.bytes = at;
+  l.q = at; at += what != 1 ? np * tile : 0;
+  l.tm = at; at += what == 2 || delta ? 2 * sq : 0;            // Tm or Z
+  l.pp = at; at += what == 0 ? np * sq : 0;
+  l.v = at; at += kChunk * tile_ld(np, rb) * (np == 2 ? 4 : 2);
+  l.gates = at; at += 2 * kChunk * 4 + 16;
+  l.bytes = (at + 15) / 16 * 16;
+  // parts of E (32 floats a lane) and, forward, of O for the others' tokens; maxima
+  l.part = nh == 1 ? 0 : rb * nh * 32 * (32 + (what == 0 ? 32 - 32 / nh : 0)) * 4;
   return l;
 }
 
-template <int DK, int NP, bool DELTA, bool SAVE>
-__device__ __forceinline__ void chain_fetch(const ScanParams &p, uint8_t *st, const ChainLayout &l,
-                                            int w, long long token0, int n, long long rec, int head,
-                                            int row0, int tid, int threads) {
-  constexpr int LD = DK + 8;
-  const int qh = head / p.share, ldv = 16 * w + 8;
-  const int cols = min(16 * w, p.dvp - row0);
+// The state rows a thread holds: rows r0 and r0 + 8, columns c0 + 8 i + t2, +1.
+template <int NTH>
+__device__ __forceinline__ void load_state(float (&S)[NTH][4], const float *src, long long tile, int d_v, int dk, int r0,
+                                           int c0) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if (DELTA) {
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.kt) + c * kChunk * LD, LD,
-                p.kt + rec * (2 * kChunk * DK) + c * kChunk * DK, DK, kChunk, DK, kChunk, DK, tid, threads);
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.tm) + c * kChunk * kLdC, kLdC,
-                p.tm + rec * (2 * kChunk * kChunk) + c * kChunk * kChunk, kChunk, kChunk, kChunk,
-                kChunk, kChunk, tid, threads);
+  for (int i = 0; i < NTH; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float2 x = make_float2(0.0f, 0.0f);
+      if (src && r0 + 8 * h < d_v)
+        x = *reinterpret_cast<const float2 *>(src + (tile * d_v + r0 + 8 * h) * dk + c0 + 8 * i);
+      S[i][2 * h] = x.x;
+      S[i][2 * h + 1] = x.y;
     }
-    if (!SAVE)
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.pp) + c * kChunk * kLdC, kLdC,
-                p.pp + rec * (2 * kChunk * kChunk) + c * kChunk * kChunk, kChunk, kChunk, kChunk,
-                kChunk, kChunk, tid, threads);
-  }
+}
+template <int NTH>
+__device__ __forceinline__ void save_state(const float (&S)[NTH][4], float *dst, long long tile, int d_v, int dk, int r0,
+                                           int c0) {
 #pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.k) + c * kChunk * LD, LD,
-              (c ? p.k.lo : p.k.hi) + token0 * p.k.stride + qh * p.k.hstride, p.k.stride, kChunk, DK,
-              n, DK, tid, threads);
-    if (!SAVE)
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.q) + c * kChunk * LD, LD,
-                (c ? p.q.lo : p.q.hi) + token0 * p.q.stride + qh * p.q.hstride, p.q.stride, kChunk,
-                DK, n, DK, tid, threads);
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.v) + c * kChunk * ldv, ldv,
-              (c ? p.v.lo : p.v.hi) + token0 * p.v.stride + (long long)head * p.v.hstride + row0,
-              p.v.stride, kChunk, cols, n, p.v.hstride - row0, tid, threads);
+  for (int i = 0; i < NTH; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (r0 + 8 * h < d_v)
+        *reinterpret_cast<float2 *>(dst + (tile * d_v + r0 + 8 * h) * dk + c0 + 8 * i) =
+            make_float2(S[i][2 * h], S[i][2 * h + 1]);
+}
+template <int NTH>
+__device__ __forceinline__ unsigned max_bits(const float (&S)[NTH][4]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < NTH; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, abs_bits(S[i][j]));
+  return m;
+}
+
+// The tile of V (or dO) as left operands V^T: x[ks][2 q], x[ks][2 q + 1] are the two entries of
+// register q of k-step ks (tokens 16 ks ..) as fp32 values of the caller's type.
+template <int NP>
+__device__ __forceinline__ void load_tokens(float (&x)[4][8], const uint8_t *tile, int ld, int col0, int dtype,
+                                            int lane) {
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    if (NP == 1) {
+      uint32_t a[4];
+      a_cols(a, reinterpret_cast<const __half *>(tile), ld, ks * 16, col0, lane);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = pair_of(a[q], dtype);
+        x[ks][2 * q] = f.x;
+        x[ks][2 * q + 1] = f.y;
+      }
+    } else {
+      const float *f = reinterpret_cast<const float *>(tile);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          x[ks][2 * q + e] = f[(ks * 16 + 8 * (q >> 1) + t2 + e) * ld + col0 + g + 8 * (q & 1)];
+    }
   }
-  const float *gates = p.gates + rec * kGateFloats;
-  for (int i = tid; i < 2 * kChunk / 4; i += threads)
-    cp16(st + l.gates + 16 * i, gates + 4 * i, true);
+}
+
+// Writes OT tiles (tokens 8 (tile0 + i) .., 16 value rows) times `by` to token rows of the
+// caller's tensor, through the warp's part of the V tile so that rows leave in 16-byte
+// pieces.
+template <int NP, int OT>
+__device__ __forceinline__ void store_tokens(const float (&O)[OT][4], float by, uint8_t *tile, int ld, int col0, int tile0,
+                                             void *dst, int dtype, long long stride, long long token0, int n, int col,
+                                             int have, bool by16, int lane) {
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  if (NP == 1) {
+    uint16_t *sm = reinterpret_cast<uint16_t *>(tile);
+#pragma unroll
+    for (int i = 0; i < OT / 2; ++i) {
+      uint32_t r[4];
+      r[0] = pack_as(dtype, O[2 * i][0] * by, O[2 * i][1] * by);
+      r[1] = pack_as(dtype, O[2 * i][2] * by, O[2 * i][3] * by);
+      r[2] = pack_as(dtype, O[2 * i + 1][0] * by, O[2 * i + 1][1] * by);
+      r[3] = pack_as(dtype, O[2 * i + 1][2] * by, O[2 * i + 1][3] * by);
+      const int tok = 8 * (tile0 + 2 * i + (lane >> 4)) + (lane & 7);
+      stsm4t(sm + tok * ld + col0 + 8 * ((lane >> 3) & 1), r);
+    }
+    __syncwarp();
+    uint16_t *out = static_cast<uint16_t *>(dst);
+#pragma unroll
+    for (int i = 0; i < OT / 2; ++i) {
+      const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 1), c = (e & 1) * 8;
+      const uint4 x = *reinterpret_cast<const uint4 *>(sm + tok * ld + col0 + c);
+      if (tok < n) {
+        uint16_t *to = out + (token0 + tok) * stride + col + c;
+        if (by16) {
+          if (c < have) *reinterpret_cast<uint4 *>(to) = x;
+        } else {
+          if (c < have) *reinterpret_cast<uint2 *>(to) = make_uint2(x.x, x.y);
+          if (c + 4 < have) *reinterpret_cast<uint2 *>(to + 4) = make_uint2(x.z, x.w);
+        }
+      }
+    }
+  } else {
+    float *sm = reinterpret_cast<float *>(tile);
+#pragma unroll
+    for (int i = 0; i < OT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        sm[(8 * (tile0 + i) + t2 + (j & 1)) * ld + col0 + g + 8 * (j >> 1)] = O[i][j] * by;
+    __syncwarp();
+    float *out = static_cast<float *>(dst);
+#pragma unroll
+    for (int i = 0; i < OT; ++i) {
+      const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 2), c = (e & 3) * 4;
+      const float4 x = *reinterpret_cast<const float4 *>(sm + tok * ld + col0 + c);
+      if (tok < n && c < have) *reinterpret_cast<float4 *>(out + (token0 + tok) * stride + col + c) = x;
+    }
+  }
+}
+
+__device__ __forceinline__ void block_barrier(int block, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + block), "r"(threads) : "memory");
 }
 
 template <int DK, int NP, bool DELTA, bool SAVE>
-__global__ void __launch_bounds__(32 * (4 + kLoadWarps)) scan_chain_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, NT = DK / 8;
+__device__ __forceinline__ void chain_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0, int n,
+                                            int slot, int head, int row0, int tid, int threads) {
+  constexpr int LD = DK + 8, SIZE = NP == 2 ? 4 : 2;
+  const long long rec = (long long)slot * p.H + head;
+  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (DELTA) {
+      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.kt) + c * kChunk * LD,
+                                 p.kt + (rec * 2 + c) * (kChunk * DK), tid, threads);
+      copy_lower(reinterpret_cast<__half *>(st + l.tm) + c * kChunk * kLdC, p.tm + (rec * 2 + c) * (kChunk * kChunk),
+                 tid, threads);
+    }
+#pragma unroll
+  for (int c = 0; c < NP; ++c) {
+    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.k) + c * kChunk * LD,
+                               p.khat + (qrec * NP + c) * (kChunk * DK), tid, threads);
+    if (!SAVE) {
+      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.q) + c * kChunk * LD,
+                                 p.qhat + (qrec * NP + c) * (kChunk * DK), tid, threads);
+      copy_lower(reinterpret_cast<__half *>(st + l.pp) + c * kChunk * kLdC, p.pp + (rec * 2 + c) * (kChunk * kChunk),
+                 tid, threads);
+    }
+  }
+  copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
+                    static_cast<const uint8_t *>(p.v) + (token0 * p.v_stride + (long long)head * p.d_v + row0) * SIZE,
+                    p.v_stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, p.v16, tid, threads);
+  const float *gates = p.gates + rec * kGateFloats;
+  for (int i = tid; i < 2 * kChunk / 4 + 1; i += threads)
+    cp16(st + l.gates + 16 * i, i < 2 * kChunk / 4 ? gates + 4 * i : gates + kGateScales, true);
+}
+
+template <int DK, int NP, bool DELTA, bool SAVE, int NH>
+__global__ void __launch_bounds__(32 * (kWalkWarps + kLoadWarps), 1) scan_chain_kernel(const ScanParams p) {
+  constexpr int LD = DK + 8, DKH = DK / NH, NTH = DKH / 8, OT = 8 / NH;
+  static_assert(NH == 1 || NH == 2, "E without the delta rule is laid out for these");
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int W = blockDim.x / 32 - kLoadWarps;
-  const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * W;
-  const ChainLayout l = chain_layout(DK, NP, W, DELTA, !SAVE);
-  const int ldv = 16 * W + 8;
+  const int blk = warp / NH, h = NH == 1 ? 0 : warp % NH;
+  const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * p.rb;
+  const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, SAVE ? 1 : 0);
+  const int ldv = tile_ld(NP, p.rb);
   long long start;
   int len;
   seq_range(p, seq, start, len);
   const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
-  const bool loader = warp >= W;
-  const int r0 = row0 + warp * 16 + g;             // this thread's value rows: r0, r0 + 8
-  const bool live = !loader && row0 + warp * 16 < p.dvp;
+  const bool loader = blk >= p.rb;
+  const int r0 = row0 + blk * 16 + g, c0 = h * DKH;    // this thread's value rows: r0, r0 + 8
+  const bool live = !loader && row0 + blk * 16 < p.dvp;
+  float4 *part = reinterpret_cast<float4 *>(smem + p.stages * l.bytes);
+  unsigned *tops = reinterpret_cast<unsigned *>(smem + p.stages * l.bytes + l.part);
 
-  float S[NT][4];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float2 x = make_float2(0.0f, 0.0f);
-      if (live && p.state_in && r0 + 8 * h < p.d_v)
-        x = *reinterpret_cast<const float2 *>(
-            p.state_in + ((long long)blockIdx.x * p.d_v + r0 + 8 * h) * DK + 8 * i + t2);
-      S[i][2 * h] = x.x;
-      S[i][2 * h + 1] = x.y;
-    }
+  float S[NTH][4];
+  load_state<NTH>(S, live ? p.state_in : nullptr, blockIdx.x, p.d_v, DK, r0, c0 + t2);
+  unsigned top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(S));
+  if (NH > 1 && live && lane == 0) tops[warp] = top;
 
-  const int ltid = tid - 32 * W, lthreads = 32 * kLoadWarps;
-  if (loader && chunks > 0) {
-    chain_fetch<DK, NP, DELTA, SAVE>(p, smem, l, W, start, min(kChunk, len), (long long)base * p.H + head,
-                                     head, row0, ltid, lthreads);
+  const int ltid = tid - 32 * NH * p.rb, lthreads = 32 * kLoadWarps;
+  auto fetch = [&](int c) {
+    chain_fetch<DK, NP, DELTA, SAVE>(p, smem + (p.stages == 2 ? (c & 1) * l.bytes : 0), l,
+                                     start + (long long)c * kChunk, min(kChunk, len - c * kChunk), base + c, head, row0,
+                                     ltid, lthreads);
     cp_commit();
-  }
+  };
+  if (loader && chunks > 0) fetch(0);
   for (int c = 0; c < chunks; ++c) {
     uint8_t *st = smem + (p.stages == 2 ? (c & 1) * l.bytes : 0);
     if (loader) cp_wait<0>();
     __syncthreads();
-    const long long rec = (long long)(base + c) * p.H + head;
-    auto fetch_next = [&]() {
-      if (loader && c + 1 < chunks) {
-        chain_fetch<DK, NP, DELTA, SAVE>(
-            p, smem + (p.stages == 2 ? ((c + 1) & 1) * l.bytes : 0), l, W,
-            start + (long long)(c + 1) * kChunk, min(kChunk, len - (c + 1) * kChunk), rec + p.H, head,
-            row0, ltid, lthreads);
-        cp_commit();
-      }
-    };
-    if (p.stages == 2) fetch_next();
+    if (p.stages == 2 && loader && c + 1 < chunks) fetch(c + 1);
     if (live) {
-      const __nv_bfloat16 *kt = reinterpret_cast<const __nv_bfloat16 *>(st + l.kt);
-      const __nv_bfloat16 *sk = reinterpret_cast<const __nv_bfloat16 *>(st + l.k);
-      const __nv_bfloat16 *sq = reinterpret_cast<const __nv_bfloat16 *>(st + l.q);
-      const __nv_bfloat16 *tm = reinterpret_cast<const __nv_bfloat16 *>(st + l.tm);
-      const __nv_bfloat16 *pp = reinterpret_cast<const __nv_bfloat16 *>(st + l.pp);
-      const __nv_bfloat16 *sv = reinterpret_cast<const __nv_bfloat16 *>(st + l.v);
+      const __half *kt = reinterpret_cast<const __half *>(st + l.kt), *sk = reinterpret_cast<const __half *>(st + l.k);
+      const __half *sq = reinterpret_cast<const __half *>(st + l.q), *tm = reinterpret_cast<const __half *>(st + l.tm);
+      const __half *pp = reinterpret_cast<const __half *>(st + l.pp);
       const float *eG = reinterpret_cast<const float *>(st + l.gates), *w = eG + kChunk;
+      const float kappa = w[kChunk], qscale = w[kChunk + 1], eC = eG[kChunk - 1];
+      const long long rec = (long long)(base + c) * p.H + head;
+      const int n = min(kChunk, len - c * kChunk);
+      // V^T and the scale of this chunk
+      float x[4][8];
+      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(x[i][j]));
+      m = max(__reduce_max_sync(0xFFFFFFFFu, m), top);
+#pragma unroll
+      for (int o = 1; o < NH; ++o) m = max(m, tops[blk * NH + ((h + o) & (NH - 1))]);
+      float inv;
+      const float scale = scale_of(m, 6, inv);
+
+      // Tile i of E and O holds tokens 8 ((i + OT h) % 8) ..: the warp's own come first.
       float E[8][4], O[8][4];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) E[i][j] = O[i][j] = 0.0f;
-      // S0 Kt^T and S0 Q^T (and the planes of S0 kept for the backward pass)
-      __nv_bfloat16 *s0 = SAVE ? p.s0 + rec * (2ll * p.dvp * DK) : nullptr;
-      {
+      __half *s0 = SAVE ? p.s0 + rec * (2ll * p.dvp * DK) : nullptr;
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          uint32_t ah[4], al[4], b[4];
-          split_tiles(S[2 * ks], S[2 * ks + 1], ah, al);
-          if (SAVE) {
+      for (int ks = 0; ks < DKH / 16; ++ks) {
+        uint32_t ah[4], al[4], b[4];
+        split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
+        if (SAVE) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const long long at = (long long)(r0 + 8 * (q & 1)) * DK + ks * 16 + 8 * (q >> 1) + t2;
-              *reinterpret_cast<uint32_t *>(s0 + at) = ah[q];
-              *reinterpret_cast<uint32_t *>(s0 + (long long)p.dvp * DK + at) = al[q];
-            }
+          for (int q = 0; q < 4; ++q) {
+            const long long at = (long long)(r0 + 8 * (q & 1)) * DK + c0 + ks * 16 + 8 * (q >> 1) + t2;
+            *reinterpret_cast<uint32_t *>(s0 + at) = ah[q];
+            *reinterpret_cast<uint32_t *>(s0 + (long long)p.dvp * DK + at) = al[q];
           }
+        }
 #pragma unroll
-          for (int np = 0; np < 4; ++np) {
-            if (DELTA) {
-              b_rows(b, kt, LD, np * 16, ks * 16, lane);
-              mma2(E[2 * np], E[2 * np + 1], ah, b);
-              mma2(E[2 * np], E[2 * np + 1], al, b);
-              b_rows(b, kt + kChunk * LD, LD, np * 16, ks * 16, lane);
-              mma2(E[2 * np], E[2 * np + 1], ah, b);
-            }
-            if (!SAVE) {
-              b_rows(b, sq, LD, np * 16, ks * 16, lane);
-              mma2(O[2 * np], O[2 * np + 1], ah, b);
-              mma2(O[2 * np], O[2 * np + 1], al, b);
-              if (NP == 2) {
-                b_rows(b, sq + kChunk * LD, LD, np * 16, ks * 16, lane);
-                mma2(O[2 * np], O[2 * np + 1], ah, b);
-              }
+        for (int i = 0; i < 4; ++i) {
+          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
+          if (DELTA) {
+            b_rows(b, kt, LD, np * 16, c0 + ks * 16, lane);
+            mma2(E[2 * i], E[2 * i + 1], ah, b);
+            mma2(E[2 * i], E[2 * i + 1], al, b);
+            b_rows(b, kt + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
+            mma2(E[2 * i], E[2 * i + 1], ah, b);
+          }
+          if (!SAVE) {
+            b_rows(b, sq, LD, np * 16, c0 + ks * 16, lane);
+            mma2(O[2 * i], O[2 * i + 1], ah, b);
+            if (NP == 2) {
+              mma2(O[2 * i], O[2 * i + 1], al, b);
+              b_rows(b, sq + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
+              mma2(O[2 * i], O[2 * i + 1], ah, b);
             }
           }
         }
       }
-      // E^T += V^T Tm^T (without the delta rule Tm = I)
+      if (SAVE && lane == 0 && h == 0) p.fscale[rec * (p.dvp / 16) + (row0 >> 4) + blk] = scale;
+      // + V^T Tm^T for the warp's own tokens (without the delta rule Tm = I and E = V for all)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t av[NP][4];
-#pragma unroll
-        for (int c2 = 0; c2 < NP; ++c2) a_cols(av[c2], sv + c2 * kChunk * ldv, ldv, ks * 16, warp * 16, lane);
+        uint32_t vh[4], vl[4];
         if (DELTA) {
 #pragma unroll
-          for (int np = ks; np < 4; ++np) {
-            uint32_t b[4];
-            b_rows(b, tm, kLdC, np * 16, ks * 16, lane);
+          for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * inv, x[ks][2 * q + 1] * inv, vh[q], vl[q]);
 #pragma unroll
-            for (int c2 = 0; c2 < NP; ++c2) mma2(E[2 * np], E[2 * np + 1], av[c2], b);
-            b_rows(b, tm + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
-            mma2(E[2 * np], E[2 * np + 1], av[0], b);
+          for (int i = 0; i < OT / 2; ++i) {
+            const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
+            if (ks <= np) {
+              uint32_t b[4];
+              b_rows(b, tm, kLdC, np * 16, ks * 16, lane);
+              mma2(E[2 * i], E[2 * i + 1], vh, b);
+              if (NP == 2) mma2(E[2 * i], E[2 * i + 1], vl, b);
+              b_rows(b, tm + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
+              mma2(E[2 * i], E[2 * i + 1], vh, b);
+            }
           }
-        } else {
+        }
+      }
+      // the other warps' parts
+      if (NH > 1) {                    // (also what keeps a warp's next maximum behind the others' reading)
+        float4 *own = part + warp * (32 * (8 + (SAVE ? 0 : 8 - OT)));
+        if (DELTA)
 #pragma unroll
-          for (int c2 = 0; c2 < NP; ++c2)
+          for (int i = 0; i < 8; ++i)
+            own[((i + OT * h) & 7) * 32 + lane] = make_float4(E[i][0], E[i][1], E[i][2], E[i][3]);
+        if (!SAVE)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 x = unpack2(av[c2][q]);
-              float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-              e[0] = __fadd_rn(e[0], x.x);
-              e[1] = __fadd_rn(e[1], x.y);
+          for (int i = OT; i < 8; ++i) own[(8 + i - OT) * 32 + lane] = make_float4(O[i][0], O[i][1], O[i][2], O[i][3]);
+        block_barrier(blk, 32 * NH);
+#pragma unroll
+        for (int o = 1; o < NH; ++o) {
+          const int other = (h + o) & (NH - 1);
+          const float4 *their = part + (blk * NH + other) * (32 * (8 + (SAVE ? 0 : 8 - OT)));
+          if (DELTA)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = their[((i + OT * h) & 7) * 32 + lane];
+              E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
+            }
+          if (!SAVE)
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+              // this warp's tokens are tile i + OT (NH - o) of the other
+              const float4 y = their[(8 + i + OT * (NH - o) - OT) * 32 + lane];
+              O[i][0] += y.x; O[i][1] += y.y; O[i][2] += y.z; O[i][3] += y.w;
             }
         }
       }
-      if (!SAVE) {
-        // O^T = diag(e^G) (S0 Q^T) + E^T P^T
+      if (!DELTA)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 e = *reinterpret_cast<const float2 *>(eG + 8 * i + t2);
-          O[i][0] *= e.x; O[i][1] *= e.y; O[i][2] *= e.x; O[i][3] *= e.y;
-        }
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t ah[4], al[4], b[4];
-          split_tiles(E[2 * ks], E[2 * ks + 1], ah, al);
-#pragma unroll
-          for (int np = ks; np < 4; ++np) {
-            b_rows(b, pp, kLdC, np * 16, ks * 16, lane);
-            mma2(O[2 * np], O[2 * np + 1], ah, b);
-            if (DELTA || NP == 2) mma2(O[2 * np], O[2 * np + 1], al, b);
-            b_rows(b, pp + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
-            mma2(O[2 * np], O[2 * np + 1], ah, b);
-          }
-        }
-        const int n = min(kChunk, len - c * kChunk);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
+          // (x is indexed by the token; with NH = 2 the halves trade places for h = 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int t = 8 * i + t2 + (j & 1), r = r0 + 8 * (j >> 1);
-            if (t < n && r < p.d_v)
-              store_as(p.o, p.dtype, (start + (long long)c * kChunk + t) * p.o_stride +
-                                         (long long)head * p.d_v + r, O[i][j]);
+            const int q = (j >> 1) + 2 * (i & 1), e = 2 * q + (j & 1);
+            E[i][j] = (NH == 2 && h == 1 ? x[(i / 2 + 2) & 3][e] : x[i / 2][e]) * inv;
           }
-      } else {
-        __nv_bfloat16 *et = p.et + rec * (2ll * p.dvp * kChunk);
+        }
+      if (SAVE) {
+        __half *et = p.et + rec * (2ll * p.dvp * kChunk);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < OT; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int r = 0; r < 2; ++r) {
             uint32_t hi, lo;
-            split2(E[i][2 * h], E[i][2 * h + 1], hi, lo);
-            const long long at = (long long)(r0 + 8 * h) * kChunk + 8 * i + t2;
+            split2(E[i][2 * r], E[i][2 * r + 1], hi, lo);
+            const long long at = (long long)(r0 + 8 * r) * kChunk + 8 * ((i + OT * h) & 7) + t2;
             *reinterpret_cast<uint32_t *>(et + at) = hi;
             *reinterpret_cast<uint32_t *>(et + (long long)p.dvp * kChunk + at) = lo;
           }
       }
       // S = e^{G_C} S0 + (diag(w) E)^T K: each tile's sum starts from zero and joins the
       // state in one fma, so that the tensor cores' rounding does not pile up in it
+      {
+        uint32_t wh[4][4], wl[4][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 x = *reinterpret_cast<const float2 *>(w + 8 * i + t2);
-        E[i][0] *= x.x; E[i][1] *= x.y; E[i][2] *= x.x; E[i][3] *= x.y;
-      }
-      uint32_t wh[4][4], wl[4][4];
+        for (int i = 0; i < 4; ++i) {
+          const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) split_tiles(E[2 * ks], E[2 * ks + 1], wh[ks], wl[ks]);
-      const float eC = eG[kChunk - 1];
-#pragma unroll
-      for (int np = 0; np < DK / 16; ++np) {
-        float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t b[4];
-          b_cols(b, sk, LD, ks * 16, np * 16, lane);
-          mma2(a0, a1, wh[ks], b);
-          mma2(a0, a1, wl[ks], b);
-          if (NP == 2) {
-            b_cols(b, sk + kChunk * LD, LD, ks * 16, np * 16, lane);
-            mma2(a0, a1, wh[ks], b);
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = *reinterpret_cast<const float2 *>(w + ks * 16 + 8 * (q >> 1) + t2);
+            const float *e = &E[2 * i + (q >> 1)][2 * (q & 1)];
+            split2(e[0] * f.x * kappa, e[1] * f.y * kappa, wh[i][q], wl[i][q]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          S[2 * np][j] = fmaf(S[2 * np][j], eC, a0[j]);
-          S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, a1[j]);
+        for (int np = 0; np < NTH / 2; ++np) {
+          float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
+            uint32_t b[4];
+            b_cols(b, sk, LD, ks * 16, c0 + np * 16, lane);
+            mma2(a0, a1, wh[i], b);
+            mma2(a0, a1, wl[i], b);
+            if (NP == 2) {
+              b_cols(b, sk + kChunk * LD, LD, ks * 16, c0 + np * 16, lane);
+              mma2(a0, a1, wh[i], b);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            S[2 * np][j] = fmaf(S[2 * np][j], eC, a0[j] * scale);
+            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, a1[j] * scale);
+          }
         }
+        top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(S));
+        if (NH > 1 && lane == 0) tops[warp] = top;
+      }
+      if (!SAVE) {
+        // O^T = diag(e^G) (S0 Q^T) + E^T P^T for the own tokens
+#pragma unroll
+        for (int i = 0; i < OT; ++i) {
+          const float2 f = *reinterpret_cast<const float2 *>(eG + 8 * ((i + OT * h) & 7) + t2);
+          O[i][0] *= f.x; O[i][1] *= f.y; O[i][2] *= f.x; O[i][3] *= f.y;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int ks = NH == 1 ? j : (j + OT / 2 * h) & 3;
+          uint32_t eh[4], el[4], b[4];
+          split_tiles(E[2 * j], E[2 * j + 1], eh, el);
+#pragma unroll
+          for (int i = 0; i < OT / 2; ++i) {
+            const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
+            if (ks <= np) {
+              b_rows(b, pp, kLdC, np * 16, ks * 16, lane);
+              mma2(O[2 * i], O[2 * i + 1], eh, b);
+              if (NP == 2) {
+                mma2(O[2 * i], O[2 * i + 1], el, b);
+                b_rows(b, pp + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
+                mma2(O[2 * i], O[2 * i + 1], eh, b);
+              }
+            }
+          }
+        }
+        float own[OT][4];
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) own[i][j] = O[i][j];
+        store_tokens<NP, OT>(own, scale * qscale, st + l.v, ldv, blk * 16, OT * h, p.o, p.dtype, p.o_stride,
+                             start + (long long)c * kChunk, n, head * p.d_v + row0 + blk * 16,
+                             p.d_v - row0 - blk * 16, p.o16, lane);
       }
     }
     if (p.stages == 1) {
       __syncthreads();
-      fetch_next();
+      if (loader && c + 1 < chunks) fetch(c + 1);
     }
   }
-  if (live && p.state_out && !SAVE)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (r0 + 8 * h < p.d_v)
-          *reinterpret_cast<float2 *>(p.state_out + ((long long)blockIdx.x * p.d_v + r0 + 8 * h) * DK +
-                                      8 * i + t2) = make_float2(S[i][2 * h], S[i][2 * h + 1]);
+  if (live && p.state_out && !SAVE) save_state<NTH>(S, p.state_out, blockIdx.x, p.d_v, DK, r0, c0 + t2);
 }
 
 // -------------------------------------------------------------------------------------
 // scan_reverse
 // -------------------------------------------------------------------------------------
-// The same grid and roles over the chunks backwards: D (at every chunk's end) and R of every
-// chunk are kept for scan_grads, dV = R and d_state_in are written.
-struct ReverseLayout {
-  int kb, k, q, z, d, gates, bytes;
-};
-__host__ __device__ inline ReverseLayout reverse_layout(int dk, int np, int w, bool delta) {
-  const int ld = dk + 8, tile = kChunk * ld * 2, sq = kChunk * kLdC * 2;
-  ReverseLayout l{};
-  int at = 0;
-  l.kb = at; at += delta ? 2 * tile : 0;
-  l.k = at; at += np * tile;
-  l.q = at; at += np * tile;
-  l.z = at; at += 2 * sq;
-  l.d = at; at += np * kChunk * (16 * w + 8) * 2;
-  l.gates = at; at += 2 * kChunk * 4;
-  l.bytes = at;
-  return l;
-}
-
+// The same grid and roles over the chunks backwards: the planes of D (at every chunk's end) and R
+// are kept for scan_grads, dV = R and d_state_in are written.
 template <int DK, int NP, bool DELTA>
-__device__ __forceinline__ void reverse_fetch(const ScanParams &p, uint8_t *st, const ReverseLayout &l,
-                                              int w, long long token0, int n, long long rec, int head,
-                                              int row0, int tid, int threads) {
-  constexpr int LD = DK + 8;
-  const int qh = head / p.share, ldv = 16 * w + 8;
-  const int cols = min(16 * w, p.dvp - row0);
+__device__ __forceinline__ void reverse_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0,
+                                              int n, int slot, int head, int row0, int tid, int threads) {
+  constexpr int LD = DK + 8, SIZE = NP == 2 ? 4 : 2;
+  const long long rec = (long long)slot * p.H + head;
+  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     if (DELTA)
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.kb) + c * kChunk * LD, LD,
-                p.kb + rec * (2 * kChunk * DK) + c * kChunk * DK, DK, kChunk, DK, kChunk, DK, tid, threads);
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.z) + c * kChunk * kLdC, kLdC,
-              (DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk) + c * kChunk * kChunk, kChunk, kChunk,
-              kChunk, kChunk, kChunk, tid, threads);
+      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.kt) + c * kChunk * LD,
+                                 p.kb + (rec * 2 + c) * (kChunk * DK), tid, threads);
+    copy_lower(reinterpret_cast<__half *>(st + l.tm) + c * kChunk * kLdC,
+               (DELTA ? p.z : p.pp) + (rec * 2 + c) * (kChunk * kChunk), tid, threads);
   }
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.k) + c * kChunk * LD, LD,
-              (c ? p.k.lo : p.k.hi) + token0 * p.k.stride + qh * p.k.hstride, p.k.stride, kChunk, DK,
-              n, DK, tid, threads);
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.q) + c * kChunk * LD, LD,
-              (c ? p.q.lo : p.q.hi) + token0 * p.q.stride + qh * p.q.hstride, p.q.stride, kChunk, DK,
-              n, DK, tid, threads);
-    copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.d) + c * kChunk * ldv, ldv,
-              (c ? p.dO.lo : p.dO.hi) + token0 * p.dO.stride + (long long)head * p.dO.hstride + row0,
-              p.dO.stride, kChunk, cols, n, p.dO.hstride - row0, tid, threads);
+    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.k) + c * kChunk * LD,
+                               p.khat + (qrec * NP + c) * (kChunk * DK), tid, threads);
+    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.q) + c * kChunk * LD,
+                               p.qhat + (qrec * NP + c) * (kChunk * DK), tid, threads);
   }
+  copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
+                    static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + row0) * SIZE,
+                    p.o_stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, p.o16, tid, threads);
   const float *gates = p.gates + rec * kGateFloats;
-  for (int i = tid; i < 2 * kChunk / 4; i += threads)
-    cp16(st + l.gates + 16 * i, gates + 4 * i, true);
+  for (int i = tid; i < 2 * kChunk / 4 + 1; i += threads)
+    cp16(st + l.gates + 16 * i, i < 2 * kChunk / 4 ? gates + 4 * i : gates + kGateScales, true);
 }
 
-template <int DK, int NP, bool DELTA>
-__global__ void __launch_bounds__(32 * (4 + kLoadWarps)) scan_reverse_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, NT = DK / 8;
+template <int DK, int NP, bool DELTA, int NH>
+__global__ void __launch_bounds__(32 * (kWalkWarps + kLoadWarps), 1) scan_reverse_kernel(const ScanParams p) {
+  constexpr int LD = DK + 8, DKH = DK / NH, NTH = DKH / 8, OT = 8 / NH;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int W = blockDim.x / 32 - kLoadWarps;
-  const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * W;
-  const ReverseLayout l = reverse_layout(DK, NP, W, DELTA);
-  const int ldv = 16 * W + 8;
+  const int blk = warp / NH, h = NH == 1 ? 0 : warp % NH;
+  const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * p.rb;
+  const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, 2);
+  const int ldv = tile_ld(NP, p.rb);
   long long start;
   int len;
   seq_range(p, seq, start, len);
   const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
-  const bool loader = warp >= W;
-  const int r0 = row0 + warp * 16 + g;
-  const bool live = !loader && row0 + warp * 16 < p.dvp;
+  const bool loader = blk >= p.rb;
+  const int r0 = row0 + blk * 16 + g, c0 = h * DKH;
+  const bool live = !loader && row0 + blk * 16 < p.dvp;
+  float4 *part = reinterpret_cast<float4 *>(smem + p.stages * l.bytes);
+  unsigned *tops = reinterpret_cast<unsigned *>(smem + p.stages * l.bytes + l.part);
 
-  float D[NT][4];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float2 x = make_float2(0.0f, 0.0f);
-      if (live && p.d_state_out && r0 + 8 * h < p.d_v)
-        x = *reinterpret_cast<const float2 *>(
-            p.d_state_out + ((long long)blockIdx.x * p.d_v + r0 + 8 * h) * DK + 8 * i + t2);
-      D[i][2 * h] = x.x;
-      D[i][2 * h + 1] = x.y;
-    }
-  const int ltid = tid - 32 * W, lthreads = 32 * kLoadWarps;
-  if (loader && chunks > 0) {
-    const int c = chunks - 1;
-    reverse_fetch<DK, NP, DELTA>(p, smem + (p.stages == 2 ? (c & 1) * l.bytes : 0), l, W,
-                                 start + (long long)c * kChunk, len - c * kChunk,
-                                 (long long)(base + c) * p.H + head, head, row0, ltid, lthreads);
+  float D[NTH][4];
+  load_state<NTH>(D, live ? p.d_state_out : nullptr, blockIdx.x, p.d_v, DK, r0, c0 + t2);
+  unsigned top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(D));
+  if (NH > 1 && live && lane == 0) tops[warp] = top;
+
+  const int ltid = tid - 32 * NH * p.rb, lthreads = 32 * kLoadWarps;
+  auto fetch = [&](int c) {
+    reverse_fetch<DK, NP, DELTA>(p, smem + (p.stages == 2 ? (c & 1) * l.bytes : 0), l, start + (long long)c * kChunk,
+                                 min(kChunk, len - c * kChunk), base + c, head, row0, ltid, lthreads);
     cp_commit();
-  }
+  };
+  if (loader && chunks > 0) fetch(chunks - 1);
   for (int c = chunks - 1; c >= 0; --c) {
     uint8_t *st = smem + (p.stages == 2 ? (c & 1) * l.bytes : 0);
     if (loader) cp_wait<0>();
     __syncthreads();
-    const long long rec = (long long)(base + c) * p.H + head;
-    auto fetch_next = [&]() {
-      if (loader && c > 0) {
-        reverse_fetch<DK, NP, DELTA>(p, smem + (p.stages == 2 ? ((c - 1) & 1) * l.bytes : 0), l, W,
-                                     start + (long long)(c - 1) * kChunk, kChunk, rec - p.H, head, row0,
-                                     ltid, lthreads);
-        cp_commit();
-      }
-    };
-    if (p.stages == 2) fetch_next();
+    if (p.stages == 2 && loader && c > 0) fetch(c - 1);
     if (live) {
-      const __nv_bfloat16 *kb = reinterpret_cast<const __nv_bfloat16 *>(st + l.kb);
-      const __nv_bfloat16 *sk = reinterpret_cast<const __nv_bfloat16 *>(st + l.k);
-      const __nv_bfloat16 *sq = reinterpret_cast<const __nv_bfloat16 *>(st + l.q);
-      const __nv_bfloat16 *z = reinterpret_cast<const __nv_bfloat16 *>(st + l.z);
-      const __nv_bfloat16 *sd = reinterpret_cast<const __nv_bfloat16 *>(st + l.d);
+      const __half *kb = reinterpret_cast<const __half *>(st + l.kt), *sk = reinterpret_cast<const __half *>(st + l.k);
+      const __half *sq = reinterpret_cast<const __half *>(st + l.q), *z = reinterpret_cast<const __half *>(st + l.tm);
       const float *eG = reinterpret_cast<const float *>(st + l.gates), *w = eG + kChunk;
+      const float kappa = w[kChunk], qscale = w[kChunk + 1], eC = eG[kChunk - 1];
+      const long long rec = (long long)(base + c) * p.H + head;
       const int n = min(kChunk, len - c * kChunk);
-      float R[8][4];
+      // dO^T (times the scale of Q, which Z and the planes of Q lack) and the chunk's scale
+      float x[4][8];
+      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[i][j] *= qscale;
+          m = max(m, abs_bits(x[i][j]));
+        }
+      m = max(__reduce_max_sync(0xFFFFFFFFu, m), top);
+#pragma unroll
+      for (int o = 1; o < NH; ++o) m = max(m, tops[blk * NH + ((h + o) & (NH - 1))]);
+      float inv;
+      const float scale = scale_of(m, 6, inv);
+
+      float R[8][4];                   // tile i: tokens 8 ((i + OT h) % 8) ..
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) R[i][j] = 0.0f;
-      __nv_bfloat16 *dd = p.dd + rec * (2ll * p.dvp * DK);
+      __half *dd = p.dd + rec * (2ll * p.dvp * DK);
       // D Kb^T; without the delta rule Kb = diag(w) K, applied below
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
+      for (int ks = 0; ks < DKH / 16; ++ks) {
         uint32_t ah[4], al[4], b[4];
-        split_tiles(D[2 * ks], D[2 * ks + 1], ah, al);
+        split_tiles(D[2 * ks], D[2 * ks + 1], inv, ah, al);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const long long at = (long long)(r0 + 8 * (q & 1)) * DK + ks * 16 + 8 * (q >> 1) + t2;
+          const long long at = (long long)(r0 + 8 * (q & 1)) * DK + c0 + ks * 16 + 8 * (q >> 1) + t2;
           *reinterpret_cast<uint32_t *>(dd + at) = ah[q];
           *reinterpret_cast<uint32_t *>(dd + (long long)p.dvp * DK + at) = al[q];
         }
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          b_rows(b, DELTA ? kb : sk, LD, np * 16, ks * 16, lane);
-          mma2(R[2 * np], R[2 * np + 1], ah, b);
-          mma2(R[2 * np], R[2 * np + 1], al, b);
+        for (int i = 0; i < 4; ++i) {
+          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
+          b_rows(b, DELTA ? kb : sk, LD, np * 16, c0 + ks * 16, lane);
+          mma2(R[2 * i], R[2 * i + 1], ah, b);
+          mma2(R[2 * i], R[2 * i + 1], al, b);
           if (DELTA || NP == 2) {
-            b_rows(b, (DELTA ? kb : sk) + kChunk * LD, LD, np * 16, ks * 16, lane);
-            mma2(R[2 * np], R[2 * np + 1], ah, b);
+            b_rows(b, (DELTA ? kb : sk) + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
+            mma2(R[2 * i], R[2 * i + 1], ah, b);
           }
         }
       }
+      if (lane == 0 && h == 0) p.bscale[rec * (p.dvp / 16) + (row0 >> 4) + blk] = scale;
       if (!DELTA)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 x = *reinterpret_cast<const float2 *>(w + 8 * i + t2);
-          R[i][0] *= x.x; R[i][1] *= x.y; R[i][2] *= x.x; R[i][3] *= x.y;
+          const float2 f = *reinterpret_cast<const float2 *>(w + 8 * ((i + OT * h) & 7) + t2);
+          R[i][0] *= f.x * kappa; R[i][1] *= f.y * kappa; R[i][2] *= f.x * kappa; R[i][3] *= f.y * kappa;
         }
-      // + dO^T Z; the same rows of dO times e^G are the left operand of D's sum
-      uint32_t oh[4][4], ol[4][4];
+      // + dO^T Z for the warp's own tokens s, from blocks t >= s
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t a[NP][4], b[4];
+        uint32_t oh[4], ol[4];
 #pragma unroll
-        for (int c2 = 0; c2 < NP; ++c2) a_cols(a[c2], sd + c2 * kChunk * ldv, ldv, ks * 16, warp * 16, lane);
+        for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * inv, x[ks][2 * q + 1] * inv, oh[q], ol[q]);
 #pragma unroll
-        for (int np = 0; np <= ks; ++np) {
-          b_cols(b, z, kLdC, ks * 16, np * 16, lane);
-#pragma unroll
-          for (int c2 = 0; c2 < NP; ++c2) mma2(R[2 * np], R[2 * np + 1], a[c2], b);
-          b_cols(b, z + kChunk * kLdC, kLdC, ks * 16, np * 16, lane);
-          mma2(R[2 * np], R[2 * np + 1], a[0], b);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 e = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
-          float2 x = unpack2(a[0][q]);
-          if (NP == 2) {
-            const float2 y = unpack2(a[NP - 1][q]);
-            x.x = __fadd_rn(x.x, y.x);
-            x.y = __fadd_rn(x.y, y.y);
+        for (int i = 0; i < OT / 2; ++i) {
+          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
+          if (np <= ks) {
+            uint32_t b[4];
+            b_cols(b, z, kLdC, ks * 16, np * 16, lane);
+            mma2(R[2 * i], R[2 * i + 1], oh, b);
+            if (NP == 2) mma2(R[2 * i], R[2 * i + 1], ol, b);
+            b_cols(b, z + kChunk * kLdC, kLdC, ks * 16, np * 16, lane);
+            mma2(R[2 * i], R[2 * i + 1], oh, b);
           }
-          split2(x.x * e.x, x.y * e.y, oh[ks][q], ol[ks][q]);
         }
       }
-      __nv_bfloat16 *rt = p.rt + rec * (2ll * p.dvp * kChunk);
+      if (NH > 1) {
+        float4 *own = part + warp * (32 * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i)
+          own[((i + OT * h) & 7) * 32 + lane] = make_float4(R[i][0], R[i][1], R[i][2], R[i][3]);
+        block_barrier(blk, 32 * NH);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi, lo;
-          split2(R[i][2 * h], R[i][2 * h + 1], hi, lo);
-          const long long at = (long long)(r0 + 8 * h) * kChunk + 8 * i + t2;
-          *reinterpret_cast<uint32_t *>(rt + at) = hi;
-          *reinterpret_cast<uint32_t *>(rt + (long long)p.dvp * kChunk + at) = lo;
+        for (int o = 1; o < NH; ++o) {
+          const float4 *their = part + (blk * NH + ((h + o) & (NH - 1))) * (32 * 8);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = their[((i + OT * h) & 7) * 32 + lane];
+            R[i][0] += y.x; R[i][1] += y.y; R[i][2] += y.z; R[i][3] += y.w;
+          }
         }
+      }
+      {
+        __half *rt = p.rt + rec * (2ll * p.dvp * kChunk);
+        float own[OT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 8 * i + t2 + (j & 1), r = r0 + 8 * (j >> 1);
-          if (t < n && r < p.d_v)
-            store_as(p.o, p.dtype, (start + (long long)c * kChunk + t) * p.o_stride +
-                                       (long long)head * p.d_v + r, R[i][j]);
+        for (int i = 0; i < OT; ++i) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t hi, lo;
+            split2(R[i][2 * r], R[i][2 * r + 1], hi, lo);
+            const long long at = (long long)(r0 + 8 * r) * kChunk + 8 * ((i + OT * h) & 7) + t2;
+            *reinterpret_cast<uint32_t *>(rt + at) = hi;
+            *reinterpret_cast<uint32_t *>(rt + (long long)p.dvp * kChunk + at) = lo;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) own[i][j] = R[i][j];
         }
+        store_tokens<NP, OT>(own, scale, st + l.v, ldv, blk * 16, OT * h, p.dv, p.dtype, p.v_stride,
+                             start + (long long)c * kChunk, n, head * p.d_v + row0 + blk * 16,
+                             p.d_v - row0 - blk * 16, p.v16, lane);
       }
       // D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K
-      uint32_t xh[4][4], xl[4][4];
-      if (DELTA) {
+      uint32_t oh[4][4], ol[4][4], rh[4][4], rl[4][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 e = *reinterpret_cast<const float2 *>(eG + 8 * i + t2);
-          R[i][0] *= -e.x; R[i][1] *= -e.y; R[i][2] *= -e.x; R[i][3] *= -e.y;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = *reinterpret_cast<const float2 *>(eG + i * 16 + 8 * (q >> 1) + t2);
+          split2(x[i][2 * q] * inv * f.x, x[i][2 * q + 1] * inv * f.y, oh[i][q], ol[i][q]);
+          if (DELTA) {
+            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
+            const float2 e = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+            const float *y = &R[2 * i + (q >> 1)][2 * (q & 1)];
+            split2(y[0] * e.x * -kappa, y[1] * e.y * -kappa, rh[i][q], rl[i][q]);
+          }
         }
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) split_tiles(R[2 * ks], R[2 * ks + 1], xh[ks], xl[ks]);
-      }
-      const float eC = eG[kChunk - 1];
-#pragma unroll
-      for (int np = 0; np < DK / 16; ++np) {
+      for (int np = 0; np < NTH / 2; ++np) {
         float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
+        for (int i = 0; i < 4; ++i) {
           uint32_t b[4];
-          b_cols(b, sq, LD, ks * 16, np * 16, lane);
-          mma2(a0, a1, oh[ks], b);
-          mma2(a0, a1, ol[ks], b);
+          b_cols(b, sq, LD, i * 16, c0 + np * 16, lane);
+          mma2(a0, a1, oh[i], b);
+          mma2(a0, a1, ol[i], b);
           if (NP == 2) {
-            b_cols(b, sq + kChunk * LD, LD, ks * 16, np * 16, lane);
-            mma2(a0, a1, oh[ks], b);
+            b_cols(b, sq + kChunk * LD, LD, i * 16, c0 + np * 16, lane);
+            mma2(a0, a1, oh[i], b);
           }
           if (DELTA) {
-            b_cols(b, sk, LD, ks * 16, np * 16, lane);
-            mma2(a0, a1, xh[ks], b);
-            mma2(a0, a1, xl[ks], b);
+            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
+            b_cols(b, sk, LD, ks * 16, c0 + np * 16, lane);
+            mma2(a0, a1, rh[i], b);
+            mma2(a0, a1, rl[i], b);
             if (NP == 2) {
-              b_cols(b, sk + kChunk * LD, LD, ks * 16, np * 16, lane);
-              mma2(a0, a1, xh[ks], b);
+              b_cols(b, sk + kChunk * LD, LD, ks * 16, c0 + np * 16, lane);
+              mma2(a0, a1, rh[i], b);
             }
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          D[2 * np][j] = fmaf(D[2 * np][j], eC, a0[j]);
-          D[2 * np + 1][j] = fmaf(D[2 * np + 1][j], eC, a1[j]);
+          D[2 * np][j] = fmaf(D[2 * np][j], eC, a0[j] * scale);
+          D[2 * np + 1][j] = fmaf(D[2 * np + 1][j], eC, a1[j] * scale);
         }
       }
+      top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(D));
+      if (NH > 1 && lane == 0) tops[warp] = top;
     }
     if (p.stages == 1) {
       __syncthreads();
-      fetch_next();
+      if (loader && c > 0) fetch(c - 1);
     }
   }
-  if (live && p.d_state_in)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (r0 + 8 * h < p.d_v)
-          *reinterpret_cast<float2 *>(p.d_state_in + ((long long)blockIdx.x * p.d_v + r0 + 8 * h) * DK +
-                                      8 * i + t2) = make_float2(D[i][2 * h], D[i][2 * h + 1]);
+  if (live && p.d_state_in) save_state<NTH>(D, p.d_state_in, blockIdx.x, p.d_v, DK, r0, c0 + t2);
 }
 
 // -------------------------------------------------------------------------------------
 // scan_grads
 // -------------------------------------------------------------------------------------
-// Grid (slot, head), 8 warps.  Warps 0-3 (group A) own 16 rows each of diag(e^G) dO S0 and
-// R S0, warps 4-7 (group B) of E D, dO E^T and R E^T; the value rows are the contraction
+// Grid (slot, head), 8 warps.  Warps 0-3 (group A) own 16 rows each of dO S0 and R S0, warps
+// 4-7 (group B) of E D, dO E^T and R E^T; the value rows are the contraction
 // axis and pass through shared memory kGradRows at a time.  With dP'_ts = b_s dec_ts dO_t.E_s
 // (s <= t), dL'_ts = -b_s dec_ts R_t.E_s (s < t):
 //   dQ = diag(e^G) dO S0 + dP' K
@@ -1170,6 +1475,9 @@ __global__ void __launch_bounds__(32 * (4 + kLoadWarps)) scan_reverse_kernel(con
 //   dlog_alpha_r = sum_{t >= r} dG_t + sum_s w_s k_s.(D^T E_s) + e^{G_C} <D, S0>
 // (the pair (t, s) enters dG_t and, through dbeta_s, -dG_s with the same value, so the sums
 // over t >= r cancel exactly where they should).
+// Scales: every product pairs a plane of the forward walk (16 value rows over c_b) with one
+// of the reverse walk (over d_b), so a 16-row step contributes in units of c_b d_b; left operands
+// are brought to the largest such unit F, and sums are held over F.
 constexpr int kGradRows = 32;
 
 struct GradLayout {
@@ -1182,21 +1490,40 @@ __host__ __device__ inline GradLayout grad_layout(int dk, int np) {
   l.k = at; at += np * kChunk * ld * 2;
   l.q = at; at += np * kChunk * ld * 2;
   l.x = at; at += 4 * kChunk * kLdC * 2;                 // dP' hi, lo, dL' hi, lo
-  l.f = at; at += (4 * kChunk + 2 * kChunk + 3 * kChunk + 4 * kChunk + 16) * 4;
-  l.stage = at;
+  l.f = at; at += (kGateFloats + 3 * kChunk + 4 * kChunk + 16) * 4;
+  l.stage = (at + 15) / 16 * 16;
   at = 0;
   l.s0 = at; at += 2 * kGradRows * ld * 2;
   l.d = at; at += 2 * kGradRows * ld * 2;
   l.e = at; at += 2 * kGradRows * kLdC * 2;
   l.r = at; at += 2 * kGradRows * kLdC * 2;
-  l.o = at; at += np * kChunk * (kGradRows + 8) * 2;
+  l.o = at; at += kChunk * tile_ld(np, kGradRows / 16) * (np == 2 ? 4 : 2);
   l.stage_bytes = at;                                    // holds the [64][dk + 4] fp32 exchange too
   return l;
 }
 
+// Rows [0, there) of kGradRows rows of a plane; the others are zeros.
+template <int COLS, int LD>
+__device__ __forceinline__ void copy_rows(__half *dst, const __half *src, int there, int tid, int threads) {
+  constexpr int per = COLS / 8;
+#pragma unroll 2
+  for (int i = tid; i < kGradRows * per; i += threads) {
+    const bool in = i / per < there;
+    cp16(dst + (i / per) * LD + (i % per) * 8, in ? src + i * 8 : src, in);
+  }
+}
+// A left operand's registers times a power of two <= 1.
+__device__ __forceinline__ void scale_frag(uint32_t (&a)[4], __half2 by) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&a[q]), by);
+    a[q] = *reinterpret_cast<const uint32_t *>(&y);
+  }
+}
+
 template <int DK, int NP, bool DELTA>
 __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, NT = DK / 8, LDO = kGradRows + 8, LDX = DK + 4;
+  constexpr int LD = DK + 8, NT = DK / 8, LDX = DK + 4, LDO = tile_ld(NP, kGradRows / 16), SIZE = NP == 2 ? 4 : 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const GradLayout l = grad_layout(DK, NP);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w4 = warp & 3, g = lane >> 2,
@@ -1206,51 +1533,49 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
   if (n == 0) return;
-  const int qh = head / p.share;
   const long long rec = (long long)slot * p.H + head;
-  __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(smem + l.k);
-  __nv_bfloat16 *sq = reinterpret_cast<__nv_bfloat16 *>(smem + l.q);
-  __nv_bfloat16 *sx = reinterpret_cast<__nv_bfloat16 *>(smem + l.x);
-  float *eG = reinterpret_cast<float *>(smem + l.f), *w = eG + kChunk, *be = w + kChunk,
-        *eC = be + kChunk;
-  double *G = reinterpret_cast<double *>(eC + kChunk);
-  float *rowv = reinterpret_cast<float *>(G + kChunk), *aq = rowv + kChunk, *kw = aq + kChunk,
-        *colp = kw + kChunk, *red = colp + 4 * kChunk;
+  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+  __half *sk = reinterpret_cast<__half *>(smem + l.k), *sq = reinterpret_cast<__half *>(smem + l.q);
+  __half *sx = reinterpret_cast<__half *>(smem + l.x);
+  float *eG = reinterpret_cast<float *>(smem + l.f), *w = eG + kChunk, *be = w + kChunk, *eC = be + kChunk;
+  const double *G = reinterpret_cast<const double *>(eC + kChunk);
+  float *rowv = eG + kGateFloats, *aq = rowv + kChunk, *kw = aq + kChunk, *colp = kw + kChunk,
+        *red = colp + 4 * kChunk;
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
-    copy_tile(sk + c * kChunk * LD, LD, (c ? p.k.lo : p.k.hi) + token0 * p.k.stride + qh * p.k.hstride,
-              p.k.stride, kChunk, DK, n, DK, tid, kGradThreads);
-    copy_tile(sq + c * kChunk * LD, LD, (c ? p.q.lo : p.q.hi) + token0 * p.q.stride + qh * p.q.hstride,
-              p.q.stride, kChunk, DK, n, DK, tid, kGradThreads);
+    copy_plane<kChunk, DK, LD>(sk + c * kChunk * LD, p.khat + (qrec * NP + c) * (kChunk * DK), tid, kGradThreads);
+    copy_plane<kChunk, DK, LD>(sq + c * kChunk * LD, p.qhat + (qrec * NP + c) * (kChunk * DK), tid, kGradThreads);
   }
   for (int i = tid; i < kGateFloats / 4; i += kGradThreads)
     cp16(eG + 4 * i, p.gates + rec * kGateFloats + 4 * i, true);
-  const int blocks = (p.dvp + kGradRows - 1) / kGradRows;
+  const int blocks = (p.dvp + kGradRows - 1) / kGradRows, blocks16 = p.dvp / 16;
   auto fetch = [&](int b) {
     uint8_t *st = smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0);
     const int v0 = b * kGradRows, rows = min(kGradRows, p.dvp - v0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.s0) + c * kGradRows * LD, LD,
-                p.s0 + (rec * 2 + c) * p.dvp * DK + (long long)v0 * DK, DK, kGradRows, DK, rows, DK, tid,
-                kGradThreads);
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.d) + c * kGradRows * LD, LD,
-                p.dd + (rec * 2 + c) * p.dvp * DK + (long long)v0 * DK, DK, kGradRows, DK, rows, DK, tid,
-                kGradThreads);
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.e) + c * kGradRows * kLdC, kLdC,
-                p.et + (rec * 2 + c) * p.dvp * kChunk + (long long)v0 * kChunk, kChunk, kGradRows, kChunk,
-                rows, kChunk, tid, kGradThreads);
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.r) + c * kGradRows * kLdC, kLdC,
-                p.rt + (rec * 2 + c) * p.dvp * kChunk + (long long)v0 * kChunk, kChunk, kGradRows, kChunk,
-                rows, kChunk, tid, kGradThreads);
+      const long long at = (rec * 2 + c) * p.dvp + v0;
+      copy_rows<DK, LD>(reinterpret_cast<__half *>(st + l.s0) + c * kGradRows * LD, p.s0 + at * DK, rows, tid, kGradThreads);
+      copy_rows<DK, LD>(reinterpret_cast<__half *>(st + l.d) + c * kGradRows * LD, p.dd + at * DK, rows, tid, kGradThreads);
+      copy_rows<kChunk, kLdC>(reinterpret_cast<__half *>(st + l.e) + c * kGradRows * kLdC, p.et + at * kChunk, rows, tid, kGradThreads);
+      copy_rows<kChunk, kLdC>(reinterpret_cast<__half *>(st + l.r) + c * kGradRows * kLdC, p.rt + at * kChunk, rows, tid, kGradThreads);
     }
-#pragma unroll
-    for (int c = 0; c < NP; ++c)
-      copy_tile(reinterpret_cast<__nv_bfloat16 *>(st + l.o) + c * kChunk * LDO, LDO,
-                (c ? p.dO.lo : p.dO.hi) + token0 * p.dO.stride + (long long)head * p.dO.hstride + v0,
-                p.dO.stride, kChunk, kGradRows, n, p.dO.hstride - v0, tid, kGradThreads);
+    copy_tokens<SIZE>(st + l.o, LDO,
+                      static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + v0) * SIZE,
+                      p.o_stride, kGradRows, n, p.d_v - v0, p.o16, tid, kGradThreads);
     cp_commit();
   };
+  fetch(0);
+  // exponents of the steps' units, the largest one
+  const unsigned *cb = reinterpret_cast<const unsigned *>(p.fscale + rec * blocks16);
+  const unsigned *db = reinterpret_cast<const unsigned *>(p.bscale + rec * blocks16);
+  int top = 0;
+  for (int b = lane; b < blocks16; b += 32) top = max(top, (int)(__ldg(cb + b) >> 23) + (int)(__ldg(db + b) >> 23));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  // F = 2^(top - 254) as two factors, each in range
+  const int f1 = (top - 254) / 2, f2 = top - 254 - f1;
+  const float F1 = __uint_as_float((unsigned)(127 + max(-126, f1)) << 23), F2 = __uint_as_float((unsigned)(127 + max(-126, f2)) << 23);
+
   // group A: acc = dO S0, acc2 = R S0; group B: acc = E D, acc2 tiles 0-7 dO E^T, 8-15 R E^T
   constexpr int N2 = NT > 16 ? NT : 16;
   float acc[NT][4], acc2[N2][4], ds = 0.0f;
@@ -1263,35 +1588,61 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc2[i][j] = 0.0f;
 
-  fetch(0);
   for (int b = 0; b < blocks; ++b) {
     cp_wait<0>();
     __syncthreads();
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
     uint8_t *st = smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0);
-    const __nv_bfloat16 *s0 = reinterpret_cast<const __nv_bfloat16 *>(st + l.s0);
-    const __nv_bfloat16 *dd = reinterpret_cast<const __nv_bfloat16 *>(st + l.d);
-    const __nv_bfloat16 *se = reinterpret_cast<const __nv_bfloat16 *>(st + l.e);
-    const __nv_bfloat16 *sr = reinterpret_cast<const __nv_bfloat16 *>(st + l.r);
-    const __nv_bfloat16 *so = reinterpret_cast<const __nv_bfloat16 *>(st + l.o);
-    for (int i = tid; i < kGradRows * DK / 2; i += kGradThreads) {        // <D, S0>
-      const int at = (i / (DK / 2)) * LD + (i % (DK / 2)) * 2;
-      auto pair = [&](const __nv_bfloat16 *x) {
-        const float2 hi = unpack2(*reinterpret_cast<const uint32_t *>(x + at));
-        const float2 lo = unpack2(*reinterpret_cast<const uint32_t *>(x + kGradRows * LD + at));
-        return make_float2(__fadd_rn(hi.x, lo.x), __fadd_rn(hi.y, lo.y));
-      };
-      const float2 x = pair(s0), y = pair(dd);
-      ds = fmaf(x.x, y.x, fmaf(x.y, y.y, ds));
-    }
+    const __half *s0 = reinterpret_cast<const __half *>(st + l.s0), *dd = reinterpret_cast<const __half *>(st + l.d);
+    const __half *se = reinterpret_cast<const __half *>(st + l.e), *sr = reinterpret_cast<const __half *>(st + l.r);
 #pragma unroll
     for (int kk = 0; kk < kGradRows; kk += 16) {
+      const int b16 = b * (kGradRows / 16) + kk / 16;
+      if (b16 >= blocks16) break;
+      const unsigned ed = __ldg(db + b16) >> 23;
+      const int gap = (int)(__ldg(cb + b16) >> 23) + (int)ed - top;       // <= 0
+      const float ratio = gap > -126 ? __uint_as_float((unsigned)(127 + gap) << 23) : 0.0f;
+      const float dinv = __uint_as_float((254u - ed) << 23);
+      const __half2 by = __float2half2_rn(ratio);
       uint32_t ao[NP][4], ar[2][4], b4[4];
+      if (NP == 1) {
+        uint32_t raw[4];
+        a_rows(raw, reinterpret_cast<const __half *>(st + l.o), LDO, m0, kk, lane);
 #pragma unroll
-      for (int c = 0; c < NP; ++c) a_rows(ao[c], so + c * kChunk * LDO, LDO, m0, kk, lane);
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = pair_of(raw[q], p.dtype);
+          ao[0][q] = pack2(f.x * dinv * ratio, f.y * dinv * ratio);
+        }
+      } else {
+        const float *so = reinterpret_cast<const float *>(st + l.o);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (DELTA) a_cols(ar[c], sr + c * kGradRows * kLdC, kLdC, kk, m0, lane);
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = *reinterpret_cast<const float2 *>(so + (m0 + g + 8 * (q & 1)) * LDO + kk + 8 * (q >> 1) + t2);
+          split2(f.x * dinv * ratio, f.y * dinv * ratio, ao[0][q], ao[NP - 1][q]);
+        }
+      }
+      if (DELTA)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          a_cols(ar[c], sr + c * kGradRows * kLdC, kLdC, kk, m0, lane);
+          scale_frag(ar[c], by);
+        }
+      // <D, S0>
+      {
+        float part = 0.0f;
+#pragma unroll
+        for (int i = tid; i < 16 * DK / 2; i += kGradThreads) {
+          const int at = (kk + i / (DK / 2)) * LD + (i % (DK / 2)) * 2;
+          auto pair = [&](const __half *x) {
+            const float2 hi = half2_of(*reinterpret_cast<const uint32_t *>(x + at));
+            const float2 lo = half2_of(*reinterpret_cast<const uint32_t *>(x + kGradRows * LD + at));
+            return make_float2(__fadd_rn(hi.x, lo.x), __fadd_rn(hi.y, lo.y));
+          };
+          const float2 x = pair(s0), y = pair(dd);
+          part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
+        }
+        ds = fmaf(part, ratio, ds);
+      }
       if (groupA) {
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
@@ -1309,7 +1660,10 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
       } else {
         uint32_t ae[2][4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) a_cols(ae[c], se + c * kGradRows * kLdC, kLdC, kk, m0, lane);
+        for (int c = 0; c < 2; ++c) {
+          a_cols(ae[c], se + c * kGradRows * kLdC, kLdC, kk, m0, lane);
+          scale_frag(ae[c], by);
+        }
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
           b_cols(b4, dd, LD, kk, np * 16, lane);
@@ -1343,12 +1697,19 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
 #pragma unroll
   for (int d = 16; d; d >>= 1) ds += __shfl_xor_sync(0xFFFFFFFFu, ds, d);
   if (lane == 0) red[warp] = ds;
+  const float kappa = eG[kGateScales], qscale = eG[kGateScales + 1];
+  const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
+  const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
+  // planes of dP', dL' are held over F and 4 dvp (rounded up to a power of two): the entries of
+  // E, R and dO over their scales stay below 2^7 (E and R somewhat above), so a sum over d_v of their
+  // products stays below 2^14 dvp
+  const int lg = 32 - __clz(p.dvp - 1);
+  const float unit = __uint_as_float((unsigned)(127 - 2 - lg) << 23), iunit = __uint_as_float((unsigned)(127 + 2 + lg) << 23);
 
-  // row i of a planed tile, columns 8c + t2, +1
-  auto row_pair = [&](const __nv_bfloat16 *x, int row, int col) {
-    float2 v = unpack2(*reinterpret_cast<const uint32_t *>(x + row * LD + col));
+  auto row_pair = [&](const __half *x, int row, int col) {
+    float2 v = half2_of(*reinterpret_cast<const uint32_t *>(x + row * LD + col));
     if (NP == 2) {
-      const float2 y = unpack2(*reinterpret_cast<const uint32_t *>(x + kChunk * LD + row * LD + col));
+      const float2 y = half2_of(*reinterpret_cast<const uint32_t *>(x + kChunk * LD + row * LD + col));
       v.x = __fadd_rn(v.x, y.x);
       v.y = __fadd_rn(v.y, y.y);
     }
@@ -1358,39 +1719,42 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
-      float s = 0.0f;
+      float s = 0.0f, r = 0.0f;
+      const float e = eG[t], to = e * unit * ikappa;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const float2 q = row_pair(sq, t, 8 * i + t2);
-        acc[i][2 * h] *= eG[t];
-        acc[i][2 * h + 1] *= eG[t];
         s = fmaf(q.x, acc[i][2 * h], fmaf(q.y, acc[i][2 * h + 1], s));
+        acc[i][2 * h] *= to;
+        acc[i][2 * h + 1] *= to;
         if (DELTA) {
           const float2 k = row_pair(sk, t, 8 * i + t2);
-          acc2[i][2 * h] *= -eG[t];
-          acc2[i][2 * h + 1] *= -eG[t];
-          s = fmaf(k.x, acc2[i][2 * h], fmaf(k.y, acc2[i][2 * h + 1], s));
+          r = fmaf(k.x, acc2[i][2 * h], fmaf(k.y, acc2[i][2 * h + 1], r));
+          acc2[i][2 * h] *= -to;
+          acc2[i][2 * h + 1] *= -to;
         }
       }
+      s = fmaf(s, qscale, -r * kappa) * e;
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      if ((lane & 3) == 0) aq[t] = s;
+      if ((lane & 3) == 0) aq[t] = s * F1 * F2;
     }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
       float s = 0.0f;
+      const float to = w[t] * unit * iqscale;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const float2 k = row_pair(sk, t, 8 * i + t2);
         s = fmaf(k.x, acc[i][2 * h], fmaf(k.y, acc[i][2 * h + 1], s));
-        acc[i][2 * h] *= w[t];
-        acc[i][2 * h + 1] *= w[t];
+        acc[i][2 * h] *= to;
+        acc[i][2 * h + 1] *= to;
       }
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      if ((lane & 3) == 0) kw[t] = s;
+      if ((lane & 3) == 0) kw[t] = s * kappa * F1 * F2;
     }
     float rs[2] = {0.0f, 0.0f}, cs[8][2];
 #pragma unroll
@@ -1403,7 +1767,7 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-      const __nv_bfloat16 *left = ps ? sk : sq;
+      const __half *left = ps ? sk : sq;
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t a[NP][4], b4[4];
@@ -1421,7 +1785,8 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
             }
           }
       }
-      __nv_bfloat16 *out = sx + ps * 2 * kChunk * kLdC;
+      const float by = (ps ? kappa : qscale) * kappa;
+      __half *out = sx + ps * 2 * kChunk * kLdC;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (i / 2 <= w4) {
@@ -1435,8 +1800,8 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
               const bool in = ps ? s < t : s <= t;
               const float dec = in ? expf((float)(G[t] - G[s])) : 0.0f;
               const float z = in ? (ps ? -acc2[8 + i][2 * h + j] : acc2[i][2 * h + j]) * dec : 0.0f;
-              const float m = z * x[i][2 * h + j];
-              y[j] = z * be[s];
+              const float m = z * (x[i][2 * h + j] * by);
+              y[j] = z * be[s] * unit;
               if (in) {
                 rs[h] = fmaf(be[s], m, rs[h]);
                 cs[i][j] += m;
@@ -1454,7 +1819,7 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
     for (int h = 0; h < 2; ++h) {
       rs[h] += __shfl_xor_sync(0xFFFFFFFFu, rs[h], 1);
       rs[h] += __shfl_xor_sync(0xFFFFFFFFu, rs[h], 2);
-      if ((lane & 3) == 0) rowv[m0 + g + 8 * h] = rs[h];
+      if ((lane & 3) == 0) rowv[m0 + g + 8 * h] = rs[h] * F1 * F2;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -1464,10 +1829,11 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 4);
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 16);
-        if (g == 0) colp[w4 * kChunk + 8 * i + t2 + j] = c;
+        if (g == 0) colp[w4 * kChunk + 8 * i + t2 + j] = c * F1 * F2;
       }
   }
   __syncthreads();
+  const float out1 = F1 * kappa, out2 = F2 * iunit;      // what the sums of dQ and dK are held over
   if (groupA) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
@@ -1499,8 +1865,9 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         if (t < n) {
-          if (p.parts) store_pair(p.dq, 0, (tok * p.H + head) * DK + 8 * i + t2, acc[i][2 * h], acc[i][2 * h + 1]);
-          else store_pair(p.dq, p.dtype, tok * p.dq_stride + (long long)head * DK + 8 * i + t2, acc[i][2 * h], acc[i][2 * h + 1]);
+          const float x = acc[i][2 * h] * out1 * out2, y = acc[i][2 * h + 1] * out1 * out2;
+          if (p.parts) store_pair(p.dq, 0, (tok * p.H + head) * DK + 8 * i + t2, x, y);
+          else store_pair(p.dq, p.dtype, tok * p.q_stride + (long long)head * DK + 8 * i + t2, x, y);
         }
         if (DELTA)
           *reinterpret_cast<float2 *>(reinterpret_cast<float *>(smem + l.stage) + t * LDX + 8 * i + t2) =
@@ -1508,12 +1875,13 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
       }
     }
   } else {
+    const float turn = qscale * ikappa;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       if (ks >= w4) {
-        uint32_t a[4][4], b4[4];
+        uint32_t a[2][4], b4[4];
 #pragma unroll
-        for (int c = 0; c < (DELTA ? 4 : 2); ++c) a_cols(a[c], sx + c * kChunk * kLdC, kLdC, ks * 16, m0, lane);
+        for (int c = 0; c < 2; ++c) a_cols(a[c], sx + c * kChunk * kLdC, kLdC, ks * 16, m0, lane);
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
           b_cols(b4, sq, LD, ks * 16, np * 16, lane);
@@ -1523,18 +1891,32 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
             b_cols(b4, sq + kChunk * LD, LD, ks * 16, np * 16, lane);
             mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
           }
-          if (DELTA) {
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] *= turn;
+    if (DELTA)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        if (ks >= w4) {
+          uint32_t a[2][4], b4[4];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) a_cols(a[c], sx + (2 + c) * kChunk * kLdC, kLdC, ks * 16, m0, lane);
+#pragma unroll
+          for (int np = 0; np < DK / 16; ++np) {
             b_cols(b4, sk, LD, ks * 16, np * 16, lane);
-            mma2(acc[2 * np], acc[2 * np + 1], a[2], b4);
-            mma2(acc[2 * np], acc[2 * np + 1], a[3], b4);
+            mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
+            mma2(acc[2 * np], acc[2 * np + 1], a[1], b4);
             if (NP == 2) {
               b_cols(b4, sk + kChunk * LD, LD, ks * 16, np * 16, lane);
-              mma2(acc[2 * np], acc[2 * np + 1], a[2], b4);
+              mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
             }
           }
         }
       }
-    }
   }
   __syncthreads();
   if (!groupA) {
@@ -1552,22 +1934,25 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
             x.x = __fadd_rn(x.x, y.x);
             x.y = __fadd_rn(x.y, y.y);
           }
+          x.x = x.x * out1 * out2;
+          x.y = x.y * out1 * out2;
           if (p.parts) store_pair(p.dk, 0, (tok * p.H + head) * DK + 8 * i + t2, x.x, x.y);
-          else store_pair(p.dk, p.dtype, tok * p.dk_stride + (long long)head * DK + 8 * i + t2, x.x, x.y);
+          else store_pair(p.dk, p.dtype, tok * p.k_stride + (long long)head * DK + 8 * i + t2, x.x, x.y);
         }
     }
   } else if (warp == 0) {
     // gates: two tokens a lane, sums over t >= r from the chunk's end
     float dsum = 0.0f;
     for (int i = 0; i < kGradThreads / 32; ++i) dsum += red[i];
+    dsum = dsum * F1 * F2;
     double dG[2], tot = 0.0;
-    float db[2];
+    float db2[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const float c = (colp[t] + colp[kChunk + t]) + (colp[2 * kChunk + t] + colp[3 * kChunk + t]);
-      db[i] = fmaf(eC[t], kw[t], c);
-      dG[i] = (double)rowv[t] - (double)be[t] * db[i] + aq[t];
+      db2[i] = fmaf(eC[t], kw[t], c);
+      dG[i] = (double)rowv[t] - (double)be[t] * db2[i] + aq[t];
       tot += (double)w[t] * kw[t];
     }
 #pragma unroll
@@ -1585,7 +1970,7 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
       if (t < n) {
         const long long at = (token0 + t) * p.H + head;
         p.dlog_alpha[at] = (float)out[i];
-        p.dbeta[at] = db[i];
+        p.dbeta[at] = db2[i];
       }
     }
   }
@@ -1607,7 +1992,7 @@ static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParam
       const float4 x = *reinterpret_cast<const float4 *>(src + (long long)m * dk);
       s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
     }
-    const long long at = tok * (second ? p.dk_stride : p.dq_stride) + (long long)h * dk + c;
+    const long long at = tok * (second ? p.k_stride : p.q_stride) + (long long)h * dk + c;
     store_pair(second ? p.dk : p.dq, p.dtype, at, s.x, s.y);
     store_pair(second ? p.dk : p.dq, p.dtype, at + 2, s.z, s.w);
   }
@@ -1656,8 +2041,8 @@ __global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanP
     for (int c = 0; c < 4; ++c) {
       float x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
       if (on) {
-        load4(p.uk, p.dtype, tok * p.uk_stride + qo + 4 * LPR * c, x);
-        load4(p.uq, p.dtype, tok * p.uq_stride + qo + 4 * LPR * c, y);
+        load4(p.k, p.dtype, tok * p.k_stride + qo + 4 * LPR * c, x);
+        load4(p.q, p.dtype, tok * p.q_stride + qo + 4 * LPR * c, y);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) { k[4 * c + e] = x[e]; q[4 * c + e] = y[e]; }
@@ -1667,12 +2052,12 @@ __global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanP
     if (on) {
       a = expf(__ldg(p.log_alpha + tok * p.H + head));
       b = __ldg(p.beta + tok * p.H + head);
-      const long long vo = tok * p.uv_stride + (long long)head * p.d_v + row;
+      const long long vo = tok * p.v_stride + (long long)head * p.d_v + row;
 #pragma unroll
       for (int r = 0; r < kRecRows; ++r)
-        v[r] = p.dtype == 0 ? __ldg(static_cast<const float *>(p.uv) + vo + r)
-               : p.dtype == 1 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.uv)[vo + r])
-                              : __half2float(static_cast<const __half *>(p.uv)[vo + r]);
+        v[r] = p.dtype == 0 ? __ldg(static_cast<const float *>(p.v) + vo + r)
+               : p.dtype == 1 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v)[vo + r])
+                              : __half2float(static_cast<const __half *>(p.v)[vo + r]);
     }
     float u[kRecRows], o[kRecRows];
 #pragma unroll
@@ -1718,11 +2103,11 @@ __global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanP
 }
 
 using ScanFn = void (*)(ScanParams);
-// kernels of one key width: [np - 1][delta]
+// kernels of one key width
 struct ScanKernels {
   ScanFn prep[2][2][2];                // [np - 1][delta][backward]
-  ScanFn chain[2][2][2];               // [np - 1][delta][save]
-  ScanFn reverse[2][2];
+  ScanFn chain[2][2][2][2];            // [np - 1][delta][save][nh - 1]
+  ScanFn reverse[2][2][2];             // [np - 1][delta][nh - 1]
   ScanFn grads[2][2];
 };
 

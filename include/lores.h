@@ -369,10 +369,11 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * may be captured into a CUDA graph.  Two calls may share a workspace only if they are ordered
  * on the GPU.
  *
- * Accuracy.  Products run on the tensor cores on operands of 16 bits of significand (two bf16 parts;
- * bf16 inputs are exact), sums and the state are fp32: outputs are within 1e-5 (relative
- * L2) of the recurrence in exact arithmetic, before their rounding to `dtype`, while
- * |k_t|^2 beta_t < 2 holds (the domain of the recurrence).  An infinity or NaN in a token's
+ * Accuracy.  Products run on the tensor cores on operands of 22 bits of significand (two fp16
+ * parts; 16-bit inputs are exact), sums and the state are fp32.  States, the gates'
+ * gradients and everything fp32 are within a few 1e-6 (relative L2) of the recurrence in exact
+ * arithmetic, 16-bit outputs within their own rounding, while |k_t|^2 beta_t < 2 holds with
+ * delta = 1 (the domain of the recurrence).  An infinity or NaN in a token's
  * inputs may turn the outputs of the whole 64-token chunk that holds it (counted from the
  * sequence's start), and what follows, to NaN; other sequences are not touched. */
 typedef struct {
