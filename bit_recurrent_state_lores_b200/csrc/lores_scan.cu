@@ -130,8 +130,7 @@ unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, ScanParams
   p.dd = w.take<__half>(recs * 2 * rows * c.d_k);
   p.et = w.take<__half>(recs * 2 * rows * kChunk);
   p.rt = w.take<__half>(recs * 2 * rows * kChunk);
-  p.fscale = w.take<float>(recs * (rows / 16));
-  p.bscale = w.take<float>(recs * (rows / 16));
+  for (float *&x : p.scales) x = w.take<float>(recs * (rows / 16));
   if (c.heads != c.heads_qk) {
     const unsigned long long n = (unsigned long long)c.total * c.heads * c.d_k;
     p.dq = w.take<float>(n);
@@ -207,19 +206,12 @@ lores_status device_ok(int device) {
   return LORES_OK;
 }
 
-// How a walk over the chunks is cut: 16-row blocks per CTA (rb) and warps per block (nh).  The chain
-// from chunk to chunk bounds it while there are fewer blocks than SM quarters, so two
-// warps then share a block; beyond that a warp per block needs no exchange.
-struct Walk {
-  int rb, nh;
-};
-Walk walk_of(const Shape &s) {
+// Blocks of 16 value rows per CTA of a walk: a CTA's blocks share one fetch of a chunk's tiles, but the CTAs
+// should fill the SMs.
+int walk_blocks(const Shape &s) {
   const long long walks = (long long)s.c.n_seq * s.c.heads;
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
-  Walk w{kWalkWarps, 1};
-  if (s.c.d_k >= 32 && walks * blocks <= 4ll * sms) w = {kWalkWarps / 2, 2};
-  while (w.rb > 1 && (blocks < w.rb || walks * ((blocks + w.rb - 1) / w.rb) < sms * 3 / 4)) w.rb >>= 1;
-  return w;
+  return blocks < kMaxBlocks || walks * ((blocks + 1) / kMaxBlocks) < sms / 2 ? 1 : kMaxBlocks;
 }
 
 bool aligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3u) == 0; }
@@ -233,20 +225,16 @@ cudaError_t run_prep(const Shape &s, bool backward, const ScanParams &p, cudaStr
                 prep_layout(c.d_k, s.np).bytes, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
 }
 
-// what = 0: forward, 1: the backward pass's recomputation, 2: reverse
-cudaError_t run_walk(const Shape &s, int what, ScanParams p, cudaStream_t st) {
+cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
-  static std::atomic<unsigned long long> raised[4][2][2][3][2];
-  const int wi = width_index(c.d_k);
-  const Walk w = walk_of(s);
-  const WalkLayout l = walk_layout(c.d_k, s.np, w.rb, w.nh, c.delta, what);
-  const int tail = l.part + 64;
-  p.rb = w.rb;
-  p.stages = 2 * l.bytes + tail <= kMaxShared ? 2 : 1;
-  const ScanKernels &k = kernels().by_width[wi];
-  const ScanFn fn = what == 2 ? k.reverse[s.np - 1][c.delta][w.nh - 1] : k.chain[s.np - 1][c.delta][what][w.nh - 1];
-  return launch(fn, dim3(c.n_seq * c.heads, (s.dvp / 16 + w.rb - 1) / w.rb), 32 * (w.rb * w.nh + kLoadWarps),
-                p.stages * l.bytes + tail, st, c.device, p, raised[wi][s.np - 1][c.delta][what][w.nh - 1]);
+  static std::atomic<unsigned long long> raised[4][2][2][3];
+  const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
+  p.rb = walk_blocks(s);
+  const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
+  p.stages = 2 * l.bytes + p.rb * l.tail <= kMaxShared ? 2 : 1;
+  return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],
+                dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * (p.rb * (nh + kSideWarps) + kLoadWarps),
+                p.stages * l.bytes + p.rb * l.tail, st, c.device, p, raised[wi][s.np - 1][c.delta][kind]);
 }
 
 cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
@@ -254,9 +242,9 @@ cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
   static std::atomic<unsigned long long> raised[4][2][2];
   const int wi = width_index(c.d_k);
   const GradLayout l = grad_layout(c.d_k, s.np);
-  p.stages = l.stage + 2 * l.stage_bytes <= kMaxShared ? 2 : 1;
+  p.stages = grad_bytes(l, c.d_k, 2) <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3(s.n_slots, c.heads), kGradThreads,
-                l.stage + p.stages * l.stage_bytes, st, c.device, p, raised[wi][s.np - 1][c.delta]);
+                grad_bytes(l, c.d_k, p.stages), st, c.device, p, raised[wi][s.np - 1][c.delta]);
 }
 
 lores_status check_inputs(const Shape &s, const void *q, const void *k, const void *v, const float *log_alpha,
@@ -318,7 +306,7 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
     return cuda_status(cudaGetLastError());
   }
   cudaError_t e = run_prep(s, false, p, cs);
-  if (e == cudaSuccess) e = run_walk(s, 0, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, kForward, p, cs);
   return cuda_status(e);
 }
 
@@ -364,8 +352,8 @@ lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, co
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = run_prep(s, true, p, cs);
-  if (e == cudaSuccess) e = run_walk(s, 1, p, cs);
-  if (e == cudaSuccess) e = run_walk(s, 2, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, kRecompute, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, kReverse, p, cs);
   if (e == cudaSuccess) e = run_grads(s, p, cs);
   if (e == cudaSuccess && p.parts && any) {
     p.dq = dq;

@@ -15,7 +15,8 @@
 //                 S_C, chunk after chunk.  Value rows are independent (as in the decode
 //                 step), so one or two warps own 16 of them, keep S [16][d_k] in their
 //                 accumulators and feed it back as the next product's left operand
-//                 without leaving registers.
+//                 without leaving registers; two more warps per 16 rows do what the
+//                 next chunk does not wait for.
 // Backward, D = dL/dS_C:
 //   R   = Z^T dO + Kb D^T (= dV)       D0 = e^{G_C} D + (diag(e^G) dO)^T Q - d (diag(e^G) R)^T K
 //   scan_reverse  the same walk backwards over R and D;
@@ -26,8 +27,8 @@
 // 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi; 16-bit inputs are
 // exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
 // K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
-// operands by one scale per 16 value rows and chunk (largest entry of S0 and V, or of D and
-// dO, in [2^6, 2^7)).  The error of states and gradients stays near 1e-7; two bf16
+// operands by one scale per 16 value rows and chunk (S0 and D: their largest entry in
+// [2^6, 2^7); E and R: the larger of that and V's or dO's).  The error of states and gradients stays near 1e-7; two bf16
 // planes would leave 3e-6 to 1e-5, one fp16 plane 2e-4.  Products that only reach a 16-bit
 // output (Q S0^T and P E) use one plane.
 #pragma once
@@ -40,11 +41,8 @@ namespace lores {
 namespace scan {
 
 constexpr int kChunk = 64;
-constexpr int kLdC = kChunk + 8;       // row stride of a [64][64] plane in shared memory (rows 16
-                                       // bytes apart modulo 128: the 8 rows that ldmatrix
-                                       // reads fall into different banks)
 constexpr int kPrepThreads = 128;
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
 
 struct ScanParams {
@@ -64,10 +62,10 @@ struct ScanParams {
   float *gates;                        // kGateFloats
   __half *khat, *qhat;                 // [NP][64][d_k], divided by their scales
   __half *kt, *kb;                     // [2][64][d_k]
-  __half *tm, *pp, *z;                 // [2][64][64]
+  __half *tm, *pp, *z;                 // [2][64][64] (pp of a 16-bit forward call: one plane)
   __half *s0, *dd;                     // [2][dvp][d_k]
   __half *et, *rt;                     // [2][dvp][64]
-  float *fscale, *bscale;              // [dvp/16]: scales of s0 and et, of dd and rt
+  float *scales[4];                    // of s0, et, dd, rt: [dvp/16]
   // backward
   const float *d_state_out;
   float *d_state_in;
@@ -76,9 +74,12 @@ struct ScanParams {
   float *dlog_alpha, *dbeta;
 };
 
-// Record of a chunk and head: e^G, w, b, e^(G_C - G) [64] each, G [64] (double), scales of K and Q
-constexpr int kGateFloats = 4 * kChunk + 2 * kChunk + 4;
-constexpr int kGateScales = 6 * kChunk;
+// Record of a chunk and head, kChunk entries each: e^G, w over the scale of K (that is, what
+// multiplies a row of khat), e^G likewise, w, b, e^(G_C - G); G (double); the scales of K and Q.
+enum GateRow { kGateE, kGateWk, kGateEk, kGateW, kGateB, kGateC, kGateG };
+constexpr int kGateScales = (kGateG + 2) * kChunk;
+constexpr int kGateFloats = kGateScales + 4;
+enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR };
 
 // -------------------------------------------------------------------------------------
 // sequences and chunk slots
@@ -161,37 +162,55 @@ __device__ __forceinline__ void check_offsets(const ScanParams &p) {
 __device__ __forceinline__ uint32_t smem_addr(const void *x) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(x));
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *row) {
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t row) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_addr(row)));
+               : "r"(row));
 }
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void *row) {
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t row) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_addr(row)));
+               : "r"(row));
 }
-__device__ __forceinline__ void stsm4t(void *row, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_addr(row)),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+__device__ __forceinline__ void stsm4t(uint32_t row, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(row), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// Fragment loads of 16x16 blocks from row-major shared memory with row stride ld.
+// Fragment loads of 16x16 blocks of a tiled matrix with COLS columns.
 //   right operand, two column tiles (r[0], r[1]: columns n0..n0+7; r[2], r[3]: n0+8..):
 //     b_rows:  stored [n][k]      b_cols: stored [k][n]
 //   left operand:
 //     a_rows:  stored [m][k]      a_cols: stored [k][m]
-__device__ __forceinline__ void b_rows(uint32_t (&r)[4], const __half *x, int ld, int n0, int k0, int lane) {
-  ldsm4(r, x + (n0 + ((lane >> 4) << 3) + (lane & 7)) * ld + k0 + (((lane >> 3) & 1) << 3));
+// ldmatrix's four tiles are (0, 0), (0, 1), (1, 0), (1, 1) of the block in the order of the registers, or with the
+// middle two exchanged; `Lane` holds a lane's part of the address for both orders.
+template <int COLS>
+struct Lane {
+  uint32_t down, across;
+  __device__ __forceinline__ explicit Lane(int lane) {
+    const int i = lane >> 3, r = (lane & 7) * 16;
+    down = ((i >> 1) * (COLS / 8) + (i & 1)) * 128 + r;
+    across = ((i & 1) * (COLS / 8) + (i >> 1)) * 128 + r;
+  }
+  __device__ __forceinline__ static uint32_t at(int row, int col) {
+    return ((row >> 3) * (COLS / 8) + (col >> 3)) * 128;
+  }
+  __device__ __forceinline__ void b_rows(uint32_t (&r)[4], uint32_t x, int n0, int k0) const { ldsm4(r, x + down + at(n0, k0)); }
+  __device__ __forceinline__ void b_cols(uint32_t (&r)[4], uint32_t x, int k0, int n0) const { ldsm4t(r, x + across + at(k0, n0)); }
+  __device__ __forceinline__ void a_rows(uint32_t (&r)[4], uint32_t x, int m0, int k0) const { ldsm4(r, x + across + at(m0, k0)); }
+  __device__ __forceinline__ void a_cols(uint32_t (&r)[4], uint32_t x, int k0, int m0) const { ldsm4t(r, x + down + at(k0, m0)); }
+};
+// The caller's token rows, in plain rows of ld elements.
+__device__ __forceinline__ void a_rows_plain(uint32_t (&r)[4], uint32_t x, int ld, int m0, int k0, int lane) {
+  ldsm4(r, x + 2 * ((m0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + k0 + ((lane >> 4) << 3)));
 }
-__device__ __forceinline__ void b_cols(uint32_t (&r)[4], const __half *x, int ld, int k0, int n0, int lane) {
-  ldsm4t(r, x + (k0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + n0 + ((lane >> 4) << 3));
+__device__ __forceinline__ void a_cols_plain(uint32_t (&r)[4], uint32_t x, int ld, int k0, int m0, int lane) {
+  ldsm4t(r, x + 2 * ((k0 + ((lane >> 4) << 3) + (lane & 7)) * ld + m0 + (((lane >> 3) & 1) << 3)));
 }
-__device__ __forceinline__ void a_rows(uint32_t (&r)[4], const __half *x, int ld, int m0, int k0, int lane) {
-  ldsm4(r, x + (m0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + k0 + ((lane >> 4) << 3));
-}
-__device__ __forceinline__ void a_cols(uint32_t (&r)[4], const __half *x, int ld, int k0, int m0, int lane) {
-  ldsm4t(r, x + (k0 + ((lane >> 4) << 3) + (lane & 7)) * ld + m0 + (((lane >> 3) & 1) << 3));
+// Element (row, col) of a tiled matrix.
+template <int COLS>
+__device__ __forceinline__ int tiled(int row, int col) {
+  return ((row >> 3) * (COLS / 8) + (col >> 3)) * 64 + (row & 7) * 8 + (col & 7);
 }
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -281,20 +300,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A [ROWS][COLS] plane of a record (dense rows) into shared rows of LD elements.
-template <int ROWS, int COLS, int LD>
-__device__ __forceinline__ void copy_plane(__half *dst, const __half *src, int tid, int threads) {
-  constexpr int per = COLS / 8;
-#pragma unroll 4
-  for (int i = tid; i < ROWS * per; i += threads)
-    cp16(dst + (i / per) * LD + (i % per) * 8, src + i * 8, true);
+// BYTES contiguous bytes (a multiple of 16).
+template <int BYTES>
+__device__ __forceinline__ void copy_flat(uint8_t *dst, const void *src, int tid, int threads) {
+  const uint8_t *s = static_cast<const uint8_t *>(src);
+#pragma unroll 8
+  for (int i = tid; i < BYTES / 16; i += threads) cp16(dst + 16 * i, s + 16 * i, true);
 }
-// The lower triangle of a [64][64] plane, by 16x16 blocks (the others are not read).
-__device__ __forceinline__ void copy_lower(__half *dst, const __half *src, int tid, int threads) {
-#pragma unroll 4
-  for (int i = tid; i < kChunk * 8; i += threads) {
-    const int r = i >> 3, c = i & 7;
-    if ((c >> 1) <= (r >> 4)) cp16(dst + r * kLdC + c * 8, src + r * kChunk + c * 8, true);
+// The tiles on and below the diagonal of a [64][64] plane, by blocks of 16 rows and columns (the others are
+// not read).
+__device__ __forceinline__ void copy_lower(uint8_t *dst, const __half *src, int tid, int threads) {
+  const uint8_t *s = reinterpret_cast<const uint8_t *>(src);
+#pragma unroll 2
+  for (int i = tid; i < kChunk * kChunk / 8; i += threads) {
+    const int tile = i >> 3;
+    if (((tile & 7) >> 1) <= (tile >> 4)) cp16(dst + 16 * i, s + 16 * i, true);
   }
 }
 // `cols` columns (a multiple of 16) of 64 token rows of the caller's tensor: rows >= n and
@@ -370,94 +390,124 @@ __device__ __forceinline__ void load8(const void *src, int dtype, long long i, b
 // X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
 // product's left operand in place.
 constexpr int kLdF = kChunk + 2;       // row stride of the fp32 matrix in shared memory
-constexpr int kLdX = 24;               // row stride of a [16][16] plane
 
 struct PrepLayout {
-  int k, q, x, xd, f, bytes;           // q: also the planes of A (48 rows) once Q is used
+  int k, q, x, xd, f, bytes;           // q: also the planes of A once Q is used
 };
 __host__ __device__ constexpr PrepLayout prep_layout(int dk, int np) {
   PrepLayout l{};
-  const int tile = np * kChunk * (dk + 8) * 2, planes = 2 * 48 * kLdC * 2;
+  const int tile = np * kChunk * dk * 2, planes = 2 * kChunk * kChunk * 2;
   l.k = 0;
   l.q = tile;
   l.x = l.q + (tile > planes ? tile : planes);
   l.xd = l.x + kChunk * kLdF * 4;
-  l.f = l.xd + 4 * 2 * 16 * kLdX * 2;
-  l.bytes = l.f + (4 * kChunk + 2 * kChunk + 16) * 4;
+  l.f = l.xd + 4 * 2 * 16 * 16 * 2;
+  l.bytes = l.f + (3 * kChunk + 2 * kChunk + 16) * 4;
   return l;
 }
 
-// Rows of K or Q of a chunk: their scale (left in *scale), planes in shared memory, and in the
-// workspace where `out` is given.
-template <int DK, int NP>
-__device__ __forceinline__ float stage_rows(const ScanParams &p, const void *src, long long stride, long long token0,
-                                            int qh, int n, __half *dst, __half *out, unsigned *red, int tid) {
-  constexpr int LD = DK + 8, PER = DK / 8;
-  unsigned m = 0;
-  for (int i = tid; i < kChunk * PER; i += kPrepThreads) {
-    const int r = i / PER, c = (i % PER) * 8;
-    if (r < n) {
-      float x[8];
-      load8(src, p.dtype, (token0 + r) * stride + (long long)qh * DK + c, p.qk16, x);
+// Rows of K or Q of a chunk.  A thread holds PASS pieces of 8 entries as they came; all loads are in flight
+// before the first is used.
+template <int DK, int NP, int PASS>
+__device__ __forceinline__ void load_rows(const ScanParams &p, const void *src, long long stride, long long token0, int qh,
+                                          int n, uint4 (&raw)[PASS][NP], int tid) {
+  constexpr int PER = DK / 8;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
+  for (int i = 0; i < PASS; ++i) {
+    const int e = tid + i * kPrepThreads, r = e / PER, c = (e % PER) * 8;
+#pragma unroll
+    for (int h = 0; h < NP; ++h) raw[i][h] = make_uint4(0, 0, 0, 0);
+    if (r < n) {
+      const long long at = (token0 + r) * stride + (long long)qh * DK + c;
+      if (NP == 2) {
+        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + at);
+#pragma unroll
+        for (int h = 0; h < NP; ++h) raw[i][h] = __ldg(s + h);
+      } else if (p.qk16) {
+        raw[i][0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at));
+      } else {
+        const uint2 *s = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(src) + at);
+        const uint2 a = __ldg(s), b = __ldg(s + 1);
+        raw[i][0] = make_uint4(a.x, a.y, b.x, b.y);
+      }
     }
   }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
-  m = max(max(red[0], red[1]), max(red[2], red[3]));
-  float inv;
-  const float scale = scale_of(m, 0, inv);
-  for (int i = tid; i < kChunk * PER; i += kPrepThreads) {
-    const int r = i / PER, c = (i % PER) * 8;
-    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (r < n) load8(src, p.dtype, (token0 + r) * stride + (long long)qh * DK + c, p.qk16, x);
+}
+template <int NP>
+__device__ __forceinline__ void unpack_row(const uint4 (&raw)[NP], int dtype, float (&x)[8]) {
+  const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                         raw[NP - 1].x, raw[NP - 1].y, raw[NP - 1].z, raw[NP - 1].w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (NP == 2) {
+      x[e] = __uint_as_float(u[e]);
+    } else if (!(e & 1)) {
+      const float2 f = pair_of(u[e >> 1], dtype);
+      x[e] = f.x;
+      x[e + 1] = f.y;
+    }
+  }
+}
+template <int NP, int PASS>
+__device__ __forceinline__ unsigned max_rows(const uint4 (&raw)[PASS][NP], int dtype) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < PASS; ++i) {
+    float x[8];
+    unpack_row<NP>(raw[i], dtype, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
+  }
+  return __reduce_max_sync(0xFFFFFFFFu, m);
+}
+// The rows over their scale as planes, in shared memory and, where `out` is given, in the workspace.
+template <int DK, int NP, int PASS>
+__device__ __forceinline__ void put_rows(const uint4 (&raw)[PASS][NP], int dtype, float inv, __half *dst, __half *out, int tid) {
+  constexpr int PER = DK / 8;
+#pragma unroll
+  for (int i = 0; i < PASS; ++i) {
+    const int e = tid + i * kPrepThreads, r = e / PER, c = (e % PER) * 8;
+    if (r >= kChunk) continue;
+    float x[8];
+    unpack_row<NP>(raw[i], dtype, x);
     uint4 hi, lo;
     split2(x[0] * inv, x[1] * inv, hi.x, lo.x);
     split2(x[2] * inv, x[3] * inv, hi.y, lo.y);
     split2(x[4] * inv, x[5] * inv, hi.z, lo.z);
     split2(x[6] * inv, x[7] * inv, hi.w, lo.w);
-    *reinterpret_cast<uint4 *>(dst + r * LD + c) = hi;
-    if (NP == 2) *reinterpret_cast<uint4 *>(dst + kChunk * LD + r * LD + c) = lo;
+    const int at = tiled<DK>(r, c);
+    *reinterpret_cast<uint4 *>(dst + at) = hi;
+    if (NP == 2) *reinterpret_cast<uint4 *>(dst + kChunk * DK + at) = lo;
     if (out) {
-      *reinterpret_cast<uint4 *>(out + r * DK + c) = hi;
-      if (NP == 2) *reinterpret_cast<uint4 *>(out + kChunk * DK + r * DK + c) = lo;
+      *reinterpret_cast<uint4 *>(out + at) = hi;
+      if (NP == 2) *reinterpret_cast<uint4 *>(out + kChunk * DK + at) = lo;
     }
   }
-  return scale;
 }
 
-// Accumulators of 16 rows [m0 ..] x COLS as planes of a record with row length COLS.
-template <int TILES>
-__device__ __forceinline__ void store_planes(__half *dst, long long plane, int cols, int m0, const float (&c)[TILES][4],
-                                             int tiles, int lane) {
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-#pragma unroll
-  for (int i = 0; i < TILES; ++i)
-    if (i < tiles)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t hi, lo;
-        split2(c[i][2 * h], c[i][2 * h + 1], hi, lo);
-        const long long at = (long long)(m0 + g + 8 * h) * cols + 8 * i + t2;
-        *reinterpret_cast<uint32_t *>(dst + at) = hi;
-        *reinterpret_cast<uint32_t *>(dst + plane + at) = lo;
-      }
+// One accumulator register pair (rows r0 + lane/4, columns c0 + 2 (lane % 4), +1 of an 8x8 tile) into a
+// tiled plane and its rest into the plane behind it.
+template <int COLS>
+__device__ __forceinline__ void put_pair(__half *dst, long long plane, int r0, int c0, float x, float y, int lane) {
+  uint32_t hi, lo;
+  split2(x, y, hi, lo);
+  const int at = tiled<COLS>(r0, c0) + 2 * lane;
+  *reinterpret_cast<uint32_t *>(dst + at) = hi;
+  *reinterpret_cast<uint32_t *>(dst + plane + at) = lo;
 }
 
 template <int DK, int NP, bool DELTA, bool BWD>
-__global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) scan_prep_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8;
+__global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kernel(const ScanParams p) {
   constexpr PrepLayout l = prep_layout(DK, NP);
+  constexpr int PASS = (kChunk * DK / 8 + kPrepThreads - 1) / kPrepThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   __half *K = reinterpret_cast<__half *>(smem + l.k), *Q = reinterpret_cast<__half *>(smem + l.q);
-  __half *A16 = Q;                                                  // [2][48][kLdC]: rows 16..63 of A
+  __half *A16 = Q;                                                  // [2][64][64]
   float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then Tm
-  __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][kLdX]: X_ii
+  __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][16]: X_ii
   double *G = reinterpret_cast<double *>(smem + l.f);
-  float *eG = reinterpret_cast<float *>(G + kChunk), *w = eG + kChunk, *be = w + kChunk;
-  unsigned *red = reinterpret_cast<unsigned *>(be + 2 * kChunk);
+  float *ek = reinterpret_cast<float *>(G + kChunk), *wk = ek + kChunk, *be = wk + kChunk;
+  unsigned *red = reinterpret_cast<unsigned *>(be + kChunk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head = blockIdx.y;
   if (slot == 0 && head == 0) check_offsets(p);
@@ -467,49 +517,90 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
   const int qh = head / p.share, hq = p.H / p.share;
   const long long rec = (long long)slot * p.H + head, qrec = (long long)slot * hq + qh;
   const bool mine = head % p.share == 0;           // the first of the heads that share K and Q keeps them
-  float *gates = p.gates + rec * kGateFloats;
-  if (warp == 0) {
-    // Sums of log_alpha in 64 bits, so that the differences below keep their digits behind a
-    // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
-    // held there and G stays finite.
-    double a[2], run;
-    float b[2];
+  // log_alpha and beta of tokens 2 lane, 2 lane + 1, in flight beside the rows
+  float la[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
+  if (warp == 3)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const long long at = (token0 + t) * p.H + head;
-      float la = t < n ? __ldg(p.log_alpha + at) : 0.0f;
-      if (la < -1000.0f) la = -1000.0f;
-      a[i] = la;
-      b[i] = t < n ? __ldg(p.beta + at) : 0.0f;
+      if (t < n) {
+        la[i] = __ldg(p.log_alpha + at);
+        b[i] = __ldg(p.beta + at);
+      }
     }
-    run = a[0] + a[1];
+  float sk, sq;
+  {
+    __half *ko = mine ? p.khat + qrec * (NP * kChunk * DK) : nullptr, *qo = mine ? p.qhat + qrec * (NP * kChunk * DK) : nullptr;
+    uint4 xk[PASS][NP];
+    float inv;
+    load_rows<DK, NP, PASS>(p, p.k, p.k_stride, token0, qh, n, xk, tid);
+    if (NP == 1) {
+      uint4 xq[PASS][NP];
+      load_rows<DK, NP, PASS>(p, p.q, p.q_stride, token0, qh, n, xq, tid);
+      const unsigned mk = max_rows<NP, PASS>(xk, p.dtype), mq = max_rows<NP, PASS>(xq, p.dtype);
+      if (lane == 0) {
+        red[warp] = mk;
+        red[4 + warp] = mq;
+      }
+      __syncthreads();
+      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), 0, inv);
+      put_rows<DK, NP, PASS>(xk, p.dtype, inv, K, ko, tid);
+      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), 0, inv);
+      put_rows<DK, NP, PASS>(xq, p.dtype, inv, Q, qo, tid);
+    } else {
+      const unsigned mk = max_rows<NP, PASS>(xk, p.dtype);
+      if (lane == 0) red[warp] = mk;
+      __syncthreads();
+      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), 0, inv);
+      put_rows<DK, NP, PASS>(xk, p.dtype, inv, K, ko, tid);
+      load_rows<DK, NP, PASS>(p, p.q, p.q_stride, token0, qh, n, xk, tid);
+      const unsigned mq = max_rows<NP, PASS>(xk, p.dtype);
+      if (lane == 0) red[4 + warp] = mq;
+      __syncthreads();
+      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), 0, inv);
+      put_rows<DK, NP, PASS>(xk, p.dtype, inv, Q, qo, tid);
+    }
+  }
+  if (warp == 3) {
+    // Sums of log_alpha in 64 bits, so that the differences below keep their digits behind a
+    // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
+    // held there and G stays finite.
+    float *gates = p.gates + rec * kGateFloats;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (la[i] < -1000.0f) la[i] = -1000.0f;
+    double run = (double)la[0] + (double)la[1];
     for (int d = 1; d < 32; d <<= 1) {
       const double up = __shfl_up_sync(0xFFFFFFFFu, run, d);
       if (lane >= d) run += up;
     }
     const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
-    const double Gt[2] = {run - a[1], run};
+    const double Gt[2] = {run - (double)la[1], run};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i]));
+      const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i])), w = b[i] * c;
       G[t] = Gt[i];
-      eG[t] = e; be[t] = b[i]; w[t] = b[i] * c;
-      gates[t] = e; gates[kChunk + t] = b[i] * c; gates[2 * kChunk + t] = b[i]; gates[3 * kChunk + t] = c;
-      reinterpret_cast<double *>(gates + 4 * kChunk)[t] = Gt[i];
+      ek[t] = e * sk; be[t] = b[i]; wk[t] = w * sk;
+      gates[kGateE * kChunk + t] = e;
+      gates[kGateWk * kChunk + t] = w * sk;
+      gates[kGateEk * kChunk + t] = e * sk;
+      gates[kGateW * kChunk + t] = w;
+      gates[kGateB * kChunk + t] = b[i];
+      gates[kGateC * kChunk + t] = c;
+      reinterpret_cast<double *>(gates + kGateG * kChunk)[t] = Gt[i];
     }
-  }
-  const float sk = stage_rows<DK, NP>(p, p.k, p.k_stride, token0, qh, n, K,
-                                      mine ? p.khat + qrec * (NP * kChunk * DK) : nullptr, red, tid);
-  const float sq = stage_rows<DK, NP>(p, p.q, p.q_stride, token0, qh, n, Q,
-                                      mine ? p.qhat + qrec * (NP * kChunk * DK) : nullptr, red + 4, tid);
-  if (tid == 0) {
-    gates[kGateScales] = sk;
-    gates[kGateScales + 1] = sq;
+    if (lane == 0) {
+      gates[kGateScales] = sk;
+      gates[kGateScales + 1] = sq;
+    }
   }
   __syncthreads();
 
+  const Lane<DK> ld(lane);
+  const uint32_t sK = smem_addr(K), sQ = smem_addr(Q);
+  constexpr uint32_t LO = kChunk * DK * 2;         // bytes from a plane to the next
   const int m0 = warp * 16;
   float P[8][4];
 #pragma unroll
@@ -527,28 +618,28 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
       uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
       for (int c = 0; c < NP; ++c) {
-        if (DELTA) a_rows(ak[c], K + c * kChunk * LD, LD, m0, ks * 16, lane);
-        a_rows(aq[c], Q + c * kChunk * LD, LD, m0, ks * 16, lane);
+        if (DELTA) ld.a_rows(ak[c], sK + c * LO, m0, ks * 16);
+        ld.a_rows(aq[c], sQ + c * LO, m0, ks * 16);
       }
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         if (np <= warp) {
-          uint32_t b[4];
-          b_rows(b, K, LD, np * 16, ks * 16, lane);
+          uint32_t r[4];
+          ld.b_rows(r, sK, np * 16, ks * 16);
 #pragma unroll
           for (int c = 0; c < NP; ++c) {
-            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], b);
-            mma2(P[2 * np], P[2 * np + 1], aq[c], b);
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], r);
+            mma2(P[2 * np], P[2 * np + 1], aq[c], r);
           }
           if (NP == 2) {
-            b_rows(b, K + kChunk * LD, LD, np * 16, ks * 16, lane);
-            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], b);
-            mma2(P[2 * np], P[2 * np + 1], aq[0], b);
+            ld.b_rows(r, sK + LO, np * 16, ks * 16);
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], r);
+            mma2(P[2 * np], P[2 * np + 1], aq[0], r);
           }
         }
       }
     }
-    __syncthreads();                   // Q's tile becomes A's planes
+    if (DELTA) __syncthreads();        // Q's tile becomes A's planes
     // P (over the scale of Q) and, strictly below the diagonal, A
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -567,10 +658,7 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
               X[t * kLdF + s] = A[i][2 * h];
               X[t * kLdF + s + 1] = A[i][2 * h + 1];
             } else {
-              uint32_t hi, lo;
-              split2(A[i][2 * h], A[i][2 * h + 1], hi, lo);
-              *reinterpret_cast<uint32_t *>(A16 + (t - 16) * kLdC + s) = hi;
-              *reinterpret_cast<uint32_t *>(A16 + 48 * kLdC + (t - 16) * kLdC + s) = lo;
+              put_pair<kChunk>(A16, kChunk * kChunk, m0 + 8 * h, 8 * i, A[i][2 * h], A[i][2 * h + 1], lane);
             }
           }
         }
@@ -578,16 +666,17 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
     }
   }
   if (!BWD || !DELTA) {
-    // 16-bit outputs need one plane of P
     __half *pp = p.pp + rec * (2 * kChunk * kChunk);
-    if (NP == 2 || BWD) store_planes<8>(pp, kChunk * kChunk, kChunk, m0, P, 2 * warp + 2, lane);
-    else
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i / 2 <= warp)
+    for (int i = 0; i < 8; ++i)
+      if (i / 2 <= warp)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<uint32_t *>(pp + (m0 + g + 8 * h) * kChunk + 8 * i + t2) = pack2(P[i][2 * h], P[i][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) {
+          if (NP == 2 || BWD)
+            put_pair<kChunk>(pp, kChunk * kChunk, m0 + 8 * h, 8 * i, P[i][2 * h], P[i][2 * h + 1], lane);
+          else             // (16-bit outputs need one plane)
+            *reinterpret_cast<uint32_t *>(pp + tiled<kChunk>(m0 + 8 * h, 8 * i) + 2 * lane) = pack2(P[i][2 * h], P[i][2 * h + 1]);
+        }
   }
   if (!DELTA) return;
   __syncwarp();
@@ -604,26 +693,25 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
       for (int i = r + 1; i < 16; ++i) x[i] = fmaf(-B[i * kLdF + r], x[r], x[i]);
     __syncwarp();
     if (lane < 16) {
-      __half *d = XD + warp * (2 * 16 * kLdX);
+      __half *d = XD + warp * 512;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         B[r * kLdF + c] = x[r];
         const __half hi = __float2half_rn(x[r]);
-        d[r * kLdX + c] = hi;
-        d[16 * kLdX + r * kLdX + c] = __float2half_rn(x[r] - __half2float(hi));
+        d[tiled<16>(r, c)] = hi;
+        d[256 + tiled<16>(r, c)] = __float2half_rn(x[r] - __half2float(hi));
       }
     }
   }
   __syncthreads();
   {
     // block column `warp`: yh, yl[k] = planes of X_kj^T
+    const Lane<16> l16(lane);
+    const Lane<kChunk> l64(lane);
+    const uint32_t sA = smem_addr(A16), sD = smem_addr(XD);
     uint32_t yh[4][4], yl[4][4];
-    {
-      // X_jj^T as a left operand: element (m, k) = X_jj[k][m], read transposed
-      const __half *d = XD + warp * (2 * 16 * kLdX);
-      a_cols(yh[0], d, kLdX, 0, 0, lane);
-      a_cols(yl[0], d + 16 * kLdX, kLdX, 0, 0, lane);
-    }
+    l16.a_cols(yh[0], sD + warp * 1024, 0, 0);     // X_jj^T: element (m, k) = X_jj[k][m]
+    l16.a_cols(yl[0], sD + warp * 1024 + 512, 0, 0);
 #pragma unroll
     for (int di = 1; di < 4; ++di) {
       const int i = warp + di;
@@ -631,28 +719,27 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
         float z0[4] = {0, 0, 0, 0}, z1[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int dk = 0; dk < di; ++dk) {
-          uint32_t b[4];
-          b_rows(b, A16, kLdC, 16 * i - 16, 16 * (warp + dk), lane);
-          mma2(z0, z1, yh[dk], b);
-          mma2(z0, z1, yl[dk], b);
-          b_rows(b, A16 + 48 * kLdC, kLdC, 16 * i - 16, 16 * (warp + dk), lane);
-          mma2(z0, z1, yh[dk], b);
+          uint32_t r[4];
+          l64.b_rows(r, sA, 16 * i, 16 * (warp + dk));
+          mma2(z0, z1, yh[dk], r);
+          mma2(z0, z1, yl[dk], r);
+          l64.b_rows(r, sA + 2 * kChunk * kChunk, 16 * i, 16 * (warp + dk));
+          mma2(z0, z1, yh[dk], r);
         }
-        uint32_t zh[4], zl[4], b[4];
+        uint32_t zh[4], zl[4], r[4];
         split_tiles(z0, z1, -1.0f, zh, zl);
         float y0[4] = {0, 0, 0, 0}, y1[4] = {0, 0, 0, 0};
-        const __half *d = XD + i * (2 * 16 * kLdX);
-        b_rows(b, d, kLdX, 0, 0, lane);
-        mma2(y0, y1, zh, b);
-        mma2(y0, y1, zl, b);
-        b_rows(b, d + 16 * kLdX, kLdX, 0, 0, lane);
-        mma2(y0, y1, zh, b);
-        split_tiles(y0, y1, yh[di & 3], yl[di & 3]);
+        l16.b_rows(r, sD + i * 1024, 0, 0);
+        mma2(y0, y1, zh, r);
+        mma2(y0, y1, zl, r);
+        l16.b_rows(r, sD + i * 1024 + 512, 0, 0);
+        mma2(y0, y1, zh, r);
+        split_tiles(y0, y1, yh[di], yl[di]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // y[c][r] -> X[16 i + r][16 warp + c]
-          const int c = g + 8 * (j >> 1), r = t2 + (j & 1);
-          X[(16 * i + r) * kLdF + m0 + c] = y0[j];
-          X[(16 * i + 8 + r) * kLdF + m0 + c] = y1[j];
+          const int c = g + 8 * (j >> 1), r2 = t2 + (j & 1);
+          X[(16 * i + r2) * kLdF + m0 + c] = y0[j];
+          X[(16 * i + 8 + r2) * kLdF + m0 + c] = y1[j];
         }
       }
     }
@@ -670,77 +757,56 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
       split2(x[2], x[3], hi.y, lo.y);
       split2(x[4], x[5], hi.z, lo.z);
       split2(x[6], x[7], hi.w, lo.w);
-      *reinterpret_cast<uint4 *>(tm + r * kChunk + c) = hi;
-      *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + r * kChunk + c) = lo;
+      const int at = tiled<kChunk>(r, c);
+      *reinterpret_cast<uint4 *>(tm + at) = hi;
+      *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + at) = lo;
     }
   }
-  // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own.  Two halves of the columns, so
-  // that the accumulators leave room for four CTAs per SM.
+  // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own; then Kb = Tm^T diag(w) K: rows s
+  // of this warp, t blocks from its own on.  Two halves of the columns, so that the
+  // accumulators leave room for four CTAs per SM.
   constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
+#pragma unroll
+  for (int which = 0; which < (BWD ? 2 : 1); ++which) {
+    __half *dst = (which ? p.kb : p.kt) + rec * (2 * kChunk * DK);
 #pragma unroll 1
-  for (int half = 0; half < HALVES; ++half) {
-    float acc[HT][4];
+    for (int half = 0; half < HALVES; ++half) {
+      float acc[HT][4];
 #pragma unroll
-    for (int i = 0; i < HT; ++i)
+      for (int i = 0; i < HT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks <= warp) {
-        uint32_t ah[4], al[4], b[4];
+      for (int ks = 0; ks < 4; ++ks) {
+        if (which ? ks >= warp : ks <= warp) {
+          uint32_t ah[4], al[4], r[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int t = m0 + g + 8 * (q & 1), s = ks * 16 + t2 + 8 * (q >> 1);
-          split2(-X[t * kLdF + s] * eG[s] * sk, -X[t * kLdF + s + 1] * eG[s + 1] * sk, ah[q], al[q]);
-        }
+          for (int q = 0; q < 4; ++q) {
+            const int m = m0 + g + 8 * (q & 1), k = ks * 16 + t2 + 8 * (q >> 1);
+            if (which) split2(X[k * kLdF + m] * wk[k], X[(k + 1) * kLdF + m] * wk[k + 1], ah[q], al[q]);
+            else split2(-X[m * kLdF + k] * ek[k], -X[m * kLdF + k + 1] * ek[k + 1], ah[q], al[q]);
+          }
 #pragma unroll
-        for (int np = 0; np < HT / 2; ++np) {
-          const int c0 = half * (DK / HALVES) + np * 16;
-          b_cols(b, K, LD, ks * 16, c0, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], ah, b);
-          mma2(acc[2 * np], acc[2 * np + 1], al, b);
-          if (NP == 2) {
-            b_cols(b, K + kChunk * LD, LD, ks * 16, c0, lane);
-            mma2(acc[2 * np], acc[2 * np + 1], ah, b);
+          for (int np = 0; np < HT / 2; ++np) {
+            const int c0 = half * (DK / HALVES) + np * 16;
+            ld.b_cols(r, sK, ks * 16, c0);
+            mma2(acc[2 * np], acc[2 * np + 1], ah, r);
+            mma2(acc[2 * np], acc[2 * np + 1], al, r);
+            if (NP == 2) {
+              ld.b_cols(r, sK + LO, ks * 16, c0);
+              mma2(acc[2 * np], acc[2 * np + 1], ah, r);
+            }
           }
         }
       }
+#pragma unroll
+      for (int i = 0; i < HT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          put_pair<DK>(dst, kChunk * DK, m0 + 8 * h, half * (DK / HALVES) + 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
     }
-    store_planes<HT>(p.kt + rec * (2 * kChunk * DK) + half * (DK / HALVES), kChunk * DK, DK, m0, acc, HT, lane);
   }
   if (!BWD) return;
-  // Kb = Tm^T diag(w) K: rows s of this warp, t blocks from its own on
-#pragma unroll 1
-  for (int half = 0; half < HALVES; ++half) {
-    float acc[HT][4];
-#pragma unroll
-    for (int i = 0; i < HT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks >= warp) {
-        uint32_t ah[4], al[4], b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int s = m0 + g + 8 * (q & 1), t = ks * 16 + t2 + 8 * (q >> 1);
-          split2(X[t * kLdF + s] * w[t] * sk, X[(t + 1) * kLdF + s] * w[t + 1] * sk, ah[q], al[q]);
-        }
-#pragma unroll
-        for (int np = 0; np < HT / 2; ++np) {
-          const int c0 = half * (DK / HALVES) + np * 16;
-          b_cols(b, K, LD, ks * 16, c0, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], ah, b);
-          mma2(acc[2 * np], acc[2 * np + 1], al, b);
-          if (NP == 2) {
-            b_cols(b, K + kChunk * LD, LD, ks * 16, c0, lane);
-            mma2(acc[2 * np], acc[2 * np + 1], ah, b);
-          }
-        }
-      }
-    }
-    store_planes<HT>(p.kb + rec * (2 * kChunk * DK) + half * (DK / HALVES), kChunk * DK, DK, m0, acc, HT, lane);
-  }
   // Z = P Tm (over the scale of Q): rows t of this warp; block (r, s) of Tm is zero for s > r
   {
     float acc[8][4];
@@ -765,49 +831,68 @@ __global__ void __launch_bounds__(kPrepThreads, DK <= 128 && NP == 1 ? 4 : 2) sc
         }
       }
     }
-    store_planes<8>(p.z + rec * (2 * kChunk * kChunk), kChunk * kChunk, kChunk, m0, acc, 2 * warp + 2, lane);
+    __half *z = p.z + rec * (2 * kChunk * kChunk);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i / 2 <= warp)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
   }
 }
 
 // -------------------------------------------------------------------------------------
-// scan_chain
+// the walks: scan_chain and scan_reverse
 // -------------------------------------------------------------------------------------
-// Grid (sequence * H + head, group of p.rb blocks of 16 value rows).  NH warps share a block: warp h
-// holds the state's columns [h d_k/NH, (h+1) d_k/NH) and forms, over its columns, a part of S0 Kt^T
-// and S0 Q^T for all 64 tokens; the parts are added through shared memory, one barrier of the
-// NH warps per chunk; then each warp finishes O for its own 64/NH tokens and S for its own
-// columns.  (NH = 2 halves the chain from chunk to chunk where there are few blocks.)  Two more
-// warps fetch the next chunk's tiles meanwhile (two stages where they fit).
-// SAVE: the backward pass's recomputation, which keeps the planes of S0 and E of every chunk;
-// otherwise o and the last state are written.
-constexpr int kLoadWarps = 2;
-constexpr int kWalkWarps = 4;          // compute warps of a CTA, at most
+// Grid (sequence * H + head, group of p.rb blocks of 16 value rows).  Per block:
+//   NH state warps: warp h holds the state's columns [h d_k/NH, (h+1) d_k/NH) in its accumulators and
+//     forms, over its columns, a part of S0 Kt^T for all 64 tokens; the parts are added
+//     through shared memory (barrier X), E follows, then S for the own columns.  The state of
+//     chunk c + 1 waits for this alone, and NH = 2 halves it.
+//   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
+//     (barrier Y, which the state warps only arrive at) P E and the output rows.
+// Two more warps fetch the next chunk's tiles meanwhile (two stages where they fit).  In the
+// backward pass's recomputation (SAVE) the planes of S0 and E are kept instead of o.
+// scan_reverse has the same roles: D for S, R for E, dO^T Z for Tm V, and the side warps also
+// form D's sum over dO^T Q before X.
+constexpr int kSideWarps = 2, kLoadWarps = 2;
+constexpr int kMaxBlocks = 2;          // blocks of value rows per CTA
+constexpr int kWalkThreads = 32 * (kMaxBlocks * (2 + kSideWarps) + kLoadWarps);
 
-struct WalkLayout {                    // byte offsets inside one stage; `part` after the stages
-  int kt, k, q, tm, pp, v, gates, bytes, part;
+enum WalkKind { kForward, kRecompute, kReverse };
+
+struct WalkLayout {
+  int kt, k, q, tm, pp, v, gates, bytes;         // byte offsets inside one stage
+  int part, side, plus, last, planes, tops, tail;   // behind the stages, one record per block of rows
 };
-// elements of a token row of the V (or dO) tile
-__host__ __device__ constexpr int tile_ld(int np, int rb) { return 16 * rb + (np == 2 ? 4 : 8); }
+// elements of a token row of the V (or dO) tile (16-bit rows unpadded: two stages just fit, and the
+// tile is read four times a chunk)
+__host__ __device__ constexpr int tile_ld(int np, int rb) { return 16 * rb + (np == 2 ? 4 : 0); }
 
-// what = 0: forward, 1: recomputation, 2: reverse
-__host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh, bool delta, int what) {
-  const int tile = kChunk * (dk + 8) * 2, sq = kChunk * kLdC * 2;
+__host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh, bool delta, int kind) {
+  const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
   WalkLayout l{};
   int at = 0;
   l.kt = at; at += delta ? 2 * tile : 0;                       // Kt or Kb
   l.k = at; at += np * tile;
-  l.q = at; at += what != 1 ? np * tile : 0;
-  l.tm = at; at += what == 2 || delta ? 2 * sq : 0;            // Tm or Z
-  l.pp = at; at += what == 0 ? np * sq : 0;
+  l.q = at; at += kind != kRecompute ? np * tile : 0;
+  l.tm = at; at += kind == kReverse || delta ? 2 * sq : 0;     // Tm or Z
+  l.pp = at; at += kind == kForward ? np * sq : 0;
   l.v = at; at += kChunk * tile_ld(np, rb) * (np == 2 ? 4 : 2);
-  l.gates = at; at += 2 * kChunk * 4 + 16;
+  l.gates = at; at += 3 * kChunk * 4 + 16;
   l.bytes = (at + 15) / 16 * 16;
-  // parts of E (32 floats a lane) and, forward, of O for the others' tokens; maxima
-  l.part = nh == 1 ? 0 : rb * nh * 32 * (32 + (what == 0 ? 32 - 32 / nh : 0)) * 4;
+  at = 0;
+  l.part = at; at += nh > 1 ? nh * 4096 : 0;                   // the state warps' parts of E or R
+  l.side = at; at += 4096;                                     // Tm V or dO^T Z
+  l.last = at; at += 4096;                                     // E or R, for the side warps
+  l.plus = at; at += kind == kReverse ? 16 * dk * 4 : 0;       // dO^T Q
+  l.planes = at; at += kind == kForward ? np * 16 * dk * 2 : 0;   // S0 as left operands
+  l.tops = at; at += 32;                                       // largest entries: state parts, V halves
+  l.tail = at;
   return l;
 }
 
-// The state rows a thread holds: rows r0 and r0 + 8, columns c0 + 8 i + t2, +1.
+// The state rows a thread holds: rows r0 and r0 + 8, columns c0 + 8 i, +1.
 template <int NTH>
 __device__ __forceinline__ void load_state(float (&S)[NTH][4], const float *src, long long tile, int d_v, int dk, int r0,
                                            int c0) {
@@ -833,14 +918,14 @@ __device__ __forceinline__ void save_state(const float (&S)[NTH][4], float *dst,
         *reinterpret_cast<float2 *>(dst + (tile * d_v + r0 + 8 * h) * dk + c0 + 8 * i) =
             make_float2(S[i][2 * h], S[i][2 * h + 1]);
 }
-template <int NTH>
-__device__ __forceinline__ unsigned max_bits(const float (&S)[NTH][4]) {
+template <int N, int M>
+__device__ __forceinline__ unsigned max_bits(const float (&x)[N][M]) {
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < NTH; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, abs_bits(S[i][j]));
-  return m;
+    for (int j = 0; j < M; ++j) m = max(m, abs_bits(x[i][j]));
+  return __reduce_max_sync(0xFFFFFFFFu, m);
 }
 
 // The tile of V (or dO) as left operands V^T: x[ks][2 q], x[ks][2 q + 1] are the two entries of
@@ -853,7 +938,7 @@ __device__ __forceinline__ void load_tokens(float (&x)[4][8], const uint8_t *til
   for (int ks = 0; ks < 4; ++ks) {
     if (NP == 1) {
       uint32_t a[4];
-      a_cols(a, reinterpret_cast<const __half *>(tile), ld, ks * 16, col0, lane);
+      a_cols_plain(a, smem_addr(tile), ld, ks * 16, col0, lane);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 f = pair_of(a[q], dtype);
@@ -871,30 +956,30 @@ __device__ __forceinline__ void load_tokens(float (&x)[4][8], const uint8_t *til
   }
 }
 
-// Writes OT tiles (tokens 8 (tile0 + i) .., 16 value rows) times `by` to token rows of the
+// Writes 4 tiles (tokens 8 (tile0 + i) .., 16 value rows) times `by` to token rows of the
 // caller's tensor, through the warp's part of the V tile so that rows leave in 16-byte
 // pieces.
-template <int NP, int OT>
-__device__ __forceinline__ void store_tokens(const float (&O)[OT][4], float by, uint8_t *tile, int ld, int col0, int tile0,
+template <int NP>
+__device__ __forceinline__ void store_tokens(const float (&O)[4][4], float by, uint8_t *tile, int ld, int col0, int tile0,
                                              void *dst, int dtype, long long stride, long long token0, int n, int col,
                                              int have, bool by16, int lane) {
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   if (NP == 1) {
     uint16_t *sm = reinterpret_cast<uint16_t *>(tile);
 #pragma unroll
-    for (int i = 0; i < OT / 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
       uint32_t r[4];
       r[0] = pack_as(dtype, O[2 * i][0] * by, O[2 * i][1] * by);
       r[1] = pack_as(dtype, O[2 * i][2] * by, O[2 * i][3] * by);
       r[2] = pack_as(dtype, O[2 * i + 1][0] * by, O[2 * i + 1][1] * by);
       r[3] = pack_as(dtype, O[2 * i + 1][2] * by, O[2 * i + 1][3] * by);
       const int tok = 8 * (tile0 + 2 * i + (lane >> 4)) + (lane & 7);
-      stsm4t(sm + tok * ld + col0 + 8 * ((lane >> 3) & 1), r);
+      stsm4t(smem_addr(sm + tok * ld + col0 + 8 * ((lane >> 3) & 1)), r);
     }
     __syncwarp();
     uint16_t *out = static_cast<uint16_t *>(dst);
 #pragma unroll
-    for (int i = 0; i < OT / 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 1), c = (e & 1) * 8;
       const uint4 x = *reinterpret_cast<const uint4 *>(sm + tok * ld + col0 + c);
       if (tok < n) {
@@ -910,14 +995,14 @@ __device__ __forceinline__ void store_tokens(const float (&O)[OT][4], float by, 
   } else {
     float *sm = reinterpret_cast<float *>(tile);
 #pragma unroll
-    for (int i = 0; i < OT; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         sm[(8 * (tile0 + i) + t2 + (j & 1)) * ld + col0 + g + 8 * (j >> 1)] = O[i][j] * by;
     __syncwarp();
     float *out = static_cast<float *>(dst);
 #pragma unroll
-    for (int i = 0; i < OT; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 2), c = (e & 3) * 4;
       const float4 x = *reinterpret_cast<const float4 *>(sm + tok * ld + col0 + c);
       if (tok < n && c < have) *reinterpret_cast<float4 *>(out + (token0 + tok) * stride + col + c) = x;
@@ -925,593 +1010,445 @@ __device__ __forceinline__ void store_tokens(const float (&O)[OT][4], float by, 
   }
 }
 
-__device__ __forceinline__ void block_barrier(int block, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + block), "r"(threads) : "memory");
+__device__ __forceinline__ void barrier_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float4 f4(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+// Tiles of 16 value rows x 64 tokens as planes in the workspace.
+__device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row0, int tile0, const float (&x)[4][4],
+                                           float by, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      put_pair<kChunk>(dst, plane, row0 + 8 * h, 8 * (tile0 + i), x[i][2 * h] * by, x[i][2 * h + 1] * by, lane);
 }
 
-template <int DK, int NP, bool DELTA, bool SAVE>
-__device__ __forceinline__ void chain_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0, int n,
-                                            int slot, int head, int row0, int tid, int threads) {
-  constexpr int LD = DK + 8, SIZE = NP == 2 ? 4 : 2;
+// A chunk's tiles.  KIND as above; `tokens` is V or dO.
+template <int DK, int NP, bool DELTA, int KIND>
+__device__ __forceinline__ void walk_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0, int n,
+                                           int slot, int head, int row0, int tid) {
+  constexpr int SIZE = NP == 2 ? 4 : 2, threads = 32 * kLoadWarps;
+  constexpr int TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
   const long long rec = (long long)slot * p.H + head;
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (DELTA) {
-      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.kt) + c * kChunk * LD,
-                                 p.kt + (rec * 2 + c) * (kChunk * DK), tid, threads);
-      copy_lower(reinterpret_cast<__half *>(st + l.tm) + c * kChunk * kLdC, p.tm + (rec * 2 + c) * (kChunk * kChunk),
-                 tid, threads);
-    }
-#pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.k) + c * kChunk * LD,
-                               p.khat + (qrec * NP + c) * (kChunk * DK), tid, threads);
-    if (!SAVE) {
-      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.q) + c * kChunk * LD,
-                                 p.qhat + (qrec * NP + c) * (kChunk * DK), tid, threads);
-      copy_lower(reinterpret_cast<__half *>(st + l.pp) + c * kChunk * kLdC, p.pp + (rec * 2 + c) * (kChunk * kChunk),
-                 tid, threads);
-    }
-  }
+  const void *tokens = KIND == kReverse ? p.o : p.v;
+  const long long stride = KIND == kReverse ? p.o_stride : p.v_stride;
   copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
-                    static_cast<const uint8_t *>(p.v) + (token0 * p.v_stride + (long long)head * p.d_v + row0) * SIZE,
-                    p.v_stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, p.v16, tid, threads);
+                    static_cast<const uint8_t *>(tokens) + (token0 * stride + (long long)head * p.d_v + row0) * SIZE,
+                    stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, KIND == kReverse ? p.o16 : p.v16, tid, threads);
   const float *gates = p.gates + rec * kGateFloats;
-  for (int i = tid; i < 2 * kChunk / 4 + 1; i += threads)
-    cp16(st + l.gates + 16 * i, i < 2 * kChunk / 4 ? gates + 4 * i : gates + kGateScales, true);
+  if (tid < 3 * kChunk / 4 + 1)
+    cp16(st + l.gates + 16 * tid, tid < 3 * kChunk / 4 ? gates + 4 * tid : gates + kGateScales, true);
+  if (DELTA) copy_flat<2 * TILE>(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), tid, threads);
+  if (DELTA || KIND == kReverse) {
+    const __half *m = (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk);
+    copy_lower(st + l.tm, m, tid, threads);
+    copy_lower(st + l.tm + SQ, m + kChunk * kChunk, tid, threads);
+  }
+  copy_flat<NP * TILE>(st + l.k, p.khat + qrec * (NP * kChunk * DK), tid, threads);
+  if (KIND != kRecompute) copy_flat<NP * TILE>(st + l.q, p.qhat + qrec * (NP * kChunk * DK), tid, threads);
+  if (KIND == kForward)
+#pragma unroll
+    for (int c = 0; c < NP; ++c)
+      copy_lower(st + l.pp + c * SQ, p.pp + (rec * 2 + c) * (kChunk * kChunk), tid, threads);
+  cp_commit();
 }
 
-template <int DK, int NP, bool DELTA, bool SAVE, int NH>
-__global__ void __launch_bounds__(32 * (kWalkWarps + kLoadWarps), 1) scan_chain_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, DKH = DK / NH, NTH = DKH / 8, OT = 8 / NH;
-  static_assert(NH == 1 || NH == 2, "E without the delta rule is laid out for these");
+template <int DK, int NP, bool DELTA, int KIND, int NH>
+__global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanParams p) {
+  constexpr bool REV = KIND == kReverse;
+  constexpr int DKH = DK / NH, NTH = DKH / 8;
+  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
+  constexpr int PER = 32 * (NH + kSideWarps);                // threads of a block of rows
+  static_assert(NH == 1 || NH == 2, "parts are exchanged between two warps at most");
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int blk = warp / NH, h = NH == 1 ? 0 : warp % NH;
   const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * p.rb;
-  const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, SAVE ? 1 : 0);
+  // state warps first, then side warps, then loaders
+  const bool loader = warp >= p.rb * (NH + kSideWarps), side = !loader && warp >= p.rb * NH;
+  const int blk = loader ? 0 : side ? (warp - p.rb * NH) / kSideWarps : warp / NH;
+  const int h = side ? (warp - p.rb * NH) % kSideWarps : NH == 1 ? 0 : warp % NH;
+  const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, KIND);
   const int ldv = tile_ld(NP, p.rb);
   long long start;
   int len;
   seq_range(p, seq, start, len);
   const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
-  const bool loader = blk >= p.rb;
-  const int r0 = row0 + blk * 16 + g, c0 = h * DKH;    // this thread's value rows: r0, r0 + 8
-  const bool live = !loader && row0 + blk * 16 < p.dvp;
-  float4 *part = reinterpret_cast<float4 *>(smem + p.stages * l.bytes);
-  unsigned *tops = reinterpret_cast<unsigned *>(smem + p.stages * l.bytes + l.part);
+  const int brow = row0 + blk * 16, r0 = brow + g, c0 = h * DKH;
+  const bool live = !loader && brow < p.dvp;
+  uint8_t *tail = smem + p.stages * l.bytes + blk * l.tail;
+  float4 *part = reinterpret_cast<float4 *>(tail + l.part), *sided = reinterpret_cast<float4 *>(tail + l.side);
+  float4 *last = reinterpret_cast<float4 *>(tail + l.last), *plus = reinterpret_cast<float4 *>(tail + l.plus);
+  uint4 *planes = reinterpret_cast<uint4 *>(tail + l.planes);
+  unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);       // [0..1] state, [2..3] V or dO
+  const Lane<DK> ld(lane);
+  const Lane<kChunk> lc(lane);
 
   float S[NTH][4];
-  load_state<NTH>(S, live ? p.state_in : nullptr, blockIdx.x, p.d_v, DK, r0, c0 + t2);
-  unsigned top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(S));
-  if (NH > 1 && live && lane == 0) tops[warp] = top;
-
-  const int ltid = tid - 32 * NH * p.rb, lthreads = 32 * kLoadWarps;
+  if (live && !side) {
+    load_state<NTH>(S, REV ? p.d_state_out : p.state_in, blockIdx.x, p.d_v, DK, r0, c0 + t2);
+    const unsigned top = max_bits(S);
+    if (lane == 0) {
+      tops[h] = top;
+      if (NH == 1) tops[1] = 0;
+    }
+  }
+  auto stage_of = [&](int c) { return smem + (p.stages == 2 ? (c & 1) * l.bytes : 0); };
   auto fetch = [&](int c) {
-    chain_fetch<DK, NP, DELTA, SAVE>(p, smem + (p.stages == 2 ? (c & 1) * l.bytes : 0), l,
-                                     start + (long long)c * kChunk, min(kChunk, len - c * kChunk), base + c, head, row0,
-                                     ltid, lthreads);
-    cp_commit();
+    walk_fetch<DK, NP, DELTA, KIND>(p, stage_of(c), l, start + (long long)c * kChunk, min(kChunk, len - c * kChunk),
+                                    base + c, head, row0, tid - 32 * p.rb * (NH + kSideWarps));
   };
-  if (loader && chunks > 0) fetch(0);
-  for (int c = 0; c < chunks; ++c) {
-    uint8_t *st = smem + (p.stages == 2 ? (c & 1) * l.bytes : 0);
+  if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0);
+  for (int i0 = 0; i0 < chunks; ++i0) {
+    const int c = REV ? chunks - 1 - i0 : i0, next = REV ? c - 1 : c + 1;
     if (loader) cp_wait<0>();
     __syncthreads();
-    if (p.stages == 2 && loader && c + 1 < chunks) fetch(c + 1);
-    if (live) {
-      const __half *kt = reinterpret_cast<const __half *>(st + l.kt), *sk = reinterpret_cast<const __half *>(st + l.k);
-      const __half *sq = reinterpret_cast<const __half *>(st + l.q), *tm = reinterpret_cast<const __half *>(st + l.tm);
-      const __half *pp = reinterpret_cast<const __half *>(st + l.pp);
-      const float *eG = reinterpret_cast<const float *>(st + l.gates), *w = eG + kChunk;
-      const float kappa = w[kChunk], qscale = w[kChunk + 1], eC = eG[kChunk - 1];
-      const long long rec = (long long)(base + c) * p.H + head;
-      const int n = min(kChunk, len - c * kChunk);
-      // V^T and the scale of this chunk
-      float x[4][8];
-      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
-      unsigned m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(x[i][j]));
-      m = max(__reduce_max_sync(0xFFFFFFFFu, m), top);
-#pragma unroll
-      for (int o = 1; o < NH; ++o) m = max(m, tops[blk * NH + ((h + o) & (NH - 1))]);
+    if (p.stages == 2 && loader && i0 + 1 < chunks) fetch(next);
+    uint8_t *st = stage_of(c);
+    const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
+                   tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp);
+    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk;
+    const float qscale = ek[kChunk + 1];
+    const long long rec = (long long)(base + c) * p.H + head;
+    const int n = min(kChunk, len - c * kChunk);
+    if (live && !side) {
+      // ---- state warp -------------------------------------------------------------------
+      const unsigned mS = max(tops[0], tops[1]);
       float inv;
-      const float scale = scale_of(m, 6, inv);
-
-      // Tile i of E and O holds tokens 8 ((i + OT h) % 8) ..: the warp's own come first.
-      float E[8][4], O[8][4];
+      const float scale = scale_of(mS, 6, inv);
+      float E[8][4];                   // 16 value rows x 64 tokens
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) E[i][j] = O[i][j] = 0.0f;
-      __half *s0 = SAVE ? p.s0 + rec * (2ll * p.dvp * DK) : nullptr;
+        for (int j = 0; j < 4; ++j) E[i][j] = 0.0f;
+      __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
 #pragma unroll
       for (int ks = 0; ks < DKH / 16; ++ks) {
         uint32_t ah[4], al[4], b[4];
         split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
-        if (SAVE) {
+        if (KIND == kForward) {
+          planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
+          if (NP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
+        } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const long long at = (long long)(r0 + 8 * (q & 1)) * DK + c0 + ks * 16 + 8 * (q >> 1) + t2;
-            *reinterpret_cast<uint32_t *>(s0 + at) = ah[q];
-            *reinterpret_cast<uint32_t *>(s0 + (long long)p.dvp * DK + at) = al[q];
+            const int at = tiled<DK>(brow + 8 * (q & 1), c0 + ks * 16 + 8 * (q >> 1)) + 2 * lane;
+            *reinterpret_cast<uint32_t *>(keep + at) = ah[q];
+            *reinterpret_cast<uint32_t *>(keep + (long long)p.dvp * DK + at) = al[q];
           }
         }
+        if (DELTA || REV) {
+          const uint32_t x = DELTA ? kt : sk;      // (reverse without the delta rule: Kb = diag(w) K)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
-          if (DELTA) {
-            b_rows(b, kt, LD, np * 16, c0 + ks * 16, lane);
-            mma2(E[2 * i], E[2 * i + 1], ah, b);
-            mma2(E[2 * i], E[2 * i + 1], al, b);
-            b_rows(b, kt + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
-            mma2(E[2 * i], E[2 * i + 1], ah, b);
-          }
-          if (!SAVE) {
-            b_rows(b, sq, LD, np * 16, c0 + ks * 16, lane);
-            mma2(O[2 * i], O[2 * i + 1], ah, b);
-            if (NP == 2) {
-              mma2(O[2 * i], O[2 * i + 1], al, b);
-              b_rows(b, sq + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
-              mma2(O[2 * i], O[2 * i + 1], ah, b);
+          for (int np = 0; np < 4; ++np) {
+            ld.b_rows(b, x, np * 16, c0 + ks * 16);
+            mma2(E[2 * np], E[2 * np + 1], ah, b);
+            mma2(E[2 * np], E[2 * np + 1], al, b);
+            if (DELTA || NP == 2) {
+              ld.b_rows(b, x + TILE, np * 16, c0 + ks * 16);
+              mma2(E[2 * np], E[2 * np + 1], ah, b);
             }
           }
         }
       }
-      if (SAVE && lane == 0 && h == 0) p.fscale[rec * (p.dvp / 16) + (row0 >> 4) + blk] = scale;
-      // + V^T Tm^T for the warp's own tokens (without the delta rule Tm = I and E = V for all)
+      if (KIND != kForward && lane == 0 && h == 0)
+        p.scales[REV ? kScaleD : kScaleS][rec * (p.dvp / 16) + brow / 16] = scale;
+      if (NH > 1 && (DELTA || REV))
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t vh[4], vl[4];
-        if (DELTA) {
+        for (int i = 0; i < 8; ++i) part[(h * 8 + i) * 32 + lane] = f4(E[i]);
+      barrier_sync(1 + 2 * blk, PER);                                   // X
 #pragma unroll
-          for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * inv, x[ks][2 * q + 1] * inv, vh[q], vl[q]);
-#pragma unroll
-          for (int i = 0; i < OT / 2; ++i) {
-            const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
-            if (ks <= np) {
-              uint32_t b[4];
-              b_rows(b, tm, kLdC, np * 16, ks * 16, lane);
-              mma2(E[2 * i], E[2 * i + 1], vh, b);
-              if (NP == 2) mma2(E[2 * i], E[2 * i + 1], vl, b);
-              b_rows(b, tm + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
-              mma2(E[2 * i], E[2 * i + 1], vh, b);
-            }
+      for (int i = 0; i < 8; ++i) {
+        const float4 u = sided[i * 32 + lane];
+        if (DELTA || REV) {
+          if (NH > 1) {
+            const float4 y = part[((h ^ 1) * 8 + i) * 32 + lane];
+            E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
           }
+          float x = scale, y = scale;
+          if (REV && !DELTA) {
+            const float2 f = *reinterpret_cast<const float2 *>(wk + 8 * i + t2);
+            x *= f.x;
+            y *= f.y;
+          }
+          E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
+          E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
+        } else {
+          E[i][0] = u.x; E[i][1] = u.y; E[i][2] = u.z; E[i][3] = u.w;
         }
       }
-      // the other warps' parts
-      if (NH > 1) {                    // (also what keeps a warp's next maximum behind the others' reading)
-        float4 *own = part + warp * (32 * (8 + (SAVE ? 0 : 8 - OT)));
-        if (DELTA)
+      // E (or R) for the side warps: each state warp hands over half of the tokens
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            own[((i + OT * h) & 7) * 32 + lane] = make_float4(E[i][0], E[i][1], E[i][2], E[i][3]);
-        if (!SAVE)
+      for (int i = 0; i < 8; ++i)
+        if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
+      barrier_arrive(2 + 2 * blk, PER);                                 // Y
+      const unsigned mE = max(mS, max(tops[2], tops[3]));
+      float invE;
+      const float scaleE = scale_of(mE, 6, invE);
+      // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
+      // sum starts from zero and joins the state in one fma, so that the tensor cores'
+      // rounding does not pile up in it
+      const float eC = eG[kChunk - 1];
+      uint32_t wh[4][4], wl[4][4];
+      if (!REV || DELTA)
 #pragma unroll
-          for (int i = OT; i < 8; ++i) own[(8 + i - OT) * 32 + lane] = make_float4(O[i][0], O[i][1], O[i][2], O[i][3]);
-        block_barrier(blk, 32 * NH);
-#pragma unroll
-        for (int o = 1; o < NH; ++o) {
-          const int other = (h + o) & (NH - 1);
-          const float4 *their = part + (blk * NH + other) * (32 * (8 + (SAVE ? 0 : 8 - OT)));
-          if (DELTA)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y = their[((i + OT * h) & 7) * 32 + lane];
-              E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
-            }
-          if (!SAVE)
-#pragma unroll
-            for (int i = 0; i < OT; ++i) {
-              // this warp's tokens are tile i + OT (NH - o) of the other
-              const float4 y = their[(8 + i + OT * (NH - o) - OT) * 32 + lane];
-              O[i][0] += y.x; O[i][1] += y.y; O[i][2] += y.z; O[i][3] += y.w;
-            }
-        }
-      }
-      if (!DELTA)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // (x is indexed by the token; with NH = 2 the halves trade places for h = 1)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int q = (j >> 1) + 2 * (i & 1), e = 2 * q + (j & 1);
-            E[i][j] = (NH == 2 && h == 1 ? x[(i / 2 + 2) & 3][e] : x[i / 2][e]) * inv;
-          }
-        }
-      if (SAVE) {
-        __half *et = p.et + rec * (2ll * p.dvp * kChunk);
-#pragma unroll
-        for (int i = 0; i < OT; ++i)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            uint32_t hi, lo;
-            split2(E[i][2 * r], E[i][2 * r + 1], hi, lo);
-            const long long at = (long long)(r0 + 8 * r) * kChunk + 8 * ((i + OT * h) & 7) + t2;
-            *reinterpret_cast<uint32_t *>(et + at) = hi;
-            *reinterpret_cast<uint32_t *>(et + (long long)p.dvp * kChunk + at) = lo;
-          }
-      }
-      // S = e^{G_C} S0 + (diag(w) E)^T K: each tile's sum starts from zero and joins the
-      // state in one fma, so that the tensor cores' rounding does not pile up in it
-      {
-        uint32_t wh[4][4], wl[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float2 f = *reinterpret_cast<const float2 *>(w + ks * 16 + 8 * (q >> 1) + t2);
-            const float *e = &E[2 * i + (q >> 1)][2 * (q & 1)];
-            split2(e[0] * f.x * kappa, e[1] * f.y * kappa, wh[i][q], wl[i][q]);
+            const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
+            const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
+            const float by = REV ? -invE : invE;
+            split2(e[0] * (f.x * by), e[1] * (f.y * by), wh[ks][q], wl[ks][q]);
           }
-        }
 #pragma unroll
-        for (int np = 0; np < NTH / 2; ++np) {
-          float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+      for (int np = 0; np < NTH / 2; ++np) {
+        float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+        if (!REV || DELTA)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
+          for (int ks = 0; ks < 4; ++ks) {
             uint32_t b[4];
-            b_cols(b, sk, LD, ks * 16, c0 + np * 16, lane);
-            mma2(a0, a1, wh[i], b);
-            mma2(a0, a1, wl[i], b);
+            ld.b_cols(b, sk, ks * 16, c0 + np * 16);
+            mma2(a0, a1, wh[ks], b);
+            mma2(a0, a1, wl[ks], b);
             if (NP == 2) {
-              b_cols(b, sk + kChunk * LD, LD, ks * 16, c0 + np * 16, lane);
-              mma2(a0, a1, wh[i], b);
+              ld.b_cols(b, sk + TILE, ks * 16, c0 + np * 16);
+              mma2(a0, a1, wh[ks], b);
             }
           }
+        if (REV) {
+          const float4 x = plus[(c0 / 8 + 2 * np) * 32 + lane], y = plus[(c0 / 8 + 2 * np + 1) * 32 + lane];
+          const float px[4] = {x.x, x.y, x.z, x.w}, py[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            S[2 * np][j] = fmaf(S[2 * np][j], eC, a0[j] * scale);
-            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, a1[j] * scale);
+            S[2 * np][j] = fmaf(S[2 * np][j], eC, fmaf(a0[j], scaleE, px[j]));
+            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, fmaf(a1[j], scaleE, py[j]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            S[2 * np][j] = fmaf(S[2 * np][j], eC, a0[j] * scaleE);
+            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, a1[j] * scaleE);
           }
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(S));
-        if (NH > 1 && lane == 0) tops[warp] = top;
       }
-      if (!SAVE) {
-        // O^T = diag(e^G) (S0 Q^T) + E^T P^T for the own tokens
+      const unsigned top = max_bits(S);
+      if (lane == 0) tops[h] = top;
+    } else if (live) {
+      // ---- side warp: tokens 32 h .. 32 h + 31 --------------------------------------------
+      float x[4][8];
+      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
+      if (REV)
 #pragma unroll
-        for (int i = 0; i < OT; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(eG + 8 * ((i + OT * h) & 7) + t2);
-          O[i][0] *= f.x; O[i][1] *= f.y; O[i][2] *= f.x; O[i][3] *= f.y;
-        }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ks = NH == 1 ? j : (j + OT / 2 * h) & 3;
-          uint32_t eh[4], el[4], b[4];
-          split_tiles(E[2 * j], E[2 * j + 1], eh, el);
+          for (int j = 0; j < 8; ++j) x[i][j] *= qscale;       // (what Z and the planes of Q lack)
+      const unsigned mV = max_bits(x), mS = max(tops[0], tops[1]);
+      float invV, inv, invE;
+      const float scaleV = scale_of(mV, 6, invV), scale = scale_of(mS, 6, inv), scaleE = scale_of(max(mS, mV), 6, invE);
+      if (lane == 0) tops[2 + h] = mV;
+      float U[4][4];                   // tokens 32 h + 8 i ..
 #pragma unroll
-          for (int i = 0; i < OT / 2; ++i) {
-            const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
-            if (ks <= np) {
-              b_rows(b, pp, kLdC, np * 16, ks * 16, lane);
-              mma2(O[2 * i], O[2 * i + 1], eh, b);
-              if (NP == 2) {
-                mma2(O[2 * i], O[2 * i + 1], el, b);
-                b_rows(b, pp + kChunk * kLdC, kLdC, np * 16, ks * 16, lane);
-                mma2(O[2 * i], O[2 * i + 1], eh, b);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
+      if (DELTA || REV) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          uint32_t vh[4], vl[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * invV, x[ks][2 * q + 1] * invV, vh[q], vl[q]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int np = 2 * h + i;
+            if (REV ? np <= ks : ks <= np) {
+              uint32_t b[4];
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2) {
+                if (REV) lc.b_cols(b, tm + c2 * SQ, ks * 16, np * 16);
+                else lc.b_rows(b, tm + c2 * SQ, np * 16, ks * 16);
+                mma2(U[2 * i], U[2 * i + 1], vh, b);
+                if (NP == 2 && c2 == 0) mma2(U[2 * i], U[2 * i + 1], vl, b);
               }
             }
           }
         }
-        float own[OT][4];
 #pragma unroll
-        for (int i = 0; i < OT; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) own[i][j] = O[i][j];
-        store_tokens<NP, OT>(own, scale * qscale, st + l.v, ldv, blk * 16, OT * h, p.o, p.dtype, p.o_stride,
-                             start + (long long)c * kChunk, n, head * p.d_v + row0 + blk * 16,
-                             p.d_v - row0 - blk * 16, p.o16, lane);
-      }
-    }
-    if (p.stages == 1) {
-      __syncthreads();
-      if (loader && c + 1 < chunks) fetch(c + 1);
-    }
-  }
-  if (live && p.state_out && !SAVE) save_state<NTH>(S, p.state_out, blockIdx.x, p.d_v, DK, r0, c0 + t2);
-}
-
-// -------------------------------------------------------------------------------------
-// scan_reverse
-// -------------------------------------------------------------------------------------
-// The same grid and roles over the chunks backwards: the planes of D (at every chunk's end) and R
-// are kept for scan_grads, dV = R and d_state_in are written.
-template <int DK, int NP, bool DELTA>
-__device__ __forceinline__ void reverse_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0,
-                                              int n, int slot, int head, int row0, int tid, int threads) {
-  constexpr int LD = DK + 8, SIZE = NP == 2 ? 4 : 2;
-  const long long rec = (long long)slot * p.H + head;
-  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+          for (int j = 0; j < 4; ++j) U[i][j] *= scaleV;
+      } else {                         // E = V
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if (DELTA)
-      copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.kt) + c * kChunk * LD,
-                                 p.kb + (rec * 2 + c) * (kChunk * DK), tid, threads);
-    copy_lower(reinterpret_cast<__half *>(st + l.tm) + c * kChunk * kLdC,
-               (DELTA ? p.z : p.pp) + (rec * 2 + c) * (kChunk * kChunk), tid, threads);
-  }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.k) + c * kChunk * LD,
-                               p.khat + (qrec * NP + c) * (kChunk * DK), tid, threads);
-    copy_plane<kChunk, DK, LD>(reinterpret_cast<__half *>(st + l.q) + c * kChunk * LD,
-                               p.qhat + (qrec * NP + c) * (kChunk * DK), tid, threads);
-  }
-  copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
-                    static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + row0) * SIZE,
-                    p.o_stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, p.o16, tid, threads);
-  const float *gates = p.gates + rec * kGateFloats;
-  for (int i = tid; i < 2 * kChunk / 4 + 1; i += threads)
-    cp16(st + l.gates + 16 * i, i < 2 * kChunk / 4 ? gates + 4 * i : gates + kGateScales, true);
-}
-
-template <int DK, int NP, bool DELTA, int NH>
-__global__ void __launch_bounds__(32 * (kWalkWarps + kLoadWarps), 1) scan_reverse_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, DKH = DK / NH, NTH = DKH / 8, OT = 8 / NH;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int blk = warp / NH, h = NH == 1 ? 0 : warp % NH;
-  const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * p.rb;
-  const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, 2);
-  const int ldv = tile_ld(NP, p.rb);
-  long long start;
-  int len;
-  seq_range(p, seq, start, len);
-  const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
-  const bool loader = blk >= p.rb;
-  const int r0 = row0 + blk * 16 + g, c0 = h * DKH;
-  const bool live = !loader && row0 + blk * 16 < p.dvp;
-  float4 *part = reinterpret_cast<float4 *>(smem + p.stages * l.bytes);
-  unsigned *tops = reinterpret_cast<unsigned *>(smem + p.stages * l.bytes + l.part);
-
-  float D[NTH][4];
-  load_state<NTH>(D, live ? p.d_state_out : nullptr, blockIdx.x, p.d_v, DK, r0, c0 + t2);
-  unsigned top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(D));
-  if (NH > 1 && live && lane == 0) tops[warp] = top;
-
-  const int ltid = tid - 32 * NH * p.rb, lthreads = 32 * kLoadWarps;
-  auto fetch = [&](int c) {
-    reverse_fetch<DK, NP, DELTA>(p, smem + (p.stages == 2 ? (c & 1) * l.bytes : 0), l, start + (long long)c * kChunk,
-                                 min(kChunk, len - c * kChunk), base + c, head, row0, ltid, lthreads);
-    cp_commit();
-  };
-  if (loader && chunks > 0) fetch(chunks - 1);
-  for (int c = chunks - 1; c >= 0; --c) {
-    uint8_t *st = smem + (p.stages == 2 ? (c & 1) * l.bytes : 0);
-    if (loader) cp_wait<0>();
-    __syncthreads();
-    if (p.stages == 2 && loader && c > 0) fetch(c - 1);
-    if (live) {
-      const __half *kb = reinterpret_cast<const __half *>(st + l.kt), *sk = reinterpret_cast<const __half *>(st + l.k);
-      const __half *sq = reinterpret_cast<const __half *>(st + l.q), *z = reinterpret_cast<const __half *>(st + l.tm);
-      const float *eG = reinterpret_cast<const float *>(st + l.gates), *w = eG + kChunk;
-      const float kappa = w[kChunk], qscale = w[kChunk + 1], eC = eG[kChunk - 1];
-      const long long rec = (long long)(base + c) * p.H + head;
-      const int n = min(kChunk, len - c * kChunk);
-      // dO^T (times the scale of Q, which Z and the planes of Q lack) and the chunk's scale
-      float x[4][8];
-      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
-      unsigned m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[i][j] *= qscale;
-          m = max(m, abs_bits(x[i][j]));
-        }
-      m = max(__reduce_max_sync(0xFFFFFFFFu, m), top);
-#pragma unroll
-      for (int o = 1; o < NH; ++o) m = max(m, tops[blk * NH + ((h + o) & (NH - 1))]);
-      float inv;
-      const float scale = scale_of(m, 6, inv);
-
-      float R[8][4];                   // tile i: tokens 8 ((i + OT h) % 8) ..
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) R[i][j] = 0.0f;
-      __half *dd = p.dd + rec * (2ll * p.dvp * DK);
-      // D Kb^T; without the delta rule Kb = diag(w) K, applied below
-#pragma unroll
-      for (int ks = 0; ks < DKH / 16; ++ks) {
-        uint32_t ah[4], al[4], b[4];
-        split_tiles(D[2 * ks], D[2 * ks + 1], inv, ah, al);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const long long at = (long long)(r0 + 8 * (q & 1)) * DK + c0 + ks * 16 + 8 * (q >> 1) + t2;
-          *reinterpret_cast<uint32_t *>(dd + at) = ah[q];
-          *reinterpret_cast<uint32_t *>(dd + (long long)p.dvp * DK + at) = al[q];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
-          b_rows(b, DELTA ? kb : sk, LD, np * 16, c0 + ks * 16, lane);
-          mma2(R[2 * i], R[2 * i + 1], ah, b);
-          mma2(R[2 * i], R[2 * i + 1], al, b);
-          if (DELTA || NP == 2) {
-            b_rows(b, (DELTA ? kb : sk) + kChunk * LD, LD, np * 16, c0 + ks * 16, lane);
-            mma2(R[2 * i], R[2 * i + 1], ah, b);
+          for (int j = 0; j < 4; ++j) {
+            const int e = 2 * ((j >> 1) + 2 * (i & 1)) + (j & 1);
+            U[i][j] = h ? x[2 + i / 2][e] : x[i / 2][e];
           }
-        }
       }
-      if (lane == 0 && h == 0) p.bscale[rec * (p.dvp / 16) + (row0 >> 4) + blk] = scale;
-      if (!DELTA)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(w + 8 * ((i + OT * h) & 7) + t2);
-          R[i][0] *= f.x * kappa; R[i][1] *= f.y * kappa; R[i][2] *= f.x * kappa; R[i][3] *= f.y * kappa;
-        }
-      // + dO^T Z for the warp's own tokens s, from blocks t >= s
+      for (int i = 0; i < 4; ++i) sided[(4 * h + i) * 32 + lane] = f4(U[i]);
+      if (REV) {
+        // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
+        uint32_t oh[4][4], ol[4][4];
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t oh[4], ol[4];
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * inv, x[ks][2 * q + 1] * inv, oh[q], ol[q]);
-#pragma unroll
-        for (int i = 0; i < OT / 2; ++i) {
-          const int np = NH == 1 ? i : (i + OT / 2 * h) & 3;
-          if (np <= ks) {
-            uint32_t b[4];
-            b_cols(b, z, kLdC, ks * 16, np * 16, lane);
-            mma2(R[2 * i], R[2 * i + 1], oh, b);
-            if (NP == 2) mma2(R[2 * i], R[2 * i + 1], ol, b);
-            b_cols(b, z + kChunk * kLdC, kLdC, ks * 16, np * 16, lane);
-            mma2(R[2 * i], R[2 * i + 1], oh, b);
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+            split2(x[ks][2 * q] * (invV * f.x), x[ks][2 * q + 1] * (invV * f.y), oh[ks][q], ol[ks][q]);
           }
-        }
+        constexpr int HALF = DK >= 32 ? DK / 2 : DK;
+        if (DK >= 32 || h == 0)
+#pragma unroll
+          for (int np = 0; np < HALF / 16; ++np) {
+            const int n0 = (DK >= 32 ? h * HALF : 0) + np * 16;
+            float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              uint32_t b[4];
+              ld.b_cols(b, sq, ks * 16, n0);
+              mma2(a0, a1, oh[ks], b);
+              mma2(a0, a1, ol[ks], b);
+              if (NP == 2) {
+                ld.b_cols(b, sq + TILE, ks * 16, n0);
+                mma2(a0, a1, oh[ks], b);
+              }
+            }
+            plus[(n0 / 8) * 32 + lane] = make_float4(a0[0] * scaleV, a0[1] * scaleV, a0[2] * scaleV, a0[3] * scaleV);
+            plus[(n0 / 8 + 1) * 32 + lane] = make_float4(a1[0] * scaleV, a1[1] * scaleV, a1[2] * scaleV, a1[3] * scaleV);
+          }
       }
-      if (NH > 1) {
-        float4 *own = part + warp * (32 * 8);
+      barrier_sync(1 + 2 * blk, PER);                                   // X
+      float O[4][4];
+      if (KIND == kForward) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          own[((i + OT * h) & 7) * 32 + lane] = make_float4(R[i][0], R[i][1], R[i][2], R[i][3]);
-        block_barrier(blk, 32 * NH);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int o = 1; o < NH; ++o) {
-          const float4 *their = part + (blk * NH + ((h + o) & (NH - 1))) * (32 * 8);
+          for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = their[((i + OT * h) & 7) * 32 + lane];
-            R[i][0] += y.x; R[i][1] += y.y; R[i][2] += y.z; R[i][3] += y.w;
-          }
-        }
-      }
-      {
-        __half *rt = p.rt + rec * (2ll * p.dvp * kChunk);
-        float own[OT][4];
-#pragma unroll
-        for (int i = 0; i < OT; ++i) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            uint32_t hi, lo;
-            split2(R[i][2 * r], R[i][2 * r + 1], hi, lo);
-            const long long at = (long long)(r0 + 8 * r) * kChunk + 8 * ((i + OT * h) & 7) + t2;
-            *reinterpret_cast<uint32_t *>(rt + at) = hi;
-            *reinterpret_cast<uint32_t *>(rt + (long long)p.dvp * kChunk + at) = lo;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) own[i][j] = R[i][j];
-        }
-        store_tokens<NP, OT>(own, scale, st + l.v, ldv, blk * 16, OT * h, p.dv, p.dtype, p.v_stride,
-                             start + (long long)c * kChunk, n, head * p.d_v + row0 + blk * 16,
-                             p.d_v - row0 - blk * 16, p.v16, lane);
-      }
-      // D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K
-      uint32_t oh[4][4], ol[4][4], rh[4][4], rl[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = *reinterpret_cast<const float2 *>(eG + i * 16 + 8 * (q >> 1) + t2);
-          split2(x[i][2 * q] * inv * f.x, x[i][2 * q + 1] * inv * f.y, oh[i][q], ol[i][q]);
-          if (DELTA) {
-            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
-            const float2 e = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
-            const float *y = &R[2 * i + (q >> 1)][2 * (q & 1)];
-            split2(y[0] * e.x * -kappa, y[1] * e.y * -kappa, rh[i][q], rl[i][q]);
-          }
-        }
-#pragma unroll
-      for (int np = 0; np < NTH / 2; ++np) {
-        float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          const uint4 y = planes[ks * 32 + lane];
+          const uint32_t ah[4] = {y.x, y.y, y.z, y.w};
           uint32_t b[4];
-          b_cols(b, sq, LD, i * 16, c0 + np * 16, lane);
-          mma2(a0, a1, oh[i], b);
-          mma2(a0, a1, ol[i], b);
-          if (NP == 2) {
-            b_cols(b, sq + kChunk * LD, LD, i * 16, c0 + np * 16, lane);
-            mma2(a0, a1, oh[i], b);
-          }
-          if (DELTA) {
-            const int ks = NH == 1 ? i : (i + OT / 2 * h) & 3;
-            b_cols(b, sk, LD, ks * 16, c0 + np * 16, lane);
-            mma2(a0, a1, rh[i], b);
-            mma2(a0, a1, rl[i], b);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ld.b_rows(b, sq, (2 * h + i) * 16, ks * 16);
+            mma2(O[2 * i], O[2 * i + 1], ah, b);
             if (NP == 2) {
-              b_cols(b, sk + kChunk * LD, LD, ks * 16, c0 + np * 16, lane);
-              mma2(a0, a1, rh[i], b);
+              const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
+              const uint32_t al[4] = {z.x, z.y, z.z, z.w};
+              mma2(O[2 * i], O[2 * i + 1], al, b);
+              ld.b_rows(b, sq + TILE, (2 * h + i) * 16, ks * 16);
+              mma2(O[2 * i], O[2 * i + 1], ah, b);
             }
           }
         }
+        const float to = scale * invE;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          D[2 * np][j] = fmaf(D[2 * np][j], eC, a0[j] * scale);
-          D[2 * np + 1][j] = fmaf(D[2 * np + 1][j], eC, a1[j] * scale);
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
+          O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
         }
       }
-      top = __reduce_max_sync(0xFFFFFFFFu, max_bits<NTH>(D));
-      if (NH > 1 && lane == 0) tops[warp] = top;
+      barrier_sync(2 + 2 * blk, PER);                                   // Y
+      if (KIND == kForward) {
+        // + E^T P^T
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (ks <= 2 * h + 1) {
+            const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
+            const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
+            uint32_t eh[4], el[4], b[4];
+            split_tiles(e0, e1, invE, eh, el);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (ks <= 2 * h + i) {
+                lc.b_rows(b, pp, (2 * h + i) * 16, ks * 16);
+                mma2(O[2 * i], O[2 * i + 1], eh, b);
+                if (NP == 2) {
+                  mma2(O[2 * i], O[2 * i + 1], el, b);
+                  lc.b_rows(b, pp + SQ, (2 * h + i) * 16, ks * 16);
+                  mma2(O[2 * i], O[2 * i + 1], eh, b);
+                }
+              }
+          }
+        }
+        store_tokens<NP>(O, scaleE * qscale, st + l.v, ldv, blk * 16, 4 * h, p.o, p.dtype, p.o_stride,
+                         start + (long long)c * kChunk, n, head * p.d_v + brow, p.d_v - brow, p.o16, lane);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = last[(4 * h + i) * 32 + lane];
+          O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+        }
+        keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
+        if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+        if (REV)
+          store_tokens<NP>(O, 1.0f, st + l.v, ldv, blk * 16, 4 * h, p.dv, p.dtype, p.v_stride,
+                           start + (long long)c * kChunk, n, head * p.d_v + brow, p.d_v - brow, p.v16, lane);
+      }
     }
     if (p.stages == 1) {
       __syncthreads();
-      if (loader && c > 0) fetch(c - 1);
+      if (loader && i0 + 1 < chunks) fetch(next);
     }
   }
-  if (live && p.d_state_in) save_state<NTH>(D, p.d_state_in, blockIdx.x, p.d_v, DK, r0, c0 + t2);
+  if (live && !side && KIND != kRecompute) {
+    float *out = REV ? p.d_state_in : p.state_out;
+    if (out) save_state<NTH>(S, out, blockIdx.x, p.d_v, DK, r0, c0 + t2);
+  }
 }
 
 // -------------------------------------------------------------------------------------
 // scan_grads
 // -------------------------------------------------------------------------------------
-// Grid (slot, head), 8 warps.  Warps 0-3 (group A) own 16 rows each of dO S0 and R S0, warps
-// 4-7 (group B) of E D, dO E^T and R E^T; the value rows are the contraction
-// axis and pass through shared memory kGradRows at a time.  With dP'_ts = b_s dec_ts dO_t.E_s
-// (s <= t), dL'_ts = -b_s dec_ts R_t.E_s (s < t):
-//   dQ = diag(e^G) dO S0 + dP' K
-//   dK = diag(w) E D - d diag(e^G) R S0 + dP'^T Q + dL' K + dL'^T K
+// Grid (slot, head), 16 warps in four groups of four; a warp owns 16 of a group's 64 token rows:
+//   group 0: dO S0     group 1: R S0     group 2: E D     group 3: dO E^T and R E^T
+// with the value rows as the contraction axis, passing through shared memory kGradRows at a time.  Then,
+// with dP'_ts = b_s dec_ts dO_t.E_s (s <= t), dL'_ts = -b_s dec_ts R_t.E_s (s < t) from group 3:
+//   dQ = diag(e^G) dO S0 + dP' K                                            group 0
+//   dK = diag(w) E D + dP'^T Q  - d diag(e^G) R S0 + dL' K  + dL'^T K        groups 2, 1, 3
 //   c_s = sum_t dec_ts (q_t.k_s dO_t.E_s - k_t.k_s R_t.E_s)
 //   dbeta_s = c_s + e^{G_C - G_s} k_s.(D^T E_s)
 //   dG_t = sum_s b_s dec_ts (...) - b_t dbeta_t + e^{G_t} (q_t.(S0^T dO_t) - d k_t.(S0^T R_t))
 //   dlog_alpha_r = sum_{t >= r} dG_t + sum_s w_s k_s.(D^T E_s) + e^{G_C} <D, S0>
 // (the pair (t, s) enters dG_t and, through dbeta_s, -dG_s with the same value, so the sums
 // over t >= r cancel exactly where they should).
-// Scales: every product pairs a plane of the forward walk (16 value rows over c_b) with one
-// of the reverse walk (over d_b), so a 16-row step contributes in units of c_b d_b; left operands
-// are brought to the largest such unit F, and sums are held over F.
+// Scales: the planes of 16 value rows are held over their own powers of two, so a 16-row step
+// contributes in units that are the product of two of them; left operands are brought to
+// the largest unit F of the group's steps, and the group's sums are held over F.
 constexpr int kGradRows = 32;
 
 struct GradLayout {
   int k, q, x, f, stage, stage_bytes, s0, d, e, r, o;
 };
 __host__ __device__ inline GradLayout grad_layout(int dk, int np) {
-  const int ld = dk + 8;
   GradLayout l{};
   int at = 0;
-  l.k = at; at += np * kChunk * ld * 2;
-  l.q = at; at += np * kChunk * ld * 2;
-  l.x = at; at += 4 * kChunk * kLdC * 2;                 // dP' hi, lo, dL' hi, lo
-  l.f = at; at += (kGateFloats + 3 * kChunk + 4 * kChunk + 16) * 4;
+  l.k = at; at += np * kChunk * dk * 2;
+  l.q = at; at += np * kChunk * dk * 2;
+  l.x = at; at += 4 * kChunk * kChunk * 2;               // dP' hi, lo, dL' hi, lo
+  l.f = at; at += (kGateFloats + 4 * kChunk + 4 * kChunk + 16) * 4;
   l.stage = (at + 15) / 16 * 16;
   at = 0;
-  l.s0 = at; at += 2 * kGradRows * ld * 2;
-  l.d = at; at += 2 * kGradRows * ld * 2;
-  l.e = at; at += 2 * kGradRows * kLdC * 2;
-  l.r = at; at += 2 * kGradRows * kLdC * 2;
-  l.o = at; at += kChunk * tile_ld(np, kGradRows / 16) * (np == 2 ? 4 : 2);
-  l.stage_bytes = at;                                    // holds the [64][dk + 4] fp32 exchange too
+  l.s0 = at; at += 2 * kGradRows * dk * 2;
+  l.d = at; at += 2 * kGradRows * dk * 2;
+  l.e = at; at += 2 * kGradRows * kChunk * 2;
+  l.r = at; at += 2 * kGradRows * kChunk * 2;
+  l.o = at; at += kChunk * (kGradRows + (np == 2 ? 4 : 8)) * (np == 2 ? 4 : 2);
+  l.stage_bytes = at;
   return l;
 }
-
-// Rows [0, there) of kGradRows rows of a plane; the others are zeros.
-template <int COLS, int LD>
-__device__ __forceinline__ void copy_rows(__half *dst, const __half *src, int there, int tid, int threads) {
-  constexpr int per = COLS / 8;
-#pragma unroll 2
-  for (int i = tid; i < kGradRows * per; i += threads) {
-    const bool in = i / per < there;
-    cp16(dst + (i / per) * LD + (i % per) * 8, in ? src + i * 8 : src, in);
-  }
+// Behind the fixed part: the stages, and later what groups 1 and 3 hand to group 2.
+__host__ __device__ inline int grad_bytes(const GradLayout &l, int dk, int stages) {
+  const int a = stages * l.stage_bytes, b = 2 * kChunk * dk * 4;
+  return l.stage + (a > b ? a : b);
 }
+
 // A left operand's registers times a power of two <= 1.
 __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], __half2 by) {
 #pragma unroll
@@ -1520,45 +1457,60 @@ __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], __half2 by) {
     a[q] = *reinterpret_cast<const uint32_t *>(&y);
   }
 }
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.0f : __uint_as_float((unsigned)(127 + min(e, 127)) << 23);
+}
+__device__ __forceinline__ int exponent(const float *x) { return (int)(__float_as_uint(__ldg(x)) >> 23) - 127; }
+// The largest exponent of a[b] c[b] over the blocks of 16 value rows.
+__device__ __forceinline__ int top_unit(const float *a, const float *c, int blocks, int lane) {
+  int top = -1000;
+  for (int b = lane; b < blocks; b += 32) top = max(top, exponent(a + b) + exponent(c + b));
+  return __reduce_max_sync(0xFFFFFFFFu, top);
+}
 
 template <int DK, int NP, bool DELTA>
-__global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanParams p) {
-  constexpr int LD = DK + 8, NT = DK / 8, LDX = DK + 4, LDO = tile_ld(NP, kGradRows / 16), SIZE = NP == 2 ? 4 : 2;
+__global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanParams p) {
+  constexpr int NT = DK / 8, LDO = kGradRows + (NP == 2 ? 4 : 8), SIZE = NP == 2 ? 4 : 2;
+  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2, SP = kGradRows * DK * 2, EP = kGradRows * kChunk * 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const GradLayout l = grad_layout(DK, NP);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w4 = warp & 3, g = lane >> 2,
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2, w4 = warp & 3, g = lane >> 2,
             t2 = (lane & 3) * 2, m0 = w4 * 16;
-  const bool groupA = warp < 4;
   const int slot = blockIdx.x, head = blockIdx.y;
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
   if (n == 0) return;
   const long long rec = (long long)slot * p.H + head;
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
-  __half *sk = reinterpret_cast<__half *>(smem + l.k), *sq = reinterpret_cast<__half *>(smem + l.q);
-  __half *sx = reinterpret_cast<__half *>(smem + l.x);
-  float *eG = reinterpret_cast<float *>(smem + l.f), *w = eG + kChunk, *be = w + kChunk, *eC = be + kChunk;
-  const double *G = reinterpret_cast<const double *>(eC + kChunk);
-  float *rowv = eG + kGateFloats, *aq = rowv + kChunk, *kw = aq + kChunk, *colp = kw + kChunk,
+  const uint32_t sk = smem_addr(smem + l.k), sq = smem_addr(smem + l.q), sx = smem_addr(smem + l.x);
+  float *gates = reinterpret_cast<float *>(smem + l.f);
+  const float *eG = gates + kGateE * kChunk, *w = gates + kGateW * kChunk, *be = gates + kGateB * kChunk,
+              *eC = gates + kGateC * kChunk;
+  const double *G = reinterpret_cast<const double *>(gates + kGateG * kChunk);
+  float *rowv = gates + kGateFloats, *aq = rowv + kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
         *red = colp + 4 * kChunk;
-#pragma unroll
-  for (int c = 0; c < NP; ++c) {
-    copy_plane<kChunk, DK, LD>(sk + c * kChunk * LD, p.khat + (qrec * NP + c) * (kChunk * DK), tid, kGradThreads);
-    copy_plane<kChunk, DK, LD>(sq + c * kChunk * LD, p.qhat + (qrec * NP + c) * (kChunk * DK), tid, kGradThreads);
-  }
+  copy_flat<NP * TILE>(smem + l.k, p.khat + qrec * (NP * kChunk * DK), tid, kGradThreads);
+  copy_flat<NP * TILE>(smem + l.q, p.qhat + qrec * (NP * kChunk * DK), tid, kGradThreads);
   for (int i = tid; i < kGateFloats / 4; i += kGradThreads)
-    cp16(eG + 4 * i, p.gates + rec * kGateFloats + 4 * i, true);
+    cp16(gates + 4 * i, p.gates + rec * kGateFloats + 4 * i, true);
   const int blocks = (p.dvp + kGradRows - 1) / kGradRows, blocks16 = p.dvp / 16;
+  auto stage_of = [&](int b) { return smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0); };
   auto fetch = [&](int b) {
-    uint8_t *st = smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0);
+    uint8_t *st = stage_of(b);
     const int v0 = b * kGradRows, rows = min(kGradRows, p.dvp - v0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const long long at = (rec * 2 + c) * p.dvp + v0;
-      copy_rows<DK, LD>(reinterpret_cast<__half *>(st + l.s0) + c * kGradRows * LD, p.s0 + at * DK, rows, tid, kGradThreads);
-      copy_rows<DK, LD>(reinterpret_cast<__half *>(st + l.d) + c * kGradRows * LD, p.dd + at * DK, rows, tid, kGradThreads);
-      copy_rows<kChunk, kLdC>(reinterpret_cast<__half *>(st + l.e) + c * kGradRows * kLdC, p.et + at * kChunk, rows, tid, kGradThreads);
-      copy_rows<kChunk, kLdC>(reinterpret_cast<__half *>(st + l.r) + c * kGradRows * kLdC, p.rt + at * kChunk, rows, tid, kGradThreads);
+      const uint8_t *s0 = reinterpret_cast<const uint8_t *>(p.s0 + at * DK), *dd = reinterpret_cast<const uint8_t *>(p.dd + at * DK);
+      const uint8_t *se = reinterpret_cast<const uint8_t *>(p.et + at * kChunk), *sr = reinterpret_cast<const uint8_t *>(p.rt + at * kChunk);
+      for (int i = tid * 16; i < rows * DK * 2; i += kGradThreads * 16) {
+        cp16(st + l.s0 + c * SP + i, s0 + i, true);
+        cp16(st + l.d + c * SP + i, dd + i, true);
+      }
+      for (int i = tid * 16; i < rows * kChunk * 2; i += kGradThreads * 16) {
+        cp16(st + l.e + c * EP + i, se + i, true);
+        if (DELTA) cp16(st + l.r + c * EP + i, sr + i, true);
+      }
     }
     copy_tokens<SIZE>(st + l.o, LDO,
                       static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + v0) * SIZE,
@@ -1566,125 +1518,111 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
     cp_commit();
   };
   fetch(0);
-  // exponents of the steps' units, the largest one
-  const unsigned *cb = reinterpret_cast<const unsigned *>(p.fscale + rec * blocks16);
-  const unsigned *db = reinterpret_cast<const unsigned *>(p.bscale + rec * blocks16);
-  int top = 0;
-  for (int b = lane; b < blocks16; b += 32) top = max(top, (int)(__ldg(cb + b) >> 23) + (int)(__ldg(db + b) >> 23));
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  // F = 2^(top - 254) as two factors, each in range
-  const int f1 = (top - 254) / 2, f2 = top - 254 - f1;
-  const float F1 = __uint_as_float((unsigned)(127 + max(-126, f1)) << 23), F2 = __uint_as_float((unsigned)(127 + max(-126, f2)) << 23);
+  const float *sS = p.scales[kScaleS] + rec * blocks16, *sE = p.scales[kScaleE] + rec * blocks16;
+  const float *sD = p.scales[kScaleD] + rec * blocks16, *sR = p.scales[kScaleR] + rec * blocks16;
+  // the group's two scales: of the left operand's planes and of the right one's
+  const float *sl = group == 2 ? sE : sR, *sr2 = group == 2 ? sD : group == 3 ? sE : sS;
+  const int topDS = top_unit(sD, sS, blocks16, lane), topRE = top_unit(sR, sE, blocks16, lane);
+  const int top = group == 3 ? topRE : top_unit(sl, sr2, blocks16, lane);
 
-  // group A: acc = dO S0, acc2 = R S0; group B: acc = E D, acc2 tiles 0-7 dO E^T, 8-15 R E^T
-  constexpr int N2 = NT > 16 ? NT : 16;
-  float acc[NT][4], acc2[N2][4], ds = 0.0f;
+  // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T
+  constexpr int NA = NT > 16 ? NT : 16;
+  float acc[NA][4], ds = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int i = 0; i < NA; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc2[i][j] = 0.0f;
+  const Lane<DK> ld(lane);
+  const Lane<kChunk> lc(lane);
 
   for (int b = 0; b < blocks; ++b) {
     cp_wait<0>();
     __syncthreads();
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
-    uint8_t *st = smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0);
-    const __half *s0 = reinterpret_cast<const __half *>(st + l.s0), *dd = reinterpret_cast<const __half *>(st + l.d);
-    const __half *se = reinterpret_cast<const __half *>(st + l.e), *sr = reinterpret_cast<const __half *>(st + l.r);
+    uint8_t *st = stage_of(b);
+    const uint32_t s0 = smem_addr(st + l.s0), dd = smem_addr(st + l.d), se = smem_addr(st + l.e), sr = smem_addr(st + l.r);
 #pragma unroll
     for (int kk = 0; kk < kGradRows; kk += 16) {
       const int b16 = b * (kGradRows / 16) + kk / 16;
       if (b16 >= blocks16) break;
-      const unsigned ed = __ldg(db + b16) >> 23;
-      const int gap = (int)(__ldg(cb + b16) >> 23) + (int)ed - top;       // <= 0
-      const float ratio = gap > -126 ? __uint_as_float((unsigned)(127 + gap) << 23) : 0.0f;
-      const float dinv = __uint_as_float((254u - ed) << 23);
-      const __half2 by = __float2half2_rn(ratio);
-      uint32_t ao[NP][4], ar[2][4], b4[4];
-      if (NP == 1) {
-        uint32_t raw[4];
-        a_rows(raw, reinterpret_cast<const __half *>(st + l.o), LDO, m0, kk, lane);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = pair_of(raw[q], p.dtype);
-          ao[0][q] = pack2(f.x * dinv * ratio, f.y * dinv * ratio);
-        }
-      } else {
-        const float *so = reinterpret_cast<const float *>(st + l.o);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = *reinterpret_cast<const float2 *>(so + (m0 + g + 8 * (q & 1)) * LDO + kk + 8 * (q >> 1) + t2);
-          split2(f.x * dinv * ratio, f.y * dinv * ratio, ao[0][q], ao[NP - 1][q]);
-        }
-      }
-      if (DELTA)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          a_cols(ar[c], sr + c * kGradRows * kLdC, kLdC, kk, m0, lane);
-          scale_frag(ar[c], by);
-        }
-      // <D, S0>
       {
+        // <D, S0>
         float part = 0.0f;
 #pragma unroll
         for (int i = tid; i < 16 * DK / 2; i += kGradThreads) {
-          const int at = (kk + i / (DK / 2)) * LD + (i % (DK / 2)) * 2;
-          auto pair = [&](const __half *x) {
-            const float2 hi = half2_of(*reinterpret_cast<const uint32_t *>(x + at));
-            const float2 lo = half2_of(*reinterpret_cast<const uint32_t *>(x + kGradRows * LD + at));
+          const int at = kk * DK * 2 + i * 4;          // (any order of the block's entries will do)
+          auto pair = [&](int off) {
+            const float2 hi = half2_of(*reinterpret_cast<const uint32_t *>(st + off + at));
+            const float2 lo = half2_of(*reinterpret_cast<const uint32_t *>(st + off + SP + at));
             return make_float2(__fadd_rn(hi.x, lo.x), __fadd_rn(hi.y, lo.y));
           };
-          const float2 x = pair(s0), y = pair(dd);
+          const float2 x = pair(l.s0), y = pair(l.d);
           part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
         }
-        ds = fmaf(part, ratio, ds);
+        ds = fmaf(part, pow2(exponent(sD + b16) + exponent(sS + b16) - topDS), ds);
       }
-      if (groupA) {
+      const int el = exponent(sl + b16);
+      const float ratio = pow2(el + exponent(sr2 + b16) - top);
+      const __half2 by = __float2half2_rn(ratio);
+      uint32_t ao[NP][4], ar[2][4], b4[4];
+      if (group == 0 || group == 3) {
+        const float to = pow2(-el) * ratio;            // dO over the scale of R
+        if (NP == 1) {
+          uint32_t raw[4];
+          a_rows_plain(raw, smem_addr(st + l.o), LDO, m0, kk, lane);
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b4, s0, LD, kk, np * 16, lane);
-#pragma unroll
-          for (int c = 0; c < NP; ++c) mma2(acc[2 * np], acc[2 * np + 1], ao[c], b4);
-          if (DELTA) {
-            mma2(acc2[2 * np], acc2[2 * np + 1], ar[0], b4);
-            mma2(acc2[2 * np], acc2[2 * np + 1], ar[1], b4);
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = pair_of(raw[q], p.dtype);
+            ao[0][q] = pack2(f.x * to, f.y * to);
           }
-          b_cols(b4, s0 + kGradRows * LD, LD, kk, np * 16, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], ao[0], b4);
-          if (DELTA) mma2(acc2[2 * np], acc2[2 * np + 1], ar[0], b4);
+        } else {
+          const float *so = reinterpret_cast<const float *>(st + l.o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = *reinterpret_cast<const float2 *>(so + (m0 + g + 8 * (q & 1)) * LDO + kk + 8 * (q >> 1) + t2);
+            split2(f.x * to, f.y * to, ao[0][q], ao[NP - 1][q]);
+          }
         }
-      } else {
-        uint32_t ae[2][4];
+      }
+      if (group == 2 || (DELTA && (group & 1)))
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          a_cols(ae[c], se + c * kGradRows * kLdC, kLdC, kk, m0, lane);
-          scale_frag(ae[c], by);
+          lc.a_cols(ar[c], (group == 2 ? se : sr) + c * EP, kk, m0);
+          scale_frag(ar[c], by);
         }
+      if (group == 0) {
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b4, dd, LD, kk, np * 16, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], ae[0], b4);
-          mma2(acc[2 * np], acc[2 * np + 1], ae[1], b4);
-          b_cols(b4, dd + kGradRows * LD, LD, kk, np * 16, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], ae[0], b4);
+          ld.b_cols(b4, s0, kk, np * 16);
+#pragma unroll
+          for (int c = 0; c < NP; ++c) mma2(acc[2 * np], acc[2 * np + 1], ao[c], b4);
+          ld.b_cols(b4, s0 + SP, kk, np * 16);
+          mma2(acc[2 * np], acc[2 * np + 1], ao[0], b4);
         }
+      } else if (group == 2 || (DELTA && group == 1)) {
+        const uint32_t x = group == 2 ? dd : s0;
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np) {
+          ld.b_cols(b4, x, kk, np * 16);
+          mma2(acc[2 * np], acc[2 * np + 1], ar[0], b4);
+          mma2(acc[2 * np], acc[2 * np + 1], ar[1], b4);
+          ld.b_cols(b4, x + SP, kk, np * 16);
+          mma2(acc[2 * np], acc[2 * np + 1], ar[0], b4);
+        }
+      } else if (group == 3) {
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           if (np <= w4) {
-            b_cols(b4, se, kLdC, kk, np * 16, lane);
+            lc.b_cols(b4, se, kk, np * 16);
 #pragma unroll
-            for (int c = 0; c < NP; ++c) mma2(acc2[2 * np], acc2[2 * np + 1], ao[c], b4);
+            for (int c = 0; c < NP; ++c) mma2(acc[2 * np], acc[2 * np + 1], ao[c], b4);
             if (DELTA) {
-              mma2(acc2[8 + 2 * np], acc2[8 + 2 * np + 1], ar[0], b4);
-              mma2(acc2[8 + 2 * np], acc2[8 + 2 * np + 1], ar[1], b4);
+              mma2(acc[8 + 2 * np], acc[8 + 2 * np + 1], ar[0], b4);
+              mma2(acc[8 + 2 * np], acc[8 + 2 * np + 1], ar[1], b4);
             }
-            b_cols(b4, se + kGradRows * kLdC, kLdC, kk, np * 16, lane);
-            mma2(acc2[2 * np], acc2[2 * np + 1], ao[0], b4);
-            if (DELTA) mma2(acc2[8 + 2 * np], acc2[8 + 2 * np + 1], ar[0], b4);
+            lc.b_cols(b4, se + EP, kk, np * 16);
+            mma2(acc[2 * np], acc[2 * np + 1], ao[0], b4);
+            if (DELTA) mma2(acc[8 + 2 * np], acc[8 + 2 * np + 1], ar[0], b4);
           }
         }
       }
@@ -1697,120 +1635,95 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
 #pragma unroll
   for (int d = 16; d; d >>= 1) ds += __shfl_xor_sync(0xFFFFFFFFu, ds, d);
   if (lane == 0) red[warp] = ds;
-  const float kappa = eG[kGateScales], qscale = eG[kGateScales + 1];
+  const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1];
   const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
   const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
-  // planes of dP', dL' are held over F and 4 dvp (rounded up to a power of two): the entries of
+  // The planes of dP', dL' are held over F of group 3 and 4 dvp (rounded up to a power of two): the entries of
   // E, R and dO over their scales stay below 2^7 (E and R somewhat above), so a sum over d_v of their
-  // products stays below 2^14 dvp
-  const int lg = 32 - __clz(p.dvp - 1);
-  const float unit = __uint_as_float((unsigned)(127 - 2 - lg) << 23), iunit = __uint_as_float((unsigned)(127 + 2 + lg) << 23);
+  // products stays below 2^14 dvp.
+  const int lg = 2 + 32 - __clz(p.dvp - 1);
+  const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // F of the group, as two factors in range
+  const float to_unit = pow2(top - topRE - lg);                          // from F to what the planes are held over
+  const float out1 = pow2(topRE / 2) * pow2(lg), out2 = pow2(topRE - topRE / 2);
 
-  auto row_pair = [&](const __half *x, int row, int col) {
-    float2 v = half2_of(*reinterpret_cast<const uint32_t *>(x + row * LD + col));
-    if (NP == 2) {
-      const float2 y = half2_of(*reinterpret_cast<const uint32_t *>(x + kChunk * LD + row * LD + col));
-      v.x = __fadd_rn(v.x, y.x);
-      v.y = __fadd_rn(v.y, y.y);
-    }
-    return v;
-  };
-  if (groupA) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = m0 + g + 8 * h;
-      float s = 0.0f, r = 0.0f;
-      const float e = eG[t], to = e * unit * ikappa;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const float2 q = row_pair(sq, t, 8 * i + t2);
-        s = fmaf(q.x, acc[i][2 * h], fmaf(q.y, acc[i][2 * h + 1], s));
-        acc[i][2 * h] *= to;
-        acc[i][2 * h + 1] *= to;
-        if (DELTA) {
-          const float2 k = row_pair(sk, t, 8 * i + t2);
-          r = fmaf(k.x, acc2[i][2 * h], fmaf(k.y, acc2[i][2 * h + 1], r));
-          acc2[i][2 * h] *= -to;
-          acc2[i][2 * h + 1] *= -to;
-        }
-      }
-      s = fmaf(s, qscale, -r * kappa) * e;
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      if ((lane & 3) == 0) aq[t] = s * F1 * F2;
-    }
-  } else {
+  if (group != 3) {
+    // the row's dot with q or k, then the row in the planes' units
+    const uint8_t *x = smem + (group == 0 ? l.q : l.k);
+    float *dots = group == 0 ? aq : group == 1 ? ak : kw;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
       float s = 0.0f;
-      const float to = w[t] * unit * iqscale;
+      const float to = group == 2 ? w[t] * to_unit * iqscale : eG[t] * to_unit * (group == 1 ? -ikappa : ikappa);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const float2 k = row_pair(sk, t, 8 * i + t2);
-        s = fmaf(k.x, acc[i][2 * h], fmaf(k.y, acc[i][2 * h + 1], s));
+        const int at = 2 * (tiled<DK>(m0 + 8 * h, 8 * i) + 2 * lane);
+        float2 v = half2_of(*reinterpret_cast<const uint32_t *>(x + at));
+        if (NP == 2) {
+          const float2 y = half2_of(*reinterpret_cast<const uint32_t *>(x + TILE + at));
+          v.x = __fadd_rn(v.x, y.x);
+          v.y = __fadd_rn(v.y, y.y);
+        }
+        s = fmaf(v.x, acc[i][2 * h], fmaf(v.y, acc[i][2 * h + 1], s));
         acc[i][2 * h] *= to;
         acc[i][2 * h + 1] *= to;
       }
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      if ((lane & 3) == 0) kw[t] = s * kappa * F1 * F2;
+      if ((lane & 3) == 0) dots[t] = s * (group == 0 ? qscale : kappa) * F1 * F2;
     }
+  } else {
     float rs[2] = {0.0f, 0.0f}, cs[8][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i][0] = cs[i][1] = 0.0f;
-    // pass 0: q_t.k_s with dO E^T -> dP'; pass 1: k_t.k_s with R E^T -> dL'
+    // pass 0: q_t.k_s with dO E^T -> dP'; pass 1: k_t.k_s with R E^T -> dL'.  By 16 columns s, so
+    // that few registers hold the products.
 #pragma unroll
     for (int ps = 0; ps < (DELTA ? 2 : 1); ++ps) {
-      float x[8][4];
+      const uint32_t left = ps ? sk : sq;
+      const float to = (ps ? kappa : qscale) * kappa;
+      __half *out = reinterpret_cast<__half *>(smem + l.x) + ps * 2 * kChunk * kChunk;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int np = 0; np < 4; ++np) {
+        if (np <= w4) {
+          float x[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-      const __half *left = ps ? sk : sq;
+          for (int j = 0; j < 4; ++j) x[0][j] = x[1][j] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t a[NP][4], b4[4];
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t a[NP][4], b4[4];
 #pragma unroll
-        for (int c = 0; c < NP; ++c) a_rows(a[c], left + c * kChunk * LD, LD, m0, ks * 16, lane);
+            for (int c = 0; c < NP; ++c) ld.a_rows(a[c], left + c * TILE, m0, ks * 16);
+            ld.b_rows(b4, sk, np * 16, ks * 16);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-          if (np <= w4) {
-            b_rows(b4, sk, LD, np * 16, ks * 16, lane);
-#pragma unroll
-            for (int c = 0; c < NP; ++c) mma2(x[2 * np], x[2 * np + 1], a[c], b4);
+            for (int c = 0; c < NP; ++c) mma2(x[0], x[1], a[c], b4);
             if (NP == 2) {
-              b_rows(b4, sk + kChunk * LD, LD, np * 16, ks * 16, lane);
-              mma2(x[2 * np], x[2 * np + 1], a[0], b4);
+              ld.b_rows(b4, sk + TILE, np * 16, ks * 16);
+              mma2(x[0], x[1], a[0], b4);
             }
           }
-      }
-      const float by = (ps ? kappa : qscale) * kappa;
-      __half *out = sx + ps * 2 * kChunk * kLdC;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i / 2 <= w4) {
+          for (int e = 0; e < 2; ++e) {
+            const int i = 2 * np + e;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int t = m0 + g + 8 * h;
-            float y[2];
+            for (int h = 0; h < 2; ++h) {
+              const int t = m0 + g + 8 * h;
+              float y[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int s = 8 * i + t2 + j;
-              const bool in = ps ? s < t : s <= t;
-              const float dec = in ? expf((float)(G[t] - G[s])) : 0.0f;
-              const float z = in ? (ps ? -acc2[8 + i][2 * h + j] : acc2[i][2 * h + j]) * dec : 0.0f;
-              const float m = z * (x[i][2 * h + j] * by);
-              y[j] = z * be[s] * unit;
-              if (in) {
-                rs[h] = fmaf(be[s], m, rs[h]);
-                cs[i][j] += m;
+              for (int j = 0; j < 2; ++j) {
+                const int s = 8 * i + t2 + j;
+                const bool in = ps ? s < t : s <= t;
+                const float dec = in ? expf((float)(G[t] - G[s])) : 0.0f;
+                const float z = in ? (ps ? -acc[8 + i][2 * h + j] : acc[i][2 * h + j]) * dec : 0.0f;
+                const float m = z * (x[e][2 * h + j] * to);
+                y[j] = z * be[s] * to_unit;
+                if (in) {
+                  rs[h] = fmaf(be[s], m, rs[h]);
+                  cs[i][j] += m;
+                }
               }
+              put_pair<kChunk>(out, kChunk * kChunk, m0 + 8 * h, 8 * i, y[0], y[1], lane);
             }
-            uint32_t hi, lo;
-            split2(y[0], y[1], hi, lo);
-            *reinterpret_cast<uint32_t *>(out + t * kLdC + 8 * i + t2) = hi;
-            *reinterpret_cast<uint32_t *>(out + kChunk * kLdC + t * kLdC + 8 * i + t2) = lo;
           }
         }
       }
@@ -1831,128 +1744,83 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 16);
         if (g == 0) colp[w4 * kChunk + 8 * i + t2 + j] = c * F1 * F2;
       }
-  }
-  __syncthreads();
-  const float out1 = F1 * kappa, out2 = F2 * iunit;      // what the sums of dQ and dK are held over
-  if (groupA) {
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks <= w4) {
-        uint32_t a[4][4], b4[4];
-#pragma unroll
-        for (int c = 0; c < (DELTA ? 4 : 2); ++c) a_rows(a[c], sx + c * kChunk * kLdC, kLdC, m0, ks * 16, lane);
-#pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b4, sk, LD, ks * 16, np * 16, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
-          mma2(acc[2 * np], acc[2 * np + 1], a[1], b4);
-          if (DELTA) {
-            mma2(acc2[2 * np], acc2[2 * np + 1], a[2], b4);
-            mma2(acc2[2 * np], acc2[2 * np + 1], a[3], b4);
-          }
-          if (NP == 2) {
-            b_cols(b4, sk + kChunk * LD, LD, ks * 16, np * 16, lane);
-            mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
-            if (DELTA) mma2(acc2[2 * np], acc2[2 * np + 1], a[2], b4);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = m0 + g + 8 * h;
-      const long long tok = token0 + t;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (t < n) {
-          const float x = acc[i][2 * h] * out1 * out2, y = acc[i][2 * h + 1] * out1 * out2;
-          if (p.parts) store_pair(p.dq, 0, (tok * p.H + head) * DK + 8 * i + t2, x, y);
-          else store_pair(p.dq, p.dtype, tok * p.q_stride + (long long)head * DK + 8 * i + t2, x, y);
-        }
-        if (DELTA)
-          *reinterpret_cast<float2 *>(reinterpret_cast<float *>(smem + l.stage) + t * LDX + 8 * i + t2) =
-              make_float2(acc2[i][2 * h], acc2[i][2 * h + 1]);
-      }
-    }
-  } else {
-    const float turn = qscale * ikappa;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks >= w4) {
-        uint32_t a[2][4], b4[4];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) a_cols(a[c], sx + c * kChunk * kLdC, kLdC, ks * 16, m0, lane);
-#pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          b_cols(b4, sq, LD, ks * 16, np * 16, lane);
-          mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
-          mma2(acc[2 * np], acc[2 * np + 1], a[1], b4);
-          if (NP == 2) {
-            b_cols(b4, sq + kChunk * LD, LD, ks * 16, np * 16, lane);
-            mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
-          }
-        }
-      }
-    }
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] *= turn;
-    if (DELTA)
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  }
+  __syncthreads();
+  {
+    // dP' K, dL' K: rows t, blocks s <= t; dP'^T Q, dL'^T K: rows s, blocks t >= s
+    const uint32_t left = sx + (group & 1 ? 2 * SQ : 0), right = group == 2 ? sq : sk;
+    if (DELTA || !(group & 1))
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        if (ks >= w4) {
+        if (group < 2 ? ks <= w4 : ks >= w4) {
           uint32_t a[2][4], b4[4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) a_cols(a[c], sx + (2 + c) * kChunk * kLdC, kLdC, ks * 16, m0, lane);
+          for (int c = 0; c < 2; ++c) {
+            if (group < 2) lc.a_rows(a[c], left + c * SQ, m0, ks * 16);
+            else lc.a_cols(a[c], left + c * SQ, ks * 16, m0);
+          }
 #pragma unroll
           for (int np = 0; np < DK / 16; ++np) {
-            b_cols(b4, sk, LD, ks * 16, np * 16, lane);
+            ld.b_cols(b4, right, ks * 16, np * 16);
             mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
             mma2(acc[2 * np], acc[2 * np + 1], a[1], b4);
             if (NP == 2) {
-              b_cols(b4, sk + kChunk * LD, LD, ks * 16, np * 16, lane);
+              ld.b_cols(b4, right + TILE, ks * 16, np * 16);
               mma2(acc[2 * np], acc[2 * np + 1], a[0], b4);
             }
           }
         }
       }
   }
-  __syncthreads();
-  if (!groupA) {
+  const float outs = out1 * (group == 2 ? qscale : kappa);
+  float4 *hand = reinterpret_cast<float4 *>(smem + l.stage);             // [2][4 warps][NT][32]
+  if (DELTA && (group & 1))
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = m0 + g + 8 * h;
-      const long long tok = token0 + t;
-      if (t < n)
+    for (int i = 0; i < NT; ++i)
+      hand[(((group >> 1) * 4 + w4) * NT + i) * 32 + lane] =
+          make_float4(acc[i][0] * outs * out2, acc[i][1] * outs * out2, acc[i][2] * outs * out2, acc[i][3] * outs * out2);
+  if (DELTA) __syncthreads();
+  if (group == 0 || group == 2) {
+    void *dst = group == 0 ? p.dq : p.dk;
+    const long long stride = group == 0 ? p.q_stride : p.k_stride;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          float2 x = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
-          if (DELTA) {
-            const float2 y = *reinterpret_cast<const float2 *>(
-                reinterpret_cast<const float *>(smem + l.stage) + t * LDX + 8 * i + t2);
-            x.x = __fadd_rn(x.x, y.x);
-            x.y = __fadd_rn(x.y, y.y);
-          }
-          x.x = x.x * out1 * out2;
-          x.y = x.y * out1 * out2;
-          if (p.parts) store_pair(p.dk, 0, (tok * p.H + head) * DK + 8 * i + t2, x.x, x.y);
-          else store_pair(p.dk, p.dtype, tok * p.k_stride + (long long)head * DK + 8 * i + t2, x.x, x.y);
+    for (int i = 0; i < NT; ++i) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = acc[i][j] * outs * out2;
+      if (DELTA && group == 2) {
+        const float4 y = hand[(w4 * NT + i) * 32 + lane], z = hand[((4 + w4) * NT + i) * 32 + lane];
+        x[0] += y.x + z.x; x[1] += y.y + z.y; x[2] += y.z + z.z; x[3] += y.w + z.w;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = m0 + g + 8 * h;
+        const long long tok = token0 + t;
+        if (t < n) {
+          if (p.parts) store_pair(dst, 0, (tok * p.H + head) * DK + 8 * i + t2, x[2 * h], x[2 * h + 1]);
+          else store_pair(dst, p.dtype, tok * stride + (long long)head * DK + 8 * i + t2, x[2 * h], x[2 * h + 1]);
         }
+      }
     }
-  } else if (warp == 0) {
+  }
+  if (warp == 4) {
     // gates: two tokens a lane, sums over t >= r from the chunk's end
     float dsum = 0.0f;
     for (int i = 0; i < kGradThreads / 32; ++i) dsum += red[i];
-    dsum = dsum * F1 * F2;
+    dsum = dsum * pow2(topDS / 2) * pow2(topDS - topDS / 2);
     double dG[2], tot = 0.0;
-    float db2[2];
+    float db[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
+      // (a token's columns are summed by the warps whose rows reach it)
       const float c = (colp[t] + colp[kChunk + t]) + (colp[2 * kChunk + t] + colp[3 * kChunk + t]);
-      db2[i] = fmaf(eC[t], kw[t], c);
-      dG[i] = (double)rowv[t] - (double)be[t] * db2[i] + aq[t];
+      db[i] = fmaf(eC[t], kw[t], c);
+      dG[i] = (double)rowv[t] - (double)be[t] * db[i] + (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
       tot += (double)w[t] * kw[t];
     }
 #pragma unroll
@@ -1970,7 +1838,7 @@ __global__ void __launch_bounds__(kGradThreads) scan_grads_kernel(const ScanPara
       if (t < n) {
         const long long at = (token0 + t) * p.H + head;
         p.dlog_alpha[at] = (float)out[i];
-        p.dbeta[at] = db2[i];
+        p.dbeta[at] = db[i];
       }
     }
   }
@@ -2106,10 +1974,11 @@ using ScanFn = void (*)(ScanParams);
 // kernels of one key width
 struct ScanKernels {
   ScanFn prep[2][2][2];                // [np - 1][delta][backward]
-  ScanFn chain[2][2][2][2];            // [np - 1][delta][save][nh - 1]
-  ScanFn reverse[2][2][2];             // [np - 1][delta][nh - 1]
+  ScanFn walk[2][2][3];                // [np - 1][delta][WalkKind]
   ScanFn grads[2][2];
 };
+// Warps that share a block's state: half a 16-column state has no whole k-step.
+constexpr int state_warps(int dk) { return dk >= 32 ? 2 : 1; }
 
 }  // namespace scan
 }  // namespace lores
