@@ -231,10 +231,10 @@ cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t s
   const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
   p.rb = walk_blocks(s);
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
-  p.stages = 2 * l.bytes + p.rb * l.tail <= kMaxShared ? 2 : 1;
+  p.stages = 2 * l.bytes + p.rb * l.tail + 32 <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],
                 dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * (p.rb * (nh + kSideWarps) + kLoadWarps),
-                p.stages * l.bytes + p.rb * l.tail, st, c.device, p, raised[wi][s.np - 1][c.delta][kind]);
+                p.stages * l.bytes + p.rb * l.tail + 32, st, c.device, p, raised[wi][s.np - 1][c.delta][kind]);
 }
 
 cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
@@ -375,6 +375,7 @@ lores_status lores_scan_check_errors(const lores_scan_config *cfg, const void *w
   cudaError_t e = cudaMemcpyAsync(&f, workspace, sizeof f, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_status(e);
+  if (f & kFlagWait) return LORES_ERR_TIMEOUT;
   return f ? LORES_ERR_INVALID_ARG : LORES_OK;
 }
 

@@ -37,6 +37,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "lores_device.cuh"
+
 namespace lores {
 namespace scan {
 
@@ -44,6 +46,7 @@ constexpr int kChunk = 64;
 constexpr int kPrepThreads = 128;
 constexpr int kGradThreads = 512;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
+constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran out
 
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
@@ -306,16 +309,6 @@ __device__ __forceinline__ void copy_flat(uint8_t *dst, const void *src, int tid
   const uint8_t *s = static_cast<const uint8_t *>(src);
 #pragma unroll 8
   for (int i = tid; i < BYTES / 16; i += threads) cp16(dst + 16 * i, s + 16 * i, true);
-}
-// The tiles on and below the diagonal of a [64][64] plane, by blocks of 16 rows and columns (the others are
-// not read).
-__device__ __forceinline__ void copy_lower(uint8_t *dst, const __half *src, int tid, int threads) {
-  const uint8_t *s = reinterpret_cast<const uint8_t *>(src);
-#pragma unroll 2
-  for (int i = tid; i < kChunk * kChunk / 8; i += threads) {
-    const int tile = i >> 3;
-    if (((tile & 7) >> 1) <= (tile >> 4)) cp16(dst + 16 * i, s + 16 * i, true);
-  }
 }
 // `cols` columns (a multiple of 16) of 64 token rows of the caller's tensor: rows >= n and
 // columns >= have (a multiple of 4) are zeros.  ld in elements.
@@ -851,7 +844,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
-// Two more warps fetch the next chunk's tiles meanwhile (two stages where they fit).  In the
+// Two more warps fetch the next chunk's tiles meanwhile (two stages where they fit): bulk copies, since 16-byte
+// cp.async of the same 96 KB took longer than the chunk's arithmetic.  In the
 // backward pass's recomputation (SAVE) the planes of S0 and E are kept instead of o.
 // scan_reverse has the same roles: D for S, R for E, dO^T Z for Tm V, and the side warps also
 // form D's sum over dO^T Q before X.
@@ -1027,34 +1021,38 @@ __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row
       put_pair<kChunk>(dst, plane, row0 + 8 * h, 8 * (tile0 + i), x[i][2 * h] * by, x[i][2 * h + 1] * by, lane);
 }
 
-// A chunk's tiles.  KIND as above; `tokens` is V or dO.
+// Bytes that walk_fetch brings by bulk copies.
+__host__ __device__ constexpr unsigned walk_bulk_bytes(int dk, int np, bool delta, int kind) {
+  const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
+  return 3 * kChunk * 4 + 16 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
+         (kind != kRecompute ? np * tile : 0) + (kind == kForward ? np * sq : 0);
+}
+// A chunk's tiles.  The matrices come as bulk copies that one thread issues and that complete on `bar`, the
+// rows of V (or dO) as 8- or 16-byte pieces.
 template <int DK, int NP, bool DELTA, int KIND>
-__device__ __forceinline__ void walk_fetch(const ScanParams &p, uint8_t *st, const WalkLayout &l, long long token0, int n,
-                                           int slot, int head, int row0, int tid) {
+__device__ __forceinline__ void walk_fetch(const ScanParams &p, uint8_t *st, uint64_t *bar, const WalkLayout &l,
+                                           long long token0, int n, int slot, int head, int row0, int tid) {
   constexpr int SIZE = NP == 2 ? 4 : 2, threads = 32 * kLoadWarps;
-  constexpr int TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
-  const long long rec = (long long)slot * p.H + head;
-  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+  constexpr unsigned TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
+  if (tid == 0) {
+    const long long rec = (long long)slot * p.H + head;
+    const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+    const float *gates = p.gates + rec * kGateFloats;
+    mbar_expect_tx(bar, walk_bulk_bytes(DK, NP, DELTA, KIND));
+    bulk_g2s(st + l.gates, gates, 3 * kChunk * 4, bar);
+    bulk_g2s(st + l.gates + 3 * kChunk * 4, gates + kGateScales, 16, bar);
+    if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
+    if (DELTA || KIND == kReverse)
+      bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk), 2 * SQ, bar);
+    bulk_g2s(st + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+    if (KIND != kRecompute) bulk_g2s(st + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+    if (KIND == kForward) bulk_g2s(st + l.pp, p.pp + rec * (2 * kChunk * kChunk), NP * SQ, bar);
+  }
   const void *tokens = KIND == kReverse ? p.o : p.v;
   const long long stride = KIND == kReverse ? p.o_stride : p.v_stride;
   copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
                     static_cast<const uint8_t *>(tokens) + (token0 * stride + (long long)head * p.d_v + row0) * SIZE,
                     stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, KIND == kReverse ? p.o16 : p.v16, tid, threads);
-  const float *gates = p.gates + rec * kGateFloats;
-  if (tid < 3 * kChunk / 4 + 1)
-    cp16(st + l.gates + 16 * tid, tid < 3 * kChunk / 4 ? gates + 4 * tid : gates + kGateScales, true);
-  if (DELTA) copy_flat<2 * TILE>(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), tid, threads);
-  if (DELTA || KIND == kReverse) {
-    const __half *m = (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk);
-    copy_lower(st + l.tm, m, tid, threads);
-    copy_lower(st + l.tm + SQ, m + kChunk * kChunk, tid, threads);
-  }
-  copy_flat<NP * TILE>(st + l.k, p.khat + qrec * (NP * kChunk * DK), tid, threads);
-  if (KIND != kRecompute) copy_flat<NP * TILE>(st + l.q, p.qhat + qrec * (NP * kChunk * DK), tid, threads);
-  if (KIND == kForward)
-#pragma unroll
-    for (int c = 0; c < NP; ++c)
-      copy_lower(st + l.pp + c * SQ, p.pp + (rec * 2 + c) * (kChunk * kChunk), tid, threads);
   cp_commit();
 }
 
@@ -1085,8 +1083,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
   float4 *last = reinterpret_cast<float4 *>(tail + l.last), *plus = reinterpret_cast<float4 *>(tail + l.plus);
   uint4 *planes = reinterpret_cast<uint4 *>(tail + l.planes);
   unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);       // [0..1] state, [2..3] V or dO
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
+  int *stop = reinterpret_cast<int *>(bars + 2);
   const Lane<DK> ld(lane);
   const Lane<kChunk> lc(lane);
+  if (tid == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    *stop = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
 
   float S[NTH][4];
   if (live && !side) {
@@ -1099,14 +1106,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
   }
   auto stage_of = [&](int c) { return smem + (p.stages == 2 ? (c & 1) * l.bytes : 0); };
   auto fetch = [&](int c) {
-    walk_fetch<DK, NP, DELTA, KIND>(p, stage_of(c), l, start + (long long)c * kChunk, min(kChunk, len - c * kChunk),
+    walk_fetch<DK, NP, DELTA, KIND>(p, stage_of(c), bars + (p.stages == 2 ? c & 1 : 0), l, start + (long long)c * kChunk, min(kChunk, len - c * kChunk),
                                     base + c, head, row0, tid - 32 * p.rb * (NH + kSideWarps));
   };
   if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0);
   for (int i0 = 0; i0 < chunks; ++i0) {
     const int c = REV ? chunks - 1 - i0 : i0, next = REV ? c - 1 : c + 1;
-    if (loader) cp_wait<0>();
+    if (loader) {
+      cp_wait<0>();
+      // the stage's copies; a wait that runs out ends the walk for the whole CTA
+      const int use = p.stages == 2 ? i0 >> 1 : i0;
+      if (tid == 32 * p.rb * (NH + kSideWarps) &&
+          !mbar_wait_bounded(bars + (p.stages == 2 ? c & 1 : 0), use & 1, kWaitNs)) {
+        *stop = 1;
+        atomicOr(p.flag, kFlagWait);
+      }
+    }
     __syncthreads();
+    if (*stop) return;
     if (p.stages == 2 && loader && i0 + 1 < chunks) fetch(next);
     uint8_t *st = stage_of(c);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
@@ -1128,7 +1145,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
       __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
 #pragma unroll
       for (int ks = 0; ks < DKH / 16; ++ks) {
-        uint32_t ah[4], al[4], b[4];
+        uint32_t ah[4], al[4];
         split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
         if (KIND == kForward) {
           planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
@@ -1142,16 +1159,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
           }
         }
         if (DELTA || REV) {
-          const uint32_t x = DELTA ? kt : sk;      // (reverse without the delta rule: Kb = diag(w) K)
+          // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
+          // instructions apart, which covers the tensor cores' latency.
+          const uint32_t x = DELTA ? kt : sk;
+          uint32_t r[4][4];
 #pragma unroll
-          for (int np = 0; np < 4; ++np) {
-            ld.b_rows(b, x, np * 16, c0 + ks * 16);
-            mma2(E[2 * np], E[2 * np + 1], ah, b);
-            mma2(E[2 * np], E[2 * np + 1], al, b);
-            if (DELTA || NP == 2) {
-              ld.b_rows(b, x + TILE, np * 16, c0 + ks * 16);
-              mma2(E[2 * np], E[2 * np + 1], ah, b);
-            }
+          for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x, np * 16, c0 + ks * 16);
+#pragma unroll
+          for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
+#pragma unroll
+          for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], al, r[np]);
+          if (DELTA || NP == 2) {
+#pragma unroll
+            for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x + TILE, np * 16, c0 + ks * 16);
+#pragma unroll
+            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
           }
         }
       }
@@ -1204,34 +1226,42 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
             const float by = REV ? -invE : invE;
             split2(e[0] * (f.x * by), e[1] * (f.y * by), wh[ks][q], wl[ks][q]);
           }
+constexpr int STEP = NTH >= 8 ? 4 : NTH / 2;         // column pairs at a time
 #pragma unroll
-      for (int np = 0; np < NTH / 2; ++np) {
-        float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+      for (int n0 = 0; n0 < NTH / 2; n0 += STEP) {
+        float a[2 * STEP][4];
+#pragma unroll
+        for (int i = 0; i < 2 * STEP; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
         if (!REV || DELTA)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            uint32_t b[4];
-            ld.b_cols(b, sk, ks * 16, c0 + np * 16);
-            mma2(a0, a1, wh[ks], b);
-            mma2(a0, a1, wl[ks], b);
+            uint32_t r[STEP][4];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk, ks * 16, c0 + (n0 + i) * 16);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wl[ks], r[i]);
             if (NP == 2) {
-              ld.b_cols(b, sk + TILE, ks * 16, c0 + np * 16);
-              mma2(a0, a1, wh[ks], b);
+#pragma unroll
+              for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk + TILE, ks * 16, c0 + (n0 + i) * 16);
+#pragma unroll
+              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
             }
           }
-        if (REV) {
-          const float4 x = plus[(c0 / 8 + 2 * np) * 32 + lane], y = plus[(c0 / 8 + 2 * np + 1) * 32 + lane];
-          const float px[4] = {x.x, x.y, x.z, x.w}, py[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            S[2 * np][j] = fmaf(S[2 * np][j], eC, fmaf(a0[j], scaleE, px[j]));
-            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, fmaf(a1[j], scaleE, py[j]));
-          }
-        } else {
+        for (int i = 0; i < 2 * STEP; ++i) {
+          float *x = S[2 * n0 + i];
+          if (REV) {
+            const float4 y = plus[(c0 / 8 + 2 * n0 + i) * 32 + lane];
+            const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            S[2 * np][j] = fmaf(S[2 * np][j], eC, a0[j] * scaleE);
-            S[2 * np + 1][j] = fmaf(S[2 * np + 1][j], eC, a1[j] * scaleE);
+            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleE, z[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleE);
           }
         }
       }
@@ -1262,12 +1292,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
 #pragma unroll
           for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * invV, x[ks][2 * q + 1] * invV, vh[q], vl[q]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int np = 2 * h + i;
-            if (REV ? np <= ks : ks <= np) {
-              uint32_t b[4];
+          for (int c2 = 0; c2 < 2; ++c2) {
 #pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2) {
+            for (int i = 0; i < 2; ++i) {
+              const int np = 2 * h + i;
+              if (REV ? np <= ks : ks <= np) {
+                uint32_t b[4];
                 if (REV) lc.b_cols(b, tm + c2 * SQ, ks * 16, np * 16);
                 else lc.b_rows(b, tm + c2 * SQ, np * 16, ks * 16);
                 mma2(U[2 * i], U[2 * i + 1], vh, b);
@@ -1301,25 +1331,35 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
             const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
             split2(x[ks][2 * q] * (invV * f.x), x[ks][2 * q + 1] * (invV * f.y), oh[ks][q], ol[ks][q]);
           }
-        constexpr int HALF = DK >= 32 ? DK / 2 : DK;
+        constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
         if (DK >= 32 || h == 0)
 #pragma unroll
-          for (int np = 0; np < HALF / 16; ++np) {
-            const int n0 = (DK >= 32 ? h * HALF : 0) + np * 16;
-            float a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0};
+          for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
+            const int col = (DK >= 32 ? h * HALF : 0) + n0;
+            float a[2 * QS][4];
+#pragma unroll
+            for (int i = 0; i < 2 * QS; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              uint32_t b[4];
-              ld.b_cols(b, sq, ks * 16, n0);
-              mma2(a0, a1, oh[ks], b);
-              mma2(a0, a1, ol[ks], b);
+              uint32_t r[QS][4];
+#pragma unroll
+              for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq, ks * 16, col + 16 * i);
+#pragma unroll
+              for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
+#pragma unroll
+              for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[i]);
               if (NP == 2) {
-                ld.b_cols(b, sq + TILE, ks * 16, n0);
-                mma2(a0, a1, oh[ks], b);
+#pragma unroll
+                for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq + TILE, ks * 16, col + 16 * i);
+#pragma unroll
+                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
               }
             }
-            plus[(n0 / 8) * 32 + lane] = make_float4(a0[0] * scaleV, a0[1] * scaleV, a0[2] * scaleV, a0[3] * scaleV);
-            plus[(n0 / 8 + 1) * 32 + lane] = make_float4(a1[0] * scaleV, a1[1] * scaleV, a1[2] * scaleV, a1[3] * scaleV);
+#pragma unroll
+            for (int i = 0; i < 2 * QS; ++i)
+              plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
           }
       }
       barrier_sync(1 + 2 * blk, PER);                                   // X
