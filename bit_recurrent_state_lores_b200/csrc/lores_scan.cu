@@ -233,7 +233,7 @@ cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t s
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
   p.stages = 2 * l.bytes + p.rb * l.tail + 32 <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],
-                dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * (p.rb * (nh + kSideWarps) + kLoadWarps),
+                dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * p.rb * (nh + kSideWarps + 1),
                 p.stages * l.bytes + p.rb * l.tail + 32, st, c.device, p, raised[wi][s.np - 1][c.delta][kind]);
 }
 

@@ -844,13 +844,15 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
-// Two more warps fetch the next chunk's tiles meanwhile (two stages where they fit): bulk copies, since 16-byte
-// cp.async of the same 96 KB took longer than the chunk's arithmetic.  In the
-// backward pass's recomputation (SAVE) the planes of S0 and E are kept instead of o.
-// scan_reverse has the same roles: D for S, R for E, dO^T Z for Tm V, and the side warps also
-// form D's sum over dO^T Q before X.
-constexpr int kSideWarps = 2, kLoadWarps = 2;
+// A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit): bulk copies,
+// since 16-byte cp.async of the same 96 KB took longer than the chunk's arithmetic; and it turns
+// the block's rows of V into fp16 over their scale.  In the backward pass's recomputation (SAVE)
+// the planes of S0 and E are kept instead of o.
+// The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
+// form D's sum over dO^T Q, which the state warps take last (barrier Z).
+constexpr int kSideWarps = 2;
 constexpr int kMaxBlocks = 2;          // blocks of value rows per CTA
+constexpr int kLoadWarps = kMaxBlocks;
 constexpr int kWalkThreads = 32 * (kMaxBlocks * (2 + kSideWarps) + kLoadWarps);
 
 enum WalkKind { kForward, kRecompute, kReverse };
@@ -859,9 +861,9 @@ struct WalkLayout {
   int kt, k, q, tm, pp, v, gates, bytes;         // byte offsets inside one stage
   int part, side, plus, last, planes, tops, tail;   // behind the stages, one record per block of rows
 };
-// elements of a token row of the V (or dO) tile (16-bit rows unpadded: two stages just fit, and the
-// tile is read four times a chunk)
-__host__ __device__ constexpr int tile_ld(int np, int rb) { return 16 * rb + (np == 2 ? 4 : 0); }
+// A block's 64 token rows of V (or dO): as they come, then as fp16 planes in tiles, then (output) again as
+// they go.
+__host__ __device__ constexpr int tile_bytes(int np) { return kChunk * 16 * 2 * np; }
 
 __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh, bool delta, int kind) {
   const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
@@ -872,16 +874,16 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   l.q = at; at += kind != kRecompute ? np * tile : 0;
   l.tm = at; at += kind == kReverse || delta ? 2 * sq : 0;     // Tm or Z
   l.pp = at; at += kind == kForward ? np * sq : 0;
-  l.v = at; at += kChunk * tile_ld(np, rb) * (np == 2 ? 4 : 2);
+  l.v = at; at += rb * tile_bytes(np);
   l.gates = at; at += 3 * kChunk * 4 + 16;
   l.bytes = (at + 15) / 16 * 16;
   at = 0;
-  l.part = at; at += nh > 1 ? nh * 4096 : 0;                   // the state warps' parts of E or R
-  l.side = at; at += 4096;                                     // Tm V or dO^T Z
+  l.part = at; at += nh > 1 && (delta || kind == kReverse) ? nh * 4096 : 0;   // the state warps' parts of E or R
+  l.side = at; at += delta || kind == kReverse ? 4096 : 0;     // Tm V or dO^T Z
   l.last = at; at += 4096;                                     // E or R, for the side warps
   l.plus = at; at += kind == kReverse ? 16 * dk * 4 : 0;       // dO^T Q
   l.planes = at; at += kind == kForward ? np * 16 * dk * 2 : 0;   // S0 as left operands
-  l.tops = at; at += 32;                                       // largest entries: state parts, V halves
+  l.tops = at; at += 32;                                       // largest entries: see below
   l.tail = at;
   return l;
 }
@@ -922,44 +924,85 @@ __device__ __forceinline__ unsigned max_bits(const float (&x)[N][M]) {
   return __reduce_max_sync(0xFFFFFFFFu, m);
 }
 
-// The tile of V (or dO) as left operands V^T: x[ks][2 q], x[ks][2 q + 1] are the two entries of
-// register q of k-step ks (tokens 16 ks ..) as fp32 values of the caller's type.
+// A warp's 64 rows of 16 columns of the caller's tensor (columns >= have, a multiple of 4, and rows >= n are zeros).
 template <int NP>
-__device__ __forceinline__ void load_tokens(float (&x)[4][8], const uint8_t *tile, int ld, int col0, int dtype,
-                                            int lane) {
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
+__device__ __forceinline__ void fetch_rows(uint8_t *dst, const void *src, long long stride, long long token0, int col, int n,
+                                           int have, bool by16, int lane) {
+  constexpr int SIZE = NP == 2 ? 4 : 2;
+  const uint8_t *s = static_cast<const uint8_t *>(src) + (token0 * stride + col) * SIZE;
+  if (by16) {
+    constexpr int PER = SIZE;              // 16-byte pieces of a row
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    if (NP == 1) {
-      uint32_t a[4];
-      a_cols_plain(a, smem_addr(tile), ld, ks * 16, col0, lane);
+    for (int i = 0; i < kChunk * PER / 32; ++i) {
+      const int e = i * 32 + lane, r = e / PER, c = e % PER * (16 / SIZE);
+      const bool in = r < n && c < have;
+      cp16(dst + e * 16, in ? s + (r * stride + c) * SIZE : s, in);
+    }
+  } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = pair_of(a[q], dtype);
-        x[ks][2 * q] = f.x;
-        x[ks][2 * q + 1] = f.y;
-      }
-    } else {
-      const float *f = reinterpret_cast<const float *>(tile);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          x[ks][2 * q + e] = f[(ks * 16 + 8 * (q >> 1) + t2 + e) * ld + col0 + g + 8 * (q & 1)];
+    for (int i = 0; i < kChunk * 4 / 32; ++i) {
+      const int e = i * 32 + lane, r = e / 4, c = e % 4 * 4;
+      const bool in = r < n && c < have;
+      cp8(dst + e * 8, in ? s + (r * stride + c) * SIZE : s, in);
     }
   }
 }
+// ... turned in place into fp16 planes [64][16] (in tiles) over their scale; returns the bits of the largest magnitude.
+template <int NP>
+__device__ __forceinline__ unsigned convert_rows(uint8_t *tile, int dtype, int lane) {
+  float x[2][16];                          // rows lane and lane + 32
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t *row = tile + (lane + 32 * h) * (16 * 2 * NP);
+    if (NP == 1) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(row + 16 * c);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = pair_of(u[e], dtype);
+          x[h][8 * c + 2 * e] = f.x;
+          x[h][8 * c + 2 * e + 1] = f.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 f = *reinterpret_cast<const float4 *>(row + 16 * c);
+        x[h][4 * c] = f.x; x[h][4 * c + 1] = f.y; x[h][4 * c + 2] = f.z; x[h][4 * c + 3] = f.w;
+      }
+    }
+  }
+  const unsigned m = max_bits(x);          // (also: every lane has read its rows)
+  float inv;
+  scale_of(m, 6, inv);
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float *y = x[h] + 8 * c;
+      uint4 hi, lo;
+      split2(y[0] * inv, y[1] * inv, hi.x, lo.x);
+      split2(y[2] * inv, y[3] * inv, hi.y, lo.y);
+      split2(y[4] * inv, y[5] * inv, hi.z, lo.z);
+      split2(y[6] * inv, y[7] * inv, hi.w, lo.w);
+      const int at = 2 * tiled<16>(lane + 32 * h, 8 * c);
+      *reinterpret_cast<uint4 *>(tile + at) = hi;
+      if (NP == 2) *reinterpret_cast<uint4 *>(tile + kChunk * 16 * 2 + at) = lo;
+    }
+  return m;
+}
 
 // Writes 4 tiles (tokens 8 (tile0 + i) .., 16 value rows) times `by` to token rows of the
-// caller's tensor, through the warp's part of the V tile so that rows leave in 16-byte
-// pieces.
+// caller's tensor, through the block's tile so that rows leave in 16-byte pieces.
 template <int NP>
-__device__ __forceinline__ void store_tokens(const float (&O)[4][4], float by, uint8_t *tile, int ld, int col0, int tile0,
-                                             void *dst, int dtype, long long stride, long long token0, int n, int col,
-                                             int have, bool by16, int lane) {
+__device__ __forceinline__ void store_tokens(const float (&O)[4][4], float by, uint8_t *tile, int tile0, void *dst, int dtype,
+                                             long long stride, long long token0, int n, int col, int have, bool by16,
+                                             int lane) {
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   if (NP == 1) {
-    uint16_t *sm = reinterpret_cast<uint16_t *>(tile);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t r[4];
@@ -968,14 +1011,14 @@ __device__ __forceinline__ void store_tokens(const float (&O)[4][4], float by, u
       r[2] = pack_as(dtype, O[2 * i + 1][0] * by, O[2 * i + 1][1] * by);
       r[3] = pack_as(dtype, O[2 * i + 1][2] * by, O[2 * i + 1][3] * by);
       const int tok = 8 * (tile0 + 2 * i + (lane >> 4)) + (lane & 7);
-      stsm4t(smem_addr(sm + tok * ld + col0 + 8 * ((lane >> 3) & 1)), r);
+      stsm4t(smem_addr(tile + tok * 32 + 16 * ((lane >> 3) & 1)), r);
     }
     __syncwarp();
     uint16_t *out = static_cast<uint16_t *>(dst);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 1), c = (e & 1) * 8;
-      const uint4 x = *reinterpret_cast<const uint4 *>(sm + tok * ld + col0 + c);
+      const uint4 x = *reinterpret_cast<const uint4 *>(tile + tok * 32 + 2 * c);
       if (tok < n) {
         uint16_t *to = out + (token0 + tok) * stride + col + c;
         if (by16) {
@@ -991,14 +1034,13 @@ __device__ __forceinline__ void store_tokens(const float (&O)[4][4], float by, u
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sm[(8 * (tile0 + i) + t2 + (j & 1)) * ld + col0 + g + 8 * (j >> 1)] = O[i][j] * by;
+      for (int j = 0; j < 4; ++j) sm[(8 * (tile0 + i) + t2 + (j & 1)) * 16 + g + 8 * (j >> 1)] = O[i][j] * by;
     __syncwarp();
     float *out = static_cast<float *>(dst);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = i * 32 + lane, tok = 8 * tile0 + (e >> 2), c = (e & 3) * 4;
-      const float4 x = *reinterpret_cast<const float4 *>(sm + tok * ld + col0 + c);
+      const float4 x = *reinterpret_cast<const float4 *>(sm + tok * 16 + c);
       if (tok < n && c < have) *reinterpret_cast<float4 *>(out + (token0 + tok) * stride + col + c) = x;
     }
   }
@@ -1021,72 +1063,67 @@ __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row
       put_pair<kChunk>(dst, plane, row0 + 8 * h, 8 * (tile0 + i), x[i][2 * h] * by, x[i][2 * h + 1] * by, lane);
 }
 
-// Bytes that walk_fetch brings by bulk copies.
+// Bytes of a chunk's bulk copies.
 __host__ __device__ constexpr unsigned walk_bulk_bytes(int dk, int np, bool delta, int kind) {
   const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
   return 3 * kChunk * 4 + 16 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
          (kind != kRecompute ? np * tile : 0) + (kind == kForward ? np * sq : 0);
 }
-// A chunk's tiles.  The matrices come as bulk copies that one thread issues and that complete on `bar`, the
-// rows of V (or dO) as 8- or 16-byte pieces.
+// The chunk's matrices: one thread issues them, they complete on `bar`.
 template <int DK, int NP, bool DELTA, int KIND>
-__device__ __forceinline__ void walk_fetch(const ScanParams &p, uint8_t *st, uint64_t *bar, const WalkLayout &l,
-                                           long long token0, int n, int slot, int head, int row0, int tid) {
-  constexpr int SIZE = NP == 2 ? 4 : 2, threads = 32 * kLoadWarps;
+__device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st, uint64_t *bar, const WalkLayout &l, int slot,
+                                               int head) {
   constexpr unsigned TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
-  if (tid == 0) {
-    const long long rec = (long long)slot * p.H + head;
-    const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
-    const float *gates = p.gates + rec * kGateFloats;
-    mbar_expect_tx(bar, walk_bulk_bytes(DK, NP, DELTA, KIND));
-    bulk_g2s(st + l.gates, gates, 3 * kChunk * 4, bar);
-    bulk_g2s(st + l.gates + 3 * kChunk * 4, gates + kGateScales, 16, bar);
-    if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
-    if (DELTA || KIND == kReverse)
-      bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk), 2 * SQ, bar);
-    bulk_g2s(st + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
-    if (KIND != kRecompute) bulk_g2s(st + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
-    if (KIND == kForward) bulk_g2s(st + l.pp, p.pp + rec * (2 * kChunk * kChunk), NP * SQ, bar);
-  }
-  const void *tokens = KIND == kReverse ? p.o : p.v;
-  const long long stride = KIND == kReverse ? p.o_stride : p.v_stride;
-  copy_tokens<SIZE>(st + l.v, tile_ld(NP, p.rb),
-                    static_cast<const uint8_t *>(tokens) + (token0 * stride + (long long)head * p.d_v + row0) * SIZE,
-                    stride, min(16 * p.rb, p.dvp - row0), n, p.d_v - row0, KIND == kReverse ? p.o16 : p.v16, tid, threads);
-  cp_commit();
+  const long long rec = (long long)slot * p.H + head;
+  const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
+  const float *gates = p.gates + rec * kGateFloats;
+  mbar_expect_tx(bar, walk_bulk_bytes(DK, NP, DELTA, KIND));
+  bulk_g2s(st + l.gates, gates, 3 * kChunk * 4, bar);
+  bulk_g2s(st + l.gates + 3 * kChunk * 4, gates + kGateScales, 16, bar);
+  if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
+  if (DELTA || KIND == kReverse)
+    bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk), 2 * SQ, bar);
+  bulk_g2s(st + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+  if (KIND != kRecompute) bulk_g2s(st + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+  if (KIND == kForward) bulk_g2s(st + l.pp, p.pp + rec * (2 * kChunk * kChunk), NP * SQ, bar);
 }
 
 template <int DK, int NP, bool DELTA, int KIND, int NH>
 __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanParams p) {
   constexpr bool REV = KIND == kReverse;
+  constexpr bool JOIN = DELTA || REV;                        // E (or R) has parts in several warps
   constexpr int DKH = DK / NH, NTH = DKH / 8;
-  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
+  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2, VP = kChunk * 16 * 2;
   constexpr int PER = 32 * (NH + kSideWarps);                // threads of a block of rows
   static_assert(NH == 1 || NH == 2, "parts are exchanged between two warps at most");
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, row0 = blockIdx.y * 16 * p.rb;
   // state warps first, then side warps, then loaders
-  const bool loader = warp >= p.rb * (NH + kSideWarps), side = !loader && warp >= p.rb * NH;
-  const int blk = loader ? 0 : side ? (warp - p.rb * NH) / kSideWarps : warp / NH;
-  const int h = side ? (warp - p.rb * NH) % kSideWarps : NH == 1 ? 0 : warp % NH;
+  const int first_side = p.rb * NH, first_load = first_side + p.rb * kSideWarps;
+  const bool loader = warp >= first_load, side = !loader && warp >= first_side;
+  const int blk = loader ? warp - first_load : side ? (warp - first_side) / kSideWarps : warp / NH;
+  const int h = loader ? 0 : side ? (warp - first_side) % kSideWarps : NH == 1 ? 0 : warp % NH;
   const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, KIND);
-  const int ldv = tile_ld(NP, p.rb);
   long long start;
   int len;
   seq_range(p, seq, start, len);
   const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
   const int brow = row0 + blk * 16, r0 = brow + g, c0 = h * DKH;
-  const bool live = !loader && brow < p.dvp;
+  const bool live = brow < p.dvp;
   uint8_t *tail = smem + p.stages * l.bytes + blk * l.tail;
   float4 *part = reinterpret_cast<float4 *>(tail + l.part), *sided = reinterpret_cast<float4 *>(tail + l.side);
   float4 *last = reinterpret_cast<float4 *>(tail + l.last), *plus = reinterpret_cast<float4 *>(tail + l.plus);
   uint4 *planes = reinterpret_cast<uint4 *>(tail + l.planes);
-  unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);       // [0..1] state, [2..3] V or dO
+  // bits of the largest magnitudes: [2 (i & 1) + h] of the state warps' columns at the start of the i-th chunk,
+  // [4 + stage] of the rows of V or dO
+  unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
   const Lane<DK> ld(lane);
   const Lane<kChunk> lc(lane);
+  const Lane<16> lv(lane);
+  const int X = 1 + 3 * blk, Y = X + 1, Z = X + 2;
   if (tid == 0) {
     mbar_init(bars, 1);
     mbar_init(bars + 1, 1);
@@ -1096,348 +1133,386 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
   __syncthreads();
 
   float S[NTH][4];
-  if (live && !side) {
+  if (live && !side && !loader) {
     load_state<NTH>(S, REV ? p.d_state_out : p.state_in, blockIdx.x, p.d_v, DK, r0, c0 + t2);
     const unsigned top = max_bits(S);
     if (lane == 0) {
       tops[h] = top;
-      if (NH == 1) tops[1] = 0;
+      if (NH == 1) tops[1] = tops[3] = 0;
     }
   }
-  auto stage_of = [&](int c) { return smem + (p.stages == 2 ? (c & 1) * l.bytes : 0); };
+  const int by = p.stages == 2 ? 1 : 0;
+  auto stage_of = [&](int c) { return smem + (c & by) * l.bytes; };
   auto fetch = [&](int c) {
-    walk_fetch<DK, NP, DELTA, KIND>(p, stage_of(c), bars + (p.stages == 2 ? c & 1 : 0), l, start + (long long)c * kChunk, min(kChunk, len - c * kChunk),
-                                    base + c, head, row0, tid - 32 * p.rb * (NH + kSideWarps));
+    const long long token0 = start + (long long)c * kChunk;
+    if (blk == 0 && lane == 0) fetch_matrices<DK, NP, DELTA, KIND>(p, stage_of(c), bars + (c & by), l, base + c, head);
+    if (live)
+      fetch_rows<NP>(stage_of(c) + l.v + blk * tile_bytes(NP), REV ? p.o : p.v, REV ? p.o_stride : p.v_stride, token0,
+                     head * p.d_v + brow, min(kChunk, len - c * kChunk), p.d_v - brow, REV ? p.o16 : p.v16, lane);
+    cp_commit();
   };
   if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0);
   for (int i0 = 0; i0 < chunks; ++i0) {
     const int c = REV ? chunks - 1 - i0 : i0, next = REV ? c - 1 : c + 1;
+    uint8_t *st = stage_of(c);
+    uint8_t *tile = st + l.v + blk * tile_bytes(NP);
     if (loader) {
       cp_wait<0>();
+      __syncwarp();
+      if (live) {
+        const unsigned m = convert_rows<NP>(tile, p.dtype, lane);
+        if (lane == 0) tops[4 + (c & by)] = m;
+      }
       // the stage's copies; a wait that runs out ends the walk for the whole CTA
-      const int use = p.stages == 2 ? i0 >> 1 : i0;
-      if (tid == 32 * p.rb * (NH + kSideWarps) &&
-          !mbar_wait_bounded(bars + (p.stages == 2 ? c & 1 : 0), use & 1, kWaitNs)) {
+      if (blk == 0 && lane == 0 && !mbar_wait_bounded(bars + (c & by), (i0 >> by) & 1, kWaitNs)) {
         *stop = 1;
         atomicOr(p.flag, kFlagWait);
       }
     }
     __syncthreads();
     if (*stop) return;
-    if (p.stages == 2 && loader && i0 + 1 < chunks) fetch(next);
-    uint8_t *st = stage_of(c);
+    if (by && loader && i0 + 1 < chunks) fetch(next);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
-                   tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp);
+                   tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
     const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk;
     const float qscale = ek[kChunk + 1];
     const long long rec = (long long)(base + c) * p.H + head;
     const int n = min(kChunk, len - c * kChunk);
-    if (live && !side) {
-      // ---- state warp -------------------------------------------------------------------
-      const unsigned mS = max(tops[0], tops[1]);
-      float inv;
+    if (loader || !live) {
+    } else {
+      // scales: of the state, of V (or dO, which takes the scale of Q that Z and the planes of Q lack), of E (or R)
+      const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]);
+      unsigned mV = tops[4 + (c & by)];
+      float inv, invV, invE;
       const float scale = scale_of(mS, 6, inv);
-      float E[8][4];                   // 16 value rows x 64 tokens
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) E[i][j] = 0.0f;
-      __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
-#pragma unroll
-      for (int ks = 0; ks < DKH / 16; ++ks) {
-        uint32_t ah[4], al[4];
-        split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
-        if (KIND == kForward) {
-          planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-          if (NP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int at = tiled<DK>(brow + 8 * (q & 1), c0 + ks * 16 + 8 * (q >> 1)) + 2 * lane;
-            *reinterpret_cast<uint32_t *>(keep + at) = ah[q];
-            *reinterpret_cast<uint32_t *>(keep + (long long)p.dvp * DK + at) = al[q];
-          }
-        }
-        if (DELTA || REV) {
-          // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
-          // instructions apart, which covers the tensor cores' latency.
-          const uint32_t x = DELTA ? kt : sk;
-          uint32_t r[4][4];
-#pragma unroll
-          for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x, np * 16, c0 + ks * 16);
-#pragma unroll
-          for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
-#pragma unroll
-          for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], al, r[np]);
-          if (DELTA || NP == 2) {
-#pragma unroll
-            for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x + TILE, np * 16, c0 + ks * 16);
-#pragma unroll
-            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
-          }
-        }
+      float scaleV = scale_of(mV, 6, invV);
+      if (REV) {
+        scaleV *= qscale;
+        mV = abs_bits(__uint_as_float(mV) * qscale);
       }
-      if (KIND != kForward && lane == 0 && h == 0)
-        p.scales[REV ? kScaleD : kScaleS][rec * (p.dvp / 16) + brow / 16] = scale;
-      if (NH > 1 && (DELTA || REV))
+      const float scaleE = scale_of(max(mS, mV), 6, invE);
+      if (!side) {
+        // ---- state warp -----------------------------------------------------------------
+        float E[8][4];                   // 16 value rows x 64 tokens
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[(h * 8 + i) * 32 + lane] = f4(E[i]);
-      barrier_sync(1 + 2 * blk, PER);                                   // X
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 u = sided[i * 32 + lane];
-        if (DELTA || REV) {
-          if (NH > 1) {
-            const float4 y = part[((h ^ 1) * 8 + i) * 32 + lane];
-            E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
-          }
-          float x = scale, y = scale;
-          if (REV && !DELTA) {
-            const float2 f = *reinterpret_cast<const float2 *>(wk + 8 * i + t2);
-            x *= f.x;
-            y *= f.y;
-          }
-          E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
-          E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
-        } else {
-          E[i][0] = u.x; E[i][1] = u.y; E[i][2] = u.z; E[i][3] = u.w;
-        }
-      }
-      // E (or R) for the side warps: each state warp hands over half of the tokens
+          for (int j = 0; j < 4; ++j) E[i][j] = 0.0f;
+        __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
-      barrier_arrive(2 + 2 * blk, PER);                                 // Y
-      const unsigned mE = max(mS, max(tops[2], tops[3]));
-      float invE;
-      const float scaleE = scale_of(mE, 6, invE);
-      // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
-      // sum starts from zero and joins the state in one fma, so that the tensor cores'
-      // rounding does not pile up in it
-      const float eC = eG[kChunk - 1];
-      uint32_t wh[4][4], wl[4][4];
-      if (!REV || DELTA)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
-            const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-            const float by = REV ? -invE : invE;
-            split2(e[0] * (f.x * by), e[1] * (f.y * by), wh[ks][q], wl[ks][q]);
-          }
-constexpr int STEP = NTH >= 8 ? 4 : NTH / 2;         // column pairs at a time
-#pragma unroll
-      for (int n0 = 0; n0 < NTH / 2; n0 += STEP) {
-        float a[2 * STEP][4];
-#pragma unroll
-        for (int i = 0; i < 2 * STEP; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
-        if (!REV || DELTA)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t r[STEP][4];
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk, ks * 16, c0 + (n0 + i) * 16);
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wl[ks], r[i]);
-            if (NP == 2) {
-#pragma unroll
-              for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk + TILE, ks * 16, c0 + (n0 + i) * 16);
-#pragma unroll
-              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
-            }
-          }
-#pragma unroll
-        for (int i = 0; i < 2 * STEP; ++i) {
-          float *x = S[2 * n0 + i];
-          if (REV) {
-            const float4 y = plus[(c0 / 8 + 2 * n0 + i) * 32 + lane];
-            const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleE, z[j]));
+        for (int ks = 0; ks < DKH / 16; ++ks) {
+          uint32_t ah[4], al[4];
+          split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
+          if (KIND == kForward) {
+            planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
+            if (NP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleE);
+            for (int q = 0; q < 4; ++q) {
+              const int at = tiled<DK>(brow + 8 * (q & 1), c0 + ks * 16 + 8 * (q >> 1)) + 2 * lane;
+              *reinterpret_cast<uint32_t *>(keep + at) = ah[q];
+              *reinterpret_cast<uint32_t *>(keep + (long long)p.dvp * DK + at) = al[q];
+            }
           }
-        }
-      }
-      const unsigned top = max_bits(S);
-      if (lane == 0) tops[h] = top;
-    } else if (live) {
-      // ---- side warp: tokens 32 h .. 32 h + 31 --------------------------------------------
-      float x[4][8];
-      load_tokens<NP>(x, st + l.v, ldv, blk * 16, p.dtype, lane);
-      if (REV)
+          if (JOIN) {
+            // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
+            // instructions apart, which covers the tensor cores' latency.
+            const uint32_t x = DELTA ? kt : sk;
+            uint32_t r[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x, np * 16, c0 + ks * 16);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[i][j] *= qscale;       // (what Z and the planes of Q lack)
-      const unsigned mV = max_bits(x), mS = max(tops[0], tops[1]);
-      float invV, inv, invE;
-      const float scaleV = scale_of(mV, 6, invV), scale = scale_of(mS, 6, inv), scaleE = scale_of(max(mS, mV), 6, invE);
-      if (lane == 0) tops[2 + h] = mV;
-      float U[4][4];                   // tokens 32 h + 8 i ..
+            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], al, r[np]);
+            if (DELTA || NP == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
-      if (DELTA || REV) {
+              for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x + TILE, np * 16, c0 + ks * 16);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t vh[4], vl[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) split2(x[ks][2 * q] * invV, x[ks][2 * q + 1] * invV, vh[q], vl[q]);
-#pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int np = 2 * h + i;
-              if (REV ? np <= ks : ks <= np) {
-                uint32_t b[4];
-                if (REV) lc.b_cols(b, tm + c2 * SQ, ks * 16, np * 16);
-                else lc.b_rows(b, tm + c2 * SQ, np * 16, ks * 16);
-                mma2(U[2 * i], U[2 * i + 1], vh, b);
-                if (NP == 2 && c2 == 0) mma2(U[2 * i], U[2 * i + 1], vl, b);
-              }
+              for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
             }
           }
         }
+        if (KIND != kForward && lane == 0 && h == 0)
+          p.scales[REV ? kScaleD : kScaleS][rec * (p.dvp / 16) + brow / 16] = scale;
+        if (JOIN) {
+          if (NH > 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i) part[(h * 8 + i) * 32 + lane] = f4(E[i]);
+          barrier_sync(X, PER);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) U[i][j] *= scaleV;
-      } else {                         // E = V
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 2 * ((j >> 1) + 2 * (i & 1)) + (j & 1);
-            U[i][j] = h ? x[2 + i / 2][e] : x[i / 2][e];
+          for (int i = 0; i < 8; ++i) {
+            const float4 u = sided[i * 32 + lane];
+            if (NH > 1) {
+              const float4 y = part[((h ^ 1) * 8 + i) * 32 + lane];
+              E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
+            }
+            float x = scale, y = scale;
+            if (REV && !DELTA) {
+              const float2 f = *reinterpret_cast<const float2 *>(wk + 8 * i + t2);
+              x *= f.x;
+              y *= f.y;
+            }
+            E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
+            E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
           }
-      }
+        } else {
+          if (KIND == kForward) barrier_arrive(X, PER);
+          // E = V
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sided[(4 * h + i) * 32 + lane] = f4(U[i]);
-      if (REV) {
-        // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
-        uint32_t oh[4][4], ol[4][4];
+          for (int ks = 0; ks < 4; ++ks) {
+            uint32_t a[NP][4];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+            for (int pl = 0; pl < NP; ++pl) lv.a_cols(a[pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
-            split2(x[ks][2 * q] * (invV * f.x), x[ks][2 * q + 1] * (invV * f.y), oh[ks][q], ol[ks][q]);
+            for (int q = 0; q < 4; ++q) {
+              float2 f = half2_of(a[0][q]);
+              if (NP == 2) {
+                const float2 y = half2_of(a[NP - 1][q]);
+                f.x = __fadd_rn(f.x, y.x);
+                f.y = __fadd_rn(f.y, y.y);
+              }
+              float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
+              e[0] = f.x * scaleV;
+              e[1] = f.y * scaleV;
+            }
           }
-        constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
-        if (DK >= 32 || h == 0)
+        }
+        // E (or R) for the side warps: each state warp hands over half of the tokens
 #pragma unroll
-          for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
-            const int col = (DK >= 32 ? h * HALF : 0) + n0;
-            float a[2 * QS][4];
+        for (int i = 0; i < 8; ++i)
+          if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
+        barrier_arrive(Y, PER);
+        // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
+        // sum starts from zero and joins the state in one fma, so that the tensor cores'
+        // rounding does not pile up in it
+        const float eC = eG[kChunk - 1];
+        uint32_t wh[4][4], wl[4][4];
+        if (!REV || DELTA)
 #pragma unroll
-            for (int i = 0; i < 2 * QS; ++i)
+          for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+            for (int q = 0; q < 4; ++q) {
+              const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
+              const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
+              const float to = REV ? -invE : invE;
+              split2(e[0] * (f.x * to), e[1] * (f.y * to), wh[ks][q], wl[ks][q]);
+            }
+        constexpr int STEP = NTH >= 8 ? 4 : NTH / 2;         // column pairs at a time
+#pragma unroll
+        for (int n0 = 0; n0 < NTH / 2; n0 += STEP) {
+          float a[2 * STEP][4];
+#pragma unroll
+          for (int i = 0; i < 2 * STEP; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+          if (!REV || DELTA)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              uint32_t r[QS][4];
+              uint32_t r[STEP][4];
 #pragma unroll
-              for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq, ks * 16, col + 16 * i);
+              for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk, ks * 16, c0 + (n0 + i) * 16);
 #pragma unroll
-              for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
+              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
 #pragma unroll
-              for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[i]);
+              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wl[ks], r[i]);
               if (NP == 2) {
 #pragma unroll
-                for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq + TILE, ks * 16, col + 16 * i);
+                for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk + TILE, ks * 16, c0 + (n0 + i) * 16);
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
+              }
+            }
+          if (REV && n0 == 0) barrier_sync(Z, PER);
+#pragma unroll
+          for (int i = 0; i < 2 * STEP; ++i) {
+            float *x = S[2 * n0 + i];
+            if (REV) {
+              const float4 y = plus[(c0 / 8 + 2 * n0 + i) * 32 + lane];
+              const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleE, z[j]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleE);
+            }
+          }
+        }
+        const unsigned top = max_bits(S);
+        if (lane == 0) tops[2 * ((i0 + 1) & 1) + h] = top;
+      } else {
+        // ---- side warp: tokens 32 h .. 32 h + 31 --------------------------------------------
+        if (JOIN) {
+          float U[4][4];                   // tokens 32 h + 8 i ..
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
+          // Tm V: blocks s <= t; dO^T Z: blocks t >= s.  (j counts the blocks of the first or the last
+          // tokens, which both warps have; the rest belongs to one.)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            if (REV ? ks >= 2 * h : ks <= 2 * h + 1) {
+              uint32_t v[NP][4], b[2][2][4];
+#pragma unroll
+              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (REV) lc.b_cols(b[c2][i], tm + c2 * SQ, ks * 16, (2 * h + i) * 16);
+                  else lc.b_rows(b[c2][i], tm + c2 * SQ, (2 * h + i) * 16, ks * 16);
+                }
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (REV ? 2 * h + i <= ks : ks <= 2 * h + i) mma2(U[2 * i], U[2 * i + 1], v[0], b[c2][i]);
+              if (NP == 2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (REV ? 2 * h + i <= ks : ks <= 2 * h + i) mma2(U[2 * i], U[2 * i + 1], v[NP - 1], b[0][i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sided[(4 * h + i) * 32 + lane] = make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
+        }
+        if (JOIN || KIND == kForward) {
+          if (REV) barrier_arrive(X, PER);
+          else barrier_sync(X, PER);
+        }
+        if (REV) {
+          // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
+          uint32_t oh[4][4], ol[4][4];
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            uint32_t v[NP][4];
+#pragma unroll
+            for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+              float2 x = half2_of(v[0][q]);
+              if (NP == 2) {
+                const float2 y = half2_of(v[NP - 1][q]);
+                x.x = __fadd_rn(x.x, y.x);
+                x.y = __fadd_rn(x.y, y.y);
+              }
+              split2(x.x * f.x, x.y * f.y, oh[ks][q], ol[ks][q]);
+            }
+          }
+          constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
+          if (DK >= 32 || h == 0)
+#pragma unroll
+            for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
+              const int col = (DK >= 32 ? h * HALF : 0) + n0;
+              float a[2 * QS][4];
+#pragma unroll
+              for (int i = 0; i < 2 * QS; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                uint32_t r[QS][4];
+#pragma unroll
+                for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq, ks * 16, col + 16 * i);
 #pragma unroll
                 for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
-              }
-            }
 #pragma unroll
-            for (int i = 0; i < 2 * QS; ++i)
-              plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
-          }
-      }
-      barrier_sync(1 + 2 * blk, PER);                                   // X
-      float O[4][4];
-      if (KIND == kForward) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint4 y = planes[ks * 32 + lane];
-          const uint32_t ah[4] = {y.x, y.y, y.z, y.w};
-          uint32_t b[4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ld.b_rows(b, sq, (2 * h + i) * 16, ks * 16);
-            mma2(O[2 * i], O[2 * i + 1], ah, b);
-            if (NP == 2) {
-              const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
-              const uint32_t al[4] = {z.x, z.y, z.z, z.w};
-              mma2(O[2 * i], O[2 * i + 1], al, b);
-              ld.b_rows(b, sq + TILE, (2 * h + i) * 16, ks * 16);
-              mma2(O[2 * i], O[2 * i + 1], ah, b);
-            }
-          }
-        }
-        const float to = scale * invE;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
-          O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
-        }
-      }
-      barrier_sync(2 + 2 * blk, PER);                                   // Y
-      if (KIND == kForward) {
-        // + E^T P^T
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks <= 2 * h + 1) {
-            const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
-            const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
-            uint32_t eh[4], el[4], b[4];
-            split_tiles(e0, e1, invE, eh, el);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (ks <= 2 * h + i) {
-                lc.b_rows(b, pp, (2 * h + i) * 16, ks * 16);
-                mma2(O[2 * i], O[2 * i + 1], eh, b);
+                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[i]);
                 if (NP == 2) {
-                  mma2(O[2 * i], O[2 * i + 1], el, b);
-                  lc.b_rows(b, pp + SQ, (2 * h + i) * 16, ks * 16);
-                  mma2(O[2 * i], O[2 * i + 1], eh, b);
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq + TILE, ks * 16, col + 16 * i);
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
                 }
               }
+#pragma unroll
+              for (int i = 0; i < 2 * QS; ++i)
+                plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+            }
+          barrier_arrive(Z, PER);
+        }
+        float O[4][4];
+        if (KIND == kForward) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            const uint4 y = planes[ks * 32 + lane];
+            const uint32_t ah[4] = {y.x, y.y, y.z, y.w};
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              ld.b_rows(b, sq, (2 * h + i) * 16, ks * 16);
+              mma2(O[2 * i], O[2 * i + 1], ah, b);
+              if (NP == 2) {
+                const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
+                const uint32_t al[4] = {z.x, z.y, z.z, z.w};
+                mma2(O[2 * i], O[2 * i + 1], al, b);
+                ld.b_rows(b, sq + TILE, (2 * h + i) * 16, ks * 16);
+                mma2(O[2 * i], O[2 * i + 1], ah, b);
+              }
+            }
+          }
+          const float to = scale * invE;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
+            O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
           }
         }
-        store_tokens<NP>(O, scaleE * qscale, st + l.v, ldv, blk * 16, 4 * h, p.o, p.dtype, p.o_stride,
-                         start + (long long)c * kChunk, n, head * p.d_v + brow, p.d_v - brow, p.o16, lane);
-      } else {
+        barrier_sync(Y, PER);
+        if (KIND == kForward) {
+          // + E^T P^T
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 y = last[(4 * h + i) * 32 + lane];
-          O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+          for (int ks = 0; ks < 4; ++ks) {
+            if (ks <= 2 * h + 1) {
+              const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
+              const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
+              uint32_t eh[4], el[4], b[4];
+              split_tiles(e0, e1, invE, eh, el);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (ks <= 2 * h + i) {
+                  lc.b_rows(b, pp, (2 * h + i) * 16, ks * 16);
+                  mma2(O[2 * i], O[2 * i + 1], eh, b);
+                  if (NP == 2) {
+                    mma2(O[2 * i], O[2 * i + 1], el, b);
+                    lc.b_rows(b, pp + SQ, (2 * h + i) * 16, ks * 16);
+                    mma2(O[2 * i], O[2 * i + 1], eh, b);
+                  }
+                }
+            }
+          }
+          store_tokens<NP>(O, scaleE * qscale, tile, 4 * h, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
+                           head * p.d_v + brow, p.d_v - brow, p.o16, lane);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = last[(4 * h + i) * 32 + lane];
+            O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+          }
+          keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
+          if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+          if (REV) {
+            // (both side warps are done with the rows of dO)
+            barrier_sync(Z + 3 * kMaxBlocks, 32 * kSideWarps);
+            store_tokens<NP>(O, 1.0f, tile, 4 * h, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
+                             head * p.d_v + brow, p.d_v - brow, p.v16, lane);
+          }
         }
-        keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
-        if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
-        if (REV)
-          store_tokens<NP>(O, 1.0f, st + l.v, ldv, blk * 16, 4 * h, p.dv, p.dtype, p.v_stride,
-                           start + (long long)c * kChunk, n, head * p.d_v + brow, p.d_v - brow, p.v16, lane);
       }
     }
-    if (p.stages == 1) {
+    if (!by) {
       __syncthreads();
       if (loader && i0 + 1 < chunks) fetch(next);
     }
   }
-  if (live && !side && KIND != kRecompute) {
+  if (live && !side && !loader && KIND != kRecompute) {
     float *out = REV ? p.d_state_in : p.state_out;
     if (out) save_state<NTH>(S, out, blockIdx.x, p.d_v, DK, r0, c0 + t2);
   }
