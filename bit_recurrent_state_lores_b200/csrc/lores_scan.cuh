@@ -916,12 +916,12 @@ __device__ __forceinline__ void save_state(const float (&S)[NTH][4], float *dst,
 }
 template <int N, int M>
 __device__ __forceinline__ unsigned max_bits(const float (&x)[N][M]) {
-  unsigned m = 0;
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};       // (a NaN is passed over: it is in the data all the same)
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < M; ++j) m = max(m, abs_bits(x[i][j]));
-  return __reduce_max_sync(0xFFFFFFFFu, m);
+    for (int j = 0; j < M; ++j) m[j & 3] = fmaxf(m[j & 3], fabsf(x[i][j]));
+  return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))));
 }
 
 // A warp's 64 rows of 16 columns of the caller's tensor (columns >= have, a multiple of 4, and rows >= n are zeros).
@@ -1052,6 +1052,10 @@ __device__ __forceinline__ void barrier_sync(int id, int threads) {
 __device__ __forceinline__ void barrier_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
 __device__ __forceinline__ float4 f4(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
 // Tiles of 16 value rows x 64 tokens as planes in the workspace.
 __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row0, int tile0, const float (&x)[4][4],
@@ -1199,6 +1203,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
 #pragma unroll
           for (int j = 0; j < 4; ++j) E[i][j] = 0.0f;
         __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
+        // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
+        // instructions apart and the next fragments are under way before the last products are
+        // issued, which covers the latencies of the tensor cores and of ldmatrix.
+        constexpr bool LO = DELTA || NP == 2;
+        const uint32_t right = DELTA ? kt : sk;
+        uint32_t rh[4][4], rl[4][4];
+        if (JOIN)
+#pragma unroll
+          for (int np = 0; np < 4; ++np) {
+            ld.b_rows(rh[np], right, np * 16, c0);
+            if (LO) ld.b_rows(rl[np], right + TILE, np * 16, c0);
+          }
 #pragma unroll
         for (int ks = 0; ks < DKH / 16; ++ks) {
           uint32_t ah[4], al[4];
@@ -1215,21 +1231,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
             }
           }
           if (JOIN) {
-            // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
-            // instructions apart, which covers the tensor cores' latency.
-            const uint32_t x = DELTA ? kt : sk;
-            uint32_t r[4][4];
+            const bool more = ks + 1 < DKH / 16;
 #pragma unroll
-            for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x, np * 16, c0 + ks * 16);
+            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, rh[np]);
 #pragma unroll
-            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
+            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], al, rh[np]);
+            if (more)
 #pragma unroll
-            for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], al, r[np]);
-            if (DELTA || NP == 2) {
+              for (int np = 0; np < 4; ++np) ld.b_rows(rh[np], right, np * 16, c0 + ks * 16 + 16);
+            if (LO) {
 #pragma unroll
-              for (int np = 0; np < 4; ++np) ld.b_rows(r[np], x + TILE, np * 16, c0 + ks * 16);
+              for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, rl[np]);
+              if (more)
 #pragma unroll
-              for (int np = 0; np < 4; ++np) mma2(E[2 * np], E[2 * np + 1], ah, r[np]);
+                for (int np = 0; np < 4; ++np) ld.b_rows(rl[np], right + TILE, np * 16, c0 + ks * 16 + 16);
             }
           }
         }
@@ -1306,23 +1321,28 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
           for (int i = 0; i < 2 * STEP; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
-          if (!REV || DELTA)
+          if (!REV || DELTA) {
+            uint32_t r[2][STEP][4];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) ld.b_cols(r[0][i], sk, 0, c0 + (n0 + i) * 16);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              uint32_t r[STEP][4];
+              if (ks < 3)
 #pragma unroll
-              for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk, ks * 16, c0 + (n0 + i) * 16);
+                for (int i = 0; i < STEP; ++i) ld.b_cols(r[(ks + 1) & 1][i], sk, ks * 16 + 16, c0 + (n0 + i) * 16);
 #pragma unroll
-              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
+              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[ks & 1][i]);
 #pragma unroll
-              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wl[ks], r[i]);
+              for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wl[ks], r[ks & 1][i]);
               if (NP == 2) {
+                uint32_t x[STEP][4];
 #pragma unroll
-                for (int i = 0; i < STEP; ++i) ld.b_cols(r[i], sk + TILE, ks * 16, c0 + (n0 + i) * 16);
+                for (int i = 0; i < STEP; ++i) ld.b_cols(x[i], sk + TILE, ks * 16, c0 + (n0 + i) * 16);
 #pragma unroll
-                for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], r[i]);
+                for (int i = 0; i < STEP; ++i) mma2(a[2 * i], a[2 * i + 1], wh[ks], x[i]);
               }
             }
+          }
           if (REV && n0 == 0) barrier_sync(Z, PER);
 #pragma unroll
           for (int i = 0; i < 2 * STEP; ++i) {
@@ -1341,170 +1361,197 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
         const unsigned top = max_bits(S);
         if (lane == 0) tops[2 * ((i0 + 1) & 1) + h] = top;
       } else {
-        // ---- side warp: tokens 32 h .. 32 h + 31 --------------------------------------------
-        if (JOIN) {
-          float U[4][4];                   // tokens 32 h + 8 i ..
+        // ---- side warp: tokens 32 h .. 32 h + 31 (a body for each half, so that every loop is straight code)
+        auto body = [&](auto half) {
+          constexpr int H = decltype(half)::value;
+          if (JOIN) {
+            float U[4][4];                   // tokens 32 H + 8 i ..
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
-          // Tm V: blocks s <= t; dO^T Z: blocks t >= s.  (j counts the blocks of the first or the last
-          // tokens, which both warps have; the rest belongs to one.)
+              for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
+            // Tm V: blocks s <= t; dO^T Z: blocks t >= s
+            constexpr int K0 = REV ? 2 * H : 0, K1 = REV ? 4 : 2 * H + 2;
+            uint32_t v[4][NP][4], b[4][2][2][4];
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            if (REV ? ks >= 2 * h : ks <= 2 * h + 1) {
-              uint32_t v[NP][4], b[2][2][4];
+            for (int ks = K0; ks < K1; ++ks) {
 #pragma unroll
-              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
-#pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (REV) lc.b_cols(b[c2][i], tm + c2 * SQ, ks * 16, (2 * h + i) * 16);
-                  else lc.b_rows(b[c2][i], tm + c2 * SQ, (2 * h + i) * 16, ks * 16);
-                }
+              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[ks][pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
               for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                  if (REV ? 2 * h + i <= ks : ks <= 2 * h + i) mma2(U[2 * i], U[2 * i + 1], v[0], b[c2][i]);
+                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) {
+                    if (REV) lc.b_cols(b[ks][c2][i], tm + c2 * SQ, ks * 16, (2 * H + i) * 16);
+                    else lc.b_rows(b[ks][c2][i], tm + c2 * SQ, (2 * H + i) * 16, ks * 16);
+                  }
+            }
+#pragma unroll
+            for (int ks = K0; ks < K1; ++ks) {
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][0], b[ks][c2][i]);
               if (NP == 2)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                  if (REV ? 2 * h + i <= ks : ks <= 2 * h + i) mma2(U[2 * i], U[2 * i + 1], v[NP - 1], b[0][i]);
+                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][NP - 1], b[ks][0][i]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sided[(4 * H + i) * 32 + lane] = make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sided[(4 * h + i) * 32 + lane] = make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
-        }
-        if (JOIN || KIND == kForward) {
-          if (REV) barrier_arrive(X, PER);
-          else barrier_sync(X, PER);
-        }
-        if (REV) {
-          // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
-          uint32_t oh[4][4], ol[4][4];
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t v[NP][4];
-#pragma unroll
-            for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
-              float2 x = half2_of(v[0][q]);
-              if (NP == 2) {
-                const float2 y = half2_of(v[NP - 1][q]);
-                x.x = __fadd_rn(x.x, y.x);
-                x.y = __fadd_rn(x.y, y.y);
-              }
-              split2(x.x * f.x, x.y * f.y, oh[ks][q], ol[ks][q]);
-            }
+          if (JOIN || KIND == kForward) {
+            if (REV) barrier_arrive(X, PER);
+            else barrier_sync(X, PER);
           }
-          constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
-          if (DK >= 32 || h == 0)
-#pragma unroll
-            for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
-              const int col = (DK >= 32 ? h * HALF : 0) + n0;
-              float a[2 * QS][4];
-#pragma unroll
-              for (int i = 0; i < 2 * QS; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+          if (REV) {
+            // (diag(e^G) dO)^T Q, columns [H d_k/2, (H+1) d_k/2)
+            constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
+            if (DK >= 32 || H == 0) {
+              uint32_t oh[4][4], ol[4][4];
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks) {
-                uint32_t r[QS][4];
+                uint32_t v[NP][4];
 #pragma unroll
-                for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq, ks * 16, col + 16 * i);
+                for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
-                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
-#pragma unroll
-                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[i]);
-                if (NP == 2) {
-#pragma unroll
-                  for (int i = 0; i < QS; ++i) ld.b_cols(r[i], sq + TILE, ks * 16, col + 16 * i);
-#pragma unroll
-                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[i]);
+                for (int q = 0; q < 4; ++q) {
+                  const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+                  float2 x = half2_of(v[0][q]);
+                  if (NP == 2) {
+                    const float2 y = half2_of(v[NP - 1][q]);
+                    x.x = __fadd_rn(x.x, y.x);
+                    x.y = __fadd_rn(x.y, y.y);
+                  }
+                  split2(x.x * f.x, x.y * f.y, oh[ks][q], ol[ks][q]);
                 }
               }
 #pragma unroll
-              for (int i = 0; i < 2 * QS; ++i)
-                plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+              for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
+                constexpr int C0 = DK >= 32 ? H * HALF : 0;
+                const int col = C0 + n0;
+                float a[2 * QS][4];
+#pragma unroll
+                for (int i = 0; i < 2 * QS; ++i)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+                uint32_t r[2][QS][4];
+#pragma unroll
+                for (int i = 0; i < QS; ++i) ld.b_cols(r[0][i], sq, 0, col + 16 * i);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                  if (ks < 3)
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) ld.b_cols(r[(ks + 1) & 1][i], sq, ks * 16 + 16, col + 16 * i);
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[ks & 1][i]);
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[ks & 1][i]);
+                  if (NP == 2) {
+                    uint32_t x[QS][4];
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) ld.b_cols(x[i], sq + TILE, ks * 16, col + 16 * i);
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], x[i]);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * QS; ++i)
+                  plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+              }
             }
-          barrier_arrive(Z, PER);
-        }
-        float O[4][4];
-        if (KIND == kForward) {
+            barrier_arrive(Z, PER);
+          }
+          float O[4][4];
+          uint32_t r[4][2][4];             // P's blocks
+          if (KIND == kForward) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
+              for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
+            uint4 y[DK / 16];
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks) {
-            const uint4 y = planes[ks * 32 + lane];
-            const uint32_t ah[4] = {y.x, y.y, y.z, y.w};
-            uint32_t b[4];
+            for (int ks = 0; ks < DK / 16; ++ks) y[ks] = planes[ks * 32 + lane];
+            uint32_t b[2][2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              ld.b_rows(b, sq, (2 * h + i) * 16, ks * 16);
-              mma2(O[2 * i], O[2 * i + 1], ah, b);
+            for (int i = 0; i < 2; ++i) ld.b_rows(b[0][i], sq, (2 * H + i) * 16, 0);
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks) {
+              const uint32_t ah[4] = {y[ks].x, y[ks].y, y[ks].z, y[ks].w};
+              if (ks + 1 < DK / 16)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ld.b_rows(b[(ks + 1) & 1][i], sq, (2 * H + i) * 16, ks * 16 + 16);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) mma2(O[2 * i], O[2 * i + 1], ah, b[ks & 1][i]);
               if (NP == 2) {
                 const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
                 const uint32_t al[4] = {z.x, z.y, z.z, z.w};
-                mma2(O[2 * i], O[2 * i + 1], al, b);
-                ld.b_rows(b, sq + TILE, (2 * h + i) * 16, ks * 16);
-                mma2(O[2 * i], O[2 * i + 1], ah, b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t x[4];
+                  mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
+                  ld.b_rows(x, sq + TILE, (2 * H + i) * 16, ks * 16);
+                  mma2(O[2 * i], O[2 * i + 1], ah, x);
+                }
               }
             }
-          }
-          const float to = scale * invE;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
-            O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
-          }
-        }
-        barrier_sync(Y, PER);
-        if (KIND == kForward) {
-          // + E^T P^T
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            if (ks <= 2 * h + 1) {
-              const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
-              const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
-              uint32_t eh[4], el[4], b[4];
-              split_tiles(e0, e1, invE, eh, el);
+            for (int ks = 0; ks < 2 * H + 2; ++ks)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (ks <= 2 * h + i) {
-                  lc.b_rows(b, pp, (2 * h + i) * 16, ks * 16);
-                  mma2(O[2 * i], O[2 * i + 1], eh, b);
-                  if (NP == 2) {
-                    mma2(O[2 * i], O[2 * i + 1], el, b);
-                    lc.b_rows(b, pp + SQ, (2 * h + i) * 16, ks * 16);
-                    mma2(O[2 * i], O[2 * i + 1], eh, b);
-                  }
-                }
+                if (ks <= 2 * H + i) lc.b_rows(r[ks][i], pp, (2 * H + i) * 16, ks * 16);
+            const float to = scale * invE;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * H + 8 * i + t2);
+              O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
             }
           }
-          store_tokens<NP>(O, scaleE * qscale, tile, 4 * h, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
-                           head * p.d_v + brow, p.d_v - brow, p.o16, lane);
-        } else {
+          barrier_sync(Y, PER);
+          if (KIND == kForward) {
+            // + E^T P^T
+            uint32_t eh[4][4], el[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 y = last[(4 * h + i) * 32 + lane];
-            O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+            for (int ks = 0; ks < 2 * H + 2; ++ks) {
+              const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
+              const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
+              split_tiles(e0, e1, invE, eh[ks], el[ks]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2 * H + 2; ++ks)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (ks <= 2 * H + i) {
+                  mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
+                  if (NP == 2) {
+                    uint32_t x[4];
+                    mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
+                    lc.b_rows(x, pp + SQ, (2 * H + i) * 16, ks * 16);
+                    mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
+                  }
+                }
+            store_tokens<NP>(O, scaleE * qscale, tile, 4 * H, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
+                             head * p.d_v + brow, p.d_v - brow, p.o16, lane);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 y = last[(4 * H + i) * 32 + lane];
+              O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+            }
+            keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * H, O, invE, lane);
+            if (lane == 0 && H == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+            if (REV) {
+              // (both side warps are done with the rows of dO)
+              barrier_sync(Z + 3 * kMaxBlocks, 32 * kSideWarps);
+              store_tokens<NP>(O, 1.0f, tile, 4 * H, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
+                               head * p.d_v + brow, p.d_v - brow, p.v16, lane);
+            }
           }
-          keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
-          if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
-          if (REV) {
-            // (both side warps are done with the rows of dO)
-            barrier_sync(Z + 3 * kMaxBlocks, 32 * kSideWarps);
-            store_tokens<NP>(O, 1.0f, tile, 4 * h, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
-                             head * p.d_v + brow, p.d_v - brow, p.v16, lane);
-          }
-        }
+        };
+        if (h == 0) body(Const<0>());
+        else body(Const<1>());
       }
     }
     if (!by) {
