@@ -1061,9 +1061,9 @@ static lores_status move_states(lores_handle *h, int32_t n, const int32_t *slots
     return LORES_ERR_INVALID_ARG;
   if (write && h->axis) return LORES_ERR_UNSUPPORTED;
   const lores_config &c = h->cfg;
-  const int rows = kPoolThreads / (c.d_k / 16);
-  const long long blocks = ((long long)c.heads * c.d_v + rows - 1) / rows;
-  if ((long long)c.heads * c.d_v > 0x7FFFFFFFll || blocks * n > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
+  const int rows = kPoolThreads / (c.d_k / 16) * kPoolRows;
+  const dim3 grid(n, c.heads, (c.d_v + rows - 1) / rows);
+  if (c.heads > 65535) return LORES_ERR_UNSUPPORTED;
   if (n == 0) return LORES_OK;
   DeviceGuard guard(c.device);
   if (!guard.ok) return LORES_ERR_CUDA;
@@ -1080,7 +1080,6 @@ static lores_status move_states(lores_handle *h, int32_t n, const int32_t *slots
   p.axis = h->axis;
   p.batch = c.batch;
   p.n = n;
-  p.blocks = (int)blocks;
   p.slots = slots;
   p.src = src;
   p.dst = dst;
@@ -1096,8 +1095,7 @@ static lores_status move_states(lores_handle *h, int32_t n, const int32_t *slots
   p.rg.base[kRgS] = buf;
   p.rg.bytes[kRgS] = bytes > h->trim[kRgS] ? bytes - h->trim[kRgS] : 0;
 #endif
-  pool_kernel_for(c.d_k, write)<<<(unsigned)(blocks * n), kPoolThreads, 0,
-                                 static_cast<cudaStream_t>(stream)>>>(p);
+  pool_kernel_for(c.d_k, write)<<<grid, kPoolThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cuda_status(cudaGetLastError());
 }
 

@@ -7,13 +7,14 @@
 //
 // Memory bound: d_k/16 lanes share a row and a lane owns 16 consecutive columns (the code
 // format's unit), i.e. 64 bytes of fp32, moved as two 32-byte accesses so that every sector
-// is touched by one instruction.
+// is touched by one instruction.  Grid (entry, head, group of rows): no division per row.
 #pragma once
 #include "lores_device.cuh"
 
 namespace lores {
 
 constexpr int kPoolThreads = 256;
+constexpr int kPoolRows = 2;    // rows per lane, whose loads are in flight together
 
 struct PoolParams {
   uint8_t *codes;
@@ -23,7 +24,6 @@ struct PoolParams {
   long long seq_bytes;
   int H, d_v, ng, G, axis, batch;
   int n;                        // entries
-  int blocks;                   // CTAs per entry
   const int *slots;             // device [n], or null: entry i is slot i
   const void *src;              // write: the caller's states
   void *dst;                    // read
@@ -122,22 +122,24 @@ __device__ __forceinline__ int pool_slot(const PoolParams &p, int entry) {
 
 template <int DK>
 __global__ void __launch_bounds__(kPoolThreads) write_states_kernel(const PoolParams p) {
-  constexpr int LPR = DK / 16;
-  const int entry = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
+  constexpr int LPR = DK / 16, STEP = kPoolThreads / LPR;
+  const int entry = blockIdx.x, head = blockIdx.y;
   const int slot = pool_slot(p, entry);
   if (slot < 0) return;
   const int lane = threadIdx.x & 31, lir = threadIdx.x % LPR, col0 = lir * 16;
-  const int gr = block * (kPoolThreads / LPR) + threadIdx.x / LPR;      // row of the entry
-  const bool active = gr < p.H * p.d_v;
-  const int grr = active ? gr : 0;
-  const int head = grr / p.d_v, row = grr % p.d_v;
-  const long long at = ((long long)entry * p.H * p.d_v + grr) * DK + col0;
-  float x[16];
-  const void *src = static_cast<const uint8_t *>(p.src) + at * (p.dtype == 0 ? 4 : 2);
-  if (LORES_IN(p, kRgS, src, p.dtype == 0 ? 64 : 32)) load_row16(p, at, x);
-  else
+  const int row0 = blockIdx.z * (STEP * kPoolRows) + threadIdx.x / LPR;
+  const long long src_tile = ((long long)entry * p.H + head) * p.d_v;
+  float x[kPoolRows][16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+  for (int r = 0; r < kPoolRows; ++r) {
+    const int row = row0 + r * STEP;
+    const long long at = (src_tile + row) * DK + col0;
+    const void *src = static_cast<const uint8_t *>(p.src) + at * (p.dtype == 0 ? 4 : 2);
+    if (row < p.d_v && LORES_IN(p, kRgS, src, p.dtype == 0 ? 64 : 32)) load_row16(p, at, x[r]);
+    else
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[r][e] = 0.0f;
+  }
   // the last of several entries with one slot is the one that counts
   int later = 0;
   if (p.slots)
@@ -145,81 +147,123 @@ __global__ void __launch_bounds__(kPoolThreads) write_states_kernel(const PoolPa
   if (__syncthreads_or(later)) return;
   const LaneFmt f = p.fmt[head * (DK / 16) + lir];
   const int bits = f.bits;
-  const long long tile = (long long)slot * p.H + head, srow = tile * p.d_v + row;
+  const long long tile = (long long)slot * p.H + head;
   const int g = col0 / p.G, lpg = p.G / 16;
-  const uint32_t n0 = (uint32_t)row * (uint32_t)(DK / 4) + (uint32_t)lir * 4u;
-  uint32_t words[4];
-  float s_new;
-  const bool bad = requantize16<LPR>(x, bits == 32 ? 8 : bits, lpg, lane, tile_key(p.step_key, (uint32_t)tile), n0,
-                                     p.stochastic, words, s_new, f.store);
-  if (!active) return;
-  if (bad && lir == 0) atomicOr(p.flag, kFlagNonFinite);
-  uint8_t *rowp = p.codes + slot * p.seq_bytes + __ldg(p.head_off + head) + (size_t)row * f.rowb;
-  if (!LORES_IN(p, kRgCodes, rowp, f.rowb)) return;
-  if (bits == 32) {
+  uint8_t *codes = p.codes + slot * p.seq_bytes + __ldg(p.head_off + head);
+  float *scales = p.scales + tile * p.d_v * p.ng + g;
+  const uint32_t tkey = tile_key(p.step_key, (uint32_t)tile);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      reinterpret_cast<float4 *>(rowp + f.off)[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-    return;
+  for (int r = 0; r < kPoolRows; ++r) {
+    const int row = row0 + r * STEP;
+    const uint32_t n0 = (uint32_t)row * (uint32_t)(DK / 4) + (uint32_t)lir * 4u;
+    uint32_t words[4];
+    float s_new;
+    const bool bad = requantize16<LPR>(x[r], bits == 32 ? 8 : bits, lpg, lane, tkey, n0, p.stochastic, words, s_new,
+                                       f.store);
+    if (row >= p.d_v) continue;
+    if (bad && lir == 0) atomicOr(p.flag, kFlagNonFinite);
+    uint8_t *rowp = codes + (size_t)row * f.rowb;
+    if (!LORES_IN(p, kRgCodes, rowp, f.rowb)) continue;
+    if (bits == 32) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        reinterpret_cast<float4 *>(rowp + f.off)[c] =
+            make_float4(x[r][4 * c], x[r][4 * c + 1], x[r][4 * c + 2], x[r][4 * c + 3]);
+      continue;
+    }
+    if (f.store >= 5 && f.store <= 7) {
+      const DenseLane dl{words[0], words[1], words[2], words[3]};
+      if (f.store == 5) st_dense<5>(rowp, DK, lir, dl);
+      else if (f.store == 6) st_dense<6>(rowp, DK, lir, dl);
+      else st_dense<7>(rowp, DK, lir, dl);
+    } else if (bits != 4) {
+      st16_a8(rowp + f.off, make_uint4(words[0], words[1], words[2], words[3]));
+    } else {
+      *reinterpret_cast<uint2 *>(rowp + f.off) = make_uint2(words[0], words[1]);
+    }
+    float *sc = scales + (long long)row * p.ng;
+    if (lir % lpg == 0 && LORES_IN(p, kRgScales, sc, 4)) *sc = s_new;
   }
-  if (f.store >= 5 && f.store <= 7) {
-    const DenseLane dl{words[0], words[1], words[2], words[3]};
-    if (f.store == 5) st_dense<5>(rowp, DK, lir, dl);
-    else if (f.store == 6) st_dense<6>(rowp, DK, lir, dl);
-    else st_dense<7>(rowp, DK, lir, dl);
-  } else if (bits != 4) {
-    st16_a8(rowp + f.off, make_uint4(words[0], words[1], words[2], words[3]));
-  } else {
-    *reinterpret_cast<uint2 *>(rowp + f.off) = make_uint2(words[0], words[1]);
-  }
-  float *sc = p.scales + srow * p.ng + g;
-  if (lir % lpg == 0 && LORES_IN(p, kRgScales, sc, 4)) *sc = s_new;
 }
 
 template <int DK>
 __global__ void __launch_bounds__(kPoolThreads) read_states_kernel(const PoolParams p) {
-  constexpr int LPR = DK / 16;
-  const int entry = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
+  constexpr int LPR = DK / 16, STEP = kPoolThreads / LPR;
+  const int entry = blockIdx.x, head = blockIdx.y;
   const int slot = pool_slot(p, entry);
   if (slot < 0) return;
   const int lir = threadIdx.x % LPR, col0 = lir * 16;
-  const int gr = block * (kPoolThreads / LPR) + threadIdx.x / LPR;
-  if (gr >= p.H * p.d_v) return;
-  const int head = gr / p.d_v, row = gr % p.d_v;
+  const int row0 = blockIdx.z * (STEP * kPoolRows) + threadIdx.x / LPR;
   const LaneFmt f = p.fmt[head * (DK / 16) + lir];
   const int bits = f.bits;
-  const long long tile = (long long)slot * p.H + head, srow = tile * p.d_v + row;
-  const uint8_t *rowp = p.codes + slot * p.seq_bytes + __ldg(p.head_off + head) + (size_t)row * f.rowb;
-  if (!LORES_IN(p, kRgCodes, rowp, f.rowb)) return;
-  const float *sc = p.axis ? p.scales + tile * DK + col0 : p.scales + srow * p.ng + col0 / p.G;
-  if (bits != 32 && !LORES_IN(p, kRgScales, sc, p.axis ? 64 : 4)) return;
-  float y[16];
-  if (bits == 32) {
+  const long long tile = (long long)slot * p.H + head;
+  const uint8_t *codes = p.codes + slot * p.seq_bytes + __ldg(p.head_off + head);
+  const float *scales = p.axis ? p.scales + tile * DK + col0 : p.scales + tile * p.d_v * p.ng + col0 / p.G;
+  const long long dst_tile = ((long long)entry * p.H + head) * p.d_v;
+  // 16 codes as they lie (fp32 heads: two rows' worth of registers hold them) and the row's scale
+  uint4 raw[kPoolRows];
+  float s[kPoolRows];
+  bool in[kPoolRows];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = reinterpret_cast<const float4 *>(rowp + f.off)[c];
-      y[4 * c] = v.x; y[4 * c + 1] = v.y; y[4 * c + 2] = v.z; y[4 * c + 3] = v.w;
+  for (int r = 0; r < kPoolRows; ++r) {
+    const int row = row0 + r * STEP;
+    const uint8_t *rowp = codes + (size_t)row * f.rowb;
+    const float *sc = p.axis ? scales : scales + (long long)row * p.ng;
+    in[r] = row < p.d_v && LORES_IN(p, kRgCodes, rowp, f.rowb) &&
+            (bits == 32 || LORES_IN(p, kRgScales, sc, p.axis ? 64 : 4));
+    raw[r] = make_uint4(0, 0, 0, 0);
+    s[r] = 0.0f;
+    if (in[r] && bits != 32) {
+      if (f.store >= 5 && f.store <= 7) {
+        const DenseLane d = f.store == 5 ? ld_dense<5>(rowp, DK, lir) : f.store == 6 ? ld_dense<6>(rowp, DK, lir) : ld_dense<7>(rowp, DK, lir);
+        raw[r] = make_uint4(d.nib0, d.nib1, d.p2, d.p1);
+      } else if (bits != 4) {
+        raw[r] = ld16_a8(rowp + f.off);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(rowp + f.off);
+        raw[r] = make_uint4(w.x, w.y, 0, 0);
+      }
+      if (!p.axis) s[r] = *sc;
     }
-  } else {
-    if (f.store >= 5 && f.store <= 7) {
-      float2 c2[8];
-      if (f.store == 5) unpack_dense<5>(ld_dense<5>(rowp, DK, lir), c2);
-      else if (f.store == 6) unpack_dense<6>(ld_dense<6>(rowp, DK, lir), c2);
-      else unpack_dense<7>(ld_dense<7>(rowp, DK, lir), c2);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) { y[2 * e] = c2[e].x; y[2 * e + 1] = c2[e].y; }
-    } else if (bits != 4) {
-      unpack_i8(ld16_a8(rowp + f.off), y);
-    } else {
-      unpack_i4(*reinterpret_cast<const uint2 *>(rowp + f.off), y);
-    }
-    const float s = p.axis ? 0.0f : *sc;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(y[e], p.axis ? sc[e] : s);
   }
-  const long long at = ((long long)entry * p.H * p.d_v + gr) * DK + col0;
-  const void *dst = static_cast<const uint8_t *>(p.dst) + at * (p.dtype == 0 ? 4 : 2);
-  if (LORES_IN(p, kRgS, dst, p.dtype == 0 ? 64 : 32)) store_row16(p, at, y);
+#pragma unroll
+  for (int r = 0; r < kPoolRows; ++r) {
+    const int row = row0 + r * STEP;
+    if (!in[r]) continue;
+    float y[16];
+    if (bits == 32) {
+      const float4 *src = reinterpret_cast<const float4 *>(codes + (size_t)row * f.rowb + f.off);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = src[c];
+        y[4 * c] = v.x; y[4 * c + 1] = v.y; y[4 * c + 2] = v.z; y[4 * c + 3] = v.w;
+      }
+    } else {
+      if (f.store >= 5 && f.store <= 7) {
+        const DenseLane d{raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+        float2 c2[8];
+        if (f.store == 5) unpack_dense<5>(d, c2);
+        else if (f.store == 6) unpack_dense<6>(d, c2);
+        else unpack_dense<7>(d, c2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { y[2 * e] = c2[e].x; y[2 * e + 1] = c2[e].y; }
+      } else if (bits != 4) {
+        unpack_i8(raw[r], y);
+      } else {
+        unpack_i4(make_uint2(raw[r].x, raw[r].y), y);
+      }
+      if (p.axis) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(y[e], scales[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(y[e], s[r]);
+      }
+    }
+    const long long at = (dst_tile + row) * DK + col0;
+    const void *dst = static_cast<const uint8_t *>(p.dst) + at * (p.dtype == 0 ? 4 : 2);
+    if (LORES_IN(p, kRgS, dst, p.dtype == 0 ? 64 : 32)) store_row16(p, at, y);
+  }
 }
 
 using PoolFn = void (*)(PoolParams);

@@ -217,12 +217,16 @@ int walk_blocks(const Shape &s) {
 bool aligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3u) == 0; }
 bool given16(const void *x, bool needed) { return aligned16(x) && (x || !needed); }
 
-cudaError_t run_prep(const Shape &s, bool backward, const ScanParams &p, cudaStream_t st) {
+cudaError_t run_prep(const Shape &s, bool backward, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
   static std::atomic<unsigned long long> raised[4][2][2][2];
   const int wi = width_index(c.d_k);
-  return launch(kernels().by_width[wi].prep[s.np - 1][c.delta][backward], dim3(s.n_slots, c.heads), kPrepThreads,
-                prep_layout(c.d_k, s.np).bytes, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
+  // as many of the heads that share q and k per CTA as leave every SM its four CTAs
+  p.hpc = 1;
+  for (int d = 2; d <= p.share; ++d)
+    if (p.share % d == 0 && (long long)s.n_slots * (c.heads / d) >= 4ll * sm_count(c.device)) p.hpc = d;
+  return launch(kernels().by_width[wi].prep[s.np - 1][c.delta][backward], dim3(s.n_slots, c.heads / p.hpc), kPrepThreads,
+                prep_layout(c.d_k, s.np, p.hpc > 1).bytes, st, c.device, p, raised[wi][s.np - 1][c.delta][backward]);
 }
 
 cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t st) {
@@ -299,10 +303,10 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
   p.o = o;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (s.recurrent) {
-    const long long lanes = (long long)c.n_seq * c.heads * (c.d_v / kRecRows) * (c.d_k / 16);
-    const long long blocks = (lanes + kRecThreads - 1) / kRecThreads;
-    if (blocks > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
-    kernels().recurrent[width_index(c.d_k)][c.delta]<<<(unsigned)blocks, kRecThreads, 0, cs>>>(p);
+    const int lpr = c.d_k / 16, groups = c.d_v / kRecRows;
+    const int threads = std::min(kRecThreads, (groups * lpr + 31) / 32 * 32), rows = threads / lpr * kRecRows;
+    kernels().recurrent[width_index(c.d_k)][c.delta]<<<dim3(c.n_seq * c.heads, (c.d_v + rows - 1) / rows), threads, 0,
+                                                       cs>>>(p);
     return cuda_status(cudaGetLastError());
   }
   cudaError_t e = run_prep(s, false, p, cs);

@@ -51,6 +51,7 @@ constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran o
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
   int rb;                              // walks: blocks of 16 value rows per CTA
+  int hpc;                             // scan_prep: heads per CTA (a divisor of share)
   int qk16, v16, o16;                  // 16-byte accesses to q and k, v (and dv), o (or d_o) rows
   long long total;
   const int *offsets;
@@ -78,8 +79,8 @@ struct ScanParams {
 };
 
 // Record of a chunk and head, kChunk entries each: e^G, w over the scale of K (that is, what
-// multiplies a row of khat), e^G likewise, w, b, e^(G_C - G); G (double); the scales of K and Q.
-enum GateRow { kGateE, kGateWk, kGateEk, kGateW, kGateB, kGateC, kGateG };
+// multiplies a row of khat), e^G likewise, w, b, e^(G_C - G); G / ln 2 as a pair of floats; the scales of K and Q.
+enum GateRow { kGateE, kGateWk, kGateEk, kGateW, kGateB, kGateC, kGateG };   // kGateG: two rows' worth of pairs
 constexpr int kGateScales = (kGateG + 2) * kChunk;
 constexpr int kGateFloats = kGateScales + 4;
 enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR };
@@ -282,6 +283,13 @@ __device__ __forceinline__ float scale_of(unsigned bits, int up, float &inv) {
   inv = __uint_as_float((unsigned)(254 - e) << 23);
   return __uint_as_float((unsigned)e << 23);
 }
+// dec_ts = 2^(g_t - g_s), g a pair of floats (48 bits, so that the difference keeps its digits behind a
+// strong decay).
+__device__ __forceinline__ float decay(float2 gt, float2 gs) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(__fsub_rn(gt.x, gs.x), __fsub_rn(gt.y, gs.y))));
+  return r;
+}
 __device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // -------------------------------------------------------------------------------------
@@ -376,8 +384,9 @@ __device__ __forceinline__ void load8(const void *src, int dtype, long long i, b
 // -------------------------------------------------------------------------------------
 // scan_prep
 // -------------------------------------------------------------------------------------
-// Grid (slot, head), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.] result, and only
-// blocks on and below the diagonal are formed.  Tm = (I + A)^-1, A = L diag(b), by 16x16 blocks:
+// Grid (slot, group of p.hpc heads that share K and Q), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.]
+// result, and only blocks on and below the diagonal are formed.  K and Q are fetched and converted
+// once for the group.  Tm = (I + A)^-1, A = L diag(b), by 16x16 blocks:
 // the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
 // forms block column j downwards, X_ij = -X_ii sum_{j <= k < i} A_ik X_kj, as
 // X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
@@ -385,14 +394,16 @@ __device__ __forceinline__ void load8(const void *src, int dtype, long long i, b
 constexpr int kLdF = kChunk + 2;       // row stride of the fp32 matrix in shared memory
 
 struct PrepLayout {
-  int k, q, x, xd, f, bytes;           // q: also the planes of A once Q is used
+  int k, q, a, x, xd, f, bytes;
 };
-__host__ __device__ constexpr PrepLayout prep_layout(int dk, int np) {
+// `several`: heads per CTA.  For one, the planes of A take Q's place once Q is used.
+__host__ __device__ constexpr PrepLayout prep_layout(int dk, int np, bool several) {
   PrepLayout l{};
   const int tile = np * kChunk * dk * 2, planes = 2 * kChunk * kChunk * 2;
   l.k = 0;
   l.q = tile;
-  l.x = l.q + (tile > planes ? tile : planes);
+  l.a = several ? l.q + tile : l.q;
+  l.x = several ? l.a + planes : l.q + (tile > planes ? tile : planes);
   l.xd = l.x + kChunk * kLdF * 4;
   l.f = l.xd + 4 * 2 * 16 * 16 * 2;
   l.bytes = l.f + (3 * kChunk + 2 * kChunk + 16) * 4;
@@ -441,15 +452,21 @@ __device__ __forceinline__ void unpack_row(const uint4 (&raw)[NP], int dtype, fl
     }
   }
 }
+// Bits (of fp32) of the warp's largest magnitude; 16-bit types are compared as integers, two at a time.
 template <int NP, int PASS>
 __device__ __forceinline__ unsigned max_rows(const uint4 (&raw)[PASS][NP], int dtype) {
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < PASS; ++i) {
-    float x[8];
-    unpack_row<NP>(raw[i], dtype, x);
+  for (int i = 0; i < PASS; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
+    for (int h = 0; h < NP; ++h) {
+      const uint32_t u[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = NP == 2 ? max(m, u[e] & 0x7FFFFFFFu) : __vmaxu2(m, u[e] & 0x7FFF7FFFu);
+    }
+  if (NP == 1) {
+    const uint32_t w = max(m & 0xFFFFu, m >> 16);
+    m = dtype == 1 ? w << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)w)));
   }
   return __reduce_max_sync(0xFFFFFFFFu, m);
 }
@@ -491,37 +508,38 @@ __device__ __forceinline__ void put_pair(__half *dst, long long plane, int r0, i
 
 template <int DK, int NP, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kernel(const ScanParams p) {
-  constexpr PrepLayout l = prep_layout(DK, NP);
   constexpr int PASS = (kChunk * DK / 8 + kPrepThreads - 1) / kPrepThreads;
+  const bool several = p.hpc > 1;
+  const PrepLayout l = prep_layout(DK, NP, several);
   extern __shared__ __align__(16) uint8_t smem[];
   __half *K = reinterpret_cast<__half *>(smem + l.k), *Q = reinterpret_cast<__half *>(smem + l.q);
-  __half *A16 = Q;                                                  // [2][64][64]
+  __half *A16 = reinterpret_cast<__half *>(smem + l.a);             // [2][64][64]
   float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then Tm
   __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][16]: X_ii
-  double *G = reinterpret_cast<double *>(smem + l.f);
-  float *ek = reinterpret_cast<float *>(G + kChunk), *wk = ek + kChunk, *be = wk + kChunk;
-  unsigned *red = reinterpret_cast<unsigned *>(be + kChunk);
+  float2 *G = reinterpret_cast<float2 *>(smem + l.f);
+  float *ek = reinterpret_cast<float *>(G + kChunk), *wk = ek + kChunk, *bk = wk + kChunk;
+  unsigned *red = reinterpret_cast<unsigned *>(bk + kChunk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int slot = blockIdx.x, head = blockIdx.y;
-  if (slot == 0 && head == 0) check_offsets(p);
+  const int slot = blockIdx.x, head0 = blockIdx.y * p.hpc;
+  if (slot == 0 && head0 == 0) check_offsets(p);
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
   if (n == 0) return;
-  const int qh = head / p.share, hq = p.H / p.share;
-  const long long rec = (long long)slot * p.H + head, qrec = (long long)slot * hq + qh;
-  const bool mine = head % p.share == 0;           // the first of the heads that share K and Q keeps them
-  // log_alpha and beta of tokens 2 lane, 2 lane + 1, in flight beside the rows
-  float la[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
-  if (warp == 3)
+  const int qh = head0 / p.share, hq = p.H / p.share;
+  const long long qrec = (long long)slot * hq + qh;
+  const bool mine = head0 % p.share == 0;          // the first of the heads that share K and Q keeps them
+  // log_alpha and beta of tokens 2 lane, 2 lane + 1 of a head, in flight one head ahead
+  float la[2], b[2];
+  auto load_gates = [&](int head) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const long long at = (token0 + t) * p.H + head;
-      if (t < n) {
-        la[i] = __ldg(p.log_alpha + at);
-        b[i] = __ldg(p.beta + at);
-      }
+      la[i] = t < n ? __ldg(p.log_alpha + at) : 0.0f;
+      b[i] = t < n ? __ldg(p.beta + at) : 0.0f;
     }
+  };
+  if (warp == 3) load_gates(head0);
   float sk, sq;
   {
     __half *ko = mine ? p.khat + qrec * (NP * kChunk * DK) : nullptr, *qo = mine ? p.qhat + qrec * (NP * kChunk * DK) : nullptr;
@@ -555,282 +573,294 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       put_rows<DK, NP, PASS>(xk, p.dtype, inv, Q, qo, tid);
     }
   }
-  if (warp == 3) {
-    // Sums of log_alpha in 64 bits, so that the differences below keep their digits behind a
-    // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
-    // held there and G stays finite.
-    float *gates = p.gates + rec * kGateFloats;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (la[i] < -1000.0f) la[i] = -1000.0f;
-    double run = (double)la[0] + (double)la[1];
-    for (int d = 1; d < 32; d <<= 1) {
-      const double up = __shfl_up_sync(0xFFFFFFFFu, run, d);
-      if (lane >= d) run += up;
-    }
-    const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
-    const double Gt[2] = {run - (double)la[1], run};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = 2 * lane + i;
-      const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i])), w = b[i] * c;
-      G[t] = Gt[i];
-      ek[t] = e * sk; be[t] = b[i]; wk[t] = w * sk;
-      gates[kGateE * kChunk + t] = e;
-      gates[kGateWk * kChunk + t] = w * sk;
-      gates[kGateEk * kChunk + t] = e * sk;
-      gates[kGateW * kChunk + t] = w;
-      gates[kGateB * kChunk + t] = b[i];
-      gates[kGateC * kChunk + t] = c;
-      reinterpret_cast<double *>(gates + kGateG * kChunk)[t] = Gt[i];
-    }
-    if (lane == 0) {
-      gates[kGateScales] = sk;
-      gates[kGateScales + 1] = sq;
-    }
-  }
-  __syncthreads();
-
   const Lane<DK> ld(lane);
   const uint32_t sK = smem_addr(K), sQ = smem_addr(Q);
   constexpr uint32_t LO = kChunk * DK * 2;         // bytes from a plane to the next
   const int m0 = warp * 16;
-  float P[8][4];
+#pragma unroll 1
+  for (int head = head0; head < head0 + p.hpc; ++head) {
+    const long long rec = (long long)slot * p.H + head;
+    if (head > head0) __syncthreads();             // the last head's gates and matrices are used
+    if (warp == 3) {
+      // Sums of log_alpha in 64 bits, so that their differences keep their digits behind a
+      // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
+      // held there and G stays finite.
+      float *gates = p.gates + rec * kGateFloats;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 2; ++i)
+        if (la[i] < -1000.0f) la[i] = -1000.0f;
+      double run = (double)la[0] + (double)la[1];
+      for (int d = 1; d < 32; d <<= 1) {
+        const double up = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (lane >= d) run += up;
+      }
+      const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
+      const double Gt[2] = {run - (double)la[1], run};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) P[i][j] = 0.0f;
-  {
-    float A[8][4];
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i])), w = b[i] * c;
+        const double l2 = Gt[i] * 1.4426950408889634;
+        const float hi = (float)l2;
+        const float2 pair = make_float2(hi, (float)(l2 - (double)hi));
+        G[t] = pair;
+        ek[t] = e * sk; bk[t] = b[i] * sk; wk[t] = w * sk;
+        gates[kGateE * kChunk + t] = e;
+        gates[kGateWk * kChunk + t] = w * sk;
+        gates[kGateEk * kChunk + t] = e * sk;
+        gates[kGateW * kChunk + t] = w;
+        gates[kGateB * kChunk + t] = b[i];
+        gates[kGateC * kChunk + t] = c;
+        reinterpret_cast<float2 *>(gates + kGateG * kChunk)[t] = pair;
+      }
+      if (lane == 0) {
+        gates[kGateScales] = sk;
+        gates[kGateScales + 1] = sq;
+      }
+      if (head + 1 < head0 + p.hpc) load_gates(head + 1);
+    }
+    __syncthreads();
+
+    float P[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) A[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) P[i][j] = 0.0f;
+    {
+      float A[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A[i][j] = 0.0f;
 #pragma unroll 2
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t ak[NP][4], aq[NP][4];
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
-      for (int c = 0; c < NP; ++c) {
-        if (DELTA) ld.a_rows(ak[c], sK + c * LO, m0, ks * 16);
-        ld.a_rows(aq[c], sQ + c * LO, m0, ks * 16);
-      }
+        for (int c = 0; c < NP; ++c) {
+          if (DELTA) ld.a_rows(ak[c], sK + c * LO, m0, ks * 16);
+          ld.a_rows(aq[c], sQ + c * LO, m0, ks * 16);
+        }
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        if (np <= warp) {
-          uint32_t r[4];
-          ld.b_rows(r, sK, np * 16, ks * 16);
+        for (int np = 0; np < 4; ++np) {
+          if (np <= warp) {
+            uint32_t r[4];
+            ld.b_rows(r, sK, np * 16, ks * 16);
 #pragma unroll
-          for (int c = 0; c < NP; ++c) {
-            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], r);
-            mma2(P[2 * np], P[2 * np + 1], aq[c], r);
-          }
-          if (NP == 2) {
-            ld.b_rows(r, sK + LO, np * 16, ks * 16);
-            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], r);
-            mma2(P[2 * np], P[2 * np + 1], aq[0], r);
+            for (int c = 0; c < NP; ++c) {
+              if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], r);
+              mma2(P[2 * np], P[2 * np + 1], aq[c], r);
+            }
+            if (NP == 2) {
+              ld.b_rows(r, sK + LO, np * 16, ks * 16);
+              if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], r);
+              mma2(P[2 * np], P[2 * np + 1], aq[0], r);
+            }
           }
         }
       }
-    }
-    if (DELTA) __syncthreads();        // Q's tile becomes A's planes
-    // P (over the scale of Q) and, strictly below the diagonal, A
+      if (DELTA && !several) __syncthreads();      // Q's tile becomes A's planes
+      // P (over the scale of Q) and, strictly below the diagonal, A
+      const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
+      __half *pp = p.pp + rec * (2 * kChunk * kChunk);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i / 2 <= warp) {
+      for (int i = 0; i < 8; ++i) {
+        if (i / 2 <= warp) {
+          const float4 gs = *reinterpret_cast<const float4 *>(G + 8 * i + t2);
+          const float2 bs = *reinterpret_cast<const float2 *>(bk + 8 * i + t2);
+          const bool diagonal = i / 2 == warp;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int t = m0 + g + 8 * h, s = 8 * i + t2;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float dec = s + j <= t ? expf((float)(G[t] - G[s + j])) * be[s + j] * sk : 0.0f;
-            P[i][2 * h + j] = s + j <= t ? P[i][2 * h + j] * dec : 0.0f;
-            if (DELTA) A[i][2 * h + j] = s + j < t ? A[i][2 * h + j] * dec * sk : 0.0f;
-          }
-          if (DELTA) {
-            if (i / 2 == warp) {
-              X[t * kLdF + s] = A[i][2 * h];
-              X[t * kLdF + s + 1] = A[i][2 * h + 1];
-            } else {
-              put_pair<kChunk>(A16, kChunk * kChunk, m0 + 8 * h, 8 * i, A[i][2 * h], A[i][2 * h + 1], lane);
+          for (int h = 0; h < 2; ++h) {
+            float d0 = decay(gt[h], make_float2(gs.x, gs.y)) * bs.x, d1 = decay(gt[h], make_float2(gs.z, gs.w)) * bs.y;
+            float a0 = A[i][2 * h] * (d0 * sk), a1 = A[i][2 * h + 1] * (d1 * sk);
+            float p0 = P[i][2 * h] * d0, p1 = P[i][2 * h + 1] * d1;
+            if (diagonal) {
+              const int t = m0 + g + 8 * h, s = 8 * i + t2;
+              p0 = s <= t ? p0 : 0.0f;
+              p1 = s + 1 <= t ? p1 : 0.0f;
+              if (DELTA) {
+                X[t * kLdF + s] = s < t ? a0 : 0.0f;
+                X[t * kLdF + s + 1] = s + 1 < t ? a1 : 0.0f;
+              }
+            } else if (DELTA) {
+              put_pair<kChunk>(A16, kChunk * kChunk, m0 + 8 * h, 8 * i, a0, a1, lane);
+            }
+            P[i][2 * h] = p0;
+            P[i][2 * h + 1] = p1;
+            if (!BWD || !DELTA) {
+              if (NP == 2 || BWD) put_pair<kChunk>(pp, kChunk * kChunk, m0 + 8 * h, 8 * i, p0, p1, lane);
+              else             // (16-bit outputs need one plane)
+                *reinterpret_cast<uint32_t *>(pp + tiled<kChunk>(m0 + 8 * h, 8 * i) + 2 * lane) = pack2(p0, p1);
             }
           }
         }
       }
     }
-  }
-  if (!BWD || !DELTA) {
-    __half *pp = p.pp + rec * (2 * kChunk * kChunk);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i / 2 <= warp)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (NP == 2 || BWD)
-            put_pair<kChunk>(pp, kChunk * kChunk, m0 + 8 * h, 8 * i, P[i][2 * h], P[i][2 * h + 1], lane);
-          else             // (16-bit outputs need one plane)
-            *reinterpret_cast<uint32_t *>(pp + tiled<kChunk>(m0 + 8 * h, 8 * i) + 2 * lane) = pack2(P[i][2 * h], P[i][2 * h + 1]);
-        }
-  }
-  if (!DELTA) return;
-  __syncwarp();
-  {
-    // this warp's diagonal block: lanes c and c + 16 hold column c of its inverse
-    const int c = lane & 15;
-    float x[16];
-    float *B = X + m0 * kLdF + m0;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) x[r] = r == c ? 1.0f : 0.0f;
-#pragma unroll
-    for (int r = 0; r < 15; ++r)
-#pragma unroll
-      for (int i = r + 1; i < 16; ++i) x[i] = fmaf(-B[i * kLdF + r], x[r], x[i]);
+    if (!DELTA) continue;
     __syncwarp();
-    if (lane < 16) {
-      __half *d = XD + warp * 512;
+    {
+      // this warp's diagonal block: lanes c and c + 16 hold column c of its inverse
+      const int c = lane & 15;
+      float x[16];
+      float *B = X + m0 * kLdF + m0;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        B[r * kLdF + c] = x[r];
-        const __half hi = __float2half_rn(x[r]);
-        d[tiled<16>(r, c)] = hi;
-        d[256 + tiled<16>(r, c)] = __float2half_rn(x[r] - __half2float(hi));
-      }
-    }
-  }
-  __syncthreads();
-  {
-    // block column `warp`: yh, yl[k] = planes of X_kj^T
-    const Lane<16> l16(lane);
-    const Lane<kChunk> l64(lane);
-    const uint32_t sA = smem_addr(A16), sD = smem_addr(XD);
-    uint32_t yh[4][4], yl[4][4];
-    l16.a_cols(yh[0], sD + warp * 1024, 0, 0);     // X_jj^T: element (m, k) = X_jj[k][m]
-    l16.a_cols(yl[0], sD + warp * 1024 + 512, 0, 0);
+      for (int r = 0; r < 16; ++r) x[r] = r == c ? 1.0f : 0.0f;
 #pragma unroll
-    for (int di = 1; di < 4; ++di) {
-      const int i = warp + di;
-      if (i < 4) {
-        float z0[4] = {0, 0, 0, 0}, z1[4] = {0, 0, 0, 0};
+      for (int r = 0; r < 15; ++r)
 #pragma unroll
-        for (int dk = 0; dk < di; ++dk) {
-          uint32_t r[4];
-          l64.b_rows(r, sA, 16 * i, 16 * (warp + dk));
-          mma2(z0, z1, yh[dk], r);
-          mma2(z0, z1, yl[dk], r);
-          l64.b_rows(r, sA + 2 * kChunk * kChunk, 16 * i, 16 * (warp + dk));
-          mma2(z0, z1, yh[dk], r);
-        }
-        uint32_t zh[4], zl[4], r[4];
-        split_tiles(z0, z1, -1.0f, zh, zl);
-        float y0[4] = {0, 0, 0, 0}, y1[4] = {0, 0, 0, 0};
-        l16.b_rows(r, sD + i * 1024, 0, 0);
-        mma2(y0, y1, zh, r);
-        mma2(y0, y1, zl, r);
-        l16.b_rows(r, sD + i * 1024 + 512, 0, 0);
-        mma2(y0, y1, zh, r);
-        split_tiles(y0, y1, yh[di], yl[di]);
+        for (int i = r + 1; i < 16; ++i) x[i] = fmaf(-B[i * kLdF + r], x[r], x[i]);
+      __syncwarp();
+      if (lane < 16) {
+        __half *d = XD + warp * 512;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // y[c][r] -> X[16 i + r][16 warp + c]
-          const int c = g + 8 * (j >> 1), r2 = t2 + (j & 1);
-          X[(16 * i + r2) * kLdF + m0 + c] = y0[j];
-          X[(16 * i + 8 + r2) * kLdF + m0 + c] = y1[j];
+        for (int r = 0; r < 16; ++r) {
+          B[r * kLdF + c] = x[r];
+          const __half hi = __float2half_rn(x[r]);
+          d[tiled<16>(r, c)] = hi;
+          d[256 + tiled<16>(r, c)] = __float2half_rn(x[r] - __half2float(hi));
         }
       }
     }
-  }
-  __syncthreads();
+    __syncthreads();
+    {
+      // block column `warp`: yh, yl[k] = planes of X_kj^T
+      const Lane<16> l16(lane);
+      const Lane<kChunk> l64(lane);
+      const uint32_t sA = smem_addr(A16), sD = smem_addr(XD);
+      uint32_t yh[4][4], yl[4][4];
+      l16.a_cols(yh[0], sD + warp * 1024, 0, 0);     // X_jj^T: element (m, k) = X_jj[k][m]
+      l16.a_cols(yl[0], sD + warp * 1024 + 512, 0, 0);
+#pragma unroll
+      for (int di = 1; di < 4; ++di) {
+        const int i = warp + di;
+        if (i < 4) {
+          float z0[4] = {0, 0, 0, 0}, z1[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int dk = 0; dk < di; ++dk) {
+            uint32_t r[4];
+            l64.b_rows(r, sA, 16 * i, 16 * (warp + dk));
+            mma2(z0, z1, yh[dk], r);
+            mma2(z0, z1, yl[dk], r);
+            l64.b_rows(r, sA + 2 * kChunk * kChunk, 16 * i, 16 * (warp + dk));
+            mma2(z0, z1, yh[dk], r);
+          }
+          uint32_t zh[4], zl[4], r[4];
+          split_tiles(z0, z1, -1.0f, zh, zl);
+          float y0[4] = {0, 0, 0, 0}, y1[4] = {0, 0, 0, 0};
+          l16.b_rows(r, sD + i * 1024, 0, 0);
+          mma2(y0, y1, zh, r);
+          mma2(y0, y1, zl, r);
+          l16.b_rows(r, sD + i * 1024 + 512, 0, 0);
+          mma2(y0, y1, zh, r);
+          split_tiles(y0, y1, yh[di], yl[di]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {   // y[c][r] -> X[16 i + r][16 warp + c]
+            const int c = g + 8 * (j >> 1), r2 = t2 + (j & 1);
+            X[(16 * i + r2) * kLdF + m0 + c] = y0[j];
+            X[(16 * i + 8 + r2) * kLdF + m0 + c] = y1[j];
+          }
+        }
+      }
+    }
+    __syncthreads();
 
-  // planes of Tm (blocks on and below the diagonal)
-  __half *tm = p.tm + rec * (2 * kChunk * kChunk);
-  for (int i = tid; i < kChunk * 8; i += kPrepThreads) {
-    const int r = i >> 3, c = (i & 7) * 8;
-    if ((c >> 4) <= (r >> 4)) {
-      uint4 hi, lo;
-      const float *x = X + r * kLdF + c;
-      split2(x[0], x[1], hi.x, lo.x);
-      split2(x[2], x[3], hi.y, lo.y);
-      split2(x[4], x[5], hi.z, lo.z);
-      split2(x[6], x[7], hi.w, lo.w);
-      const int at = tiled<kChunk>(r, c);
-      *reinterpret_cast<uint4 *>(tm + at) = hi;
-      *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + at) = lo;
+    // planes of Tm (blocks on and below the diagonal)
+    __half *tm = p.tm + rec * (2 * kChunk * kChunk);
+#pragma unroll
+    for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
+      const int i = tid + j * kPrepThreads, r = i >> 3, c = (i & 7) * 8;
+      if ((c >> 4) <= (r >> 4)) {
+        uint4 hi, lo;
+        const float *x = X + r * kLdF + c;
+        split2(x[0], x[1], hi.x, lo.x);
+        split2(x[2], x[3], hi.y, lo.y);
+        split2(x[4], x[5], hi.z, lo.z);
+        split2(x[6], x[7], hi.w, lo.w);
+        const int at = tiled<kChunk>(r, c);
+        *reinterpret_cast<uint4 *>(tm + at) = hi;
+        *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + at) = lo;
+      }
     }
-  }
-  // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own; then Kb = Tm^T diag(w) K: rows s
-  // of this warp, t blocks from its own on.  Two halves of the columns, so that the
-  // accumulators leave room for four CTAs per SM.
-  constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
+    if (BWD) {
+      // Z = P Tm (over the scale of Q): rows t of this warp; block (r, s) of Tm is zero for s > r
+      float acc[8][4];
 #pragma unroll
-  for (int which = 0; which < (BWD ? 2 : 1); ++which) {
-    __half *dst = (which ? p.kb : p.kt) + rec * (2 * kChunk * DK);
-#pragma unroll 1
-    for (int half = 0; half < HALVES; ++half) {
-      float acc[HT][4];
-#pragma unroll
-      for (int i = 0; i < HT; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        if (which ? ks >= warp : ks <= warp) {
-          uint32_t ah[4], al[4], r[4];
+        if (ks <= warp) {
+          uint32_t ah[4], al[4];
+          split_tiles(P[2 * ks], P[2 * ks + 1], ah, al);
+#pragma unroll
+          for (int i = 0; i < 2 * ks + 2; ++i) {
+            const float *c = X + (ks * 16 + t2) * kLdF + 8 * i + g;
+            uint32_t h0, l0, h1, l1;
+            split2(c[0], c[kLdF], h0, l0);
+            split2(c[8 * kLdF], c[9 * kLdF], h1, l1);
+            mma(acc[i], ah, h0, h1);
+            mma(acc[i], ah, l0, l1);
+            mma(acc[i], al, h0, h1);
+          }
+        }
+      }
+      __half *z = p.z + rec * (2 * kChunk * kChunk);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i / 2 <= warp)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
+    }
+    // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own; then Kb = Tm^T diag(w) K: rows s
+    // of this warp, t blocks from its own on.  Two halves of the columns, so that the
+    // accumulators leave room for four CTAs per SM.
+    constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
+#pragma unroll
+    for (int which = 0; which < (BWD ? 2 : 1); ++which) {
+      __half *dst = (which ? p.kb : p.kt) + rec * (2 * kChunk * DK);
+      uint32_t ah[4][4], al[4][4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        if (which ? ks >= warp : ks <= warp)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int m = m0 + g + 8 * (q & 1), k = ks * 16 + t2 + 8 * (q >> 1);
-            if (which) split2(X[k * kLdF + m] * wk[k], X[(k + 1) * kLdF + m] * wk[k + 1], ah[q], al[q]);
-            else split2(-X[m * kLdF + k] * ek[k], -X[m * kLdF + k + 1] * ek[k + 1], ah[q], al[q]);
+            if (which) split2(X[k * kLdF + m] * wk[k], X[(k + 1) * kLdF + m] * wk[k + 1], ah[ks][q], al[ks][q]);
+            else split2(-X[m * kLdF + k] * ek[k], -X[m * kLdF + k + 1] * ek[k + 1], ah[ks][q], al[ks][q]);
           }
+#pragma unroll 1
+      for (int half = 0; half < HALVES; ++half) {
+        float acc[HT][4];
 #pragma unroll
-          for (int np = 0; np < HT / 2; ++np) {
-            const int c0 = half * (DK / HALVES) + np * 16;
-            ld.b_cols(r, sK, ks * 16, c0);
-            mma2(acc[2 * np], acc[2 * np + 1], ah, r);
-            mma2(acc[2 * np], acc[2 * np + 1], al, r);
+        for (int i = 0; i < HT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (which ? ks >= warp : ks <= warp) {
+            uint32_t r[HT / 2][4];
+#pragma unroll
+            for (int np = 0; np < HT / 2; ++np) ld.b_cols(r[np], sK, ks * 16, half * (DK / HALVES) + np * 16);
+#pragma unroll
+            for (int np = 0; np < HT / 2; ++np) mma2(acc[2 * np], acc[2 * np + 1], ah[ks], r[np]);
+#pragma unroll
+            for (int np = 0; np < HT / 2; ++np) mma2(acc[2 * np], acc[2 * np + 1], al[ks], r[np]);
             if (NP == 2) {
-              ld.b_cols(r, sK + LO, ks * 16, c0);
-              mma2(acc[2 * np], acc[2 * np + 1], ah, r);
+#pragma unroll
+              for (int np = 0; np < HT / 2; ++np) ld.b_cols(r[np], sK + LO, ks * 16, half * (DK / HALVES) + np * 16);
+#pragma unroll
+              for (int np = 0; np < HT / 2; ++np) mma2(acc[2 * np], acc[2 * np + 1], ah[ks], r[np]);
             }
           }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < HT; ++i)
+        for (int i = 0; i < HT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          put_pair<DK>(dst, kChunk * DK, m0 + 8 * h, half * (DK / HALVES) + 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
-    }
-  }
-  if (!BWD) return;
-  // Z = P Tm (over the scale of Q): rows t of this warp; block (r, s) of Tm is zero for s > r
-  {
-    float acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks <= warp) {
-        uint32_t ah[4], al[4];
-        split_tiles(P[2 * ks], P[2 * ks + 1], ah, al);
-#pragma unroll
-        for (int i = 0; i < 2 * ks + 2; ++i) {
-          const float *c = X + (ks * 16 + t2) * kLdF + 8 * i + g;
-          uint32_t h0, l0, h1, l1;
-          split2(c[0], c[kLdF], h0, l0);
-          split2(c[8 * kLdF], c[9 * kLdF], h1, l1);
-          mma(acc[i], ah, h0, h1);
-          mma(acc[i], ah, l0, l1);
-          mma(acc[i], al, h0, h1);
-        }
+          for (int h = 0; h < 2; ++h)
+            put_pair<DK>(dst, kChunk * DK, m0 + 8 * h, half * (DK / HALVES) + 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
       }
     }
-    __half *z = p.z + rec * (2 * kChunk * kChunk);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i / 2 <= warp)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
   }
 }
 
@@ -1648,7 +1678,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   float *gates = reinterpret_cast<float *>(smem + l.f);
   const float *eG = gates + kGateE * kChunk, *w = gates + kGateW * kChunk, *be = gates + kGateB * kChunk,
               *eC = gates + kGateC * kChunk;
-  const double *G = reinterpret_cast<const double *>(gates + kGateG * kChunk);
+  const float2 *G = reinterpret_cast<const float2 *>(gates + kGateG * kChunk);
   float *rowv = gates + kGateFloats, *aq = rowv + kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
         *red = colp + 4 * kChunk;
   copy_flat<NP * TILE>(smem + l.k, p.khat + qrec * (NP * kChunk * DK), tid, kGradThreads);
@@ -1838,54 +1868,67 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
     float rs[2] = {0.0f, 0.0f}, cs[8][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i][0] = cs[i][1] = 0.0f;
-    // pass 0: q_t.k_s with dO E^T -> dP'; pass 1: k_t.k_s with R E^T -> dL'.  By 16 columns s, so
-    // that few registers hold the products.
+    // q_t.k_s with dO E^T -> dP', k_t.k_s with R E^T -> dL', by 16 columns s, so that few registers hold the products
+    const float toq = qscale * kappa, tok = -kappa * kappa;
+    __half *out = reinterpret_cast<__half *>(smem + l.x);
+    const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
 #pragma unroll
-    for (int ps = 0; ps < (DELTA ? 2 : 1); ++ps) {
-      const uint32_t left = ps ? sk : sq;
-      const float to = (ps ? kappa : qscale) * kappa;
-      __half *out = reinterpret_cast<__half *>(smem + l.x) + ps * 2 * kChunk * kChunk;
+    for (int np = 0; np < 4; ++np) {
+      if (np <= w4) {
+        float x[2][2][4];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        if (np <= w4) {
-          float x[2][4];
+        for (int j = 0; j < 4; ++j) x[0][0][j] = x[0][1][j] = x[1][0][j] = x[1][1][j] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[0][j] = x[1][j] = 0.0f;
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          uint32_t a[2][NP][4], b4[4];
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks) {
-            uint32_t a[NP][4], b4[4];
-#pragma unroll
-            for (int c = 0; c < NP; ++c) ld.a_rows(a[c], left + c * TILE, m0, ks * 16);
-            ld.b_rows(b4, sk, np * 16, ks * 16);
-#pragma unroll
-            for (int c = 0; c < NP; ++c) mma2(x[0], x[1], a[c], b4);
-            if (NP == 2) {
-              ld.b_rows(b4, sk + TILE, np * 16, ks * 16);
-              mma2(x[0], x[1], a[0], b4);
-            }
+          for (int c = 0; c < NP; ++c) {
+            ld.a_rows(a[0][c], sq + c * TILE, m0, ks * 16);
+            if (DELTA) ld.a_rows(a[1][c], sk + c * TILE, m0, ks * 16);
           }
+          ld.b_rows(b4, sk, np * 16, ks * 16);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = 2 * np + e;
+          for (int ps = 0; ps < (DELTA ? 2 : 1); ++ps)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int t = m0 + g + 8 * h;
-              float y[2];
+            for (int c = 0; c < NP; ++c) mma2(x[ps][0], x[ps][1], a[ps][c], b4);
+          if (NP == 2) {
+            ld.b_rows(b4, sk + TILE, np * 16, ks * 16);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int s = 8 * i + t2 + j;
-                const bool in = ps ? s < t : s <= t;
-                const float dec = in ? expf((float)(G[t] - G[s])) : 0.0f;
-                const float z = in ? (ps ? -acc[8 + i][2 * h + j] : acc[i][2 * h + j]) * dec : 0.0f;
-                const float m = z * (x[e][2 * h + j] * to);
-                y[j] = z * be[s] * to_unit;
-                if (in) {
-                  rs[h] = fmaf(be[s], m, rs[h]);
-                  cs[i][j] += m;
-                }
+            for (int ps = 0; ps < (DELTA ? 2 : 1); ++ps) mma2(x[ps][0], x[ps][1], a[ps][0], b4);
+          }
+        }
+        const bool diagonal = np == w4;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * np + e;
+          const float4 gs = *reinterpret_cast<const float4 *>(G + 8 * i + t2);
+          const float2 bs = *reinterpret_cast<const float2 *>(be + 8 * i + t2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = m0 + g + 8 * h;
+            float y[2], z[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int s = 8 * i + t2 + j;
+              const float dec = decay(gt[h], j ? make_float2(gs.z, gs.w) : make_float2(gs.x, gs.y));
+              const float b = j ? bs.y : bs.x;
+              y[j] = acc[i][2 * h + j] * dec;
+              z[j] = DELTA ? acc[8 + i][2 * h + j] * dec : 0.0f;
+              if (diagonal) {
+                y[j] = s <= t ? y[j] : 0.0f;
+                z[j] = s < t ? z[j] : 0.0f;
               }
-              put_pair<kChunk>(out, kChunk * kChunk, m0 + 8 * h, 8 * i, y[0], y[1], lane);
+              float m = y[j] * (x[0][e][2 * h + j] * toq);
+              if (DELTA) m = fmaf(z[j], x[1][e][2 * h + j] * tok, m);
+              // (a pair that the mask leaves out gives nothing, not 0 times a decay that overflowed)
+              if (diagonal && s > t) m = 0.0f;
+              rs[h] = fmaf(b, m, rs[h]);
+              cs[i][j] += m;
+              y[j] *= b * to_unit;
+              z[j] *= -b * to_unit;
             }
+            put_pair<kChunk>(out, kChunk * kChunk, m0 + 8 * h, 8 * i, y[0], y[1], lane);
+            if (DELTA) put_pair<kChunk>(out + 2 * kChunk * kChunk, kChunk * kChunk, m0 + 8 * h, 8 * i, z[0], z[1], lane);
           }
         }
       }
@@ -2031,97 +2074,108 @@ static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParam
 // -------------------------------------------------------------------------------------
 // scan_recurrent: short sequences, token by token in fp32
 // -------------------------------------------------------------------------------------
-// d_k/16 lanes share a value row (16 of its columns each, in groups of 4 so that the lanes'
-// 16-byte accesses are contiguous) and two rows are in flight per lane.
-constexpr int kRecThreads = 128, kRecRows = 2;
+// Grid (sequence * H + head, group of value rows).  d_k/16 lanes share a value row (16 of its columns each, in
+// groups of 4 so that the lanes' 16-byte accesses are contiguous) and two rows are in flight per
+// lane, their arithmetic as packed pairs.  q, k, v and the gates of kRecTokens tokens at a time pass through
+// shared memory as fp32, while the state's loads are under way.
+constexpr int kRecThreads = 128, kRecRows = 2, kRecTokens = 8;
 
 template <int DK, bool DELTA>
 __global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanParams p) {
-  constexpr int LPR = DK / 16;
-  if (blockIdx.x == 0) check_offsets(p);
-  const int lane = threadIdx.x & 31, lir = lane % LPR;
-  const int per = p.d_v / kRecRows;                               // row pairs of one head
-  const long long pairs = (long long)p.n_seq * p.H * per;
-  const long long id = (blockIdx.x * (long long)kRecThreads + threadIdx.x) / LPR;
-  const bool live = id < pairs;
-  const long long gr = live ? id : pairs - 1;
-  const long long tile = gr / per;
-  const int row = (int)(gr % per) * kRecRows, head = (int)(tile % p.H), seq = (int)(tile / p.H);
-  long long start;
-  int len;
-  seq_range(p, seq, start, len);
-  if (!live) len = 0;
-  const int most = __reduce_max_sync(0xFFFFFFFFu, len);
-  float S[kRecRows][16];
+  constexpr int LPR = DK / 16, ROWS = kRecThreads / LPR * kRecRows;
+  __shared__ float4 sk[kRecTokens][DK / 4], sq[kRecTokens][DK / 4];
+  __shared__ float sv[kRecTokens][ROWS];
+  __shared__ float2 sg[kRecTokens];                   // a, b
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p);
+  const int tid = threadIdx.x, lir = tid % LPR, threads = blockDim.x;
+  const int rows = threads / LPR * kRecRows;          // of this block
+  const int row0 = blockIdx.y * rows, row = row0 + tid / LPR * kRecRows;
+  const long long tile = blockIdx.x;
+  const int head = (int)(tile % p.H), seq = (int)(tile / p.H);
+  const bool live = row < p.d_v;                      // (d_v is even)
   const long long at = (tile * p.d_v + row) * DK + 4 * lir;
+  float2 S[kRecRows][8];
 #pragma unroll
   for (int r = 0; r < kRecRows; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (p.state_in && live) x = *reinterpret_cast<const float4 *>(p.state_in + at + r * DK + 4 * LPR * c);
-      S[r][4 * c] = x.x; S[r][4 * c + 1] = x.y; S[r][4 * c + 2] = x.z; S[r][4 * c + 3] = x.w;
+      S[r][2 * c] = make_float2(x.x, x.y);
+      S[r][2 * c + 1] = make_float2(x.z, x.w);
     }
-  const long long qo = (long long)(head / p.share) * DK + 4 * lir;
-  for (int t = 0; t < most; ++t) {
-    const bool on = t < len;
-    const long long tok = start + (on ? t : 0);
-    float k[16], q[16], v[kRecRows], a = 1.0f, b = 0.0f;
+  long long start;
+  int len;
+  seq_range(p, seq, start, len);
+  const long long qo = (long long)(head / p.share) * DK;
+  for (int t0 = 0; t0 < len; t0 += kRecTokens) {
+    const int n = min(kRecTokens, len - t0);
+    if (t0) __syncthreads();
+    for (int i = tid; i < n * (DK / 4); i += threads) {
+      const int t = i / (DK / 4), c = i % (DK / 4);
+      float x[4];
+      load4(p.k, p.dtype, (start + t0 + t) * p.k_stride + qo + 4 * c, x);
+      sk[t][c] = make_float4(x[0], x[1], x[2], x[3]);
+      load4(p.q, p.dtype, (start + t0 + t) * p.q_stride + qo + 4 * c, x);
+      sq[t][c] = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    const int vrows = min(rows, p.d_v - row0) / 4;    // (d_v and rows are multiples of 4)
+    for (int i = tid; i < n * vrows; i += threads) {
+      const int t = i / vrows, c = (i % vrows) * 4;
+      float x[4];
+      load4(p.v, p.dtype, (start + t0 + t) * p.v_stride + (long long)head * p.d_v + row0 + c, x);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
-      if (on) {
-        load4(p.k, p.dtype, tok * p.k_stride + qo + 4 * LPR * c, x);
-        load4(p.q, p.dtype, tok * p.q_stride + qo + 4 * LPR * c, y);
+      for (int e = 0; e < 4; ++e) sv[t][c + e] = x[e];
+    }
+    if (tid < n) {
+      const long long g = (start + t0 + tid) * p.H + head;
+      sg[tid] = make_float2(expf(__ldg(p.log_alpha + g)), __ldg(p.beta + g));
+    }
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      const float2 ab = sg[t], aa = make_float2(ab.x, ab.x);
+      float2 k[8], q[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = sk[t][LPR * c + lir], y = sq[t][LPR * c + lir];
+        k[2 * c] = make_float2(x.x, x.y); k[2 * c + 1] = make_float2(x.z, x.w);
+        q[2 * c] = make_float2(y.x, y.y); q[2 * c + 1] = make_float2(y.z, y.w);
       }
+      float u[kRecRows], o[kRecRows];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) { k[4 * c + e] = x[e]; q[4 * c + e] = y[e]; }
-    }
+      for (int r = 0; r < kRecRows; ++r) {
+        float2 y = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int r = 0; r < kRecRows; ++r) v[r] = 0.0f;
-    if (on) {
-      a = expf(__ldg(p.log_alpha + tok * p.H + head));
-      b = __ldg(p.beta + tok * p.H + head);
-      const long long vo = tok * p.v_stride + (long long)head * p.d_v + row;
-#pragma unroll
-      for (int r = 0; r < kRecRows; ++r)
-        v[r] = p.dtype == 0 ? __ldg(static_cast<const float *>(p.v) + vo + r)
-               : p.dtype == 1 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v)[vo + r])
-                              : __half2float(static_cast<const __half *>(p.v)[vo + r]);
-    }
-    float u[kRecRows], o[kRecRows];
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) {
-      u[r] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        S[r][e] *= a;
-        if (DELTA) u[r] = fmaf(S[r][e], k[e], u[r]);
+        for (int e = 0; e < 8; ++e) {
+          S[r][e] = __fmul2_rn(S[r][e], aa);
+          if (DELTA) y = __ffma2_rn(S[r][e], k[e], y);
+        }
+        u[r] = y.x + y.y;
       }
-    }
-    if (DELTA)
+      if (DELTA)
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1)
+#pragma unroll
+          for (int r = 0; r < kRecRows; ++r) u[r] += __shfl_xor_sync(0xFFFFFFFFu, u[r], d);
+#pragma unroll
+      for (int r = 0; r < kRecRows; ++r) {
+        const float w = ab.y * (sv[t][tid / LPR * kRecRows + r] - u[r]);
+        const float2 ww = make_float2(w, w);
+        float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          S[r][e] = __ffma2_rn(ww, k[e], S[r][e]);
+          y = __ffma2_rn(S[r][e], q[e], y);
+        }
+        o[r] = y.x + y.y;
+      }
 #pragma unroll
       for (int d = 1; d < LPR; d <<= 1)
 #pragma unroll
-        for (int r = 0; r < kRecRows; ++r) u[r] += __shfl_xor_sync(0xFFFFFFFFu, u[r], d);
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) {
-      const float wr = b * (v[r] - u[r]);
-      o[r] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        S[r][e] = fmaf(wr, k[e], S[r][e]);
-        o[r] = fmaf(S[r][e], q[e], o[r]);
-      }
+        for (int r = 0; r < kRecRows; ++r) o[r] += __shfl_xor_sync(0xFFFFFFFFu, o[r], d);
+      if (live && lir == 0)
+        store_pair(p.o, p.dtype, (start + t0 + t) * p.o_stride + (long long)head * p.d_v + row, o[0], o[1]);
     }
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1)
-#pragma unroll
-      for (int r = 0; r < kRecRows; ++r) o[r] += __shfl_xor_sync(0xFFFFFFFFu, o[r], d);
-    if (on && lir == 0)
-#pragma unroll
-      for (int r = 0; r < kRecRows; ++r)
-        store_as(p.o, p.dtype, tok * p.o_stride + (long long)head * p.d_v + row + r, o[r]);
   }
   if (p.state_out && live)
 #pragma unroll
@@ -2129,7 +2183,7 @@ __global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanP
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         *reinterpret_cast<float4 *>(p.state_out + at + r * DK + 4 * LPR * c) =
-            make_float4(S[r][4 * c], S[r][4 * c + 1], S[r][4 * c + 2], S[r][4 * c + 3]);
+            make_float4(S[r][2 * c].x, S[r][2 * c].y, S[r][2 * c + 1].x, S[r][2 * c + 1].y);
 }
 
 using ScanFn = void (*)(ScanParams);
