@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
+// Without the delta rule E = V and the state warps have no products before X; two CTAs then share an SM.
 // A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit): bulk copies,
 // since 16-byte cp.async of the same 96 KB took longer than the chunk's arithmetic; and it turns
 // the block's rows of V into fp16 over their scale.  In the backward pass's recomputation (SAVE)
@@ -910,7 +911,7 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   at = 0;
   l.part = at; at += nh > 1 && (delta || kind == kReverse) ? nh * 4096 : 0;   // the state warps' parts of E or R
   l.side = at; at += delta || kind == kReverse ? 4096 : 0;     // Tm V or dO^T Z
-  l.last = at; at += 4096;                                     // E or R, for the side warps
+  l.last = at; at += delta || kind == kReverse ? 4096 : 0;     // E or R, for the side warps
   l.plus = at; at += kind == kReverse ? 16 * dk * 4 : 0;       // dO^T Q
   l.planes = at; at += kind == kForward ? np * 16 * dk * 2 : 0;   // S0 as left operands
   l.tops = at; at += 32;                                       // largest entries: see below
@@ -1123,7 +1124,7 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
 }
 
 template <int DK, int NP, bool DELTA, int KIND, int NH>
-__global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP == 2 ? 1 : 2) scan_walk_kernel(const ScanParams p) {
   constexpr bool REV = KIND == kReverse;
   constexpr bool JOIN = DELTA || REV;                        // E (or R) has parts in several warps
   constexpr int DKH = DK / NH, NTH = DKH / 8;
@@ -1224,7 +1225,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
         scaleV *= qscale;
         mV = abs_bits(__uint_as_float(mV) * qscale);
       }
-      const float scaleE = scale_of(max(mS, mV), 6, invE);
+      float scaleE = scale_of(max(mS, mV), 6, invE);
+      if (!JOIN) {
+        scaleE = scaleV;
+        invE = invV;
+      }
       if (!side) {
         // ---- state warp -----------------------------------------------------------------
         float E[8][4];                   // 16 value rows x 64 tokens
@@ -1303,31 +1308,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
           }
         } else {
           if (KIND == kForward) barrier_arrive(X, PER);
-          // E = V
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t a[NP][4];
-#pragma unroll
-            for (int pl = 0; pl < NP; ++pl) lv.a_cols(a[pl], sv + pl * VP, ks * 16, 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float2 f = half2_of(a[0][q]);
-              if (NP == 2) {
-                const float2 y = half2_of(a[NP - 1][q]);
-                f.x = __fadd_rn(f.x, y.x);
-                f.y = __fadd_rn(f.y, y.y);
-              }
-              float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-              e[0] = f.x * scaleV;
-              e[1] = f.y * scaleV;
-            }
-          }
         }
-        // E (or R) for the side warps: each state warp hands over half of the tokens
+        if (JOIN) {
+          // E (or R) for the side warps: each state warp hands over half of the tokens
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
-        barrier_arrive(Y, PER);
+          for (int i = 0; i < 8; ++i)
+            if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
+          barrier_arrive(Y, PER);
+        }
         // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
         // sum starts from zero and joins the state in one fma, so that the tensor cores'
         // rounding does not pile up in it
@@ -1335,15 +1323,31 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
         uint32_t wh[4][4], wl[4][4];
         if (!REV || DELTA)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+          for (int ks = 0; ks < 4; ++ks) {
+            uint32_t v[NP][4];
+            if (!JOIN)                   // E = V: the planes of V are over its own scale
+#pragma unroll
+              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
-              const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-              const float to = REV ? -invE : invE;
-              split2(e[0] * (f.x * to), e[1] * (f.y * to), wh[ks][q], wl[ks][q]);
+              if (JOIN) {
+                const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
+                const float to = REV ? -invE : invE;
+                split2(e[0] * (f.x * to), e[1] * (f.y * to), wh[ks][q], wl[ks][q]);
+              } else {
+                float2 x = half2_of(v[0][q]);
+                if (NP == 2) {
+                  const float2 y = half2_of(v[NP - 1][q]);
+                  x.x = __fadd_rn(x.x, y.x);
+                  x.y = __fadd_rn(x.y, y.y);
+                }
+                split2(x.x * f.x, x.y * f.y, wh[ks][q], wl[ks][q]);
+              }
             }
-        constexpr int STEP = NTH >= 8 ? 4 : NTH / 2;         // column pairs at a time
+          }
+        if (!JOIN && KIND == kForward) barrier_arrive(Y, PER);    // (V is read)
+        constexpr int STEP = JOIN && NTH >= 8 ? 4 : NTH >= 4 ? 2 : 1;   // column pairs at a time
 #pragma unroll
         for (int n0 = 0; n0 < NTH / 2; n0 += STEP) {
           float a[2 * STEP][4];
@@ -1432,10 +1436,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
             for (int i = 0; i < 4; ++i)
               sided[(4 * H + i) * 32 + lane] = make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
           }
-          if (JOIN || KIND == kForward) {
-            if (REV) barrier_arrive(X, PER);
-            else barrier_sync(X, PER);
-          }
+          // (in reverse the sum over dO^T Q waits too: it then runs beside the state warps' additions and not
+          // beside their products, which the chain waits for)
+          if (JOIN || KIND == kForward) barrier_sync(X, PER);
           if (REV) {
             // (diag(e^G) dO)^T Q, columns [H d_k/2, (H+1) d_k/2)
             constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
@@ -1539,12 +1542,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
               O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
             }
           }
-          barrier_sync(Y, PER);
+          if (JOIN) barrier_sync(Y, PER);
           if (KIND == kForward) {
             // + E^T P^T
             uint32_t eh[4][4], el[4][4];
 #pragma unroll
             for (int ks = 0; ks < 2 * H + 2; ++ks) {
+              if (!JOIN) {
+                lv.a_cols(eh[ks], sv, ks * 16, 0);
+                if (NP == 2) lv.a_cols(el[ks], sv + VP, ks * 16, 0);
+                continue;
+              }
               const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
               const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
               split_tiles(e0, e1, invE, eh[ks], el[ks]);
@@ -1562,8 +1570,25 @@ __global__ void __launch_bounds__(kWalkThreads, 1) scan_walk_kernel(const ScanPa
                     mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
                   }
                 }
+            // (without the delta rule the tile holds V until every warp of the block has read it)
+            if (!JOIN) barrier_sync(Y, PER);
             store_tokens<NP>(O, scaleE * qscale, tile, 4 * H, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
                              head * p.d_v + brow, p.d_v - brow, p.o16, lane);
+          } else if (!JOIN) {
+            // the planes of V, tile by tile (a tile of [64 tokens][16 rows] is kept transposed)
+            __half *et = p.et + rec * (2ll * p.dvp * kChunk);
+#pragma unroll
+            for (int ks = 2 * H; ks < 2 * H + 2; ++ks)
+#pragma unroll
+              for (int pl = 0; pl < 2; ++pl) {
+                uint32_t v[4] = {0, 0, 0, 0};
+                if (pl < NP) lv.a_cols(v, sv + pl * VP, ks * 16, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  *reinterpret_cast<uint32_t *>(et + pl * (long long)p.dvp * kChunk +
+                                                tiled<kChunk>(brow + 8 * (q & 1), ks * 16 + 8 * (q >> 1)) + 2 * lane) = v[q];
+              }
+            if (lane == 0 && H == 0) p.scales[kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
