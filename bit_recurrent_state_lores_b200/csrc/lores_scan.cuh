@@ -410,15 +410,15 @@ __host__ __device__ constexpr PrepLayout prep_layout(int dk, int np, bool severa
   return l;
 }
 
-// Rows of K or Q of a chunk.  A thread holds PASS pieces of 8 entries as they came; all loads are in flight
-// before the first is used.
+// Rows of K or Q of a chunk.  A thread holds PASS pieces of 8 entries as they came, piece e being row e % 8 of tile
+// e / 8 (so that the planes are written in order); all loads are in flight before the first is used.
 template <int DK, int NP, int PASS>
 __device__ __forceinline__ void load_rows(const ScanParams &p, const void *src, long long stride, long long token0, int qh,
                                           int n, uint4 (&raw)[PASS][NP], int tid) {
   constexpr int PER = DK / 8;
 #pragma unroll
   for (int i = 0; i < PASS; ++i) {
-    const int e = tid + i * kPrepThreads, r = e / PER, c = (e % PER) * 8;
+    const int e = tid + i * kPrepThreads, r = (e >> 3) / PER * 8 + (e & 7), c = (e >> 3) % PER * 8;
 #pragma unroll
     for (int h = 0; h < NP; ++h) raw[i][h] = make_uint4(0, 0, 0, 0);
     if (r < n) {
@@ -473,11 +473,10 @@ __device__ __forceinline__ unsigned max_rows(const uint4 (&raw)[PASS][NP], int d
 // The rows over their scale as planes, in shared memory and, where `out` is given, in the workspace.
 template <int DK, int NP, int PASS>
 __device__ __forceinline__ void put_rows(const uint4 (&raw)[PASS][NP], int dtype, float inv, __half *dst, __half *out, int tid) {
-  constexpr int PER = DK / 8;
 #pragma unroll
   for (int i = 0; i < PASS; ++i) {
-    const int e = tid + i * kPrepThreads, r = e / PER, c = (e % PER) * 8;
-    if (r >= kChunk) continue;
+    const int e = tid + i * kPrepThreads, at = e * 8;
+    if (at >= kChunk * DK) continue;
     float x[8];
     unpack_row<NP>(raw[i], dtype, x);
     uint4 hi, lo;
@@ -485,7 +484,6 @@ __device__ __forceinline__ void put_rows(const uint4 (&raw)[PASS][NP], int dtype
     split2(x[2] * inv, x[3] * inv, hi.y, lo.y);
     split2(x[4] * inv, x[5] * inv, hi.z, lo.z);
     split2(x[6] * inv, x[7] * inv, hi.w, lo.w);
-    const int at = tiled<DK>(r, c);
     *reinterpret_cast<uint4 *>(dst + at) = hi;
     if (NP == 2) *reinterpret_cast<uint4 *>(dst + kChunk * DK + at) = lo;
     if (out) {
@@ -767,7 +765,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     __half *tm = p.tm + rec * (2 * kChunk * kChunk);
 #pragma unroll
     for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
-      const int i = tid + j * kPrepThreads, r = i >> 3, c = (i & 7) * 8;
+      const int i = tid + j * kPrepThreads, r = (i >> 6) * 8 + (i & 7), c = ((i >> 3) & 7) * 8;
       if ((c >> 4) <= (r >> 4)) {
         uint4 hi, lo;
         const float *x = X + r * kLdF + c;
@@ -775,9 +773,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         split2(x[2], x[3], hi.y, lo.y);
         split2(x[4], x[5], hi.z, lo.z);
         split2(x[6], x[7], hi.w, lo.w);
-        const int at = tiled<kChunk>(r, c);
-        *reinterpret_cast<uint4 *>(tm + at) = hi;
-        *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + at) = lo;
+        *reinterpret_cast<uint4 *>(tm + 8 * i) = hi;
+        *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + 8 * i) = lo;
       }
     }
     if (BWD) {
