@@ -5,21 +5,25 @@
 // (General recurrence form; a_t = exp(log_alpha_t), d = delta).  Sequences are cut into
 // chunks of kChunk = 64 tokens.  With G_t the sum of log_alpha over the chunk up to t, S0 the
 // state at its start, rows t of Q, K, V, E its tokens and dec_ts = exp(G_t - G_s):
-//   L_ts = dec_ts k_t.k_s (s < t)      P_ts = dec_ts q_t.k_s b_s (s <= t)
-//   Tm   = (I + d L diag(b))^-1        E = Tm (V - d diag(e^G) K S0^T)
+//   A_ts = k_t.k_s b_s (s < t)         P_ts = dec_ts q_t.k_s b_s (s <= t)
+//   T    = (I + d A)^-1                Tm_ts = dec_ts T_ts
+//   E    = Tm V - d diag(e^G) T K S0^T
 //   O    = diag(e^G) Q S0^T + P E      S_C = e^{G_C} S0 + (diag(w) E)^T K,  w = b e^{G_C - G}
 // Only S0 -> S_C is sequential, so the work is split in two:
-//   scan_prep     all chunks at once: gates, Tm, P, Kt = -d Tm diag(e^G) K (and, for the
-//                 backward pass, Z = P Tm and Kb = Tm^T diag(w) K)
-//   scan_chain    per (sequence, head, block of value rows): E^T = S0 Kt^T + (Tm V)^T, O^T and
+//   scan_prep     all chunks at once: gates, Tm, P, Kt = -d T K (and, for the backward pass,
+//                 Z = P Tm and Kb = T^T diag(b) K).  (With Gam = diag(e^G), (I + L diag(b))^-1 for
+//                 L_ts = dec_ts k_t.k_s is Gam T Gam^-1: the decays leave the inverse, whose entries stay of size
+//                 one, and come back as factors of its rows.)
+//   scan_walk     per (sequence, head, block of value rows): E^T = S0 Kt^T diag(e^G) + (Tm V)^T, O^T and
 //                 S_C, chunk after chunk.  Value rows are independent (as in the decode
 //                 step), so one or two warps own 16 of them, keep S [16][d_k] in their
 //                 accumulators and feed it back as the next product's left operand
 //                 without leaving registers; two more warps per 16 rows do what the
 //                 next chunk does not wait for.
 // Backward, D = dL/dS_C:
-//   R   = Z^T dO + Kb D^T (= dV)       D0 = e^{G_C} D + (diag(e^G) dO)^T Q - d (diag(e^G) R)^T K
-//   scan_reverse  the same walk backwards over R and D;
+//   R   = Z^T dO + diag(e^{G_C - G}) Kb D^T (= dV)
+//   D0  = e^{G_C} D + (diag(e^G) dO)^T Q - d (diag(e^G) R)^T K
+//   scan_walk     the same backwards over R and D;
 //   scan_grads    all chunks at once: dQ, dK and the gates' gradients from S0, D, E, R.
 //
 // Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
@@ -79,10 +83,12 @@ struct ScanParams {
 };
 
 // Record of a chunk and head, kChunk entries each: e^G, w over the scale of K (that is, what
-// multiplies a row of khat), e^G likewise, w, b, e^(G_C - G); G / ln 2 as a pair of floats; the scales of K and Q.
-enum GateRow { kGateE, kGateWk, kGateEk, kGateW, kGateB, kGateC, kGateG };   // kGateG: two rows' worth of pairs
+// multiplies a row of khat), e^G likewise, e^(G_C - G), w, b; G / ln 2 as a pair of floats.  Then the scales of K and Q,
+// and the largest magnitudes of the second row, of b over the scale of K and of the third row.
+enum GateRow { kGateE, kGateWk, kGateEk, kGateC, kGateW, kGateB, kGateG };   // kGateG: two rows' worth of pairs
 constexpr int kGateScales = (kGateG + 2) * kChunk;
-constexpr int kGateFloats = kGateScales + 4;
+constexpr int kGateFloats = kGateScales + 8;
+constexpr int kGateStage = 4 * kChunk + 8;     // what a walk takes of it: the first four rows, the scalars
 enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR };
 
 // -------------------------------------------------------------------------------------
@@ -283,6 +289,9 @@ __device__ __forceinline__ float scale_of(unsigned bits, int up, float &inv) {
   inv = __uint_as_float((unsigned)(254 - e) << 23);
   return __uint_as_float((unsigned)e << 23);
 }
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.0f : __uint_as_float((unsigned)(127 + min(e, 127)) << 23);
+}
 // dec_ts = 2^(g_t - g_s), g a pair of floats (48 bits, so that the difference keeps its digits behind a
 // strong decay).
 __device__ __forceinline__ float decay(float2 gt, float2 gs) {
@@ -386,7 +395,7 @@ __device__ __forceinline__ void load8(const void *src, int dtype, long long i, b
 // -------------------------------------------------------------------------------------
 // Grid (slot, group of p.hpc heads that share K and Q), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.]
 // result, and only blocks on and below the diagonal are formed.  K and Q are fetched and converted
-// once for the group.  Tm = (I + A)^-1, A = L diag(b), by 16x16 blocks:
+// once for the group.  T = (I + A)^-1 by 16x16 blocks:
 // the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
 // forms block column j downwards, X_ij = -X_ii sum_{j <= k < i} A_ik X_kj, as
 // X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
@@ -406,7 +415,7 @@ __host__ __device__ constexpr PrepLayout prep_layout(int dk, int np, bool severa
   l.x = several ? l.a + planes : l.q + (tile > planes ? tile : planes);
   l.xd = l.x + kChunk * kLdF * 4;
   l.f = l.xd + 4 * 2 * 16 * 16 * 2;
-  l.bytes = l.f + (3 * kChunk + 2 * kChunk + 16) * 4;
+  l.bytes = l.f + (kChunk + 2 * kChunk + 16) * 4;
   return l;
 }
 
@@ -512,10 +521,10 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   extern __shared__ __align__(16) uint8_t smem[];
   __half *K = reinterpret_cast<__half *>(smem + l.k), *Q = reinterpret_cast<__half *>(smem + l.q);
   __half *A16 = reinterpret_cast<__half *>(smem + l.a);             // [2][64][64]
-  float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then Tm
+  float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then T
   __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][16]: X_ii
   float2 *G = reinterpret_cast<float2 *>(smem + l.f);
-  float *ek = reinterpret_cast<float *>(G + kChunk), *wk = ek + kChunk, *bk = wk + kChunk;
+  float *bk = reinterpret_cast<float *>(G + kChunk);                // b times the scale of K
   unsigned *red = reinterpret_cast<unsigned *>(bk + kChunk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head0 = blockIdx.y * p.hpc;
@@ -594,6 +603,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       }
       const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
       const double Gt[2] = {run - (double)la[1], run};
+      float tops[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
@@ -602,7 +612,10 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         const float hi = (float)l2;
         const float2 pair = make_float2(hi, (float)(l2 - (double)hi));
         G[t] = pair;
-        ek[t] = e * sk; bk[t] = b[i] * sk; wk[t] = w * sk;
+        bk[t] = b[i] * sk;
+        tops[0] = fmaxf(tops[0], fabsf(w * sk));
+        tops[1] = fmaxf(tops[1], fabsf(b[i] * sk));
+        tops[2] = fmaxf(tops[2], fabsf(e * sk));
         gates[kGateE * kChunk + t] = e;
         gates[kGateWk * kChunk + t] = w * sk;
         gates[kGateEk * kChunk + t] = e * sk;
@@ -610,6 +623,11 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         gates[kGateB * kChunk + t] = b[i];
         gates[kGateC * kChunk + t] = c;
         reinterpret_cast<float2 *>(gates + kGateG * kChunk)[t] = pair;
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tops[i]));
+        if (lane == 0) gates[kGateScales + 2 + i] = __uint_as_float(m);
       }
       if (lane == 0) {
         gates[kGateScales] = sk;
@@ -657,7 +675,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         }
       }
       if (DELTA && !several) __syncthreads();      // Q's tile becomes A's planes
-      // P (over the scale of Q) and, strictly below the diagonal, A
+      // P over the scale of Q (for Z without its decays) and, strictly below the diagonal, A
+      constexpr bool KEEP = !BWD || !DELTA;        // P itself is wanted
       const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
       __half *pp = p.pp + rec * (2 * kChunk * kChunk);
 #pragma unroll
@@ -668,9 +687,12 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
           const bool diagonal = i / 2 == warp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float d0 = decay(gt[h], make_float2(gs.x, gs.y)) * bs.x, d1 = decay(gt[h], make_float2(gs.z, gs.w)) * bs.y;
-            float a0 = A[i][2 * h] * (d0 * sk), a1 = A[i][2 * h + 1] * (d1 * sk);
-            float p0 = P[i][2 * h] * d0, p1 = P[i][2 * h + 1] * d1;
+            float p0 = P[i][2 * h] * bs.x, p1 = P[i][2 * h + 1] * bs.y;
+            if (KEEP) {
+              p0 *= decay(gt[h], make_float2(gs.x, gs.y));
+              p1 *= decay(gt[h], make_float2(gs.z, gs.w));
+            }
+            const float a0 = A[i][2 * h] * (bs.x * sk), a1 = A[i][2 * h + 1] * (bs.y * sk);
             if (diagonal) {
               const int t = m0 + g + 8 * h, s = 8 * i + t2;
               p0 = s <= t ? p0 : 0.0f;
@@ -684,7 +706,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             }
             P[i][2 * h] = p0;
             P[i][2 * h + 1] = p1;
-            if (!BWD || !DELTA) {
+            if (KEEP) {
               if (NP == 2 || BWD) put_pair<kChunk>(pp, kChunk * kChunk, m0 + 8 * h, 8 * i, p0, p1, lane);
               else             // (16-bit outputs need one plane)
                 *reinterpret_cast<uint32_t *>(pp + tiled<kChunk>(m0 + 8 * h, 8 * i) + 2 * lane) = pack2(p0, p1);
@@ -761,24 +783,30 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     }
     __syncthreads();
 
-    // planes of Tm (blocks on and below the diagonal)
-    __half *tm = p.tm + rec * (2 * kChunk * kChunk);
+    {
+      // planes of Tm (blocks on and below the diagonal)
+      __half *tm = p.tm + rec * (2 * kChunk * kChunk);
 #pragma unroll
-    for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
-      const int i = tid + j * kPrepThreads, r = (i >> 6) * 8 + (i & 7), c = ((i >> 3) & 7) * 8;
-      if ((c >> 4) <= (r >> 4)) {
-        uint4 hi, lo;
-        const float *x = X + r * kLdF + c;
-        split2(x[0], x[1], hi.x, lo.x);
-        split2(x[2], x[3], hi.y, lo.y);
-        split2(x[4], x[5], hi.z, lo.z);
-        split2(x[6], x[7], hi.w, lo.w);
-        *reinterpret_cast<uint4 *>(tm + 8 * i) = hi;
-        *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + 8 * i) = lo;
+      for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
+        const int i = tid + j * kPrepThreads, r = (i >> 6) * 8 + (i & 7), c = ((i >> 3) & 7) * 8;
+        if ((c >> 4) <= (r >> 4)) {
+          uint4 hi, lo;
+          float x[8];
+          const float2 gr = G[r];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = c + e <= r ? X[r * kLdF + c + e] * decay(gr, G[c + e]) : 0.0f;
+          split2(x[0], x[1], hi.x, lo.x);
+          split2(x[2], x[3], hi.y, lo.y);
+          split2(x[4], x[5], hi.z, lo.z);
+          split2(x[6], x[7], hi.w, lo.w);
+          *reinterpret_cast<uint4 *>(tm + 8 * i) = hi;
+          *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + 8 * i) = lo;
+        }
       }
     }
     if (BWD) {
-      // Z = P Tm (over the scale of Q): rows t of this warp; block (r, s) of Tm is zero for s > r
+      // Z = P Tm (over the scale of Q), that is dec times the product without decays: rows t of this warp; block (r, s)
+      // of T is zero for s > r
       float acc[8][4];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -802,16 +830,23 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         }
       }
       __half *z = p.z + rec * (2 * kChunk * kChunk);
+      const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i / 2 <= warp)
+        if (i / 2 <= warp) {
+          const float4 gs = *reinterpret_cast<const float4 *>(G + 8 * i + t2);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
+          for (int h = 0; h < 2; ++h) {
+            const int t = m0 + g + 8 * h, s = 8 * i + t2;
+            const float z0 = s <= t ? acc[i][2 * h] * decay(gt[h], make_float2(gs.x, gs.y)) : 0.0f;
+            const float z1 = s + 1 <= t ? acc[i][2 * h + 1] * decay(gt[h], make_float2(gs.z, gs.w)) : 0.0f;
+            put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, z0, z1, lane);
+          }
+        }
     }
-    // Kt = -Tm diag(e^G) K: rows t of this warp, s blocks up to its own; then Kb = Tm^T diag(w) K: rows s
-    // of this warp, t blocks from its own on.  Two halves of the columns, so that the
-    // accumulators leave room for four CTAs per SM.
+    // Kt = -T K: rows t of this warp, s blocks up to its own; then Kb = T^T diag(b) K: rows s of this warp, t
+    // blocks from its own on.  Two halves of the columns, so that the accumulators leave room for
+    // four CTAs per SM.
     constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
 #pragma unroll
     for (int which = 0; which < (BWD ? 2 : 1); ++which) {
@@ -823,8 +858,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int m = m0 + g + 8 * (q & 1), k = ks * 16 + t2 + 8 * (q >> 1);
-            if (which) split2(X[k * kLdF + m] * wk[k], X[(k + 1) * kLdF + m] * wk[k + 1], ah[ks][q], al[ks][q]);
-            else split2(-X[m * kLdF + k] * ek[k], -X[m * kLdF + k + 1] * ek[k + 1], ah[ks][q], al[ks][q]);
+            if (which) split2(X[k * kLdF + m] * bk[k], X[(k + 1) * kLdF + m] * bk[k + 1], ah[ks][q], al[ks][q]);
+            else split2(-X[m * kLdF + k] * sk, -X[m * kLdF + k + 1] * sk, ah[ks][q], al[ks][q]);
           }
 #pragma unroll 1
       for (int half = 0; half < HALVES; ++half) {
@@ -903,7 +938,7 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   l.tm = at; at += kind == kReverse || delta ? 2 * sq : 0;     // Tm or Z
   l.pp = at; at += kind == kForward ? np * sq : 0;
   l.v = at; at += rb * tile_bytes(np);
-  l.gates = at; at += 3 * kChunk * 4 + 16;
+  l.gates = at; at += kGateStage * 4;
   l.bytes = (at + 15) / 16 * 16;
   at = 0;
   l.part = at; at += nh > 1 && (delta || kind == kReverse) ? nh * 4096 : 0;   // the state warps' parts of E or R
@@ -1098,7 +1133,7 @@ __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row
 // Bytes of a chunk's bulk copies.
 __host__ __device__ constexpr unsigned walk_bulk_bytes(int dk, int np, bool delta, int kind) {
   const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
-  return 3 * kChunk * 4 + 16 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
+  return kGateStage * 4 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
          (kind != kRecompute ? np * tile : 0) + (kind == kForward ? np * sq : 0);
 }
 // The chunk's matrices: one thread issues them, they complete on `bar`.
@@ -1110,8 +1145,8 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
   const float *gates = p.gates + rec * kGateFloats;
   mbar_expect_tx(bar, walk_bulk_bytes(DK, NP, DELTA, KIND));
-  bulk_g2s(st + l.gates, gates, 3 * kChunk * 4, bar);
-  bulk_g2s(st + l.gates + 3 * kChunk * 4, gates + kGateScales, 16, bar);
+  bulk_g2s(st + l.gates, gates, 4 * kChunk * 4, bar);
+  bulk_g2s(st + l.gates + 4 * kChunk * 4, gates + kGateScales, 32, bar);
   if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
   if (DELTA || KIND == kReverse)
     bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk), 2 * SQ, bar);
@@ -1206,8 +1241,8 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
     if (by && loader && i0 + 1 < chunks) fetch(next);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
                    tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
-    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk;
-    const float qscale = ek[kChunk + 1];
+    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk, *lead = REV ? ek + kChunk : eG, *scalars = ek + 2 * kChunk;
+    const float qscale = scalars[1];
     const long long rec = (long long)(base + c) * p.H + head;
     const int n = min(kChunk, len - c * kChunk);
     if (loader || !live) {
@@ -1294,12 +1329,8 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
               const float4 y = part[((h ^ 1) * 8 + i) * 32 + lane];
               E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
             }
-            float x = scale, y = scale;
-            if (REV && !DELTA) {
-              const float2 f = *reinterpret_cast<const float2 *>(wk + 8 * i + t2);
-              x *= f.x;
-              y *= f.y;
-            }
+            const float2 f = *reinterpret_cast<const float2 *>((DELTA ? lead : wk) + 8 * i + t2);
+            const float x = scale * f.x, y = scale * f.y;
             E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
             E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
           }
@@ -1317,6 +1348,11 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
         // sum starts from zero and joins the state in one fma, so that the tensor cores'
         // rounding does not pile up in it
         const float eC = eG[kChunk - 1];
+        // the scale of that operand: |E_t w_t| stays near max(|V| max w, |S0| e^{G_C} max b), likewise in reverse
+        // (without the delta rule E = V)
+        float invW;
+        const float topW = __uint_as_float(mV) * scalars[REV ? 4 : 2];
+        const float scaleW = scale_of(abs_bits(JOIN ? fmaxf(topW, __uint_as_float(mS) * eC * scalars[3]) : topW), 6, invW);
         uint32_t wh[4][4], wl[4][4];
         if (!REV || DELTA)
 #pragma unroll
@@ -1330,7 +1366,7 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
               const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
               if (JOIN) {
                 const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-                const float to = REV ? -invE : invE;
+                const float to = REV ? -invW : invW;
                 split2(e[0] * (f.x * to), e[1] * (f.y * to), wh[ks][q], wl[ks][q]);
               } else {
                 float2 x = half2_of(v[0][q]);
@@ -1339,7 +1375,7 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
                   x.x = __fadd_rn(x.x, y.x);
                   x.y = __fadd_rn(x.y, y.y);
                 }
-                split2(x.x * f.x, x.y * f.y, wh[ks][q], wl[ks][q]);
+                split2(x.x * scaleV * (f.x * invW), x.y * scaleV * (f.y * invW), wh[ks][q], wl[ks][q]);
               }
             }
           }
@@ -1382,10 +1418,10 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
               const float4 y = plus[(c0 / 8 + 2 * n0 + i) * 32 + lane];
               const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleE, z[j]));
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleW, z[j]));
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleE);
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleW);
             }
           }
         }
@@ -1671,9 +1707,6 @@ __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], __half2 by) {
     a[q] = *reinterpret_cast<const uint32_t *>(&y);
   }
 }
-__device__ __forceinline__ float pow2(int e) {
-  return e < -126 ? 0.0f : __uint_as_float((unsigned)(127 + min(e, 127)) << 23);
-}
 __device__ __forceinline__ int exponent(const float *x) { return (int)(__float_as_uint(__ldg(x)) >> 23) - 127; }
 // The largest exponent of a[b] c[b] over the blocks of 16 value rows.
 __device__ __forceinline__ int top_unit(const float *a, const float *c, int blocks, int lane) {
@@ -1852,10 +1885,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1];
   const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
   const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
-  // The planes of dP', dL' are held over F of group 3 and 4 dvp (rounded up to a power of two): the entries of
-  // E, R and dO over their scales stay below 2^7 (E and R somewhat above), so a sum over d_v of their
-  // products stays below 2^14 dvp.
-  const int lg = 2 + 32 - __clz(p.dvp - 1);
+  // The planes of dP', dL' are held over F of group 3 and 2^8 dvp (rounded up to a power of two).  Entries of S0, V, D
+  // and dO over their scales are below 2^7; E = V - S k and R alike reach 1 + sqrt(d_k) |k| < 2^4 times that, so a sum
+  // over d_v of products of two is below 2^22 dvp, and with b up to 2 the planes' entries are below 2^15.
+  const int lg = 8 + 32 - __clz(p.dvp - 1);
   const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // F of the group, as two factors in range
   const float to_unit = pow2(top - topRE - lg);                          // from F to what the planes are held over
   const float out1 = pow2(topRE / 2) * pow2(lg), out2 = pow2(topRE - topRE / 2);
@@ -2064,7 +2097,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       const int t = 2 * lane + i;
       if (t < n) {
         const long long at = (token0 + t) * p.H + head;
-        p.dlog_alpha[at] = (float)out[i];
+        // (a state that was dropped has no gradient through its decay: not even the rounding of the sums)
+        p.dlog_alpha[at] = __ldg(p.log_alpha + at) < -1000.0f ? 0.0f : (float)out[i];
         p.dbeta[at] = db[i];
       }
     }
