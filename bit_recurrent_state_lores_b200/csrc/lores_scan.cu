@@ -76,8 +76,8 @@ lores_status shape_of(const lores_scan_config *cfg, bool backward, Shape &s) {
   if (c.heads_qk == 0) c.heads_qk = c.heads;
   if (c.heads % c.heads_qk) return LORES_ERR_INVALID_ARG;
   if (c.max_len == 0 || c.max_len > c.total) c.max_len = c.total;
-  if ((long long)c.n_seq * c.heads > 0x7FFFFFFFll || c.total / kChunk + c.n_seq > 0x7FFFFFFFll)
-    return LORES_ERR_INVALID_ARG;
+  // (grids count sequences and chunks times heads in 31 bits)
+  if ((c.total / kChunk + c.n_seq) * c.heads > 0x7FFFFFFFll) return LORES_ERR_INVALID_ARG;
   const long long wq = (long long)c.heads_qk * c.d_k, wv = (long long)c.heads * c.d_v;
   int64_t *st[4] = {&c.q_stride, &c.k_stride, &c.v_stride, &c.o_stride};
   for (int i = 0; i < 4; ++i) {
@@ -131,6 +131,7 @@ unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, ScanParams
   p.et = w.take<__half>(recs * 2 * rows * kChunk);
   p.rt = w.take<__half>(recs * 2 * rows * kChunk);
   for (float *&x : p.scales) x = w.take<float>(recs * (rows / 16));
+  p.slot_tokens = w.take<longlong2>(s.n_slots);
   if (c.heads != c.heads_qk) {
     const unsigned long long n = (unsigned long long)c.total * c.heads * c.d_k;
     p.dq = w.take<float>(n);
@@ -245,9 +246,9 @@ cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
   static std::atomic<unsigned long long> raised[4][2][2];
   const int wi = width_index(c.d_k);
-  const GradLayout l = grad_layout(c.d_k, s.np);
+  const GradLayout l = grad_layout(c.d_k, s.np, s.dvp);
   p.stages = grad_bytes(l, c.d_k, 2) <= kMaxShared ? 2 : 1;
-  return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3(s.n_slots, c.heads), kGradThreads,
+  return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3((unsigned)s.n_slots * c.heads), kGradThreads,
                 grad_bytes(l, c.d_k, p.stages), st, c.device, p, raised[wi][s.np - 1][c.delta]);
 }
 

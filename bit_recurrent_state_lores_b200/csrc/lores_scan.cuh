@@ -66,7 +66,9 @@ struct ScanParams {
   float *state_out;                    // likewise or null
   void *o;                             // forward: o; backward: d_o (read)
   unsigned *flag;
-  // workspace, records of one (slot, head); khat, qhat of one (slot, q/k head)
+  // workspace
+  longlong2 *slot_tokens;              // [n_slots] first token, tokens (written by scan_prep for the backward pass)
+  // records of one (slot, head); khat, qhat of one (slot, q/k head)
   float *gates;                        // kGateFloats
   __half *khat, *qhat;                 // [NP][64][d_k], divided by their scales
   __half *kt, *kb;                     // [2][64][d_k]
@@ -314,6 +316,9 @@ __device__ __forceinline__ void cp8(void *dst, const void *src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
                : "memory");
 }
+__device__ __forceinline__ void cp4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -531,6 +536,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   if (slot == 0 && head0 == 0) check_offsets(p);
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
+  if (BWD && head0 == 0 && tid == 0) p.slot_tokens[slot] = make_longlong2(token0, n);
   if (n == 0) return;
   const int qh = head0 / p.share, hq = p.H / p.share;
   const long long qrec = (long long)slot * hq + qh;
@@ -1674,15 +1680,16 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
 constexpr int kGradRows = 32;
 
 struct GradLayout {
-  int k, q, x, f, stage, stage_bytes, s0, d, e, r, o;
+  int k, q, x, f, scales, stage, stage_bytes, s0, d, e, r, o;
 };
-__host__ __device__ inline GradLayout grad_layout(int dk, int np) {
+__host__ __device__ inline GradLayout grad_layout(int dk, int np, int dvp) {
   GradLayout l{};
   int at = 0;
   l.k = at; at += np * kChunk * dk * 2;
   l.q = at; at += np * kChunk * dk * 2;
   l.x = at; at += 4 * kChunk * kChunk * 2;               // dP' hi, lo, dL' hi, lo
-  l.f = at; at += (kGateFloats + 4 * kChunk + 4 * kChunk + 16) * 4;
+  l.f = at; at += (kGateFloats + 4 * kChunk + 4 * kChunk + 16 + 8) * 4;
+  l.scales = at; at += 4 * (dvp / 16) * 4;
   l.stage = (at + 15) / 16 * 16;
   at = 0;
   l.s0 = at; at += 2 * kGradRows * dk * 2;
@@ -1707,11 +1714,11 @@ __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], __half2 by) {
     a[q] = *reinterpret_cast<const uint32_t *>(&y);
   }
 }
-__device__ __forceinline__ int exponent(const float *x) { return (int)(__float_as_uint(__ldg(x)) >> 23) - 127; }
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 // The largest exponent of a[b] c[b] over the blocks of 16 value rows.
 __device__ __forceinline__ int top_unit(const float *a, const float *c, int blocks, int lane) {
   int top = -1000;
-  for (int b = lane; b < blocks; b += 32) top = max(top, exponent(a + b) + exponent(c + b));
+  for (int b = lane; b < blocks; b += 32) top = max(top, exponent(a[b]) + exponent(c[b]));
   return __reduce_max_sync(0xFFFFFFFFu, top);
 }
 
@@ -1720,12 +1727,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   constexpr int NT = DK / 8, LDO = kGradRows + (NP == 2 ? 4 : 8), SIZE = NP == 2 ? 4 : 2;
   constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2, SP = kGradRows * DK * 2, EP = kGradRows * kChunk * 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  const GradLayout l = grad_layout(DK, NP);
+  const GradLayout l = grad_layout(DK, NP, p.dvp);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2, w4 = warp & 3, g = lane >> 2,
             t2 = (lane & 3) * 2, m0 = w4 * 16;
-  const int slot = blockIdx.x, head = blockIdx.y;
-  long long token0 = 0;
-  const int n = slot_tokens(p, slot, token0);
+  const int slot = blockIdx.x / p.H, head = blockIdx.x % p.H;    // (heads that share K and Q run side by side)
+  const longlong2 tokens = p.slot_tokens[slot];
+  const long long token0 = tokens.x;
+  const int n = (int)tokens.y;
   if (n == 0) return;
   const long long rec = (long long)slot * p.H + head;
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
@@ -1736,41 +1744,52 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const float2 *G = reinterpret_cast<const float2 *>(gates + kGateG * kChunk);
   float *rowv = gates + kGateFloats, *aq = rowv + kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
         *red = colp + 4 * kChunk;
-  copy_flat<NP * TILE>(smem + l.k, p.khat + qrec * (NP * kChunk * DK), tid, kGradThreads);
-  copy_flat<NP * TILE>(smem + l.q, p.qhat + qrec * (NP * kChunk * DK), tid, kGradThreads);
-  for (int i = tid; i < kGateFloats / 4; i += kGradThreads)
-    cp16(gates + 4 * i, p.gates + rec * kGateFloats + 4 * i, true);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(red + 16);                // one per stage
+  int *stop = reinterpret_cast<int *>(bars + 2);
+  if (tid == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    *stop = 0;
+    fence_mbar_init();
+  }
   const int blocks = (p.dvp + kGradRows - 1) / kGradRows, blocks16 = p.dvp / 16;
+  // A block of value rows, with the first one all that belongs to the item: bulk copies of one thread (they complete on
+  // the stage's barrier), the rows of dO in 8- or 16-byte pieces.
   auto stage_of = [&](int b) { return smem + l.stage + (p.stages == 2 ? (b & 1) * l.stage_bytes : 0); };
   auto fetch = [&](int b) {
     uint8_t *st = stage_of(b);
     const int v0 = b * kGradRows, rows = min(kGradRows, p.dvp - v0);
+    if (tid == 0) {
+      uint64_t *bar = bars + (p.stages == 2 ? b & 1 : 0);
+      mbar_expect_tx(bar, rows * (DK * 8 + kChunk * (DELTA ? 8 : 4)) + (b == 0 ? 2 * NP * TILE + kGateFloats * 4 : 0));
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const long long at = (rec * 2 + c) * p.dvp + v0;
-      const uint8_t *s0 = reinterpret_cast<const uint8_t *>(p.s0 + at * DK), *dd = reinterpret_cast<const uint8_t *>(p.dd + at * DK);
-      const uint8_t *se = reinterpret_cast<const uint8_t *>(p.et + at * kChunk), *sr = reinterpret_cast<const uint8_t *>(p.rt + at * kChunk);
-      for (int i = tid * 16; i < rows * DK * 2; i += kGradThreads * 16) {
-        cp16(st + l.s0 + c * SP + i, s0 + i, true);
-        cp16(st + l.d + c * SP + i, dd + i, true);
+      for (int c = 0; c < 2; ++c) {
+        const long long at = (rec * 2 + c) * p.dvp + v0;
+        bulk_g2s(st + l.s0 + c * SP, p.s0 + at * DK, rows * DK * 2, bar);
+        bulk_g2s(st + l.d + c * SP, p.dd + at * DK, rows * DK * 2, bar);
+        bulk_g2s(st + l.e + c * EP, p.et + at * kChunk, rows * kChunk * 2, bar);
+        if (DELTA) bulk_g2s(st + l.r + c * EP, p.rt + at * kChunk, rows * kChunk * 2, bar);
       }
-      for (int i = tid * 16; i < rows * kChunk * 2; i += kGradThreads * 16) {
-        cp16(st + l.e + c * EP + i, se + i, true);
-        if (DELTA) cp16(st + l.r + c * EP + i, sr + i, true);
+      if (b == 0) {
+        bulk_g2s(smem + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+        bulk_g2s(smem + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
+        bulk_g2s(gates, p.gates + rec * kGateFloats, kGateFloats * 4, bar);
       }
     }
+    if (b == 0)
+      for (int i = tid; i < 4 * blocks16; i += kGradThreads)
+        cp4(smem + l.scales + 4 * i, p.scales[i / blocks16] + rec * blocks16 + i % blocks16);
     copy_tokens<SIZE>(st + l.o, LDO,
                       static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + v0) * SIZE,
                       p.o_stride, kGradRows, n, p.d_v - v0, p.o16, tid, kGradThreads);
     cp_commit();
   };
   fetch(0);
-  const float *sS = p.scales[kScaleS] + rec * blocks16, *sE = p.scales[kScaleE] + rec * blocks16;
-  const float *sD = p.scales[kScaleD] + rec * blocks16, *sR = p.scales[kScaleR] + rec * blocks16;
+  const float *sS = reinterpret_cast<const float *>(smem + l.scales), *sE = sS + blocks16, *sD = sE + blocks16,
+              *sR = sD + blocks16;
   // the group's two scales: of the left operand's planes and of the right one's
   const float *sl = group == 2 ? sE : sR, *sr2 = group == 2 ? sD : group == 3 ? sE : sS;
-  const int topDS = top_unit(sD, sS, blocks16, lane), topRE = top_unit(sR, sE, blocks16, lane);
-  const int top = group == 3 ? topRE : top_unit(sl, sr2, blocks16, lane);
+  int topDS = 0, topRE = 0, top = 0;
 
   // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T
   constexpr int NA = NT > 16 ? NT : 16;
@@ -1784,7 +1803,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
 
   for (int b = 0; b < blocks; ++b) {
     cp_wait<0>();
+    if (tid == 0 && !mbar_wait_bounded(bars + (p.stages == 2 ? b & 1 : 0), (p.stages == 2 ? b >> 1 : b) & 1, kWaitNs)) {
+      *stop = 1;
+      atomicOr(p.flag, kFlagWait);
+    }
     __syncthreads();
+    if (*stop) return;
+    if (b == 0) {
+      topDS = top_unit(sD, sS, blocks16, lane);
+      topRE = top_unit(sR, sE, blocks16, lane);
+      top = group == 3 ? topRE : top_unit(sl, sr2, blocks16, lane);
+    }
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
     uint8_t *st = stage_of(b);
     const uint32_t s0 = smem_addr(st + l.s0), dd = smem_addr(st + l.d), se = smem_addr(st + l.e), sr = smem_addr(st + l.r);
@@ -1806,10 +1835,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
           const float2 x = pair(l.s0), y = pair(l.d);
           part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
         }
-        ds = fmaf(part, pow2(exponent(sD + b16) + exponent(sS + b16) - topDS), ds);
+        ds = fmaf(part, pow2(exponent(sD[b16]) + exponent(sS[b16]) - topDS), ds);
       }
-      const int el = exponent(sl + b16);
-      const float ratio = pow2(el + exponent(sr2 + b16) - top);
+      const int el = exponent(sl[b16]);
+      const float ratio = pow2(el + exponent(sr2[b16]) - top);
       const __half2 by = __float2half2_rn(ratio);
       uint32_t ao[NP][4], ar[2][4], b4[4];
       if (group == 0 || group == 3) {
@@ -2046,23 +2075,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   if (DELTA) __syncthreads();
   if (group == 0 || group == 2) {
     void *dst = group == 0 ? p.dq : p.dk;
-    const long long stride = group == 0 ? p.q_stride : p.k_stride;
+    const long long stride = p.parts ? (long long)p.H * DK : group == 0 ? p.q_stride : p.k_stride;
+    const int type = p.parts ? 0 : p.dtype;
+    const bool odd = lane & 1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      float x[4];
+    for (int i = 0; i < NT; i += 2) {
+      float x[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = acc[i][j] * outs * out2;
-      if (DELTA && group == 2) {
-        const float4 y = hand[(w4 * NT + i) * 32 + lane], z = hand[((4 + w4) * NT + i) * 32 + lane];
-        x[0] += y.x + z.x; x[1] += y.y + z.y; x[2] += y.z + z.z; x[3] += y.w + z.w;
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[e][j] = acc[i + e][j] * outs * out2;
+        if (DELTA && group == 2) {
+          const float4 y = hand[(w4 * NT + i + e) * 32 + lane], z = hand[((4 + w4) * NT + i + e) * 32 + lane];
+          x[e][0] += y.x + z.x; x[e][1] += y.y + z.y; x[e][2] += y.z + z.z; x[e][3] += y.w + z.w;
+        }
       }
+      // neighbouring lanes trade halves, so that each holds four columns of one of the two tiles
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const float rx = __shfl_xor_sync(0xFFFFFFFFu, odd ? x[0][2 * h] : x[1][2 * h], 1);
+        const float ry = __shfl_xor_sync(0xFFFFFFFFu, odd ? x[0][2 * h + 1] : x[1][2 * h + 1], 1);
+        const float4 y = odd ? make_float4(rx, ry, x[1][2 * h], x[1][2 * h + 1]) : make_float4(x[0][2 * h], x[0][2 * h + 1], rx, ry);
         const int t = m0 + g + 8 * h;
-        const long long tok = token0 + t;
         if (t < n) {
-          if (p.parts) store_pair(dst, 0, (tok * p.H + head) * DK + 8 * i + t2, x[2 * h], x[2 * h + 1]);
-          else store_pair(dst, p.dtype, tok * stride + (long long)head * DK + 8 * i + t2, x[2 * h], x[2 * h + 1]);
+          const long long at = (token0 + t) * stride + (long long)head * DK + 8 * (i + odd) + (t2 & 4);
+          if (type == 0) *reinterpret_cast<float4 *>(static_cast<float *>(dst) + at) = y;
+          else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) = make_uint2(pack_as(type, y.x, y.y), pack_as(type, y.z, y.w));
         }
       }
     }
