@@ -13,7 +13,12 @@ struct DeviceGuard {
   bool ok = false;
   explicit DeviceGuard(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = cudaSetDevice(dev) == cudaSuccess;
+    if (prev == dev) {                 // the usual case: nothing to set, nothing to restore
+      prev = -1;
+      ok = true;
+    } else {
+      ok = cudaSetDevice(dev) == cudaSuccess;
+    }
   }
   ~DeviceGuard() {
     if (prev >= 0) cudaSetDevice(prev);

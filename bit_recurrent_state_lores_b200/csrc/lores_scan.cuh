@@ -420,7 +420,7 @@ __host__ __device__ constexpr PrepLayout prep_layout(int dk, int np, bool severa
   l.x = several ? l.a + planes : l.q + (tile > planes ? tile : planes);
   l.xd = l.x + kChunk * kLdF * 4;
   l.f = l.xd + 4 * 2 * 16 * 16 * 2;
-  l.bytes = l.f + (kChunk + 2 * kChunk + 16) * 4;
+  l.bytes = l.f + 2 * (kChunk + 2 * kChunk) * 4 + 16 * 4;
   return l;
 }
 
@@ -528,9 +528,9 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   __half *A16 = reinterpret_cast<__half *>(smem + l.a);             // [2][64][64]
   float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then T
   __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][16]: X_ii
-  float2 *G = reinterpret_cast<float2 *>(smem + l.f);
-  float *bk = reinterpret_cast<float *>(G + kChunk);                // b times the scale of K
-  unsigned *red = reinterpret_cast<unsigned *>(bk + kChunk);
+  // of this head and of the next: G / ln 2, b times the scale of K
+  auto gate_at = [&](int which) { return reinterpret_cast<float2 *>(smem + l.f + which * (3 * kChunk * 4)); };
+  unsigned *red = reinterpret_cast<unsigned *>(smem + l.f + 2 * (3 * kChunk * 4));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head0 = blockIdx.y * p.hpc;
   if (slot == 0 && head0 == 0) check_offsets(p);
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       b[i] = t < n ? __ldg(p.beta + at) : 0.0f;
     }
   };
-  if (warp == 3) load_gates(head0);
+  if (warp == 0) load_gates(head0);
   float sk, sq;
   {
     __half *ko = mine ? p.khat + qrec * (NP * kChunk * DK) : nullptr, *qo = mine ? p.qhat + qrec * (NP * kChunk * DK) : nullptr;
@@ -590,96 +590,121 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   const uint32_t sK = smem_addr(K), sQ = smem_addr(Q);
   constexpr uint32_t LO = kChunk * DK * 2;         // bytes from a plane to the next
   const int m0 = warp * 16;
-#pragma unroll 1
-  for (int head = head0; head < head0 + p.hpc; ++head) {
-    const long long rec = (long long)slot * p.H + head;
-    if (head > head0) __syncthreads();             // the last head's gates and matrices are used
-    if (warp == 3) {
-      // Sums of log_alpha in 64 bits, so that their differences keep their digits behind a
-      // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
-      // held there and G stays finite.
-      float *gates = p.gates + rec * kGateFloats;
+  // one warp, a head's gates
+  auto form_gates = [&](int head) {
+    // Sums of log_alpha in 64 bits, so that their differences keep their digits behind a
+    // strong decay.  Below -1000 exp() is 0 in fp32 whatever follows, so -inf (a = 0) is
+    // held there and G stays finite.
+    float *gates = p.gates + ((long long)slot * p.H + head) * kGateFloats;
+    float2 *G = gate_at((head - head0) & 1);
+    float *bk = reinterpret_cast<float *>(G + kChunk);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (la[i] < -1000.0f) la[i] = -1000.0f;
-      double run = (double)la[0] + (double)la[1];
-      for (int d = 1; d < 32; d <<= 1) {
-        const double up = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (lane >= d) run += up;
-      }
-      const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
-      const double Gt[2] = {run - (double)la[1], run};
-      float tops[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i])), w = b[i] * c;
-        const double l2 = Gt[i] * 1.4426950408889634;
-        const float hi = (float)l2;
-        const float2 pair = make_float2(hi, (float)(l2 - (double)hi));
-        G[t] = pair;
-        bk[t] = b[i] * sk;
-        tops[0] = fmaxf(tops[0], fabsf(w * sk));
-        tops[1] = fmaxf(tops[1], fabsf(b[i] * sk));
-        tops[2] = fmaxf(tops[2], fabsf(e * sk));
-        gates[kGateE * kChunk + t] = e;
-        gates[kGateWk * kChunk + t] = w * sk;
-        gates[kGateEk * kChunk + t] = e * sk;
-        gates[kGateW * kChunk + t] = w;
-        gates[kGateB * kChunk + t] = b[i];
-        gates[kGateC * kChunk + t] = c;
-        reinterpret_cast<float2 *>(gates + kGateG * kChunk)[t] = pair;
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tops[i]));
-        if (lane == 0) gates[kGateScales + 2 + i] = __uint_as_float(m);
-      }
-      if (lane == 0) {
-        gates[kGateScales] = sk;
-        gates[kGateScales + 1] = sq;
-      }
-      if (head + 1 < head0 + p.hpc) load_gates(head + 1);
+    for (int i = 0; i < 2; ++i)
+      if (la[i] < -1000.0f) la[i] = -1000.0f;
+    double run = (double)la[0] + (double)la[1];
+    for (int d = 1; d < 32; d <<= 1) {
+      const double up = __shfl_up_sync(0xFFFFFFFFu, run, d);
+      if (lane >= d) run += up;
     }
-    __syncthreads();
-
-    float P[8][4];
+    const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
+    const double Gt[2] = {run - (double)la[1], run};
+    float tops[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      const float e = expf((float)Gt[i]), c = expf((float)(end - Gt[i])), w = b[i] * c;
+      const double l2 = Gt[i] * 1.4426950408889634;
+      const float hi = (float)l2;
+      const float2 pair = make_float2(hi, (float)(l2 - (double)hi));
+      G[t] = pair;
+      bk[t] = b[i] * sk;
+      tops[0] = fmaxf(tops[0], fabsf(w * sk));
+      tops[1] = fmaxf(tops[1], fabsf(b[i] * sk));
+      tops[2] = fmaxf(tops[2], fabsf(e * sk));
+      gates[kGateE * kChunk + t] = e;
+      gates[kGateWk * kChunk + t] = w * sk;
+      gates[kGateEk * kChunk + t] = e * sk;
+      gates[kGateW * kChunk + t] = w;
+      gates[kGateB * kChunk + t] = b[i];
+      gates[kGateC * kChunk + t] = c;
+      reinterpret_cast<float2 *>(gates + kGateG * kChunk)[t] = pair;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tops[i]));
+      if (lane == 0) gates[kGateScales + 2 + i] = __uint_as_float(m);
+    }
+    if (lane == 0) {
+      gates[kGateScales] = sk;
+      gates[kGateScales + 1] = sq;
+    }
+  };
+  if (warp == 0) {
+    form_gates(head0);
+    if (p.hpc > 1) load_gates(head0 + 1);
+  }
+  // Q K^T and K K^T, the warp's rows
+  auto products = [&](float (&P)[8][4], float (&A)[8][4]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) P[i][j] = 0.0f;
-    {
-      float A[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) A[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) P[i][j] = A[i][j] = 0.0f;
 #pragma unroll 2
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t ak[NP][4], aq[NP][4];
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
-        for (int c = 0; c < NP; ++c) {
-          if (DELTA) ld.a_rows(ak[c], sK + c * LO, m0, ks * 16);
-          ld.a_rows(aq[c], sQ + c * LO, m0, ks * 16);
-        }
+      for (int c = 0; c < NP; ++c) {
+        if (DELTA) ld.a_rows(ak[c], sK + c * LO, m0, ks * 16);
+        ld.a_rows(aq[c], sQ + c * LO, m0, ks * 16);
+      }
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          if (np <= warp) {
-            uint32_t r[4];
-            ld.b_rows(r, sK, np * 16, ks * 16);
+      for (int np = 0; np < 4; ++np) {
+        if (np <= warp) {
+          uint32_t r[4];
+          ld.b_rows(r, sK, np * 16, ks * 16);
 #pragma unroll
-            for (int c = 0; c < NP; ++c) {
-              if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], r);
-              mma2(P[2 * np], P[2 * np + 1], aq[c], r);
-            }
-            if (NP == 2) {
-              ld.b_rows(r, sK + LO, np * 16, ks * 16);
-              if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], r);
-              mma2(P[2 * np], P[2 * np + 1], aq[0], r);
-            }
+          for (int c = 0; c < NP; ++c) {
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[c], r);
+            mma2(P[2 * np], P[2 * np + 1], aq[c], r);
+          }
+          if (NP == 2) {
+            ld.b_rows(r, sK + LO, np * 16, ks * 16);
+            if (DELTA) mma2(A[2 * np], A[2 * np + 1], ak[0], r);
+            mma2(P[2 * np], P[2 * np + 1], aq[0], r);
           }
         }
       }
+    }
+  };
+  float QK[8][4];                      // without the delta rule one product serves all heads of the group
+  if (!DELTA) {
+    __syncthreads();
+    float none[8][4];
+    products(QK, none);
+  }
+#pragma unroll 1
+  for (int head = head0; head < head0 + p.hpc; ++head) {
+    const long long rec = (long long)slot * p.H + head;
+    __syncthreads();                   // this head's gates are formed, the last head's matrices are used
+    const float2 *G = gate_at((head - head0) & 1);
+    const float *bk = reinterpret_cast<const float *>(G + kChunk);
+    // the next head's gates, by the warp that has the fewest blocks
+    auto next_gates = [&]() {
+      if (warp == 0 && head + 1 < head0 + p.hpc) {
+        form_gates(head + 1);
+        if (head + 2 < head0 + p.hpc) load_gates(head + 2);
+      }
+    };
+
+    float P[8][4];
+    {
+      float A[8][4];
+      if (DELTA) products(P, A);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) P[i][j] = QK[i][j];
       if (DELTA && !several) __syncthreads();      // Q's tile becomes A's planes
       // P over the scale of Q (for Z without its decays) and, strictly below the diagonal, A
       constexpr bool KEEP = !BWD || !DELTA;        // P itself is wanted
@@ -721,7 +746,10 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         }
       }
     }
-    if (!DELTA) continue;
+    if (!DELTA) {
+      next_gates();
+      continue;
+    }
     __syncwarp();
     {
       // this warp's diagonal block: lanes c and c + 16 hold column c of its inverse
@@ -899,6 +927,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             put_pair<DK>(dst, kChunk * DK, m0 + 8 * h, half * (DK / HALVES) + 8 * i, acc[i][2 * h], acc[i][2 * h + 1], lane);
       }
     }
+    next_gates();
   }
 }
 
@@ -2175,7 +2204,7 @@ static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParam
 constexpr int kRecThreads = 128, kRecRows = 2, kRecTokens = 8;
 
 template <int DK, bool DELTA>
-__global__ void __launch_bounds__(kRecThreads) scan_recurrent_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kRecThreads, 7) scan_recurrent_kernel(const ScanParams p) {
   constexpr int LPR = DK / 16, ROWS = kRecThreads / LPR * kRecRows;
   __shared__ float4 sk[kRecTokens][DK / 4], sq[kRecTokens][DK / 4];
   __shared__ float sv[kRecTokens][ROWS];
