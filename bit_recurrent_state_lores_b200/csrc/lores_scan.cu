@@ -208,11 +208,15 @@ lores_status device_ok(int device) {
 }
 
 // Blocks of 16 value rows per CTA of a walk: a CTA's blocks share one fetch of a chunk's tiles, but the CTAs
-// should fill the SMs.
-int walk_blocks(const Shape &s) {
+// should fill the SMs.  Two blocks even where that leaves a quarter of the SMs idle (one block per CTA took 516 us
+// against 300 for one sequence of 8192 tokens and 32 heads of 128 x 128), four only for several rounds of CTAs
+// (322 us against 334 with 512 CTAs of four, 159 against 146 with 192).
+int walk_blocks(const Shape &s, WalkKind kind) {
   const long long walks = (long long)s.c.n_seq * s.c.heads;
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
-  return blocks < kMaxBlocks || walks * ((blocks + 1) / kMaxBlocks) < sms / 2 ? 1 : kMaxBlocks;
+  const auto ctas = [&](int rb) { return walks * ((blocks + rb - 1) / rb); };
+  if (max_blocks(s.np, s.c.delta, kind) == 4 && blocks >= 4 && ctas(4) >= 3ll * sms) return 4;
+  return blocks >= 2 && ctas(2) >= sms / 2 ? 2 : 1;
 }
 
 bool aligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3u) == 0; }
@@ -234,7 +238,7 @@ cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t s
   const lores_scan_config &c = s.c;
   static std::atomic<unsigned long long> raised[4][2][2][3];
   const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
-  p.rb = walk_blocks(s);
+  p.rb = walk_blocks(s, kind);
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
   p.stages = 2 * l.bytes + p.rb * l.tail + 32 <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],

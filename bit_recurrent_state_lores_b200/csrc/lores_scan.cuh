@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
-// Without the delta rule E = V and the state warps have no products before X; two CTAs then share an SM.
+// Without the delta rule E = V and the state warps have no products before X; a CTA then takes four blocks.
 // A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit): bulk copies,
 // since 16-byte cp.async of the same 96 KB took longer than the chunk's arithmetic; and it turns
 // the block's rows of V into fp16 over their scale.  In the backward pass's recomputation (SAVE)
@@ -949,11 +949,14 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 // The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
 // form D's sum over dO^T Q, which the state warps take last (barrier Z).
 constexpr int kSideWarps = 2;
-constexpr int kMaxBlocks = 2;          // blocks of value rows per CTA
-constexpr int kLoadWarps = kMaxBlocks;
-constexpr int kWalkThreads = 32 * (kMaxBlocks * (2 + kSideWarps) + kLoadWarps);
+constexpr int kReverseBlocks = 2;
 
 enum WalkKind { kForward, kRecompute, kReverse };
+// Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
+__host__ __device__ constexpr int max_blocks(int np, bool delta, int kind) {
+  return !delta && kind != kReverse && np == 1 ? 4 : 2;
+}
+__host__ __device__ constexpr int walk_threads(int blocks) { return 32 * blocks * (2 + kSideWarps + 1); }
 
 struct WalkLayout {
   int kt, k, q, tm, pp, v, gates, bytes;         // byte offsets inside one stage
@@ -1191,7 +1194,7 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
 }
 
 template <int DK, int NP, bool DELTA, int KIND, int NH>
-__global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP == 2 ? 1 : 2) scan_walk_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) scan_walk_kernel(const ScanParams p) {
   constexpr bool REV = KIND == kReverse;
   constexpr bool JOIN = DELTA || REV;                        // E (or R) has parts in several warps
   constexpr int DKH = DK / NH, NTH = DKH / 8;
@@ -1667,7 +1670,7 @@ __global__ void __launch_bounds__(kWalkThreads, DELTA || KIND == kReverse || NP 
             if (lane == 0 && H == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
             if (REV) {
               // (both side warps are done with the rows of dO)
-              barrier_sync(Z + 3 * kMaxBlocks, 32 * kSideWarps);
+              barrier_sync(Z + 3 * kReverseBlocks, 32 * kSideWarps);
               store_tokens<NP>(O, 1.0f, tile, 4 * H, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
                                head * p.d_v + brow, p.d_v - brow, p.v16, lane);
             }
