@@ -216,9 +216,6 @@ struct Lane {
 __device__ __forceinline__ void a_rows_plain(uint32_t (&r)[4], uint32_t x, int ld, int m0, int k0, int lane) {
   ldsm4(r, x + 2 * ((m0 + (((lane >> 3) & 1) << 3) + (lane & 7)) * ld + k0 + ((lane >> 4) << 3)));
 }
-__device__ __forceinline__ void a_cols_plain(uint32_t (&r)[4], uint32_t x, int ld, int k0, int m0, int lane) {
-  ldsm4t(r, x + 2 * ((k0 + ((lane >> 4) << 3) + (lane & 7)) * ld + m0 + (((lane >> 3) & 1) << 3)));
-}
 // Element (row, col) of a tiled matrix.
 template <int COLS>
 __device__ __forceinline__ int tiled(int row, int col) {
@@ -325,13 +322,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// BYTES contiguous bytes (a multiple of 16).
-template <int BYTES>
-__device__ __forceinline__ void copy_flat(uint8_t *dst, const void *src, int tid, int threads) {
-  const uint8_t *s = static_cast<const uint8_t *>(src);
-#pragma unroll 8
-  for (int i = tid; i < BYTES / 16; i += threads) cp16(dst + 16 * i, s + 16 * i, true);
-}
 // `cols` columns (a multiple of 16) of 64 token rows of the caller's tensor: rows >= n and
 // columns >= have (a multiple of 4) are zeros.  ld in elements.
 template <int SIZE>
@@ -347,11 +337,6 @@ __device__ __forceinline__ void copy_tokens(uint8_t *dst, int ld, const uint8_t 
   }
 }
 
-__device__ __forceinline__ void store_as(void *base, int dtype, long long i, float x) {
-  if (dtype == 0) static_cast<float *>(base)[i] = x;
-  else if (dtype == 1) static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(x);
-  else static_cast<__half *>(base)[i] = __float2half_rn(x);
-}
 // Two values of a 16-bit type, x low.
 __device__ __forceinline__ uint32_t pack_as(int dtype, float x, float y) {
   if (dtype != 1) return pack2(x, y);
@@ -373,28 +358,6 @@ __device__ __forceinline__ void load4(const void *src, int dtype, long long i, f
   const float2 a = pair_of(w.x, dtype), b = pair_of(w.y, dtype);
   x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
-// 8 entries of a row of the caller's tensor.
-__device__ __forceinline__ void load8(const void *src, int dtype, long long i, bool by16, float (&x)[8]) {
-  if (dtype != 0 && by16) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + i));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = pair_of(u[e], dtype);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
-    }
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float y[4];
-    load4(src, dtype, i + 4 * h, y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * h + e] = y[e];
-  }
-}
-
 // -------------------------------------------------------------------------------------
 // scan_prep
 // -------------------------------------------------------------------------------------
@@ -1709,7 +1672,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 // Scales: the planes of 16 value rows are held over their own powers of two, so a 16-row step
 // contributes in units that are the product of two of them; left operands are brought to
 // the largest unit F of the group's steps, and the group's sums are held over F.
-constexpr int kGradRows = 32;
+// The tensor cores cut their sums off instead of rounding them: 768 products in a row (d_v = 4096) leave 1.6e-5, all
+// to one side.  So every kGradSum value rows (48 products, below 1.5e-6) the sums are added, rounded, to a copy in the
+// thread's local memory; narrower heads (the usual 64 to 256) never touch it.
+constexpr int kGradRows = 32, kGradSum = 256;
 
 struct GradLayout {
   int k, q, x, f, scales, stage, stage_bytes, s0, d, e, r, o;
@@ -1830,6 +1796,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   for (int i = 0; i < NA; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  float kept[NA * 4], *far = kept;
+  asm volatile("" : "+l"(far));                          // (memory, not registers)
   const Lane<DK> ld(lane);
   const Lane<kChunk> lc(lane);
 
@@ -1938,6 +1906,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
     if (p.stages == 1) {
       __syncthreads();
       if (b + 1 < blocks) fetch(b + 1);
+    }
+    if (blocks > kGradSum / kGradRows && ((b + 1) % (kGradSum / kGradRows) == 0 || b + 1 == blocks)) {
+      const bool begun = b >= kGradSum / kGradRows, done = b + 1 == blocks;
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = acc[i][j] + (begun ? far[4 * i + j] : 0.0f);
+          if (!done) far[4 * i + j] = x;
+          acc[i][j] = done ? x : 0.0f;
+        }
     }
   }
 #pragma unroll

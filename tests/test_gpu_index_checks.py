@@ -232,3 +232,37 @@ def test_ordinary_build_has_no_checks():
         assert e.value.status == L.LORES_ERR_INVALID_ARG
     finally:
         L.lores_destroy(h)
+
+
+POOL_CASES = [("bytes", 128, 40, 128, [8, 4, 32], {}),
+              ("dense", 64, 24, 32, [5, 6, 7], {"dense": 1})]
+
+
+@pytest.mark.parametrize("name,dk,dv,G,bits,kw", POOL_CASES, ids=[c[0] for c in POOL_CASES])
+def test_chosen_slots_in_the_checked_build(name, dk, dv, G, bits, kw, use_checked):
+    """Writing and reading slots: bit-identical, no flag; a trimmed buffer is flagged."""
+    L = lib()
+    wl = synth.Workload("ic-pool", B=4, H=len(bits), d_k=dk, d_v=dv, steps=1, group=G)
+    S = torch.randn(3, wl.H, dv, dk, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    slots = torch.tensor([2, 0, 3], dtype=torch.int32, device="cuda")
+    outs = []
+    for checked in (False, True):
+        use_checked(checked)
+        g = GpuRun(wl, bits, seed=6, **kw)
+        try:
+            L.lores_write_states(g.h, 3, slots, S, 5)
+            out = torch.full((3, wl.H, dv, dk), 777.0, device="cuda")
+            L.lores_read_states(g.h, 3, slots, out)
+            assert g.check() == L.LORES_OK
+            outs.append((out, g.export()))
+            if checked:
+                L.lores_debug_trim_range(g.h, STATE, 64)         # the last 16 floats of the caller's states
+                out = torch.full((3, wl.H, dv, dk), 777.0, device="cuda")
+                L.lores_read_states(g.h, 3, slots, out)
+                assert g.check() == L.LORES_ERR_INDEX
+                assert L.lores_debug_last_flags(g.h) == INDEX_BIT | (256 << STATE)
+                assert (out.reshape(-1)[-16:] == 777).all()
+                assert torch.equal(out.reshape(-1)[:-16], outs[0][0].reshape(-1)[:-16])
+        finally:
+            g.close()
+    assert torch.equal(outs[0][0], outs[1][0]) and same(outs[0][1], outs[1][1])

@@ -205,3 +205,20 @@ def test_prompt_through_the_pool():
     finally:
         a.close()
         b.close()
+
+
+def test_slots_beyond_32_bits():
+    """A pool of more than 4 GB: the last slot's state goes in and out, the others stay zero."""
+    L = lib()
+    B, H, d = 2100, 32, 128
+    h = L.lores_create(B, H, d, d, head_bits=[32] * H)
+    try:
+        S = states(2, H, d, d, seed=7)
+        L.lores_write_states(h, 2, slots_of(B - 1, 1040), S, 0)
+        back = torch.full((3, H, d, d), 777.0, device="cuda")
+        L.lores_read_states(h, 3, slots_of(1040, 0, B - 1), back)
+        assert torch.equal(back[0], S[1]) and torch.equal(back[2], S[0])
+        assert (back[1] == 0).all()
+        assert L.lores_check_errors(h) == L.LORES_OK
+    finally:
+        L.lores_destroy(h)

@@ -516,3 +516,87 @@ def test_a_long_sequence_with_a_state_that_does_not_decay():
     w = x["beta"][:, 0, None] * x["v"][:, 0]
     rS = x["state"][0, 0] + w.T @ x["k"][:, 0]
     assert rel(S[0, 0], rS) <= FP32
+
+
+@pytest.mark.parametrize("delta", [0, 1])
+@pytest.mark.parametrize("longest", [24, 25, 32, 33])
+def test_lengths_around_the_change_of_kernels(longest, delta):
+    lens = [longest, 3, 0, longest - 1]
+    x, offs = inputs(lens, 2, 1, 64, 36, BF16, seed=120 + longest)
+    c = Call(x, offs, delta, BF16, max_len=longest)
+    o, S = c.forward()
+    ro, rS = scan64(*(x[n] for n in NAMES[:5]), offs, x["state"], delta)
+    assert rel(o, ro) <= tol(BF16, planes=True) and rel(S, rS) <= FP32
+    assert c.check() == c.L.LORES_OK
+
+
+@pytest.mark.parametrize("dv,dtype", [(64, BF16), (80, F16), (64, F32)])
+def test_enough_heads_for_several_rounds(dv, dtype):
+    """Enough heads that CTAs take four blocks of value rows (the last CTA of a walk not all of them) and the
+    preparation two heads."""
+    x, offs = inputs([300, 33, 1, 130], 128, 2, 16, dv, dtype, seed=dv)
+    names = [x[n].requires_grad_() for n in NAMES]
+    ro, rS = scan64(*names[:5], offs, names[5], 0)
+    g = torch.Generator().manual_seed(3)
+    d_o = torch.randn(ro.shape, generator=g).to(dtype).double().cuda()
+    d_S = torch.randn(rS.shape, generator=g).double().cuda()
+    want = torch.autograd.grad([ro, rS], names, [d_o, d_S])
+    x = {n: t.detach() for n, t in x.items()}
+    c = Call(x, offs, 0, dtype, pad=8)
+    o, S = c.forward()
+    assert rel(o, ro.detach()) <= tol(dtype, planes=True) and rel(S, rS.detach()) <= FP32
+    got = c.backward(d_o, d_S)
+    for n, w in zip(NAMES, want):
+        t = tol(dtype) if n in "qkv" else 4 * FP32 if n in ("log_alpha", "beta") else FP32
+        assert rel(got[n], w) <= t, n
+    assert c.check() == c.L.LORES_OK
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_widest_values(dtype):
+    x, offs = inputs([70, 5], 1, 1, 64, 4096, dtype, seed=131)
+    names = [x[n].requires_grad_() for n in NAMES]
+    ro, rS = scan64(*names[:5], offs, names[5], 1)
+    d_o = torch.randn(ro.shape, generator=torch.Generator().manual_seed(4)).to(dtype).double().cuda()
+    want = torch.autograd.grad([ro], names, [d_o])
+    x = {n: t.detach() for n, t in x.items()}
+    c = Call(x, offs, 1, dtype)
+    o, S = c.forward()
+    assert rel(o, ro.detach()) <= tol(dtype, planes=True) and rel(S, rS.detach()) <= FP32
+    got = c.backward(d_o, None)
+    for n, w in zip(NAMES, want):
+        t = tol(dtype) if n in "qkv" else 4 * FP32 if n in ("log_alpha", "beta") else FP32
+        assert rel(got[n], w) <= t, n
+
+
+@pytest.mark.parametrize("max_len", [0, 8])
+def test_rows_beyond_32_bits(max_len):
+    """Token rows so far apart that the last ones lie past 2^31 elements: same bits as back to back."""
+    L = lib()
+    T, n_seq, stride = 144, (18 if max_len else 2), 16_000_000
+    x, offs = inputs([T // n_seq] * n_seq, 2, 2, 64, 64, BF16, seed=141)
+    near = Call(x, offs, 1, BF16, max_len=max_len)
+    o, S = (t.clone() for t in near.forward())
+    g = {n: t.clone() for n, t in near.backward(x["v"], x["state"]).items()}
+    ins, outs = (torch.zeros(T * stride, dtype=BF16, device="cuda") for _ in range(2))
+    assert (T - 1) * stride > 2 ** 31
+
+    def rows(buf, i):                                    # the i-th tensor: 128 columns from 128 i on
+        return torch.as_strided(buf, (T, 128), (stride, 1), 128 * i)
+
+    for i, n in enumerate("qkv"):
+        rows(ins, i).copy_(getattr(near, n))
+    rows(ins, 3).copy_(near.d_o)
+    cfg = L.make_scan_config(n_seq, T, 2, 64, 64, dtype=BF16, max_len=max_len, q_stride=stride, k_stride=stride,
+                             v_stride=stride, o_stride=stride)
+    q, k, v, d_o = (rows(ins, i) for i in range(4))
+    far_S = torch.empty_like(S)
+    L.lores_scan_forward(cfg, q, k, v, near.la, near.be, near.offsets, near.state, rows(outs, 0), far_S, near.work)
+    assert torch.equal(rows(outs, 0), o.reshape(T, 128)) and torch.equal(far_S, S)
+    dla, dbe, ds = (torch.empty_like(t) for t in (near.dla, near.dbe, near.ds))
+    L.lores_scan_backward(cfg, q, k, v, near.la, near.be, near.offsets, near.state, d_o, near.d_state_out,
+                          rows(outs, 1), rows(outs, 2), rows(outs, 3), dla, dbe, ds, near.work)
+    for i, n in enumerate("qkv"):
+        assert torch.equal(rows(outs, 1 + i), g[n].reshape(T, 128)), n
+    assert torch.equal(dla, g["log_alpha"]) and torch.equal(dbe, g["beta"]) and torch.equal(ds, g["state"])
+    assert int(torch.count_nonzero(outs.view(T, stride)[:, 512:1024])) == 0
