@@ -375,12 +375,13 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * arithmetic, 16-bit outputs within their own rounding, while |k_t|^2 beta_t < 2 holds with
  * delta = 1 (the domain of the recurrence).  An infinity or NaN in a token's
  * inputs may turn the outputs of the whole 64-token chunk that holds it (counted from the
- * sequence's start), and what follows, to NaN; other sequences are not touched. */
+ * sequence's start), and what follows (in the backward pass also what comes before), to NaN,
+ * for the heads that read them; other heads and sequences are not touched. */
 typedef struct {
     int32_t n_seq;      /* sequences, >= 1                                                   */
     int64_t total;      /* tokens of all of them, 0 .. 2^31 - 1                              */
-    int64_t max_len;    /* no sequence is longer than this (0: total).  At most 16 (or        */
-                        /* d_k = 256) selects the token-by-token kernel                      */
+    int64_t max_len;    /* no sequence is longer than this (0: total).  At most 32 (24 with   */
+                        /* delta = 0), or d_k = 256, selects the token-by-token kernel       */
     int32_t heads;      /* H: heads of v, o, the gates and the states                        */
     int32_t heads_qk;   /* heads of q and k; divides H (0: H).  Head h reads head            */
                         /* h / (H / heads_qk); dq and dk are summed over such heads           */
@@ -436,7 +437,8 @@ lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, co
                                  void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Wait for `stream` and report what the last call on this workspace found: INVALID_ARG if a
- * sequence's offsets did not fit, else OK. */
+ * sequence's offsets did not fit, TIMEOUT if a kernel gave up waiting for its own copies (one
+ * second; the call's outputs are then incomplete), else OK. */
 lores_status lores_scan_check_errors(const lores_scan_config *cfg, const void *workspace,
                                      void *stream);
 
