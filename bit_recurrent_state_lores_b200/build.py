@@ -6,8 +6,8 @@ csrc/lores.cu (host side, loader, dequantizer) and 45 compilations of csrc/lores
 (one decode-step kernel family per key width x single/multi-token x storage family --
 plain; dense and per-lane; per-lane only --, one two-rows-per-lane family per key width x
 single/multi-token, and one key-axis family per key width) and of the state scan
-(csrc/lores_scan.cu and one csrc/lores_scan_inst.cu per key width and number of input planes) build in parallel, one nvcc
-process per CPU core, then link.
+(csrc/lores_scan.cu and one csrc/lores_scan_inst.cu per key width and number of input
+planes) build in parallel, one nvcc process per CPU core, then link.
 
 --checked builds liblores_checked.so instead: the same sources compiled with
 LORES_INDEX_CHECKS, so that every global access of the kernels is checked against the

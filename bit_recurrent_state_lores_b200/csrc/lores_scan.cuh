@@ -11,11 +11,11 @@
 //   O    = diag(e^G) Q S0^T + P E      S_C = e^{G_C} S0 + (diag(w) E)^T K,  w = b e^{G_C - G}
 // Only S0 -> S_C is sequential, so the work is split in two:
 //   scan_prep     all chunks at once: gates, Tm, P, Kt = -d T K (and, for the backward pass,
-//                 Z = P Tm and Kb = T^T diag(b) K).  (With Gam = diag(e^G), (I + L diag(b))^-1 for
-//                 L_ts = dec_ts k_t.k_s is Gam T Gam^-1: the decays leave the inverse, whose entries stay of size
-//                 one, and come back as factors of its rows.)
-//   scan_walk     per (sequence, head, block of value rows): E^T = S0 Kt^T diag(e^G) + (Tm V)^T, O^T and
-//                 S_C, chunk after chunk.  Value rows are independent (as in the decode
+//                 Z = P Tm and Kb = T^T diag(b) K).  (With Gam = diag(e^G), (I + L diag(b))^-1
+//                 for L_ts = dec_ts k_t.k_s is Gam T Gam^-1: the decays leave the inverse,
+//                 whose entries stay of size one, and come back as factors of its rows.)
+//   scan_walk     per (sequence, head, block of value rows): E^T = S0 Kt^T diag(e^G) +
+//                 (Tm V)^T, O^T and S_C, chunk after chunk.  Value rows are independent (as in the decode
 //                 step), so one or two warps own 16 of them, keep S [16][d_k] in their
 //                 accumulators and feed it back as the next product's left operand
 //                 without leaving registers; two more warps per 16 rows do what the
@@ -25,6 +25,13 @@
 //   D0  = e^{G_C} D + (diag(e^G) dO)^T Q - d (diag(e^G) R)^T K
 //   scan_walk     the same backwards over R and D;
 //   scan_grads    all chunks at once: dQ, dK and the gates' gradients from S0, D, E, R.
+//
+// Tensor cores.  The products are mma.sync m16n8k16: a walk's blocks have 16 rows, because 32 heads
+// of 128 value rows must spread over 148 SMs, and the state has to be an accumulator and the next
+// product's left operand within a few hundred cycles; tcgen05 wants 64 rows at least and keeps
+// accumulators in TMEM, so that every chunk would pay two trips through it on the critical path.
+// Nothing here is bound by the rate of the products: mma.sync measured 555 TFLOP/s on this card, and
+// the walk keeps the tensor cores busy for 1850 of a chunk's 4350 cycles.
 //
 // Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
 // as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
@@ -207,10 +214,18 @@ struct Lane {
   __device__ __forceinline__ static uint32_t at(int row, int col) {
     return ((row >> 3) * (COLS / 8) + (col >> 3)) * 128;
   }
-  __device__ __forceinline__ void b_rows(uint32_t (&r)[4], uint32_t x, int n0, int k0) const { ldsm4(r, x + down + at(n0, k0)); }
-  __device__ __forceinline__ void b_cols(uint32_t (&r)[4], uint32_t x, int k0, int n0) const { ldsm4t(r, x + across + at(k0, n0)); }
-  __device__ __forceinline__ void a_rows(uint32_t (&r)[4], uint32_t x, int m0, int k0) const { ldsm4(r, x + across + at(m0, k0)); }
-  __device__ __forceinline__ void a_cols(uint32_t (&r)[4], uint32_t x, int k0, int m0) const { ldsm4t(r, x + down + at(k0, m0)); }
+  __device__ __forceinline__ void b_rows(uint32_t (&r)[4], uint32_t x, int n0, int k0) const {
+    ldsm4(r, x + down + at(n0, k0));
+  }
+  __device__ __forceinline__ void b_cols(uint32_t (&r)[4], uint32_t x, int k0, int n0) const {
+    ldsm4t(r, x + across + at(k0, n0));
+  }
+  __device__ __forceinline__ void a_rows(uint32_t (&r)[4], uint32_t x, int m0, int k0) const {
+    ldsm4(r, x + across + at(m0, k0));
+  }
+  __device__ __forceinline__ void a_cols(uint32_t (&r)[4], uint32_t x, int k0, int m0) const {
+    ldsm4t(r, x + down + at(k0, m0));
+  }
 };
 // The caller's token rows, in plain rows of ld elements.
 __device__ __forceinline__ void a_rows_plain(uint32_t (&r)[4], uint32_t x, int ld, int m0, int k0, int lane) {
@@ -363,7 +378,10 @@ __device__ __forceinline__ void load4(const void *src, int dtype, long long i, f
 // -------------------------------------------------------------------------------------
 // Grid (slot, group of p.hpc heads that share K and Q), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.]
 // result, and only blocks on and below the diagonal are formed.  K and Q are fetched and converted
-// once for the group.  T = (I + A)^-1 by 16x16 blocks:
+// once for the group.  Bound by latency: a chain of short products with four CTAs per SM to hide it.
+// 8192 tokens, 32 heads, d_k = 128, bf16 (4096 items, 370 MB of matrices written): 146 us, 2.5 TB/s;
+// without the delta rule and with 16 heads on one pair of Q and K (7800 tokens, 128 heads): 76 us.
+// A CTA per head took 343 us there.  T = (I + A)^-1 by 16x16 blocks:
 // the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
 // forms block column j downwards, X_ij = -X_ii sum_{j <= k < i} A_ik X_kj, as
 // X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
@@ -895,7 +913,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 }
 
 // -------------------------------------------------------------------------------------
-// the walks: scan_chain and scan_reverse
+// scan_walk
 // -------------------------------------------------------------------------------------
 // Grid (sequence * H + head, group of p.rb blocks of 16 value rows).  Per block:
 //   NH state warps: warp h holds the state's columns [h d_k/NH, (h+1) d_k/NH) in its accumulators and
@@ -905,10 +923,15 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
 // Without the delta rule E = V and the state warps have no products before X; a CTA then takes four blocks.
-// A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit): bulk copies,
-// since 16-byte cp.async of the same 96 KB took longer than the chunk's arithmetic; and it turns
-// the block's rows of V into fp16 over their scale.  In the backward pass's recomputation (SAVE)
-// the planes of S0 and E are kept instead of o.
+// A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit; one
+// took 465 us where two take 300): bulk copies, since 16-byte cp.async of the same 96 KB took longer
+// than the chunk's arithmetic (665 against 500 us); and it turns the block's rows of V into fp16 over
+// their scale.  In the backward pass's recomputation (kRecompute) the planes of S0 and E are kept
+// instead of o.
+// Bound by the latency of a chunk's chain, close behind it by shared memory (3000 of 4350 cycles:
+// fragments, exchanged parts, copies).  One sequence of 8192 tokens, 32 heads of 128 x 128, bf16: 128
+// chunks in 300 us, 2.3 us a chunk; the same recomputed for 2 x 4096 tokens and 16 heads: 145 us;
+// reverse: 200 to 220 us.
 // The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
 // form D's sum over dO^T Q, which the state warps take last (barrier Z).
 constexpr int kSideWarps = 2;
@@ -1242,7 +1265,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     if (by && loader && i0 + 1 < chunks) fetch(next);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
                    tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
-    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk, *lead = REV ? ek + kChunk : eG, *scalars = ek + 2 * kChunk;
+    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk,
+                *lead = REV ? ek + kChunk : eG, *scalars = ek + 2 * kChunk;
     const float qscale = scalars[1];
     const long long rec = (long long)(base + c) * p.H + head;
     const int n = min(kChunk, len - c * kChunk);
@@ -1468,7 +1492,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              sided[(4 * H + i) * 32 + lane] = make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
+              sided[(4 * H + i) * 32 + lane] =
+                  make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
           }
           // (in reverse the sum over dO^T Q waits too: it then runs beside the state warps' additions and not
           // beside their products, which the chain waits for)
@@ -1526,7 +1551,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * QS; ++i)
-                  plus[(col / 8 + i) * 32 + lane] = make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+                  plus[(col / 8 + i) * 32 + lane] =
+                      make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
               }
             }
             barrier_arrive(Z, PER);
@@ -1672,6 +1698,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 // Scales: the planes of 16 value rows are held over their own powers of two, so a 16-row step
 // contributes in units that are the product of two of them; left operands are brought to
 // the largest unit F of the group's steps, and the group's sums are held over F.
+// Bound by latency and the tensor cores in turn: of an item's 35000 cycles 4300 wait for the first
+// copies, 17000 are the sums over value rows (10800 of products), 4200 the matrices dP' and dL', 3200
+// their products and 3600 the stores.  2 x 4096 tokens, 16 heads of 128 x 128, bf16 (2048 items): 280
+// us.  Items of a CTA one behind the other, the next one's copies under way: 357 us (registers).
 // The tensor cores cut their sums off instead of rounding them: 768 products in a row (d_v = 4096) leave 1.6e-5, all
 // to one side.  So every kGradSum value rows (48 products, below 1.5e-6) the sums are added, rounded, to a copy in the
 // thread's local memory; narrower heads (the usual 64 to 256) never touch it.
@@ -2106,12 +2136,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       for (int h = 0; h < 2; ++h) {
         const float rx = __shfl_xor_sync(0xFFFFFFFFu, odd ? x[0][2 * h] : x[1][2 * h], 1);
         const float ry = __shfl_xor_sync(0xFFFFFFFFu, odd ? x[0][2 * h + 1] : x[1][2 * h + 1], 1);
-        const float4 y = odd ? make_float4(rx, ry, x[1][2 * h], x[1][2 * h + 1]) : make_float4(x[0][2 * h], x[0][2 * h + 1], rx, ry);
+        const float4 y = odd ? make_float4(rx, ry, x[1][2 * h], x[1][2 * h + 1])
+                             : make_float4(x[0][2 * h], x[0][2 * h + 1], rx, ry);
         const int t = m0 + g + 8 * h;
         if (t < n) {
           const long long at = (token0 + t) * stride + (long long)head * DK + 8 * (i + odd) + (t2 & 4);
           if (type == 0) *reinterpret_cast<float4 *>(static_cast<float *>(dst) + at) = y;
-          else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) = make_uint2(pack_as(type, y.x, y.y), pack_as(type, y.z, y.w));
+          else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) =
+                make_uint2(pack_as(type, y.x, y.y), pack_as(type, y.z, y.w));
         }
       }
     }
@@ -2154,7 +2187,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   }
 }
 
-// Sums the heads' parts of dq and dk where heads share q and k, in head order.
+// Sums the heads' parts of dq and dk where heads share q and k, in head order.  Memory bound: 8192
+// tokens, 16 heads on 8, d_k = 128, bf16: 40 us, 4.2 TB/s.  (scan_grads adding its part to the last
+// head's instead, heads of a group one behind the other: it took 497 us in place of 320.)
 static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParams p, const float *parts_q,
                                                                  const float *parts_k, int dk) {
   const int hq = p.H / p.share, per = hq * (dk / 4);
@@ -2182,7 +2217,10 @@ static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParam
 // Grid (sequence * H + head, group of value rows).  d_k/16 lanes share a value row (16 of its columns each, in
 // groups of 4 so that the lanes' 16-byte accesses are contiguous) and two rows are in flight per
 // lane, their arithmetic as packed pairs.  q, k, v and the gates of kRecTokens tokens at a time pass through
-// shared memory as fp32, while the state's loads are under way.
+// shared memory as fp32, while the state's loads are under way.  Memory bound for a few tokens (the
+// state in and out): 64 sequences of up to 5, 32 heads of 128 x 128: 61 us, 4.6 TB/s; then by issue,
+// 8.5 us a token there.  Seven CTAs per SM (72 registers) took 63 us a call where eight
+// took 65.
 constexpr int kRecThreads = 128, kRecRows = 2, kRecTokens = 8;
 
 template <int DK, bool DELTA>
