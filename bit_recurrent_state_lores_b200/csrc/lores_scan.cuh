@@ -176,6 +176,17 @@ __device__ __forceinline__ void check_offsets(const ScanParams &p) {
 }
 
 // -------------------------------------------------------------------------------------
+// launches that overlap
+// -------------------------------------------------------------------------------------
+// A call's kernels are launched so that each may start once every CTA of the one before it has
+// started and called launch_next(); what reads the other's results calls wait_before() first, which
+// returns when the kernels before this one are complete and their writes visible.  The first kernel
+// is launched the ordinary way, and every kernel waits before it ends, so that a call is
+// ordered as a whole.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// -------------------------------------------------------------------------------------
 // fragments
 // -------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void *x) {
@@ -514,6 +525,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   unsigned *red = reinterpret_cast<unsigned *>(smem + l.f + 2 * (3 * kChunk * 4));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head0 = blockIdx.y * p.hpc;
+  launch_next();
   if (slot == 0 && head0 == 0) check_offsets(p);
   long long token0 = 0;
   const int n = slot_tokens(p, slot, token0);
@@ -1242,6 +1254,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
                      head * p.d_v + brow, min(kChunk, len - c * kChunk), p.d_v - brow, REV ? p.o16 : p.v16, lane);
     cp_commit();
   };
+  // The reverse walk reads nothing of the recomputation, which has waited for scan_prep: it may run beside it, on the
+  // SMs that it leaves free, and waits for it at its own end.
+  if (!REV) wait_before();
+  launch_next();
   if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0);
   for (int i0 = 0; i0 < chunks; ++i0) {
     const int c = REV ? chunks - 1 - i0 : i0, next = REV ? c - 1 : c + 1;
@@ -1261,7 +1277,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
       }
     }
     __syncthreads();
-    if (*stop) return;
+    if (*stop) break;
     if (by && loader && i0 + 1 < chunks) fetch(next);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
                    tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
@@ -1674,10 +1690,11 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
       if (loader && i0 + 1 < chunks) fetch(next);
     }
   }
-  if (live && !side && !loader && KIND != kRecompute) {
+  if (live && !side && !loader && KIND != kRecompute && !*stop) {
     float *out = REV ? p.d_state_in : p.state_out;
     if (out) save_state<NTH>(S, out, blockIdx.x, p.d_v, DK, r0, c0 + t2);
   }
+  if (REV) wait_before();
 }
 
 // -------------------------------------------------------------------------------------
@@ -1759,6 +1776,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2, w4 = warp & 3, g = lane >> 2,
             t2 = (lane & 3) * 2, m0 = w4 * 16;
   const int slot = blockIdx.x / p.H, head = blockIdx.x % p.H;    // (heads that share K and Q run side by side)
+  wait_before();
+  launch_next();
   const longlong2 tokens = p.slot_tokens[slot];
   const long long token0 = tokens.x;
   const int n = (int)tokens.y;
@@ -2192,6 +2211,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
 // head's instead, heads of a group one behind the other: it took 497 us in place of 320.)
 static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParams p, const float *parts_q,
                                                                  const float *parts_k, int dk) {
+  wait_before();
   const int hq = p.H / p.share, per = hq * (dk / 4);
   const long long n = p.total * per, all = 2 * n;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
