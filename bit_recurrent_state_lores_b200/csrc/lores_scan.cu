@@ -114,7 +114,7 @@ unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, ScanParams
   Carver w{ws};
   p.flag = reinterpret_cast<unsigned *>(ws);
   if (s.recurrent) return w.at;
-  const unsigned long long recs = (unsigned long long)s.n_slots * c.heads, sq = 2 * kChunk * kChunk,
+  const unsigned long long recs = (unsigned long long)s.n_slots * c.heads, sq = 2 * kTri,
                            tile = 2ull * kChunk * c.d_k, rows = (unsigned long long)s.dvp;
   p.khat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
   p.qhat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
@@ -236,7 +236,7 @@ int walk_blocks(const Shape &s, WalkKind kind) {
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
   const auto ctas = [&](int rb) { return walks * ((blocks + rb - 1) / rb); };
   // the two walks of a backward call side by side, where one of these numbers lets them
-  if (kind != kForward)
+  if (!is_forward(kind))
     for (int rb = 1; rb <= std::min(2, blocks); ++rb)
       if (2 * ctas(rb) <= sms) return rb;
   if (max_blocks(s.np, s.c.delta, kind) == 4 && blocks >= 4 && ctas(4) >= 3ll * sms) return 4;
@@ -279,7 +279,7 @@ bool early_grads(const Shape &s) { return (long long)s.n_slots * s.c.heads <= sm
 
 cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
-  static std::atomic<unsigned long long> raised[4][2][2][3];
+  static std::atomic<unsigned long long> raised[4][2][2][kWalkKinds];
   const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
   p.rb = walk_blocks(s, kind);
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
@@ -359,8 +359,9 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
                                                        cs>>>(p);
     return cuda_status(cudaGetLastError());
   }
+  p.fine = c.dtype == LORES_F16;
   cudaError_t e = run_prep(s, false, p, cs);
-  if (e == cudaSuccess) e = run_walk(s, kForward, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, p.fine ? kForwardFine : kForward, p, cs);
   return cuda_status(e);
 }
 

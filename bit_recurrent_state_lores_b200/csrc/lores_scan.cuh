@@ -40,8 +40,10 @@
 // K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
 // operands by one scale per 16 value rows and chunk (S0 and D: their largest entry in
 // [2^6, 2^7); E and R: the larger of that and V's or dO's).  The error of states and gradients stays near 1e-7; two bf16
-// planes would leave 3e-6 to 1e-5, one fp16 plane 2e-4.  Products that only reach a 16-bit
-// output (Q S0^T and P E) use one plane.
+// planes would leave 3e-6 to 1e-5, one fp16 plane 2e-4.  Products that only reach a bf16
+// output (Q S0^T and P E) use one plane: three roundings of at most 2^-11 of an operand beside the
+// output's own 2^-8.  An fp16 output's is 2^-11 too, so it gets two (one plane left o 1.6 times as far
+// from exact as its rounding does).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -62,6 +64,7 @@ constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran o
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
   int rb;                              // walks: blocks of 16 value rows per CTA
+  int fine;                            // two planes of what only reaches o
   int hpc;                             // scan_prep: heads per CTA (a divisor of share)
   int qk16, v16, o16;                  // 16-byte accesses to q and k, v (and dv), o (or d_o) rows
   long long total;
@@ -247,6 +250,11 @@ template <int COLS>
 __device__ __forceinline__ int tiled(int row, int col) {
   return ((row >> 3) * (COLS / 8) + (col >> 3)) * 64 + (row & 7) * 8 + (col & 7);
 }
+
+// Tm, P and Z are zero above the diagonal: their planes hold the ten 16x16 blocks (i, k), k <= i, one behind the other,
+// each as a tiled matrix of 16 columns.  The first entry of a block:
+constexpr int kTri = 10 * 256;
+__host__ __device__ constexpr int tri(int i, int k) { return (i * (i + 1) / 2 + k) * 256; }
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -499,15 +507,17 @@ __device__ __forceinline__ void put_rows(const uint4 (&raw)[PASS][NP], int dtype
   }
 }
 
-// One accumulator register pair (rows r0 + lane/4, columns c0 + 2 (lane % 4), +1 of an 8x8 tile) into a
-// tiled plane and its rest into the plane behind it.
-template <int COLS>
-__device__ __forceinline__ void put_pair(__half *dst, long long plane, int r0, int c0, float x, float y, int lane) {
+// Two neighbouring entries into a plane and their rest into the plane behind it.
+__device__ __forceinline__ void put_at(__half *dst, long long plane, int at, float x, float y) {
   uint32_t hi, lo;
   split2(x, y, hi, lo);
-  const int at = tiled<COLS>(r0, c0) + 2 * lane;
   *reinterpret_cast<uint32_t *>(dst + at) = hi;
   *reinterpret_cast<uint32_t *>(dst + plane + at) = lo;
+}
+// One accumulator register pair (rows r0 + lane/4, columns c0 + 2 (lane % 4), +1 of an 8x8 tile) into tiled planes.
+template <int COLS>
+__device__ __forceinline__ void put_pair(__half *dst, long long plane, int r0, int c0, float x, float y, int lane) {
+  put_at(dst, plane, tiled<COLS>(r0, c0) + 2 * lane, x, y);
 }
 
 template <int DK, int NP, bool DELTA, bool BWD>
@@ -702,7 +712,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       // P over the scale of Q (for Z without its decays) and, strictly below the diagonal, A
       constexpr bool KEEP = !BWD || !DELTA;        // P itself is wanted
       const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
-      __half *pp = p.pp + rec * (2 * kChunk * kChunk);
+      __half *pp = p.pp + rec * (2 * kTri);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (i / 2 <= warp) {
@@ -731,9 +741,9 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             P[i][2 * h] = p0;
             P[i][2 * h + 1] = p1;
             if (KEEP) {
-              if (NP == 2 || BWD) put_pair<kChunk>(pp, kChunk * kChunk, m0 + 8 * h, 8 * i, p0, p1, lane);
-              else             // (16-bit outputs need one plane)
-                *reinterpret_cast<uint32_t *>(pp + tiled<kChunk>(m0 + 8 * h, 8 * i) + 2 * lane) = pack2(p0, p1);
+              const int at = tri(warp, i / 2) + (2 * h + (i & 1)) * 64 + 2 * lane;
+              if (NP == 2 || BWD || p.fine) put_at(pp, kTri, at, p0, p1);
+              else *reinterpret_cast<uint32_t *>(pp + at) = pack2(p0, p1);
             }
           }
         }
@@ -812,7 +822,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 
     {
       // planes of Tm (blocks on and below the diagonal)
-      __half *tm = p.tm + rec * (2 * kChunk * kChunk);
+      __half *tm = p.tm + rec * (2 * kTri);
 #pragma unroll
       for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
         const int i = tid + j * kPrepThreads, r = (i >> 6) * 8 + (i & 7), c = ((i >> 3) & 7) * 8;
@@ -826,8 +836,9 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
           split2(x[2], x[3], hi.y, lo.y);
           split2(x[4], x[5], hi.z, lo.z);
           split2(x[6], x[7], hi.w, lo.w);
-          *reinterpret_cast<uint4 *>(tm + 8 * i) = hi;
-          *reinterpret_cast<uint4 *>(tm + kChunk * kChunk + 8 * i) = lo;
+          const int at = tri(r >> 4, c >> 4) + ((r >> 2 & 2) + (c >> 3 & 1)) * 64 + (r & 7) * 8;
+          *reinterpret_cast<uint4 *>(tm + at) = hi;
+          *reinterpret_cast<uint4 *>(tm + kTri + at) = lo;
         }
       }
     }
@@ -856,7 +867,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
           }
         }
       }
-      __half *z = p.z + rec * (2 * kChunk * kChunk);
+      __half *z = p.z + rec * (2 * kTri);
       const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -867,7 +878,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             const int t = m0 + g + 8 * h, s = 8 * i + t2;
             const float z0 = s <= t ? acc[i][2 * h] * decay(gt[h], make_float2(gs.x, gs.y)) : 0.0f;
             const float z1 = s + 1 <= t ? acc[i][2 * h + 1] * decay(gt[h], make_float2(gs.z, gs.w)) : 0.0f;
-            put_pair<kChunk>(z, kChunk * kChunk, m0 + 8 * h, 8 * i, z0, z1, lane);
+            put_at(z, kTri, tri(warp, i / 2) + (2 * h + (i & 1)) * 64 + 2 * lane, z0, z1);
           }
         }
     }
@@ -949,7 +960,10 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 constexpr int kSideWarps = 2;
 constexpr int kReverseBlocks = 2;
 
-enum WalkKind { kForward, kRecompute, kReverse };
+// kForwardFine: a forward walk whose products that only reach o have two planes (see below).
+enum WalkKind { kForward, kRecompute, kReverse, kForwardFine, kWalkKinds };
+__host__ __device__ constexpr bool is_forward(int kind) { return kind == kForward || kind == kForwardFine; }
+__host__ __device__ constexpr int o_planes(int np, int kind) { return kind == kForwardFine ? 2 : np; }
 // Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
 __host__ __device__ constexpr int max_blocks(int np, bool delta, int kind) {
   return !delta && kind != kReverse && np == 1 ? 4 : 2;
@@ -965,14 +979,14 @@ struct WalkLayout {
 __host__ __device__ constexpr int tile_bytes(int np) { return kChunk * 16 * 2 * np; }
 
 __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh, bool delta, int kind) {
-  const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
+  const int tile = kChunk * dk * 2, sq = kTri * 2;
   WalkLayout l{};
   int at = 0;
   l.kt = at; at += delta ? 2 * tile : 0;                       // Kt or Kb
   l.k = at; at += np * tile;
   l.q = at; at += kind != kRecompute ? np * tile : 0;
   l.tm = at; at += kind == kReverse || delta ? 2 * sq : 0;     // Tm or Z
-  l.pp = at; at += kind == kForward ? np * sq : 0;
+  l.pp = at; at += is_forward(kind) ? o_planes(np, kind) * sq : 0;
   l.v = at; at += rb * tile_bytes(np);
   l.gates = at; at += kGateStage * 4;
   l.bytes = (at + 15) / 16 * 16;
@@ -981,7 +995,7 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   l.side = at; at += delta || kind == kReverse ? 4096 : 0;     // Tm V or dO^T Z
   l.last = at; at += delta || kind == kReverse ? 4096 : 0;     // E or R, for the side warps
   l.plus = at; at += kind == kReverse ? 16 * dk * 4 : 0;       // dO^T Q
-  l.planes = at; at += kind == kForward ? np * 16 * dk * 2 : 0;   // S0 as left operands
+  l.planes = at; at += is_forward(kind) ? o_planes(np, kind) * 16 * dk * 2 : 0;   // S0 as left operands
   l.tops = at; at += 32;                                       // largest entries: see below
   l.tail = at;
   return l;
@@ -1168,15 +1182,15 @@ __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row
 
 // Bytes of a chunk's bulk copies.
 __host__ __device__ constexpr unsigned walk_bulk_bytes(int dk, int np, bool delta, int kind) {
-  const int tile = kChunk * dk * 2, sq = kChunk * kChunk * 2;
+  const int tile = kChunk * dk * 2, sq = kTri * 2;
   return kGateStage * 4 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
-         (kind != kRecompute ? np * tile : 0) + (kind == kForward ? np * sq : 0);
+         (kind != kRecompute ? np * tile : 0) + (is_forward(kind) ? o_planes(np, kind) * sq : 0);
 }
 // The chunk's matrices: one thread issues them, they complete on `bar`.
 template <int DK, int NP, bool DELTA, int KIND>
 __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st, uint64_t *bar, const WalkLayout &l, int slot,
                                                int head) {
-  constexpr unsigned TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2;
+  constexpr unsigned TILE = kChunk * DK * 2, SQ = kTri * 2;
   const long long rec = (long long)slot * p.H + head;
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
   const float *gates = p.gates + rec * kGateFloats;
@@ -1185,18 +1199,19 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
   bulk_g2s(st + l.gates + 4 * kChunk * 4, gates + kGateScales, 32, bar);
   if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
   if (DELTA || KIND == kReverse)
-    bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kChunk * kChunk), 2 * SQ, bar);
+    bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kTri), 2 * SQ, bar);
   bulk_g2s(st + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
   if (KIND != kRecompute) bulk_g2s(st + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
-  if (KIND == kForward) bulk_g2s(st + l.pp, p.pp + rec * (2 * kChunk * kChunk), NP * SQ, bar);
+  if (is_forward(KIND)) bulk_g2s(st + l.pp, p.pp + rec * (2 * kTri), o_planes(NP, KIND) * SQ, bar);
 }
 
 template <int DK, int NP, bool DELTA, int KIND, int NH>
 __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) scan_walk_kernel(const ScanParams p) {
-  constexpr bool REV = KIND == kReverse;
+  constexpr bool REV = KIND == kReverse, FWD = is_forward(KIND);
+  constexpr int OP = o_planes(NP, KIND);                     // planes of S0, P and E where they only reach o
   constexpr bool JOIN = DELTA || REV;                        // E (or R) has parts in several warps
   constexpr int DKH = DK / NH, NTH = DKH / 8;
-  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2, VP = kChunk * 16 * 2;
+  constexpr uint32_t TILE = kChunk * DK * 2, SQ = kTri * 2, VP = kChunk * 16 * 2;
   constexpr int PER = 32 * (NH + kSideWarps);                // threads of a block of rows
   static_assert(NH == 1 || NH == 2, "parts are exchanged between two warps at most");
   extern __shared__ __align__(16) uint8_t smem[];
@@ -1224,7 +1239,6 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
   const Lane<DK> ld(lane);
-  const Lane<kChunk> lc(lane);
   const Lane<16> lv(lane);
   const int X = 1 + 3 * blk, Y = X + 1, Z = X + 2;
   if (tid == 0) {
@@ -1310,7 +1324,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) E[i][j] = 0.0f;
-        __half *keep = KIND == kForward ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
+        __half *keep = FWD ? nullptr : (REV ? p.dd : p.s0) + rec * (2ll * p.dvp * DK);
         // (reverse without the delta rule: Kb = diag(w) K.)  Products that share an accumulator are eight
         // instructions apart and the next fragments are under way before the last products are
         // issued, which covers the latencies of the tensor cores and of ldmatrix.
@@ -1327,9 +1341,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         for (int ks = 0; ks < DKH / 16; ++ks) {
           uint32_t ah[4], al[4];
           split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
-          if (KIND == kForward) {
+          if (FWD) {
             planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-            if (NP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
+            if (OP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1356,7 +1370,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             }
           }
         }
-        if (KIND != kForward && lane == 0 && h == 0)
+        if (!FWD && lane == 0 && h == 0)
           p.scales[REV ? kScaleD : kScaleS][rec * (p.dvp / 16) + brow / 16] = scale;
         if (JOIN) {
           if (NH > 1)
@@ -1376,7 +1390,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
           }
         } else {
-          if (KIND == kForward) barrier_arrive(X, PER);
+          if (FWD) barrier_arrive(X, PER);
         }
         if (JOIN) {
           // E (or R) for the side warps: each state warp hands over half of the tokens
@@ -1420,7 +1434,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               }
             }
           }
-        if (!JOIN && KIND == kForward) barrier_arrive(Y, PER);    // (V is read)
+        if (!JOIN && FWD) barrier_arrive(Y, PER);    // (V is read)
         constexpr int STEP = JOIN && NTH >= 8 ? 4 : NTH >= 4 ? 2 : 1;   // column pairs at a time
 #pragma unroll
         for (int n0 = 0; n0 < NTH / 2; n0 += STEP) {
@@ -1490,8 +1504,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                   if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) {
-                    if (REV) lc.b_cols(b[ks][c2][i], tm + c2 * SQ, ks * 16, (2 * H + i) * 16);
-                    else lc.b_rows(b[ks][c2][i], tm + c2 * SQ, (2 * H + i) * 16, ks * 16);
+                    if (REV) lv.b_cols(b[ks][c2][i], tm + c2 * SQ + 2 * tri(ks, 2 * H + i), 0, 0);
+                    else lv.b_rows(b[ks][c2][i], tm + c2 * SQ + 2 * tri(2 * H + i, ks), 0, 0);
                   }
             }
 #pragma unroll
@@ -1513,7 +1527,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           }
           // (in reverse the sum over dO^T Q waits too: it then runs beside the state warps' additions and not
           // beside their products, which the chain waits for)
-          if (JOIN || KIND == kForward) barrier_sync(X, PER);
+          if (JOIN || FWD) barrier_sync(X, PER);
           if (REV) {
             // (diag(e^G) dO)^T Q, columns [H d_k/2, (H+1) d_k/2)
             constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
@@ -1575,7 +1589,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           }
           float O[4][4];
           uint32_t r[4][2][4];             // P's blocks
-          if (KIND == kForward) {
+          if (FWD) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1594,15 +1608,17 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
                 for (int i = 0; i < 2; ++i) ld.b_rows(b[(ks + 1) & 1][i], sq, (2 * H + i) * 16, ks * 16 + 16);
 #pragma unroll
               for (int i = 0; i < 2; ++i) mma2(O[2 * i], O[2 * i + 1], ah, b[ks & 1][i]);
-              if (NP == 2) {
+              if (OP == 2) {
                 const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
                 const uint32_t al[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  uint32_t x[4];
                   mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
-                  ld.b_rows(x, sq + TILE, (2 * H + i) * 16, ks * 16);
-                  mma2(O[2 * i], O[2 * i + 1], ah, x);
+                  if (NP == 2) {
+                    uint32_t x[4];
+                    ld.b_rows(x, sq + TILE, (2 * H + i) * 16, ks * 16);
+                    mma2(O[2 * i], O[2 * i + 1], ah, x);
+                  }
                 }
               }
             }
@@ -1610,7 +1626,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             for (int ks = 0; ks < 2 * H + 2; ++ks)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (ks <= 2 * H + i) lc.b_rows(r[ks][i], pp, (2 * H + i) * 16, ks * 16);
+                if (ks <= 2 * H + i) lv.b_rows(r[ks][i], pp + 2 * tri(2 * H + i, ks), 0, 0);
             const float to = scale * invE;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1619,8 +1635,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             }
           }
           if (JOIN) barrier_sync(Y, PER);
-          if (KIND == kForward) {
-            // + E^T P^T
+          if (FWD) {
+            // + E^T P^T (E = V of a 16-bit type is exact in one plane)
+            constexpr bool EL = JOIN ? OP == 2 : NP == 2;
             uint32_t eh[4][4], el[4][4];
 #pragma unroll
             for (int ks = 0; ks < 2 * H + 2; ++ks) {
@@ -1639,10 +1656,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               for (int i = 0; i < 2; ++i)
                 if (ks <= 2 * H + i) {
                   mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
-                  if (NP == 2) {
+                  if (EL) mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
+                  if (OP == 2) {
                     uint32_t x[4];
-                    mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
-                    lc.b_rows(x, pp + SQ, (2 * H + i) * 16, ks * 16);
+                    lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
                     mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
                   }
                 }
@@ -2353,7 +2370,7 @@ using ScanFn = void (*)(ScanParams);
 // kernels of one key width
 struct ScanKernels {
   ScanFn prep[2][2][2];                // [np - 1][delta][backward]
-  ScanFn walk[2][2][3];                // [np - 1][delta][WalkKind]
+  ScanFn walk[2][2][kWalkKinds];       // [np - 1][delta][WalkKind]; kForwardFine: for one plane
   ScanFn grads[2][2];
 };
 // Warps that share a block's state: half a 16-column state has no whole k-step.
