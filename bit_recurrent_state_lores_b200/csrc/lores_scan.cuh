@@ -1483,223 +1483,230 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         const unsigned top = max_bits(S);
         if (lane == 0) tops[2 * ((i0 + 1) & 1) + h] = top;
       } else {
-        // ---- side warp: tokens 32 h .. 32 h + 31 (a body for each half, so that every loop is straight code)
-        auto body = [&](auto half) {
+        // ---- side warp: tokens 32 h .. 32 h + 31 (where a half meets a triangle, a body for each, so that every loop is
+        // straight code; nowhere else, since both bodies and the state warps' share the instruction cache)
+        auto with_v = [&](auto half) {
           constexpr int H = decltype(half)::value;
-          if (JOIN) {
-            float U[4][4];                   // tokens 32 H + 8 i ..
+          float U[4][4];                   // tokens 32 H + 8 i ..
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
-            // Tm V: blocks s <= t; dO^T Z: blocks t >= s
-            constexpr int K0 = REV ? 2 * H : 0, K1 = REV ? 4 : 2 * H + 2;
-            uint32_t v[4][NP][4], b[4][2][2][4];
+            for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
+          // Tm V: blocks s <= t; dO^T Z: blocks t >= s
+          constexpr int K0 = REV ? 2 * H : 0, K1 = REV ? 4 : 2 * H + 2;
+          uint32_t v[4][NP][4], b[4][2][2][4];
 #pragma unroll
-            for (int ks = K0; ks < K1; ++ks) {
+          for (int ks = K0; ks < K1; ++ks) {
 #pragma unroll
-              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[ks][pl], sv + pl * VP, ks * 16, 0);
+            for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[ks][pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2)
+            for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) {
-                    if (REV) lv.b_cols(b[ks][c2][i], tm + c2 * SQ + 2 * tri(ks, 2 * H + i), 0, 0);
-                    else lv.b_rows(b[ks][c2][i], tm + c2 * SQ + 2 * tri(2 * H + i, ks), 0, 0);
-                  }
-            }
-#pragma unroll
-            for (int ks = K0; ks < K1; ++ks) {
-#pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][0], b[ks][c2][i]);
-              if (NP == 2)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][NP - 1], b[ks][0][i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sided[(4 * H + i) * 32 + lane] =
-                  make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
+              for (int i = 0; i < 2; ++i)
+                if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) {
+                  if (REV) lv.b_cols(b[ks][c2][i], tm + c2 * SQ + 2 * tri(ks, 2 * H + i), 0, 0);
+                  else lv.b_rows(b[ks][c2][i], tm + c2 * SQ + 2 * tri(2 * H + i, ks), 0, 0);
+                }
           }
-          // (in reverse the sum over dO^T Q waits too: it then runs beside the state warps' additions and not
-          // beside their products, which the chain waits for)
-          if (JOIN || FWD) barrier_sync(X, PER);
-          if (REV) {
-            // (diag(e^G) dO)^T Q, columns [H d_k/2, (H+1) d_k/2)
-            constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
-            if (DK >= 32 || H == 0) {
-              uint32_t oh[4][4], ol[4][4];
+#pragma unroll
+          for (int ks = K0; ks < K1; ++ks) {
+#pragma unroll
+            for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][0], b[ks][c2][i]);
+            if (NP == 2)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][NP - 1], b[ks][0][i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sided[(4 * H + i) * 32 + lane] =
+                make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
+        };
+        if (JOIN) {
+          if (h == 0) with_v(Const<0>());
+          else with_v(Const<1>());
+        }
+        // (in reverse the sum over dO^T Q waits too: it then runs beside the state warps' additions and not
+        // beside their products, which the chain waits for)
+        if (JOIN || FWD) barrier_sync(X, PER);
+        if (REV) {
+          // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
+          constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
+          if (DK >= 32 || h == 0) {
+            uint32_t oh[4][4], ol[4][4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              uint32_t v[NP][4];
+#pragma unroll
+              for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+                float2 x = half2_of(v[0][q]);
+                if (NP == 2) {
+                  const float2 y = half2_of(v[NP - 1][q]);
+                  x.x = __fadd_rn(x.x, y.x);
+                  x.y = __fadd_rn(x.y, y.y);
+                }
+                split2(x.x * f.x, x.y * f.y, oh[ks][q], ol[ks][q]);
+              }
+            }
+#pragma unroll
+            for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
+              const int col = (DK >= 32 ? h * HALF : 0) + n0;
+              float a[2 * QS][4];
+#pragma unroll
+              for (int i = 0; i < 2 * QS; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+              uint32_t r[2][QS][4];
+#pragma unroll
+              for (int i = 0; i < QS; ++i) ld.b_cols(r[0][i], sq, 0, col + 16 * i);
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks) {
-                uint32_t v[NP][4];
+                if (ks < 3)
 #pragma unroll
-                for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
+                  for (int i = 0; i < QS; ++i) ld.b_cols(r[(ks + 1) & 1][i], sq, ks * 16 + 16, col + 16 * i);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
-                  float2 x = half2_of(v[0][q]);
-                  if (NP == 2) {
-                    const float2 y = half2_of(v[NP - 1][q]);
-                    x.x = __fadd_rn(x.x, y.x);
-                    x.y = __fadd_rn(x.y, y.y);
-                  }
-                  split2(x.x * f.x, x.y * f.y, oh[ks][q], ol[ks][q]);
+                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[ks & 1][i]);
+#pragma unroll
+                for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[ks & 1][i]);
+                if (NP == 2) {
+                  uint32_t x[QS][4];
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) ld.b_cols(x[i], sq + TILE, ks * 16, col + 16 * i);
+#pragma unroll
+                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], x[i]);
                 }
               }
 #pragma unroll
-              for (int n0 = 0; n0 < HALF; n0 += 16 * QS) {
-                constexpr int C0 = DK >= 32 ? H * HALF : 0;
-                const int col = C0 + n0;
-                float a[2 * QS][4];
+              for (int i = 0; i < 2 * QS; ++i)
+                plus[(col / 8 + i) * 32 + lane] =
+                    make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+            }
+          }
+          barrier_arrive(Z, PER);
+        }
+        float O[4][4];
+        if (FWD) {
 #pragma unroll
-                for (int i = 0; i < 2 * QS; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
-                uint32_t r[2][QS][4];
+            for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
+          uint4 y[DK / 16];
 #pragma unroll
-                for (int i = 0; i < QS; ++i) ld.b_cols(r[0][i], sq, 0, col + 16 * i);
+          for (int ks = 0; ks < DK / 16; ++ks) y[ks] = planes[ks * 32 + lane];
+          uint32_t b[2][2][4];
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                  if (ks < 3)
+          for (int i = 0; i < 2; ++i) ld.b_rows(b[0][i], sq, (2 * h + i) * 16, 0);
 #pragma unroll
-                    for (int i = 0; i < QS; ++i) ld.b_cols(r[(ks + 1) & 1][i], sq, ks * 16 + 16, col + 16 * i);
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            const uint32_t ah[4] = {y[ks].x, y[ks].y, y[ks].z, y[ks].w};
+            if (ks + 1 < DK / 16)
 #pragma unroll
-                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], r[ks & 1][i]);
+              for (int i = 0; i < 2; ++i) ld.b_rows(b[(ks + 1) & 1][i], sq, (2 * h + i) * 16, ks * 16 + 16);
 #pragma unroll
-                  for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], ol[ks], r[ks & 1][i]);
-                  if (NP == 2) {
-                    uint32_t x[QS][4];
+            for (int i = 0; i < 2; ++i) mma2(O[2 * i], O[2 * i + 1], ah, b[ks & 1][i]);
+            if (OP == 2) {
+              const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
+              const uint32_t al[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                    for (int i = 0; i < QS; ++i) ld.b_cols(x[i], sq + TILE, ks * 16, col + 16 * i);
-#pragma unroll
-                    for (int i = 0; i < QS; ++i) mma2(a[2 * i], a[2 * i + 1], oh[ks], x[i]);
-                  }
+              for (int i = 0; i < 2; ++i) {
+                mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
+                if (NP == 2) {
+                  uint32_t x[4];
+                  ld.b_rows(x, sq + TILE, (2 * h + i) * 16, ks * 16);
+                  mma2(O[2 * i], O[2 * i + 1], ah, x);
                 }
-#pragma unroll
-                for (int i = 0; i < 2 * QS; ++i)
-                  plus[(col / 8 + i) * 32 + lane] =
-                      make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
               }
             }
-            barrier_arrive(Z, PER);
           }
-          float O[4][4];
+          const float to = scale * invE;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
+            O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
+          }
+        }
+        auto with_p = [&](auto half) {
+          constexpr int H = decltype(half)::value;
           uint32_t r[4][2][4];             // P's blocks
-          if (FWD) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+          for (int ks = 0; ks < 2 * H + 2; ++ks)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) O[i][j] = 0.0f;
-            uint4 y[DK / 16];
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) y[ks] = planes[ks * 32 + lane];
-            uint32_t b[2][2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ld.b_rows(b[0][i], sq, (2 * H + i) * 16, 0);
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-              const uint32_t ah[4] = {y[ks].x, y[ks].y, y[ks].z, y[ks].w};
-              if (ks + 1 < DK / 16)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) ld.b_rows(b[(ks + 1) & 1][i], sq, (2 * H + i) * 16, ks * 16 + 16);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) mma2(O[2 * i], O[2 * i + 1], ah, b[ks & 1][i]);
-              if (OP == 2) {
-                const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
-                const uint32_t al[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
-                  if (NP == 2) {
-                    uint32_t x[4];
-                    ld.b_rows(x, sq + TILE, (2 * H + i) * 16, ks * 16);
-                    mma2(O[2 * i], O[2 * i + 1], ah, x);
-                  }
-                }
-              }
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2 * H + 2; ++ks)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (ks <= 2 * H + i) lv.b_rows(r[ks][i], pp + 2 * tri(2 * H + i, ks), 0, 0);
-            const float to = scale * invE;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * H + 8 * i + t2);
-              O[i][0] *= f.x * to; O[i][1] *= f.y * to; O[i][2] *= f.x * to; O[i][3] *= f.y * to;
-            }
-          }
+            for (int i = 0; i < 2; ++i)
+              if (ks <= 2 * H + i) lv.b_rows(r[ks][i], pp + 2 * tri(2 * H + i, ks), 0, 0);
           if (JOIN) barrier_sync(Y, PER);
-          if (FWD) {
-            // + E^T P^T (E = V of a 16-bit type is exact in one plane)
-            constexpr bool EL = JOIN ? OP == 2 : NP == 2;
-            uint32_t eh[4][4], el[4][4];
+          // + E^T P^T (E = V of a 16-bit type is exact in one plane)
+          constexpr bool EL = JOIN ? OP == 2 : NP == 2;
+          uint32_t eh[4][4], el[4][4];
 #pragma unroll
-            for (int ks = 0; ks < 2 * H + 2; ++ks) {
-              if (!JOIN) {
-                lv.a_cols(eh[ks], sv, ks * 16, 0);
-                if (NP == 2) lv.a_cols(el[ks], sv + VP, ks * 16, 0);
-                continue;
-              }
-              const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
-              const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
-              split_tiles(e0, e1, invE, eh[ks], el[ks]);
+          for (int ks = 0; ks < 2 * H + 2; ++ks) {
+            if (!JOIN) {
+              lv.a_cols(eh[ks], sv, ks * 16, 0);
+              if (NP == 2) lv.a_cols(el[ks], sv + VP, ks * 16, 0);
+              continue;
             }
-#pragma unroll
-            for (int ks = 0; ks < 2 * H + 2; ++ks)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (ks <= 2 * H + i) {
-                  mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
-                  if (EL) mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
-                  if (OP == 2) {
-                    uint32_t x[4];
-                    lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
-                    mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
-                  }
-                }
-            // (without the delta rule the tile holds V until every warp of the block has read it)
-            if (!JOIN) barrier_sync(Y, PER);
-            store_tokens<NP>(O, scaleE * qscale, tile, 4 * H, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
-                             head * p.d_v + brow, p.d_v - brow, p.o16, lane);
-          } else if (!JOIN) {
-            // the planes of V, tile by tile (a tile of [64 tokens][16 rows] is kept transposed)
-            __half *et = p.et + rec * (2ll * p.dvp * kChunk);
-#pragma unroll
-            for (int ks = 2 * H; ks < 2 * H + 2; ++ks)
-#pragma unroll
-              for (int pl = 0; pl < 2; ++pl) {
-                uint32_t v[4] = {0, 0, 0, 0};
-                if (pl < NP) lv.a_cols(v, sv + pl * VP, ks * 16, 0);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  *reinterpret_cast<uint32_t *>(et + pl * (long long)p.dvp * kChunk +
-                                                tiled<kChunk>(brow + 8 * (q & 1), ks * 16 + 8 * (q >> 1)) + 2 * lane) = v[q];
-              }
-            if (lane == 0 && H == 0) p.scales[kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 y = last[(4 * H + i) * 32 + lane];
-              O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
-            }
-            keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * H, O, invE, lane);
-            if (lane == 0 && H == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
-            if (REV) {
-              // (both side warps are done with the rows of dO)
-              barrier_sync(Z + 3 * kReverseBlocks, 32 * kSideWarps);
-              store_tokens<NP>(O, 1.0f, tile, 4 * H, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
-                               head * p.d_v + brow, p.d_v - brow, p.v16, lane);
-            }
+            const float4 y = last[(2 * ks) * 32 + lane], z = last[(2 * ks + 1) * 32 + lane];
+            const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
+            split_tiles(e0, e1, invE, eh[ks], el[ks]);
           }
+#pragma unroll
+          for (int ks = 0; ks < 2 * H + 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (ks <= 2 * H + i) {
+                mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
+                if (EL) mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
+                if (OP == 2) {
+                  uint32_t x[4];
+                  lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
+                  mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
+                }
+              }
         };
-        if (h == 0) body(Const<0>());
-        else body(Const<1>());
+        if (FWD) {
+          if (h == 0) with_p(Const<0>());
+          else with_p(Const<1>());
+          // (without the delta rule the tile holds V until every warp of the block has read it)
+          if (!JOIN) barrier_sync(Y, PER);
+          store_tokens<NP>(O, scaleE * qscale, tile, 4 * h, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
+                           head * p.d_v + brow, p.d_v - brow, p.o16, lane);
+        } else if (!JOIN) {
+          // the planes of V, tile by tile (a tile of [64 tokens][16 rows] is kept transposed)
+          __half *et = p.et + rec * (2ll * p.dvp * kChunk);
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl) {
+              const int ks = 2 * h + k2;
+              uint32_t v[4] = {0, 0, 0, 0};
+              if (pl < NP) lv.a_cols(v, sv + pl * VP, ks * 16, 0);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint32_t *>(et + pl * (long long)p.dvp * kChunk +
+                                              tiled<kChunk>(brow + 8 * (q & 1), ks * 16 + 8 * (q >> 1)) + 2 * lane) = v[q];
+            }
+          if (lane == 0 && h == 0) p.scales[kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+        } else {
+          barrier_sync(Y, PER);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = last[(4 * h + i) * 32 + lane];
+            O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
+          }
+          keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
+          if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+          if (REV) {
+            // (both side warps are done with the rows of dO)
+            barrier_sync(Z + 3 * kReverseBlocks, 32 * kSideWarps);
+            store_tokens<NP>(O, 1.0f, tile, 4 * h, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
+                             head * p.d_v + brow, p.d_v - brow, p.v16, lane);
+          }
+        }
       }
     }
     if (!by) {
