@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     {
       // planes of Tm (blocks on and below the diagonal)
       __half *tm = p.tm + rec * (2 * kTri);
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < kChunk * 8 / kPrepThreads; ++j) {
         const int i = tid + j * kPrepThreads, r = (i >> 6) * 8 + (i & 7), c = ((i >> 3) & 7) * 8;
         if ((c >> 4) <= (r >> 4)) {
