@@ -31,7 +31,7 @@
 // product's left operand within a few hundred cycles; tcgen05 wants 64 rows at least and keeps
 // accumulators in TMEM, so that every chunk would pay two trips through it on the critical path.
 // Nothing here is bound by the rate of the products: mma.sync measured 555 TFLOP/s on this card, and
-// the walk keeps the tensor cores busy for 1850 of a chunk's 4350 cycles.
+// the walk keeps the tensor cores busy for 1850 of a chunk's 4200 cycles.
 //
 // Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
 // as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
@@ -398,7 +398,7 @@ __device__ __forceinline__ void load4(const void *src, int dtype, long long i, f
 // Grid (slot, group of p.hpc heads that share K and Q), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.]
 // result, and only blocks on and below the diagonal are formed.  K and Q are fetched and converted
 // once for the group.  Bound by latency: a chain of short products with four CTAs per SM to hide it.
-// 8192 tokens, 32 heads, d_k = 128, bf16 (4096 items, 370 MB of matrices written): 146 us, 2.5 TB/s;
+// 8192 tokens, 32 heads, d_k = 128, bf16 (4096 items, 330 MB of matrices written): 147 us, 2.3 TB/s;
 // without the delta rule and with 16 heads on one pair of Q and K (7800 tokens, 128 heads): 76 us.
 // A CTA per head took 343 us there.  T = (I + A)^-1 by 16x16 blocks:
 // the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
@@ -947,14 +947,14 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
 // Without the delta rule E = V and the state warps have no products before X; a CTA then takes four blocks.
 // A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit; one
-// took 465 us where two take 300): bulk copies, since 16-byte cp.async of the same 96 KB took longer
+// took 465 us where two took 300): bulk copies, since 16-byte cp.async of the same 96 KB took longer
 // than the chunk's arithmetic (665 against 500 us); and it turns the block's rows of V into fp16 over
 // their scale.  In the backward pass's recomputation (kRecompute) the planes of S0 and E are kept
 // instead of o.
-// Bound by the latency of a chunk's chain, close behind it by shared memory (3000 of 4350 cycles:
+// Bound by the latency of a chunk's chain, close behind it by shared memory (3000 of 4200 cycles:
 // fragments, exchanged parts, copies).  One sequence of 8192 tokens, 32 heads of 128 x 128, bf16: 128
-// chunks in 300 us, 2.3 us a chunk; the same recomputed for 2 x 4096 tokens and 16 heads: 145 us;
-// reverse: 200 to 220 us.
+// chunks in 286 us, 2.2 us a chunk; the same recomputed for 2 x 4096 tokens and 16 heads: 136 us;
+// reverse: 172 us (200 to 220 with 67 KB of code in place of 60: the instruction cache).
 // The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
 // form D's sum over dO^T Q, which the state warps take last (barrier Z).
 constexpr int kSideWarps = 2;

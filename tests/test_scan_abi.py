@@ -47,7 +47,10 @@ def test_workspace_sizes():
     # short sequences need no per-chunk matrices
     assert L.lores_scan_workspace(config(max_len=16)) == 256
     assert L.lores_scan_workspace(config(d_k=256)) == 256
-    assert L.lores_scan_workspace(config(max_len=17)) == fwd
+    assert L.lores_scan_workspace(config(max_len=32)) == 256
+    assert L.lores_scan_workspace(config(max_len=33)) == fwd
+    assert L.lores_scan_workspace(config(max_len=24, delta=0)) == 256
+    assert L.lores_scan_workspace(config(max_len=25, delta=0)) > 256
     # no tokens: still a workspace (the error word)
     assert L.lores_scan_workspace(config(total=0)) >= 256
     # shared q and k take less of it, sums over heads that share them more of the backward pass's
