@@ -294,10 +294,11 @@ cudaError_t run_grads(const Shape &s, ScanParams p, cudaStream_t st) {
   const lores_scan_config &c = s.c;
   static std::atomic<unsigned long long> raised[4][2][2];
   const int wi = width_index(c.d_k);
-  const GradLayout l = grad_layout(c.d_k, s.np, s.dvp);
-  p.stages = grad_bytes(l, c.d_k, 2) <= kMaxShared ? 2 : 1;
-  return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3((unsigned)s.n_slots * c.heads), kGradThreads,
-                grad_bytes(l, c.d_k, p.stages), st, c.device, p, early_grads(s),
+  const GradLayout l = grad_layout(c.d_k, s.np, s.dvp, c.delta);
+  const int most = grad_halves(s.np, c.delta) ? (kMaxShared + 1024) / 2 - 1024 : kMaxShared;
+  p.stages = grad_bytes(l, c.d_k, 2, c.delta) <= most ? 2 : 1;
+  return launch(kernels().by_width[wi].grads[s.np - 1][c.delta], dim3((unsigned)s.n_slots * c.heads),
+                grad_threads(s.np, c.delta), grad_bytes(l, c.d_k, p.stages, c.delta), st, c.device, p, early_grads(s),
                 raised[wi][s.np - 1][c.delta]);
 }
 

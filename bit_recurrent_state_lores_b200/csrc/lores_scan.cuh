@@ -57,7 +57,6 @@ namespace scan {
 
 constexpr int kChunk = 64;
 constexpr int kPrepThreads = 128;
-constexpr int kGradThreads = 512;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
 constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran out
 
@@ -1747,31 +1746,36 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 // to one side.  So every kGradSum value rows (48 products, below 1.5e-6) the sums are added, rounded, to a copy in the
 // thread's local memory; narrower heads (the usual 64 to 256) never touch it.
 constexpr int kGradRows = 32, kGradSum = 256;
+// Without the delta rule and with one plane of K and Q an item fits half an SM: 8 warps in two groups (dO S0, E D), each
+// with every other 16 columns of dO E^T beside it, and two CTAs per SM cover each other's waits (7050
+// tokens, 64 heads of 64 x 128, bf16: 379 us where four groups in one CTA took 487).
+__host__ __device__ constexpr bool grad_halves(int np, bool delta) { return np == 1 && !delta; }
+__host__ __device__ constexpr int grad_threads(int np, bool delta) { return grad_halves(np, delta) ? 256 : 512; }
 
 struct GradLayout {
   int k, q, x, f, scales, stage, stage_bytes, s0, d, e, r, o;
 };
-__host__ __device__ inline GradLayout grad_layout(int dk, int np, int dvp) {
+__host__ __device__ inline GradLayout grad_layout(int dk, int np, int dvp, bool delta) {
   GradLayout l{};
   int at = 0;
   l.k = at; at += np * kChunk * dk * 2;
   l.q = at; at += np * kChunk * dk * 2;
-  l.x = at; at += 4 * kChunk * kChunk * 2;               // dP' hi, lo, dL' hi, lo
-  l.f = at; at += (kGateFloats + 4 * kChunk + 4 * kChunk + 16 + 8) * 4;
+  l.x = at; at += (delta ? 4 : 2) * kChunk * kChunk * 2;  // dP' hi, lo, dL' hi, lo
+  l.f = at; at += (kGateFloats + 5 * kChunk + 4 * kChunk + 16 + 8) * 4;
   l.scales = at; at += 4 * (dvp / 16) * 4;
   l.stage = (at + 15) / 16 * 16;
   at = 0;
   l.s0 = at; at += 2 * kGradRows * dk * 2;
   l.d = at; at += 2 * kGradRows * dk * 2;
   l.e = at; at += 2 * kGradRows * kChunk * 2;
-  l.r = at; at += 2 * kGradRows * kChunk * 2;
+  l.r = at; at += delta ? 2 * kGradRows * kChunk * 2 : 0;
   l.o = at; at += kChunk * (kGradRows + (np == 2 ? 4 : 8)) * (np == 2 ? 4 : 2);
   l.stage_bytes = at;
   return l;
 }
 // Behind the fixed part: the stages, and later what groups 1 and 3 hand to group 2.
-__host__ __device__ inline int grad_bytes(const GradLayout &l, int dk, int stages) {
-  const int a = stages * l.stage_bytes, b = 2 * kChunk * dk * 4;
+__host__ __device__ inline int grad_bytes(const GradLayout &l, int dk, int stages, bool delta) {
+  const int a = stages * l.stage_bytes, b = delta ? 2 * kChunk * dk * 4 : 0;
   return l.stage + (a > b ? a : b);
 }
 
@@ -1792,11 +1796,13 @@ __device__ __forceinline__ int top_unit(const float *a, const float *c, int bloc
 }
 
 template <int DK, int NP, bool DELTA>
-__global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA) ? 2 : 1) scan_grads_kernel(const ScanParams p) {
+  constexpr bool HALF = grad_halves(NP, DELTA);
+  constexpr int kGradThreads = grad_threads(NP, DELTA), KGROUP = HALF ? 1 : 2;     // KGROUP: the group of dK
   constexpr int NT = DK / 8, LDO = kGradRows + (NP == 2 ? 4 : 8), SIZE = NP == 2 ? 4 : 2;
   constexpr uint32_t TILE = kChunk * DK * 2, SQ = kChunk * kChunk * 2, SP = kGradRows * DK * 2, EP = kGradRows * kChunk * 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  const GradLayout l = grad_layout(DK, NP, p.dvp);
+  const GradLayout l = grad_layout(DK, NP, p.dvp, DELTA);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2, w4 = warp & 3, g = lane >> 2,
             t2 = (lane & 3) * 2, m0 = w4 * 16;
   const int slot = blockIdx.x / p.H, head = blockIdx.x % p.H;    // (heads that share K and Q run side by side)
@@ -1813,7 +1819,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const float *eG = gates + kGateE * kChunk, *w = gates + kGateW * kChunk, *be = gates + kGateB * kChunk,
               *eC = gates + kGateC * kChunk;
   const float2 *G = reinterpret_cast<const float2 *>(gates + kGateG * kChunk);
-  float *rowv = gates + kGateFloats, *aq = rowv + kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
+  float *rowv = gates + kGateFloats, *aq = rowv + 2 * kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
         *red = colp + 4 * kChunk;
   uint64_t *bars = reinterpret_cast<uint64_t *>(red + 16);                // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
@@ -1859,11 +1865,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const float *sS = reinterpret_cast<const float *>(smem + l.scales), *sE = sS + blocks16, *sD = sE + blocks16,
               *sR = sD + blocks16;
   // the group's two scales: of the left operand's planes and of the right one's
-  const float *sl = group == 2 ? sE : sR, *sr2 = group == 2 ? sD : group == 3 ? sE : sS;
+  const float *sl = group == KGROUP ? sE : sR, *sr2 = group == KGROUP ? sD : group == 3 ? sE : sS;
   int topDS = 0, topRE = 0, top = 0;
 
-  // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T
-  constexpr int NA = NT > 16 ? NT : 16;
+  // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T (in halves: tiles NT .. NT + 3 dO E^T)
+  constexpr int NA = HALF ? NT + 4 : NT > 16 ? NT : 16;
   float acc[NA][4], ds = 0.0f;
 #pragma unroll
   for (int i = 0; i < NA; ++i)
@@ -1914,7 +1920,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       const float ratio = pow2(el + exponent(sr2[b16]) - top);
       const __half2 by = __float2half2_rn(ratio);
       uint32_t ao[NP][4], ar[2][4], b4[4];
-      if (group == 0 || group == 3) {
+      if (HALF) {
+        // dO over the scale of R, in the unit of dO E^T; of this warp's columns every other 16
+        const int er = exponent(sR[b16]);
+        const float to = pow2(-er) * pow2(er + exponent(sE[b16]) - topRE);
+        uint32_t raw[4], ae[4];
+        a_rows_plain(raw, smem_addr(st + l.o), LDO, m0, kk, lane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = pair_of(raw[q], p.dtype);
+          ae[q] = pack2(f.x * to, f.y * to);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int np = 2 * j + group;
+          if (np <= w4) {
+            lc.b_cols(b4, se, kk, np * 16);
+            mma2(acc[NT + 2 * j], acc[NT + 2 * j + 1], ae, b4);
+            lc.b_cols(b4, se + EP, kk, np * 16);
+            mma2(acc[NT + 2 * j], acc[NT + 2 * j + 1], ae, b4);
+          }
+        }
+      }
+      if (group == 0 || (!HALF && group == 3)) {
         const float to = pow2(-el) * ratio;            // dO over the scale of R
         if (NP == 1) {
           uint32_t raw[4];
@@ -1933,10 +1961,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
           }
         }
       }
-      if (group == 2 || (DELTA && (group & 1)))
+      if (group == KGROUP || (DELTA && (group & 1)))
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          lc.a_cols(ar[c], (group == 2 ? se : sr) + c * EP, kk, m0);
+          lc.a_cols(ar[c], (group == KGROUP ? se : sr) + c * EP, kk, m0);
           scale_frag(ar[c], by);
         }
       if (group == 0) {
@@ -1948,8 +1976,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
           ld.b_cols(b4, s0 + SP, kk, np * 16);
           mma2(acc[2 * np], acc[2 * np + 1], ao[0], b4);
         }
-      } else if (group == 2 || (DELTA && group == 1)) {
-        const uint32_t x = group == 2 ? dd : s0;
+      } else if (group == KGROUP || (DELTA && group == 1)) {
+        const uint32_t x = group == KGROUP ? dd : s0;
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
           ld.b_cols(b4, x, kk, np * 16);
@@ -1958,7 +1986,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
           ld.b_cols(b4, x + SP, kk, np * 16);
           mma2(acc[2 * np], acc[2 * np + 1], ar[0], b4);
         }
-      } else if (group == 3) {
+      } else if (!HALF && group == 3) {
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           if (np <= w4) {
@@ -2006,15 +2034,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
   const float to_unit = pow2(top - topRE - lg);                          // from F to what the planes are held over
   const float out1 = pow2(topRE / 2) * pow2(lg), out2 = pow2(topRE - topRE / 2);
 
-  if (group != 3) {
+  auto finish_rows = [&]() {
     // the row's dot with q or k, then the row in the planes' units
     const uint8_t *x = smem + (group == 0 ? l.q : l.k);
-    float *dots = group == 0 ? aq : group == 1 ? ak : kw;
+    float *dots = group == 0 ? aq : group == KGROUP ? kw : ak;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
       float s = 0.0f;
-      const float to = group == 2 ? w[t] * to_unit * iqscale : eG[t] * to_unit * (group == 1 ? -ikappa : ikappa);
+      const float to = group == KGROUP ? w[t] * to_unit * iqscale : eG[t] * to_unit * (group == 1 ? -ikappa : ikappa);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int at = 2 * (tiled<DK>(m0 + 8 * h, 8 * i) + 2 * lane);
@@ -2032,16 +2060,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
       if ((lane & 3) == 0) dots[t] = s * (group == 0 ? qscale : kappa) * F1 * F2;
     }
-  } else {
-    float rs[2] = {0.0f, 0.0f}, cs[8][2];
+  };
+  auto form_planes = [&]() {
+    constexpr int STEPS = HALF ? 2 : 4;
+    const float U1 = HALF ? pow2(topRE / 2) : F1, U2 = HALF ? pow2(topRE - topRE / 2) : F2,    // (F of dO E^T)
+                to_planes = HALF ? pow2(-lg) : to_unit;
+    float rs[2] = {0.0f, 0.0f}, cs[2 * STEPS][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i][0] = cs[i][1] = 0.0f;
+    for (int i = 0; i < 2 * STEPS; ++i) cs[i][0] = cs[i][1] = 0.0f;
     // q_t.k_s with dO E^T -> dP', k_t.k_s with R E^T -> dL', by 16 columns s, so that few registers hold the products
     const float toq = qscale * kappa, tok = -kappa * kappa;
     __half *out = reinterpret_cast<__half *>(smem + l.x);
     const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
+    for (int step = 0; step < STEPS; ++step) {
+      const int np = HALF ? 2 * step + group : step;
       if (np <= w4) {
         float x[2][2][4];
 #pragma unroll
@@ -2068,7 +2101,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
         const bool diagonal = np == w4;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = 2 * np + e;
+          const int i = 2 * np + e, own = (HALF ? NT : 0) + 2 * step + e;
           const float4 gs = *reinterpret_cast<const float4 *>(G + 8 * i + t2);
           const float2 bs = *reinterpret_cast<const float2 *>(be + 8 * i + t2);
 #pragma unroll
@@ -2080,8 +2113,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
               const int s = 8 * i + t2 + j;
               const float dec = decay(gt[h], j ? make_float2(gs.z, gs.w) : make_float2(gs.x, gs.y));
               const float b = j ? bs.y : bs.x;
-              y[j] = acc[i][2 * h + j] * dec;
-              z[j] = DELTA ? acc[8 + i][2 * h + j] * dec : 0.0f;
+              y[j] = acc[own][2 * h + j] * dec;
+              z[j] = DELTA ? acc[(DELTA ? 8 : 0) + own][2 * h + j] * dec : 0.0f;
               if (diagonal) {
                 y[j] = s <= t ? y[j] : 0.0f;
                 z[j] = s < t ? z[j] : 0.0f;
@@ -2091,9 +2124,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
               // (a pair that the mask leaves out gives nothing, not 0 times a decay that overflowed)
               if (diagonal && s > t) m = 0.0f;
               rs[h] = fmaf(b, m, rs[h]);
-              cs[i][j] += m;
-              y[j] *= b * to_unit;
-              z[j] *= -b * to_unit;
+              cs[2 * step + e][j] += m;
+              y[j] *= b * to_planes;
+              z[j] *= -b * to_planes;
             }
             put_pair<kChunk>(out, kChunk * kChunk, m0 + 8 * h, 8 * i, y[0], y[1], lane);
             if (DELTA) put_pair<kChunk>(out + 2 * kChunk * kChunk, kChunk * kChunk, m0 + 8 * h, 8 * i, z[0], z[1], lane);
@@ -2105,35 +2138,40 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
     for (int h = 0; h < 2; ++h) {
       rs[h] += __shfl_xor_sync(0xFFFFFFFFu, rs[h], 1);
       rs[h] += __shfl_xor_sync(0xFFFFFFFFu, rs[h], 2);
-      if ((lane & 3) == 0) rowv[m0 + g + 8 * h] = rs[h] * F1 * F2;
+      if ((lane & 3) == 0) rowv[(HALF ? group * kChunk : 0) + m0 + g + 8 * h] = rs[h] * U1 * U2;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2 * STEPS; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        const int tile = HALF ? 2 * (2 * (i >> 1) + group) + (i & 1) : i;
         float c = cs[i][j];
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 4);
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
         c += __shfl_xor_sync(0xFFFFFFFFu, c, 16);
-        if (g == 0) colp[w4 * kChunk + 8 * i + t2 + j] = c * F1 * F2;
+        if (g == 0) colp[w4 * kChunk + 8 * tile + t2 + j] = c * U1 * U2;
       }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < (HALF ? 0 : NT); ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  }
+  };
+  if (HALF || group != 3) finish_rows();
+  else form_planes();
+  if (HALF) form_planes();
   __syncthreads();
   {
     // dP' K, dL' K: rows t, blocks s <= t; dP'^T Q, dL'^T K: rows s, blocks t >= s
-    const uint32_t left = sx + (group & 1 ? 2 * SQ : 0), right = group == 2 ? sq : sk;
-    if (DELTA || !(group & 1))
+    const bool rows_t = HALF ? group == 0 : group < 2;
+    const uint32_t left = sx + (DELTA && (group & 1) ? 2 * SQ : 0), right = group == KGROUP ? sq : sk;
+    if (DELTA || HALF || !(group & 1))
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        if (group < 2 ? ks <= w4 : ks >= w4) {
+        if (rows_t ? ks <= w4 : ks >= w4) {
           uint32_t a[2][4], b4[4];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (group < 2) lc.a_rows(a[c], left + c * SQ, m0, ks * 16);
+            if (rows_t) lc.a_rows(a[c], left + c * SQ, m0, ks * 16);
             else lc.a_cols(a[c], left + c * SQ, ks * 16, m0);
           }
 #pragma unroll
@@ -2149,7 +2187,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
         }
       }
   }
-  const float outs = out1 * (group == 2 ? qscale : kappa);
+  const float outs = out1 * (group == KGROUP ? qscale : kappa);
   float4 *hand = reinterpret_cast<float4 *>(smem + l.stage);             // [2][4 warps][NT][32]
   if (DELTA && (group & 1))
 #pragma unroll
@@ -2157,7 +2195,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       hand[(((group >> 1) * 4 + w4) * NT + i) * 32 + lane] =
           make_float4(acc[i][0] * outs * out2, acc[i][1] * outs * out2, acc[i][2] * outs * out2, acc[i][3] * outs * out2);
   if (DELTA) __syncthreads();
-  if (group == 0 || group == 2) {
+  if (group == 0 || group == KGROUP) {
     void *dst = group == 0 ? p.dq : p.dk;
     const long long stride = p.parts ? (long long)p.H * DK : group == 0 ? p.q_stride : p.k_stride;
     const int type = p.parts ? 0 : p.dtype;
@@ -2205,7 +2243,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) scan_grads_kernel(const ScanP
       // (a token's columns are summed by the warps whose rows reach it)
       const float c = (colp[t] + colp[kChunk + t]) + (colp[2 * kChunk + t] + colp[3 * kChunk + t]);
       db[i] = fmaf(eC[t], kw[t], c);
-      dG[i] = (double)rowv[t] - (double)be[t] * db[i] + (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
+      dG[i] = (double)rowv[t] + (HALF ? (double)rowv[kChunk + t] : 0.0) - (double)be[t] * db[i] + (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
       tot += (double)w[t] * kw[t];
     }
 #pragma unroll
