@@ -413,7 +413,8 @@ lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward
  *   state_out  as state_in, may be the same buffer; NULL: not wanted.  An empty sequence's
  *              state is copied.
  *   workspace  workspace_bytes >= lores_scan_workspace(cfg, 0) of device memory
- * All pointers 16-byte aligned (gates and offsets 4-byte).  Asynchronous on `stream`.
+ * All pointers 16-byte aligned (gates and offsets 4-byte); apart from state_out no output may
+ * overlap an input.  Asynchronous on `stream`.
  * Errors: INVALID_ARG (shapes, strides, NULL or misaligned pointers, workspace too small, NULL
  * offsets where n_seq does not divide total), UNSUPPORTED (device without sm_100), CUDA. */
 lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, const void *k,
@@ -424,7 +425,8 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
 
 /* Gradients of the same call.  d_o [total, H, d_v] of dtype and d_state_out (fp32, NULL: zero)
  * are the gradients of o and state_out; dq, dk, dv (dtype), dlog_alpha, dbeta [total, H] fp32
- * and d_state_in (fp32, may be NULL, may be d_state_out's buffer) receive those of the inputs.
+ * and d_state_in (fp32, may be NULL, may be d_state_out's buffer; no other output may overlap an
+ * input) receive those of the inputs.
  * The forward pass is recomputed from the inputs; nothing of an earlier call is used.  Every
  * sum has a fixed order, so equal calls give equal bits.  Where log_alpha is below -1000 its
  * gradient is zero.  Rows of tokens in no sequence are left as they were.  Errors as above;

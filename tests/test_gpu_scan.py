@@ -611,3 +611,26 @@ def test_fp16_outputs_are_off_by_their_rounding(dk, dv, lens, delta):
     o, _ = Call(x, offs, delta, F16).forward()
     ro, _ = scan64(*(x[n] for n in NAMES[:5]), offs, x["state"], delta)
     assert rel(o, ro) <= 1.01 * rel(ro.half(), ro) + FP32
+
+
+@pytest.mark.parametrize("lens,H", [([300, 77], 4), ([40], 2), ([1000, 30], 64)])
+def test_calls_one_behind_the_other(lens, H):
+    """Kernels of a call may overlap, those of two calls may not: two problems in turn on one workspace, without waiting."""
+    xs = [inputs(lens, H, H // 2, 64, 64, BF16, seed=160 + i) for i in range(2)]
+    cs = [Call(x, offs, 1, BF16) for x, offs in xs]
+    cs[1].work = cs[0].workspace(True)
+    want = []
+    for c in cs:
+        o, S = (t.clone() for t in c.forward())
+        g = {n: t.clone() for n, t in c.backward(c.x["v"], c.x["state"]).items()}
+        torch.cuda.synchronize()
+        want.append((o, S, g))
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(40):
+        c, (o, S, g) = cs[i % 2], want[i % 2]
+        for _ in range(2):
+            c.forward()
+            got = c.backward(c.x["v"], c.x["state"])
+        o2, S2 = c.forward()
+        bad += (o2 != o).sum() + (S2 != S).sum() + sum((got[n] != g[n]).sum() for n in NAMES)
+    assert int(bad) == 0
