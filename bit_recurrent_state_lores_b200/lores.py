@@ -311,7 +311,8 @@ def lores_scan_backward(cfg, q, k, v, log_alpha, beta, offsets, state_in, d_o, d
 
 
 def lores_scan_check_errors(cfg, workspace, stream=None):
-    """LORES_OK, or LORES_ERR_INVALID_ARG if the last call found offsets that do not fit."""
+    """LORES_OK, or LORES_ERR_INVALID_ARG if the last call found offsets that do not fit; raises
+    LoresError for anything else (a kernel that gave up waiting, a CUDA error)."""
     st = _lib.lores_scan_check_errors(C.byref(cfg), _ptr(workspace), _stream(stream))
     if st not in (LORES_OK, LORES_ERR_INVALID_ARG):
         raise LoresError(st, "lores_scan_check_errors")
