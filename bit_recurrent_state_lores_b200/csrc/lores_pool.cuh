@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPoolThreads) write_states_kernel(const PoolPa
   for (int r = 0; r < kPoolRows; ++r) {
     const int row = row0 + r * STEP;
     const long long at = (src_tile + row) * DK + col0;
-    const void *src = static_cast<const uint8_t *>(p.src) + at * (p.dtype == 0 ? 4 : 2);
+    [[maybe_unused]] const void *src = static_cast<const uint8_t *>(p.src) + at * (p.dtype == 0 ? 4 : 2);
     if (row < p.d_v && LORES_IN(p, kRgS, src, p.dtype == 0 ? 64 : 32)) load_row16(p, at, x[r]);
     else
 #pragma unroll
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kPoolThreads) read_states_kernel(const PoolPar
       }
     }
     const long long at = (dst_tile + row) * DK + col0;
-    const void *dst = static_cast<const uint8_t *>(p.dst) + at * (p.dtype == 0 ? 4 : 2);
+    [[maybe_unused]] const void *dst = static_cast<const uint8_t *>(p.dst) + at * (p.dtype == 0 ? 4 : 2);
     if (LORES_IN(p, kRgS, dst, p.dtype == 0 ? 64 : 32)) store_row16(p, at, y);
   }
 }
