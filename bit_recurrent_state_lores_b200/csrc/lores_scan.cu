@@ -236,7 +236,7 @@ int walk_blocks(const Shape &s, WalkKind kind) {
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
   const auto ctas = [&](int rb) { return walks * ((blocks + rb - 1) / rb); };
   // the two walks of a backward call side by side, where one of these numbers lets them
-  if (!is_forward(kind))
+  if (kind != kForward)
     for (int rb = 1; rb <= std::min(2, blocks); ++rb)
       if (2 * ctas(rb) <= sms) return rb;
   if (max_blocks(s.np, s.c.delta, kind) == 4 && blocks >= 4 && ctas(4) >= 3ll * sms) return 4;
@@ -360,9 +360,8 @@ lores_status lores_scan_forward(const lores_scan_config *cfg, const void *q, con
                                                        cs>>>(p);
     return cuda_status(cudaGetLastError());
   }
-  p.fine = c.dtype == LORES_F16;
   cudaError_t e = run_prep(s, false, p, cs);
-  if (e == cudaSuccess) e = run_walk(s, p.fine ? kForwardFine : kForward, p, cs);
+  if (e == cudaSuccess) e = run_walk(s, kForward, p, cs);
   return cuda_status(e);
 }
 

@@ -39,11 +39,10 @@
 // exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
 // K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
 // operands by one scale per 16 value rows and chunk (S0 and D: their largest entry in
-// [2^6, 2^7); E and R: the larger of that and V's or dO's).  The error of states and gradients stays near 1e-7; two bf16
-// planes would leave 3e-6 to 1e-5, one fp16 plane 2e-4.  Products that only reach a bf16
-// output (Q S0^T and P E) use one plane: three roundings of at most 2^-11 of an operand beside the
-// output's own 2^-8.  An fp16 output's is 2^-11 too, so it gets two (one plane left o 1.6 times as far
-// from exact as its rounding does).
+// [2^6, 2^7); E and R: the larger of that and V's or dO's).  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
+// (fp32 sums leave 2e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
+// they only reach a 16-bit o is not enough either: entries of o came out 1e-3 from the rounded exact value in bf16
+// (1.68e-3 from exact, where the rounding leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -63,7 +62,6 @@ constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran o
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
   int rb;                              // walks: blocks of 16 value rows per CTA
-  int fine;                            // two planes of what only reaches o
   int hpc;                             // scan_prep: heads per CTA (a divisor of share)
   int qk16, v16, o16;                  // 16-byte accesses to q and k, v (and dv), o (or d_o) rows
   long long total;
@@ -81,7 +79,7 @@ struct ScanParams {
   float *gates;                        // kGateFloats
   __half *khat, *qhat;                 // [NP][64][d_k], divided by their scales
   __half *kt, *kb;                     // [2][64][d_k]
-  __half *tm, *pp, *z;                 // [2][64][64] (pp of a 16-bit forward call: one plane)
+  __half *tm, *pp, *z;                 // [2], ten blocks of [16][16] (see tri)
   __half *s0, *dd;                     // [2][dvp][d_k]
   __half *et, *rt;                     // [2][dvp][64]
   float *scales[4];                    // of s0, et, dd, rt: [dvp/16]
@@ -741,8 +739,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             P[i][2 * h + 1] = p1;
             if (KEEP) {
               const int at = tri(warp, i / 2) + (2 * h + (i & 1)) * 64 + 2 * lane;
-              if (NP == 2 || BWD || p.fine) put_at(pp, kTri, at, p0, p1);
-              else *reinterpret_cast<uint32_t *>(pp + at) = pack2(p0, p1);
+              put_at(pp, kTri, at, p0, p1);
             }
           }
         }
@@ -959,10 +956,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 constexpr int kSideWarps = 2;
 constexpr int kReverseBlocks = 2;
 
-// kForwardFine: a forward walk whose products that only reach o have two planes (see below).
-enum WalkKind { kForward, kRecompute, kReverse, kForwardFine, kWalkKinds };
-__host__ __device__ constexpr bool is_forward(int kind) { return kind == kForward || kind == kForwardFine; }
-__host__ __device__ constexpr int o_planes(int np, int kind) { return kind == kForwardFine ? 2 : np; }
+enum WalkKind { kForward, kRecompute, kReverse, kWalkKinds };
 // Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
 __host__ __device__ constexpr int max_blocks(int np, bool delta, int kind) {
   return !delta && kind != kReverse && np == 1 ? 4 : 2;
@@ -985,7 +979,7 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   l.k = at; at += np * tile;
   l.q = at; at += kind != kRecompute ? np * tile : 0;
   l.tm = at; at += kind == kReverse || delta ? 2 * sq : 0;     // Tm or Z
-  l.pp = at; at += is_forward(kind) ? o_planes(np, kind) * sq : 0;
+  l.pp = at; at += kind == kForward ? 2 * sq : 0;
   l.v = at; at += rb * tile_bytes(np);
   l.gates = at; at += kGateStage * 4;
   l.bytes = (at + 15) / 16 * 16;
@@ -994,7 +988,7 @@ __host__ __device__ inline WalkLayout walk_layout(int dk, int np, int rb, int nh
   l.side = at; at += delta || kind == kReverse ? 4096 : 0;     // Tm V or dO^T Z
   l.last = at; at += delta || kind == kReverse ? 4096 : 0;     // E or R, for the side warps
   l.plus = at; at += kind == kReverse ? 16 * dk * 4 : 0;       // dO^T Q
-  l.planes = at; at += is_forward(kind) ? o_planes(np, kind) * 16 * dk * 2 : 0;   // S0 as left operands
+  l.planes = at; at += kind == kForward ? 2 * 16 * dk * 2 : 0;   // S0 as left operands
   l.tops = at; at += 32;                                       // largest entries: see below
   l.tail = at;
   return l;
@@ -1183,7 +1177,7 @@ __device__ __forceinline__ void keep_tiles(__half *dst, long long plane, int row
 __host__ __device__ constexpr unsigned walk_bulk_bytes(int dk, int np, bool delta, int kind) {
   const int tile = kChunk * dk * 2, sq = kTri * 2;
   return kGateStage * 4 + (delta ? 2 * tile : 0) + (delta || kind == kReverse ? 2 * sq : 0) + np * tile +
-         (kind != kRecompute ? np * tile : 0) + (is_forward(kind) ? o_planes(np, kind) * sq : 0);
+         (kind != kRecompute ? np * tile : 0) + (kind == kForward ? 2 * sq : 0);
 }
 // The chunk's matrices: one thread issues them, they complete on `bar`.
 template <int DK, int NP, bool DELTA, int KIND>
@@ -1201,13 +1195,12 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
     bulk_g2s(st + l.tm, (KIND != kReverse ? p.tm : DELTA ? p.z : p.pp) + rec * (2 * kTri), 2 * SQ, bar);
   bulk_g2s(st + l.k, p.khat + qrec * (NP * kChunk * DK), NP * TILE, bar);
   if (KIND != kRecompute) bulk_g2s(st + l.q, p.qhat + qrec * (NP * kChunk * DK), NP * TILE, bar);
-  if (is_forward(KIND)) bulk_g2s(st + l.pp, p.pp + rec * (2 * kTri), o_planes(NP, KIND) * SQ, bar);
+  if (KIND == kForward) bulk_g2s(st + l.pp, p.pp + rec * (2 * kTri), 2 * SQ, bar);
 }
 
 template <int DK, int NP, bool DELTA, int KIND, int NH>
 __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) scan_walk_kernel(const ScanParams p) {
-  constexpr bool REV = KIND == kReverse, FWD = is_forward(KIND);
-  constexpr int OP = o_planes(NP, KIND);                     // planes of S0, P and E where they only reach o
+  constexpr bool REV = KIND == kReverse, FWD = KIND == kForward;
   constexpr bool JOIN = DELTA || REV;                        // E (or R) has parts in several warps
   constexpr int DKH = DK / NH, NTH = DKH / 8;
   constexpr uint32_t TILE = kChunk * DK * 2, SQ = kTri * 2, VP = kChunk * 16 * 2;
@@ -1342,7 +1335,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           split_tiles(S[2 * ks], S[2 * ks + 1], inv, ah, al);
           if (FWD) {
             planes[(c0 / 16 + ks) * 32 + lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-            if (OP == 2) planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
+            planes[(DK / 16 + c0 / 16 + ks) * 32 + lane] = make_uint4(al[0], al[1], al[2], al[3]);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1609,17 +1602,15 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               for (int i = 0; i < 2; ++i) ld.b_rows(b[(ks + 1) & 1][i], sq, (2 * h + i) * 16, ks * 16 + 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i) mma2(O[2 * i], O[2 * i + 1], ah, b[ks & 1][i]);
-            if (OP == 2) {
-              const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
-              const uint32_t al[4] = {z.x, z.y, z.z, z.w};
+            const uint4 z = planes[(DK / 16 + ks) * 32 + lane];
+            const uint32_t al[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
-                if (NP == 2) {
-                  uint32_t x[4];
-                  ld.b_rows(x, sq + TILE, (2 * h + i) * 16, ks * 16);
-                  mma2(O[2 * i], O[2 * i + 1], ah, x);
-                }
+            for (int i = 0; i < 2; ++i) {
+              mma2(O[2 * i], O[2 * i + 1], al, b[ks & 1][i]);
+              if (NP == 2) {
+                uint32_t x[4];
+                ld.b_rows(x, sq + TILE, (2 * h + i) * 16, ks * 16);
+                mma2(O[2 * i], O[2 * i + 1], ah, x);
               }
             }
           }
@@ -1640,7 +1631,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               if (ks <= 2 * H + i) lv.b_rows(r[ks][i], pp + 2 * tri(2 * H + i, ks), 0, 0);
           if (JOIN) barrier_sync(Y, PER);
           // + E^T P^T (E = V of a 16-bit type is exact in one plane)
-          constexpr bool EL = JOIN ? OP == 2 : NP == 2;
+          constexpr bool EL = JOIN || NP == 2;
           uint32_t eh[4][4], el[4][4];
 #pragma unroll
           for (int ks = 0; ks < 2 * H + 2; ++ks) {
@@ -1660,11 +1651,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               if (ks <= 2 * H + i) {
                 mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
                 if (EL) mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
-                if (OP == 2) {
-                  uint32_t x[4];
-                  lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
-                  mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
-                }
+                uint32_t x[4];
+                lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
+                mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
               }
         };
         if (FWD) {
@@ -2415,7 +2404,7 @@ using ScanFn = void (*)(ScanParams);
 // kernels of one key width
 struct ScanKernels {
   ScanFn prep[2][2][2];                // [np - 1][delta][backward]
-  ScanFn walk[2][2][kWalkKinds];       // [np - 1][delta][WalkKind]; kForwardFine: for one plane
+  ScanFn walk[2][2][kWalkKinds];       // [np - 1][delta][WalkKind]
   ScanFn grads[2][2];
 };
 // Warps that share a block's state: half a 16-column state has no whole k-step.

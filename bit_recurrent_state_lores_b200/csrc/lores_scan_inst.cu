@@ -13,7 +13,6 @@ static void fill(ScanKernels &t) {
   t.walk[NP - 1][DELTA][kForward] = scan_walk_kernel<DK, NP, DELTA, kForward, NH>;
   t.walk[NP - 1][DELTA][kRecompute] = scan_walk_kernel<DK, NP, DELTA, kRecompute, NH>;
   t.walk[NP - 1][DELTA][kReverse] = scan_walk_kernel<DK, NP, DELTA, kReverse, NH>;
-  if constexpr (NP == 1) t.walk[0][DELTA][kForwardFine] = scan_walk_kernel<DK, 1, DELTA, kForwardFine, NH>;
   t.grads[NP - 1][DELTA] = scan_grads_kernel<DK, NP, DELTA>;
 }
 

@@ -1,0 +1,53 @@
+"""The state scan at the ends of its domain: rounding of 16-bit outputs, magnitudes far from one in a part of the
+inputs, values that are not finite, offsets that do not fit.
+
+References and tolerances as in test_gpu_scan: FP32 is what a dozen products of operands of 22 bits may be off by.
+"""
+import pytest
+import torch
+
+from .scan_reference import inputs, rel, scan64
+from .test_gpu_scan import BF16, F16, F32, FP32, NAMES, Call, lib, tol
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def normal(like, seed, by=1.0, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(like.shape, generator=g, dtype=torch.float64) * by).to(dtype).double().cuda()
+
+
+def forward64(x, offs, delta):
+    return scan64(*(x[n] for n in NAMES[:5]), offs, x["state"], delta)
+
+
+def backward64(x, offs, delta, d_o, d_S):
+    leaves = [x[n].clone().requires_grad_(True) for n in NAMES]
+    o, S = scan64(*leaves[:5], offs, leaves[5], delta)
+    loss = (o * d_o).sum() if d_S is None else (o * d_o).sum() + (S * d_S).sum()
+    return dict(zip(NAMES, torch.autograd.grad(loss, leaves)))
+
+
+def check_gradients(got, want, dtype, times=1.0):
+    # (a gate's gradient sums terms of either sign, up to four times its size: as in test_gpu_scan)
+    for n in NAMES:
+        t = tol(dtype) if n in "qkv" else FP32
+        assert rel(got[n], want[n]) <= t * times * (4 if n in ("log_alpha", "beta") else 1), n
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dk,dv,lens,delta", [(128, 128, [300, 77], 1), (64, 100, [300], 1), (128, 64, [150, 77], 0),
+                                              (16, 16, [300], 1), (32, 4, [9, 130], 1)])
+def test_16_bit_outputs_round_the_fp32_result(dk, dv, lens, delta, dtype):
+    """An entry x whose fp32 result is off by e rounds to the other neighbour with probability 2 |e| / u at most, u <=
+    eps |x| the distance between neighbours, and is then off by u: the squares sum to at most 2 eps sum |e| |x| <=
+    2 eps FP32 |x|^2 (Cauchy), beside e itself."""
+    x, offs = inputs(lens, 4, 2, dk, dv, dtype, seed=250 + dk)
+    o, _ = Call(x, offs, delta, dtype).forward()
+    ro, _ = forward64(x, offs, delta)
+    assert rel(o, ro.to(dtype)) <= (2 * torch.finfo(dtype).eps * FP32) ** 0.5 + FP32
