@@ -59,6 +59,8 @@ constexpr int kPrepThreads = 128;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
 constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran out
 
+enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR, kScaleO, kScales };
+
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
   int rb;                              // walks: blocks of 16 value rows per CTA
@@ -82,7 +84,7 @@ struct ScanParams {
   __half *tm, *pp, *z;                 // [2], ten blocks of [16][16] (see tri)
   __half *s0, *dd;                     // [2][dvp][d_k]
   __half *et, *rt;                     // [2][dvp][64]
-  float *scales[4];                    // of s0, et, dd, rt: [dvp/16]
+  float *scales[kScales];              // of s0, et, dd, rt and of d_o: [dvp/16]
   // backward
   const float *d_state_out;
   float *d_state_in;
@@ -98,7 +100,6 @@ enum GateRow { kGateE, kGateWk, kGateEk, kGateC, kGateW, kGateB, kGateG };   // 
 constexpr int kGateScales = (kGateG + 2) * kChunk;
 constexpr int kGateFloats = kGateScales + 8;
 constexpr int kGateStage = 4 * kChunk + 8;     // what a walk takes of it: the first four rows, the scalars
-enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR };
 
 // -------------------------------------------------------------------------------------
 // sequences and chunk slots
@@ -1300,6 +1301,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
       float inv, invV, invE;
       const float scale = scale_of(mS, 6, inv);
       float scaleV = scale_of(mV, 6, invV);
+      [[maybe_unused]] const float scaleO = scaleV;          // reverse: dO's own
       if (REV) {
         scaleV *= qscale;
         mV = abs_bits(__uint_as_float(mV) * qscale);
@@ -1687,7 +1689,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
           }
           keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
-          if (lane == 0 && h == 0) p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+          if (lane == 0 && h == 0) {
+            p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+            if (REV) p.scales[kScaleO][rec * (p.dvp / 16) + brow / 16] = scaleO;
+          }
           if (REV) {
             // (both side warps are done with the rows of dO)
             barrier_sync(Z + 3 * kReverseBlocks, 32 * kSideWarps);
@@ -1751,7 +1756,7 @@ __host__ __device__ inline GradLayout grad_layout(int dk, int np, int dvp, bool 
   l.q = at; at += np * kChunk * dk * 2;
   l.x = at; at += (delta ? 4 : 2) * kChunk * kChunk * 2;  // dP' hi, lo, dL' hi, lo
   l.f = at; at += (kGateFloats + 5 * kChunk + 4 * kChunk + 16 + 8) * 4;
-  l.scales = at; at += 4 * (dvp / 16) * 4;
+  l.scales = at; at += kScales * (dvp / 16) * 4;
   l.stage = (at + 15) / 16 * 16;
   at = 0;
   l.s0 = at; at += 2 * kGradRows * dk * 2;
@@ -1843,7 +1848,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
       }
     }
     if (b == 0)
-      for (int i = tid; i < 4 * blocks16; i += kGradThreads)
+      for (int i = tid; i < kScales * blocks16; i += kGradThreads)
         cp4(smem + l.scales + 4 * i, p.scales[i / blocks16] + rec * blocks16 + i % blocks16);
     copy_tokens<SIZE>(st + l.o, LDO,
                       static_cast<const uint8_t *>(p.o) + (token0 * p.o_stride + (long long)head * p.d_v + v0) * SIZE,
@@ -1852,10 +1857,11 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   };
   fetch(0);
   const float *sS = reinterpret_cast<const float *>(smem + l.scales), *sE = sS + blocks16, *sD = sE + blocks16,
-              *sR = sD + blocks16;
+              *sR = sD + blocks16, *sO = sR + blocks16;
   // the group's two scales: of the left operand's planes and of the right one's
-  const float *sl = group == KGROUP ? sE : sR, *sr2 = group == KGROUP ? sD : group == 3 ? sE : sS;
-  int topDS = 0, topRE = 0, top = 0;
+  const float *sl = group == KGROUP ? sE : group == 0 || !DELTA ? sO : sR,
+              *sr2 = group == KGROUP ? sD : group == 3 ? sE : sS;
+  int topDS = 0, topRE = 0, topOE = 0, top = 0;
 
   // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T (in halves: tiles NT .. NT + 3 dO E^T)
   constexpr int NA = HALF ? NT + 4 : NT > 16 ? NT : 16;
@@ -1879,8 +1885,9 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     if (*stop) return;
     if (b == 0) {
       topDS = top_unit(sD, sS, blocks16, lane);
-      topRE = top_unit(sR, sE, blocks16, lane);
-      top = group == 3 ? topRE : top_unit(sl, sr2, blocks16, lane);
+      topOE = top_unit(sO, sE, blocks16, lane);
+      if (DELTA) topRE = top_unit(sR, sE, blocks16, lane);
+      top = top_unit(sl, sr2, blocks16, lane);
     }
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
     uint8_t *st = stage_of(b);
@@ -1910,9 +1917,9 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
       const __half2 by = __float2half2_rn(ratio);
       uint32_t ao[NP][4], ar[2][4], b4[4];
       if (HALF) {
-        // dO over the scale of R, in the unit of dO E^T; of this warp's columns every other 16
-        const int er = exponent(sR[b16]);
-        const float to = pow2(-er) * pow2(er + exponent(sE[b16]) - topRE);
+        // dO over its scale, in the unit of dO E^T; of this warp's columns every other 16
+        const int eo = exponent(sO[b16]);
+        const float to = pow2(-eo) * pow2(eo + exponent(sE[b16]) - topOE);
         uint32_t raw[4], ae[4];
         a_rows_plain(raw, smem_addr(st + l.o), LDO, m0, kk, lane);
 #pragma unroll
@@ -1932,7 +1939,9 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
         }
       }
       if (group == 0 || (!HALF && group == 3)) {
-        const float to = pow2(-el) * ratio;            // dO over the scale of R
+        // dO over its scale, in the unit of the group's product
+        const int eo = exponent(sO[b16]);
+        const float to = pow2(-eo) * (group == 0 ? ratio : pow2(eo + exponent(sE[b16]) - topOE));
         if (NP == 1) {
           uint32_t raw[4];
           a_rows_plain(raw, smem_addr(st + l.o), LDO, m0, kk, lane);
@@ -2015,13 +2024,14 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1];
   const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
   const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
-  // The planes of dP', dL' are held over F of group 3 and 2^8 dvp (rounded up to a power of two).  Entries of S0, V, D
-  // and dO over their scales are below 2^7; E = V - S k and R alike reach 1 + sqrt(d_k) |k| < 2^4 times that, so a sum
-  // over d_v of products of two is below 2^22 dvp, and with b up to 2 the planes' entries are below 2^15.
+  // The planes of dP' are held over the unit of dO E^T and 2^8 dvp (rounded up to a power of two), those of dL' over
+  // that of R E^T likewise.  Entries of dO over its scale are below 2^7, E and R reach 1 + sqrt(d_k) |k| < 2^4 times
+  // that, so a sum over d_v of products of two is below 2^22 dvp, and with b up to 2 the planes' entries are below 2^15.
   const int lg = 8 + 32 - __clz(p.dvp - 1);
-  const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // F of the group, as two factors in range
-  const float to_unit = pow2(top - topRE - lg);                          // from F to what the planes are held over
-  const float out1 = pow2(topRE / 2) * pow2(lg), out2 = pow2(topRE - topRE / 2);
+  const int topP = DELTA && (group & 1) ? topRE : topOE;                 // of the planes that the group multiplies
+  const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // unit of the group's sums, as two factors in range
+  const float to_unit = pow2(top - topP - lg);                           // from it to what the planes are held over
+  const float out1 = pow2(topP / 2) * pow2(lg), out2 = pow2(topP - topP / 2);
 
   auto finish_rows = [&]() {
     // the row's dot with q or k, then the row in the planes' units
@@ -2052,13 +2062,14 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   };
   auto form_planes = [&]() {
     constexpr int STEPS = HALF ? 2 : 4;
-    const float U1 = HALF ? pow2(topRE / 2) : F1, U2 = HALF ? pow2(topRE - topRE / 2) : F2,    // (F of dO E^T)
-                to_planes = HALF ? pow2(-lg) : to_unit;
+    // the larger of the units of dO E^T and R E^T
+    const int topM = DELTA ? max(topOE, topRE) : topOE;
+    const float U1 = pow2(topM / 2), U2 = pow2(topM - topM / 2), to_planes = pow2(-lg);
     float rs[2] = {0.0f, 0.0f}, cs[2 * STEPS][2];
 #pragma unroll
     for (int i = 0; i < 2 * STEPS; ++i) cs[i][0] = cs[i][1] = 0.0f;
     // q_t.k_s with dO E^T -> dP', k_t.k_s with R E^T -> dL', by 16 columns s, so that few registers hold the products
-    const float toq = qscale * kappa, tok = -kappa * kappa;
+    const float toq = qscale * kappa * pow2(topOE - topM), tok = -kappa * kappa * pow2(topRE - topM);
     __half *out = reinterpret_cast<__half *>(smem + l.x);
     const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
 #pragma unroll

@@ -51,3 +51,16 @@ def test_16_bit_outputs_round_the_fp32_result(dk, dv, lens, delta, dtype):
     o, _ = Call(x, offs, delta, dtype).forward()
     ro, _ = forward64(x, offs, delta)
     assert rel(o, ro.to(dtype)) <= (2 * torch.finfo(dtype).eps * FP32) ** 0.5 + FP32
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("delta,heads_qk", [(1, 2), (1, 1), (0, 2), (0, 1)])
+@pytest.mark.parametrize("qs,os,ss", [(4e-3, 1.0, None), (1e-3, 1.0, None), (1e-6, 1.0, None), (1e-6, 1.0, 1.0),
+                                      (1e3, 1.0, None), (1e3, 1.0, 1.0), (1.0, 1e-6, 1.0), (1.0, 1.0, 1e-6)])
+def test_gradients_of_outputs_and_of_states_of_different_sizes(qs, os, ss, delta, heads_qk, dtype):
+    """q far from unit norm, d_o and d_state_out (None: not given) of different sizes."""
+    x, offs = inputs([130, 40], 2, heads_qk, 64, 48, dtype, seed=201)
+    x["q"] = (x["q"] * qs).to(dtype).double()
+    d_o, d_S = normal(x["v"], 7, os, dtype), None if ss is None else normal(x["state"], 8, ss)
+    got = Call(x, offs, delta, dtype).backward(d_o, d_S)
+    check_gradients(got, backward64(x, offs, delta, d_o, d_S), dtype)
