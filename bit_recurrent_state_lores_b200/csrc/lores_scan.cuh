@@ -38,8 +38,8 @@
 // 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi; 16-bit inputs are
 // exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
 // K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
-// operands by one scale per 16 value rows and chunk (S0 and D: their largest entry in
-// [2^6, 2^7); E and R: the larger of that and V's or dO's).  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
+// operands by one scale per 16 value rows and chunk (their largest entry in
+// [2^6, 2^7)).  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
 // (fp32 sums leave 2e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
 // they only reach a 16-bit o is not enough either: entries of o came out 1e-3 from the rounded exact value in bf16
 // (1.68e-3 from exact, where the rounding leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 // The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
 // form D's sum over dO^T Q, which the state warps take last (barrier Z).
 constexpr int kSideWarps = 2;
-constexpr int kReverseBlocks = 2;
+constexpr int kReverseBlocks = 2;        // at most, where E or R has a barrier of the side warps'
 
 enum WalkKind { kForward, kRecompute, kReverse, kWalkKinds };
 // Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
@@ -1227,13 +1227,13 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   float4 *last = reinterpret_cast<float4 *>(tail + l.last), *plus = reinterpret_cast<float4 *>(tail + l.plus);
   uint4 *planes = reinterpret_cast<uint4 *>(tail + l.planes);
   // bits of the largest magnitudes: [2 (i & 1) + h] of the state warps' columns at the start of the i-th chunk,
-  // [4 + stage] of the rows of V or dO
+  // [4 + stage] of the rows of V or dO, [6 + h] of the side warps' tokens of E or R
   unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
   const Lane<DK> ld(lane);
   const Lane<16> lv(lane);
-  const int X = 1 + 3 * blk, Y = X + 1, Z = X + 2;
+  const int X = 1 + 3 * blk, Y = X + 1, Z = X + 2, sides = Z + 3 * kReverseBlocks;
   if (tid == 0) {
     mbar_init(bars, 1);
     mbar_init(bars + 1, 1);
@@ -1295,22 +1295,13 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     const int n = min(kChunk, len - c * kChunk);
     if (loader || !live) {
     } else {
-      // scales: of the state, of V (or dO, which takes the scale of Q that Z and the planes of Q lack), of E (or R)
-      const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]);
-      unsigned mV = tops[4 + (c & by)];
-      float inv, invV, invE;
+      // scales: of the state, of V (or dO, which takes the scale of Q that Z and the planes of Q lack)
+      const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), mV = tops[4 + (c & by)];
+      float inv, invV;
       const float scale = scale_of(mS, 6, inv);
       float scaleV = scale_of(mV, 6, invV);
       [[maybe_unused]] const float scaleO = scaleV;          // reverse: dO's own
-      if (REV) {
-        scaleV *= qscale;
-        mV = abs_bits(__uint_as_float(mV) * qscale);
-      }
-      float scaleE = scale_of(max(mS, mV), 6, invE);
-      if (!JOIN) {
-        scaleE = scaleV;
-        invE = invV;
-      }
+      if (REV) scaleV *= qscale;
       if (!side) {
         // ---- state warp -----------------------------------------------------------------
         float E[8][4];                   // 16 value rows x 64 tokens
@@ -1397,37 +1388,39 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         // sum starts from zero and joins the state in one fma, so that the tensor cores'
         // rounding does not pile up in it
         const float eC = eG[kChunk - 1];
-        // the scale of that operand: |E_t w_t| stays near max(|V| max w, |S0| e^{G_C} max b), likewise in reverse
-        // (without the delta rule E = V)
-        float invW;
-        const float topW = __uint_as_float(mV) * scalars[REV ? 4 : 2];
-        const float scaleW = scale_of(abs_bits(JOIN ? fmaxf(topW, __uint_as_float(mS) * eC * scalars[3]) : topW), 6, invW);
+        // that operand, in fp32, then over its scale
+        float scaleW = 1.0f;
         uint32_t wh[4][4], wl[4][4];
-        if (!REV || DELTA)
+        if (!REV || DELTA) {
+          if (!JOIN)                     // E = V: the planes of V are over its own scale
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            uint32_t v[NP][4];
-            if (!JOIN)                   // E = V: the planes of V are over its own scale
+            for (int ks = 0; ks < 4; ++ks) {
+              uint32_t v[NP][4];
 #pragma unroll
               for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + ks * 16 + 8 * (q >> 1) + t2);
-              if (JOIN) {
-                const float *e = &E[2 * ks + (q >> 1)][2 * (q & 1)];
-                const float to = REV ? -invW : invW;
-                split2(e[0] * (f.x * to), e[1] * (f.y * to), wh[ks][q], wl[ks][q]);
-              } else {
+              for (int q = 0; q < 4; ++q) {
                 float2 x = half2_of(v[0][q]);
                 if (NP == 2) {
                   const float2 y = half2_of(v[NP - 1][q]);
                   x.x = __fadd_rn(x.x, y.x);
                   x.y = __fadd_rn(x.y, y.y);
                 }
-                split2(x.x * scaleV * (f.x * invW), x.y * scaleV * (f.y * invW), wh[ks][q], wl[ks][q]);
+                E[2 * ks + (q >> 1)][2 * (q & 1)] = x.x * scaleV;
+                E[2 * ks + (q >> 1)][2 * (q & 1) + 1] = x.y * scaleV;
               }
             }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>((REV ? ek : wk) + 8 * i + t2);
+            E[i][0] *= f.x; E[i][1] *= f.y; E[i][2] *= f.x; E[i][3] *= f.y;
           }
+          float invW;
+          scaleW = scale_of(max_bits(E), 6, invW);
+          if (REV) invW = -invW;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) split_tiles(E[2 * ks], E[2 * ks + 1], invW, wh[ks], wl[ks]);
+        }
         if (!JOIN && FWD) barrier_arrive(Y, PER);    // (V is read)
         constexpr int STEP = JOIN && NTH >= 8 ? 4 : NTH >= 4 ? 2 : 1;   // column pairs at a time
 #pragma unroll
@@ -1616,7 +1609,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               }
             }
           }
-          const float to = scale * invE;
+          const float to = scale * qscale;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = *reinterpret_cast<const float2 *>(eG + 32 * h + 8 * i + t2);
@@ -1635,6 +1628,11 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           // + E^T P^T (E = V of a 16-bit type is exact in one plane)
           constexpr bool EL = JOIN || NP == 2;
           uint32_t eh[4][4], el[4][4];
+          // E = V - S k over a bound of it: |S k| of the chunk's start is below max |S| d_k 2 sk, and the delta rule's
+          // tokens together add at most 64 times max |V| (where |k|^2 b < 2); planes then stay below 2^14
+          float scaleE = scaleV, invE;
+          if (JOIN)
+            scaleE = scale_of(max(mV, abs_bits(__uint_as_float(mS) * (2.0f * DK * scalars[0]))), 6, invE);
 #pragma unroll
           for (int ks = 0; ks < 2 * H + 2; ++ks) {
             if (!JOIN) {
@@ -1646,24 +1644,34 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             const float e0[4] = {y.x, y.y, y.z, y.w}, e1[4] = {z.x, z.y, z.z, z.w};
             split_tiles(e0, e1, invE, eh[ks], el[ks]);
           }
+          float a[4][4];                   // (a sum of its own: E and S0 may be of very different sizes)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < 2 * H + 2; ++ks)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (ks <= 2 * H + i) {
-                mma2(O[2 * i], O[2 * i + 1], eh[ks], r[ks][i]);
-                if (EL) mma2(O[2 * i], O[2 * i + 1], el[ks], r[ks][i]);
+                mma2(a[2 * i], a[2 * i + 1], eh[ks], r[ks][i]);
+                if (EL) mma2(a[2 * i], a[2 * i + 1], el[ks], r[ks][i]);
                 uint32_t x[4];
                 lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
-                mma2(O[2 * i], O[2 * i + 1], eh[ks], x);
+                mma2(a[2 * i], a[2 * i + 1], eh[ks], x);
               }
+          const float to = scaleE * qscale;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[i][j] = fmaf(a[i][j], to, O[i][j]);
         };
         if (FWD) {
           if (h == 0) with_p(Const<0>());
           else with_p(Const<1>());
           // (without the delta rule the tile holds V until every warp of the block has read it)
           if (!JOIN) barrier_sync(Y, PER);
-          store_tokens<NP>(O, scaleE * qscale, tile, 4 * h, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
+          store_tokens<NP>(O, 1.0f, tile, 4 * h, p.o, p.dtype, p.o_stride, start + (long long)c * kChunk, n,
                            head * p.d_v + brow, p.d_v - brow, p.o16, lane);
         } else if (!JOIN) {
           // the planes of V, tile by tile (a tile of [64 tokens][16 rows] is kept transposed)
@@ -1680,7 +1688,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
                 *reinterpret_cast<uint32_t *>(et + pl * (long long)p.dvp * kChunk +
                                               tiled<kChunk>(brow + 8 * (q & 1), ks * 16 + 8 * (q >> 1)) + 2 * lane) = v[q];
             }
-          if (lane == 0 && h == 0) p.scales[kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
+          if (lane == 0 && h == 0) p.scales[kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleV;
         } else {
           barrier_sync(Y, PER);
 #pragma unroll
@@ -1688,6 +1696,11 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             const float4 y = last[(4 * h + i) * 32 + lane];
             O[i][0] = y.x; O[i][1] = y.y; O[i][2] = y.z; O[i][3] = y.w;
           }
+          const unsigned top = max_bits(O);
+          if (lane == 0) tops[6 + h] = top;
+          barrier_sync(sides, 32 * kSideWarps);
+          float invE;
+          const float scaleE = scale_of(max(tops[6], tops[7]), 6, invE);
           keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
           if (lane == 0 && h == 0) {
             p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
@@ -1695,7 +1708,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           }
           if (REV) {
             // (both side warps are done with the rows of dO)
-            barrier_sync(Z + 3 * kReverseBlocks, 32 * kSideWarps);
+            barrier_sync(sides, 32 * kSideWarps);
             store_tokens<NP>(O, 1.0f, tile, 4 * h, p.dv, p.dtype, p.v_stride, start + (long long)c * kChunk, n,
                              head * p.d_v + brow, p.d_v - brow, p.v16, lane);
           }
@@ -2024,10 +2037,10 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1];
   const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
   const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
-  // The planes of dP' are held over the unit of dO E^T and 2^8 dvp (rounded up to a power of two), those of dL' over
-  // that of R E^T likewise.  Entries of dO over its scale are below 2^7, E and R reach 1 + sqrt(d_k) |k| < 2^4 times
-  // that, so a sum over d_v of products of two is below 2^22 dvp, and with b up to 2 the planes' entries are below 2^15.
-  const int lg = 8 + 32 - __clz(p.dvp - 1);
+  // The planes of dP' are held over the unit of dO E^T and dvp (rounded up to a power of two), those of dL' over that of
+  // R E^T likewise.  Entries of dO, E and R over their scales are below 2^7, so a sum over d_v of products of two is below
+  // 2^14 dvp, and with b up to 2 the planes' entries are below 2^15.
+  const int lg = 32 - __clz(p.dvp - 1);
   const int topP = DELTA && (group & 1) ? topRE : topOE;                 // of the planes that the group multiplies
   const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // unit of the group's sums, as two factors in range
   const float to_unit = pow2(top - topP - lg);                           // from it to what the planes are held over

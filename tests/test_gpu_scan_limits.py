@@ -64,3 +64,21 @@ def test_gradients_of_outputs_and_of_states_of_different_sizes(qs, os, ss, delta
     d_o, d_S = normal(x["v"], 7, os, dtype), None if ss is None else normal(x["state"], 8, ss)
     got = Call(x, offs, delta, dtype).backward(d_o, d_S)
     check_gradients(got, backward64(x, offs, delta, d_o, d_S), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ks", [300.0, 1e3, 3e3, 3e4])
+def test_large_keys_inside_the_domain(ks, dtype):
+    """|k|^2 beta < 1: v - S k is as large as |k| then, however small beta.  (What carries beta k, of size 1 / (18 |k|),
+    is held to an absolute 2^-25 at worst; a dozen such: FP32 |k|.)"""
+    x, offs = inputs([150], 2, 1, 64, 48, dtype, seed=211)
+    x["k"] = (x["k"] * ks).to(dtype).double()
+    x["beta"] = (x["beta"] * 0.9 / ks ** 2).float().double()
+    c = Call(x, offs, 1, dtype)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, 1)
+    assert rel(o, ro) <= tol(dtype) + FP32 * ks and rel(S, rS) <= FP32 * ks
+    d_o, d_S = normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8)
+    got, want = c.backward(d_o, d_S), backward64(x, offs, 1, d_o, d_S)
+    for n in NAMES:
+        assert rel(got[n], want[n]) <= tol(dtype) + 4 * FP32 * ks, n
