@@ -37,7 +37,8 @@
 // as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
 // 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi; 16-bit inputs are
 // exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
-// K and Q are divided by one scale per chunk and head (largest entry in [1, 2)), the walks'
+// K and Q are divided by one scale per chunk and head (largest entry in [1, 2)) and so are the betas in Z, Kb, dP' and
+// dL', P by one per row, the walks'
 // operands by one scale per 16 value rows and chunk (their largest entry in
 // [2^6, 2^7)).  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
 // (fp32 sums leave 2e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
@@ -93,13 +94,13 @@ struct ScanParams {
   float *dlog_alpha, *dbeta;
 };
 
-// Record of a chunk and head, kChunk entries each: e^G, w over the scale of K (that is, what
-// multiplies a row of khat), e^G likewise, e^(G_C - G), w, b; G / ln 2 as a pair of floats.  Then the scales of K and Q,
-// and the largest magnitudes of the second row, of b over the scale of K and of the third row.
-enum GateRow { kGateE, kGateWk, kGateEk, kGateC, kGateW, kGateB, kGateG };   // kGateG: two rows' worth of pairs
+// Record of a chunk and head, kChunk entries each: e^(G_C - G); e^G; w over the scale of K (that is, what multiplies a
+// row of khat); e^G likewise; what multiplies a row of P's planes (forward); w; b; G / ln 2 as a pair of floats.  Then
+// the scales of K, Q and b.
+enum GateRow { kGateC, kGateE, kGateWk, kGateEk, kGateP, kGateW, kGateB, kGateG };   // kGateG: two rows' worth of pairs
 constexpr int kGateScales = (kGateG + 2) * kChunk;
 constexpr int kGateFloats = kGateScales + 8;
-constexpr int kGateStage = 4 * kChunk + 8;     // what a walk takes of it: the first four rows, the scalars
+constexpr int kGateStage = 4 * kChunk + 8;     // what a walk takes of it: four rows, the scales
 
 // -------------------------------------------------------------------------------------
 // sequences and chunk slots
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   __half *A16 = reinterpret_cast<__half *>(smem + l.a);             // [2][64][64]
   float *X = reinterpret_cast<float *>(smem + l.x);                 // diagonal blocks of A, then T
   __half *XD = reinterpret_cast<__half *>(smem + l.xd);             // [4][2][16][16]: X_ii
-  // of this head and of the next: G / ln 2, b times the scale of K
+  // of this head and of the next: G / ln 2, b over its scale (which is in red[8], red[9])
   auto gate_at = [&](int which) { return reinterpret_cast<float2 *>(smem + l.f + which * (3 * kChunk * 4)); };
   unsigned *red = reinterpret_cast<unsigned *>(smem + l.f + 2 * (3 * kChunk * 4));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
@@ -598,7 +599,11 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     // held there and G stays finite.
     float *gates = p.gates + ((long long)slot * p.H + head) * kGateFloats;
     float2 *G = gate_at((head - head0) & 1);
-    float *bk = reinterpret_cast<float *>(G + kChunk);
+    float *bn = reinterpret_cast<float *>(G + kChunk);
+    // (b below 2^-60 everywhere counts with fewer digits: the scales of what it multiplies have to stay in range)
+    float inv;
+    const float sb = scale_of(max(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(b[0]), fabsf(b[1])))), 0x21800000u),
+                              0, inv);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (la[i] < -1000.0f) la[i] = -1000.0f;
@@ -609,7 +614,6 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     }
     const double end = __shfl_sync(0xFFFFFFFFu, run, 31);
     const double Gt[2] = {run - (double)la[1], run};
-    float tops[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
@@ -618,10 +622,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       const float hi = (float)l2;
       const float2 pair = make_float2(hi, (float)(l2 - (double)hi));
       G[t] = pair;
-      bk[t] = b[i] * sk;
-      tops[0] = fmaxf(tops[0], fabsf(w * sk));
-      tops[1] = fmaxf(tops[1], fabsf(b[i] * sk));
-      tops[2] = fmaxf(tops[2], fabsf(e * sk));
+      bn[t] = b[i] * inv;
       gates[kGateE * kChunk + t] = e;
       gates[kGateWk * kChunk + t] = w * sk;
       gates[kGateEk * kChunk + t] = e * sk;
@@ -630,14 +631,11 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       gates[kGateC * kChunk + t] = c;
       reinterpret_cast<float2 *>(gates + kGateG * kChunk)[t] = pair;
     }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tops[i]));
-      if (lane == 0) gates[kGateScales + 2 + i] = __uint_as_float(m);
-    }
     if (lane == 0) {
       gates[kGateScales] = sk;
       gates[kGateScales + 1] = sq;
+      gates[kGateScales + 2] = sb;
+      red[8 + ((head - head0) & 1)] = __float_as_uint(sb);
     }
   };
   if (warp == 0) {
@@ -688,7 +686,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     const long long rec = (long long)slot * p.H + head;
     __syncthreads();                   // this head's gates are formed, the last head's matrices are used
     const float2 *G = gate_at((head - head0) & 1);
-    const float *bk = reinterpret_cast<const float *>(G + kChunk);
+    const float *bn = reinterpret_cast<const float *>(G + kChunk);
+    const float sb = __uint_as_float(red[8 + ((head - head0) & 1)]), sbk = sb * sk;
     // the next head's gates, by the warp that has the fewest blocks
     auto next_gates = [&]() {
       if (warp == 0 && head + 1 < head0 + p.hpc) {
@@ -707,7 +706,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 #pragma unroll
           for (int j = 0; j < 4; ++j) P[i][j] = QK[i][j];
       if (DELTA && !several) __syncthreads();      // Q's tile becomes A's planes
-      // P over the scale of Q (for Z without its decays) and, strictly below the diagonal, A
+      // P over the scales of Q, K and b (for Z without its decays) and, strictly below the diagonal, A
       constexpr bool KEEP = !BWD || !DELTA;        // P itself is wanted
       const float2 gt[2] = {G[m0 + g], G[m0 + g + 8]};
       __half *pp = p.pp + rec * (2 * kTri);
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       for (int i = 0; i < 8; ++i) {
         if (i / 2 <= warp) {
           const float4 gs = *reinterpret_cast<const float4 *>(G + 8 * i + t2);
-          const float2 bs = *reinterpret_cast<const float2 *>(bk + 8 * i + t2);
+          const float2 bs = *reinterpret_cast<const float2 *>(bn + 8 * i + t2);
           const bool diagonal = i / 2 == warp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -724,7 +723,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
               p0 *= decay(gt[h], make_float2(gs.x, gs.y));
               p1 *= decay(gt[h], make_float2(gs.z, gs.w));
             }
-            const float a0 = A[i][2 * h] * (bs.x * sk), a1 = A[i][2 * h + 1] * (bs.y * sk);
+            const float a0 = A[i][2 * h] * (bs.x * sbk) * sk, a1 = A[i][2 * h + 1] * (bs.y * sbk) * sk;
             if (diagonal) {
               const int t = m0 + g + 8 * h, s = 8 * i + t2;
               p0 = s <= t ? p0 : 0.0f;
@@ -738,12 +737,31 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
             }
             P[i][2 * h] = p0;
             P[i][2 * h + 1] = p1;
-            if (KEEP) {
-              const int at = tri(warp, i / 2) + (2 * h + (i & 1)) * 64 + 2 * lane;
-              put_at(pp, kTri, at, p0, p1);
-            }
           }
         }
+      }
+      if (KEEP) {
+        // forward: each row over a scale of its own, since an output takes one row (and is linear in q)
+        float to[2] = {1.0f, 1.0f};
+        if (!BWD)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i / 2 <= warp) m = fmaxf(m, fmaxf(fabsf(P[i][2 * h]), fabsf(P[i][2 * h + 1])));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            const float row = scale_of(__float_as_uint(m), 6, to[h]);
+            if ((lane & 3) == 0) p.gates[rec * kGateFloats + kGateP * kChunk + m0 + g + 8 * h] = row * sbk * sq;
+          }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i / 2 <= warp)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              put_at(pp, kTri, tri(warp, i / 2) + (2 * h + (i & 1)) * 64 + 2 * lane, P[i][2 * h] * to[h],
+                     P[i][2 * h + 1] * to[h]);
       }
     }
     if (!DELTA) {
@@ -840,7 +858,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       }
     }
     if (BWD) {
-      // Z = P Tm (over the scale of Q), that is dec times the product without decays: rows t of this warp; block (r, s)
+      // Z = P Tm (over P's scales), that is dec times the product without decays: rows t of this warp; block (r, s)
       // of T is zero for s > r
       float acc[8][4];
 #pragma unroll
@@ -879,7 +897,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
           }
         }
     }
-    // Kt = -T K: rows t of this warp, s blocks up to its own; then Kb = T^T diag(b) K: rows s of this warp, t
+    // Kt = -T K over the scale of K: rows t of this warp, s blocks up to its own; then Kb = T^T diag(b) K over those of
+    // K and b: rows s of this warp, t
     // blocks from its own on.  Two halves of the columns, so that the accumulators leave room for
     // four CTAs per SM.
     constexpr int HALVES = DK >= 64 ? 2 : 1, HT = DK / 8 / HALVES;
@@ -893,8 +912,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int m = m0 + g + 8 * (q & 1), k = ks * 16 + t2 + 8 * (q >> 1);
-            if (which) split2(X[k * kLdF + m] * bk[k], X[(k + 1) * kLdF + m] * bk[k + 1], ah[ks][q], al[ks][q]);
-            else split2(-X[m * kLdF + k] * sk, -X[m * kLdF + k + 1] * sk, ah[ks][q], al[ks][q]);
+            if (which) split2(X[k * kLdF + m] * bn[k], X[(k + 1) * kLdF + m] * bn[k + 1], ah[ks][q], al[ks][q]);
+            else split2(-X[m * kLdF + k], -X[m * kLdF + k + 1], ah[ks][q], al[ks][q]);
           }
 #pragma unroll 1
       for (int half = 0; half < HALVES; ++half) {
@@ -1189,7 +1208,7 @@ __device__ __forceinline__ void fetch_matrices(const ScanParams &p, uint8_t *st,
   const long long qrec = (long long)slot * (p.H / p.share) + head / p.share;
   const float *gates = p.gates + rec * kGateFloats;
   mbar_expect_tx(bar, walk_bulk_bytes(DK, NP, DELTA, KIND));
-  bulk_g2s(st + l.gates, gates, 4 * kChunk * 4, bar);
+  bulk_g2s(st + l.gates, gates + (KIND == kForward ? kGateE : kGateC) * kChunk, 4 * kChunk * 4, bar);
   bulk_g2s(st + l.gates + 4 * kChunk * 4, gates + kGateScales, 32, bar);
   if (DELTA) bulk_g2s(st + l.kt, (KIND == kReverse ? p.kb : p.kt) + rec * (2 * kChunk * DK), 2 * TILE, bar);
   if (DELTA || KIND == kReverse)
@@ -1288,14 +1307,16 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     if (by && loader && i0 + 1 < chunks) fetch(next);
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
                    tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
-    const float *eG = reinterpret_cast<const float *>(st + l.gates), *wk = eG + kChunk, *ek = wk + kChunk,
-                *lead = REV ? ek + kChunk : eG, *scalars = ek + 2 * kChunk;
-    const float qscale = scalars[1];
+    // (forward: rows kGateE .. kGateP, else kGateC .. kGateEk)
+    const float *eC = reinterpret_cast<const float *>(st + l.gates), *eG = FWD ? eC : eC + kChunk, *wk = eG + kChunk,
+                *ek = wk + kChunk, *rowP = ek + kChunk, *scalars = eC + 4 * kChunk;
+    const float kscale = scalars[0], qscale = scalars[1], bkscale = scalars[2] * kscale;
     const long long rec = (long long)(base + c) * p.H + head;
     const int n = min(kChunk, len - c * kChunk);
     if (loader || !live) {
     } else {
-      // scales: of the state, of V (or dO, which takes the scale of Q that Z and the planes of Q lack)
+      // scales: of the state, of V (or dO, which takes the scale of Q that the planes of Q and Z lack; Z those of K and
+      // b too)
       const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), mV = tops[4 + (c & by)];
       float inv, invV;
       const float scale = scale_of(mS, 6, inv);
@@ -1369,8 +1390,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               const float4 y = part[((h ^ 1) * 8 + i) * 32 + lane];
               E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
             }
-            const float2 f = *reinterpret_cast<const float2 *>((DELTA ? lead : wk) + 8 * i + t2);
-            const float x = scale * f.x, y = scale * f.y;
+            const float2 f = *reinterpret_cast<const float2 *>((!DELTA ? wk : REV ? eC : ek) + 8 * i + t2);
+            const float s = REV && DELTA ? scale * bkscale : scale, x = s * f.x, y = s * f.y;
             E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
             E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
           }
@@ -1387,7 +1408,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
         // sum starts from zero and joins the state in one fma, so that the tensor cores'
         // rounding does not pile up in it
-        const float eC = eG[kChunk - 1];
+        const float eEnd = eG[kChunk - 1];
         // that operand, in fp32, then over its scale
         float scaleW = 1.0f;
         uint32_t wh[4][4], wl[4][4];
@@ -1460,10 +1481,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               const float4 y = plus[(c0 / 8 + 2 * n0 + i) * 32 + lane];
               const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, fmaf(a[i][j], scaleW, z[j]));
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eEnd, fmaf(a[i][j], scaleW, z[j]));
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eC, a[i][j] * scaleW);
+              for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], eEnd, a[i][j] * scaleW);
             }
           }
         }
@@ -1507,10 +1528,10 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               for (int i = 0; i < 2; ++i)
                 if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][NP - 1], b[ks][0][i]);
           }
+          const float to = REV ? scaleV * bkscale : scaleV;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            sided[(4 * H + i) * 32 + lane] =
-                make_float4(U[i][0] * scaleV, U[i][1] * scaleV, U[i][2] * scaleV, U[i][3] * scaleV);
+            sided[(4 * H + i) * 32 + lane] = make_float4(U[i][0] * to, U[i][1] * to, U[i][2] * to, U[i][3] * to);
         };
         if (JOIN) {
           if (h == 0) with_v(Const<0>());
@@ -1632,7 +1653,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           // tokens together add at most 64 times max |V| (where |k|^2 b < 2); planes then stay below 2^14
           float scaleE = scaleV, invE;
           if (JOIN)
-            scaleE = scale_of(max(mV, abs_bits(__uint_as_float(mS) * (2.0f * DK * scalars[0]))), 6, invE);
+            scaleE = scale_of(max(mV, abs_bits(__uint_as_float(mS) * (2.0f * DK * kscale))), 6, invE);
 #pragma unroll
           for (int ks = 0; ks < 2 * H + 2; ++ks) {
             if (!JOIN) {
@@ -1660,11 +1681,12 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
                 lv.b_rows(x, pp + SQ + 2 * tri(2 * H + i, ks), 0, 0);
                 mma2(a[2 * i], a[2 * i + 1], eh[ks], x);
               }
-          const float to = scaleE * qscale;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>(rowP + 32 * h + 8 * i + t2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) O[i][j] = fmaf(a[i][j], to, O[i][j]);
+            for (int j = 0; j < 4; ++j) O[i][j] = fmaf(a[i][j], scaleE * (j & 1 ? f.y : f.x), O[i][j]);
+          }
         };
         if (FWD) {
           if (h == 0) with_p(Const<0>());
@@ -2034,12 +2056,13 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
 #pragma unroll
   for (int d = 16; d; d >>= 1) ds += __shfl_xor_sync(0xFFFFFFFFu, ds, d);
   if (lane == 0) red[warp] = ds;
-  const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1];
+  const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1], sb = gates[kGateScales + 2];
+  const float isb = __uint_as_float((254u << 23) - __float_as_uint(sb));
   const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
   const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
-  // The planes of dP' are held over the unit of dO E^T and dvp (rounded up to a power of two), those of dL' over that of
-  // R E^T likewise.  Entries of dO, E and R over their scales are below 2^7, so a sum over d_v of products of two is below
-  // 2^14 dvp, and with b up to 2 the planes' entries are below 2^15.
+  // The planes of dP' are held over the unit of dO E^T, dvp (rounded up to a power of two) and the scale of b, those of
+  // dL' over that of R E^T likewise.  Entries of dO, E and R over their scales are below 2^7, so a sum over d_v of
+  // products of two is below 2^14 dvp, and b over its scale below 2: the planes' entries are below 2^15.
   const int lg = 32 - __clz(p.dvp - 1);
   const int topP = DELTA && (group & 1) ? topRE : topOE;                 // of the planes that the group multiplies
   const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // unit of the group's sums, as two factors in range
@@ -2054,7 +2077,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
       float s = 0.0f;
-      const float to = group == KGROUP ? w[t] * to_unit * iqscale : eG[t] * to_unit * (group == 1 ? -ikappa : ikappa);
+      const float to = (group == KGROUP ? w[t] * isb * iqscale : eG[t] * isb * (group == 1 ? -ikappa : ikappa)) * to_unit;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int at = 2 * (tiled<DK>(m0 + 8 * h, 8 * i) + 2 * lane);
@@ -2138,8 +2161,8 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
               if (diagonal && s > t) m = 0.0f;
               rs[h] = fmaf(b, m, rs[h]);
               cs[2 * step + e][j] += m;
-              y[j] *= b * to_planes;
-              z[j] *= -b * to_planes;
+              y[j] *= b * isb * to_planes;
+              z[j] *= -b * isb * to_planes;
             }
             put_pair<kChunk>(out, kChunk * kChunk, m0 + 8 * h, 8 * i, y[0], y[1], lane);
             if (DELTA) put_pair<kChunk>(out + 2 * kChunk * kChunk, kChunk * kChunk, m0 + 8 * h, 8 * i, z[0], z[1], lane);
@@ -2200,7 +2223,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
         }
       }
   }
-  const float outs = out1 * (group == KGROUP ? qscale : kappa);
+  const float outs = out1 * (group == KGROUP ? qscale : kappa) * sb;
   float4 *hand = reinterpret_cast<float4 *>(smem + l.stage);             // [2][4 warps][NT][32]
   if (DELTA && (group & 1))
 #pragma unroll

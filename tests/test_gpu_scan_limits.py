@@ -82,3 +82,69 @@ def test_large_keys_inside_the_domain(ks, dtype):
     got, want = c.backward(d_o, d_S), backward64(x, offs, 1, d_o, d_S)
     for n in NAMES:
         assert rel(got[n], want[n]) <= tol(dtype) + 4 * FP32 * ks, n
+
+
+@pytest.mark.parametrize("delta,b", [(1, 1e-2), (1, 1e-4), (1, 1e-6), (1, 1e-12), (0, 1e-2), (0, 1e-6), (0, 1e-12),
+                                     (0, 100.0), (0, 1e6)])
+@pytest.mark.parametrize("heads_qk", [1, 2])
+def test_beta_far_from_one(delta, b, heads_qk):
+    """Zero first states, so that every result but dv's part through d_state_out and d_state_in is of beta's size."""
+    x, offs = inputs([130, 30], 2, heads_qk, 64, 48, F32, seed=221)
+    x["beta"] = (x["beta"] * b).float().double()
+    x["state"].zero_()
+    c = Call(x, offs, delta, F32)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, delta)
+    assert rel(o, ro) <= FP32 and rel(S, rS) <= FP32
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    check_gradients(c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S), F32)
+
+
+@pytest.mark.parametrize("delta", [0, 1])
+@pytest.mark.parametrize("ks", [1e-3, 1e-6, 1e-10])
+def test_small_keys(ks, delta):
+    x, offs = inputs([130], 2, 1, 64, 48, F32, seed=222)
+    x["k"] = (x["k"] * ks).float().double()
+    x["state"].zero_()
+    c = Call(x, offs, delta, F32)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, delta)
+    assert rel(o, ro) <= FP32 and rel(S, rS) <= FP32
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    check_gradients(c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S), F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ks", [100.0, 1e3, 1e-2])
+def test_keys_of_other_norms_inside_the_domain(ks, dtype):
+    """|k|^2 beta < 1 is what the delta rule asks for, whatever |k| is."""
+    x, offs = inputs([150], 2, 1, 64, 48, dtype, seed=211)
+    x["k"] = (x["k"] * ks).to(dtype).double()
+    x["beta"] = (x["beta"] * 0.9 / ks ** 2).float().double()
+    c = Call(x, offs, 1, dtype)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, 1)
+    # v - S k and its products carry up to |S k| / |v| times the terms
+    assert rel(o, ro) <= tol(dtype) + 3 * FP32 and rel(S, rS) <= 4 * FP32
+    d_o, d_S = normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8)
+    check_gradients(c.backward(d_o, d_S), backward64(x, offs, 1, d_o, d_S), dtype, 4)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("delta", [0, 1])
+def test_equal_queries_and_gradients_that_add_up(delta, dtype):
+    """Every q and k alike, d_o all ones, q of norm 50: dv sums as much as it can."""
+    x, offs = inputs([200], 2, 2, 128, 32, dtype, seed=212)
+    x["k"].fill_(128 ** -0.5)
+    x["k"] = x["k"].to(dtype).double()
+    x["q"].fill_(50 * 128 ** -0.5)
+    x["q"] = x["q"].to(dtype).double()
+    x["log_alpha"].zero_()
+    x["beta"].fill_(1.0 / 64)
+    d_o = torch.ones_like(x["v"])
+    got = Call(x, offs, delta, dtype).backward(d_o, None)
+    want = backward64(x, offs, delta, d_o, None)
+    for n in ("q", "k", "v", "state"):
+        assert rel(got[n], want[n]) <= (tol(dtype) if n in "qkv" else FP32) * 4, n
+    for n in ("log_alpha", "beta"):
+        assert torch.isfinite(got[n]).all(), n
