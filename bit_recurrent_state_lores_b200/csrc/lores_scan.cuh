@@ -1544,6 +1544,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           // (diag(e^G) dO)^T Q, columns [h d_k/2, (h+1) d_k/2)
           constexpr int HALF = DK >= 32 ? DK / 2 : DK, QS = HALF >= 64 ? 4 : HALF / 16;
           if (DK >= 32 || h == 0) {
+            // (e^G over a scale of its own: behind a strong decay at the chunk's start all of it is small)
+            float invG;
+            const float scaleG = scale_of(__float_as_uint(eG[0]), 0, invG), to = scaleV * scaleG;
             uint32_t oh[4][4], ol[4][4];
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -1552,7 +1555,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               for (int pl = 0; pl < NP; ++pl) lv.a_cols(v[pl], sv + pl * VP, ks * 16, 0);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+                float2 f = *reinterpret_cast<const float2 *>(eG + ks * 16 + 8 * (q >> 1) + t2);
+                f.x *= invG;
+                f.y *= invG;
                 float2 x = half2_of(v[0][q]);
                 if (NP == 2) {
                   const float2 y = half2_of(v[NP - 1][q]);
@@ -1593,7 +1598,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 #pragma unroll
               for (int i = 0; i < 2 * QS; ++i)
                 plus[(col / 8 + i) * 32 + lane] =
-                    make_float4(a[i][0] * scaleV, a[i][1] * scaleV, a[i][2] * scaleV, a[i][3] * scaleV);
+                    make_float4(a[i][0] * to, a[i][1] * to, a[i][2] * to, a[i][3] * to);
             }
           }
           barrier_arrive(Z, PER);

@@ -148,3 +148,16 @@ def test_equal_queries_and_gradients_that_add_up(delta, dtype):
         assert rel(got[n], want[n]) <= (tol(dtype) if n in "qkv" else FP32) * 4, n
     for n in ("log_alpha", "beta"):
         assert torch.isfinite(got[n]).all(), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("delta", [0, 1])
+@pytest.mark.parametrize("la", [-20.0, -60.0])
+def test_the_first_states_gradient_behind_a_strong_decay(la, delta, dtype):
+    """The first token of a chunk fades the state to 1e-9 or 1e-26: so is the gradient, with all its digits."""
+    x, offs = inputs([100, 64, 65], 2, 2, 64, 48, dtype, seed=231)
+    for t in offs[:3]:
+        x["log_alpha"][t] = la
+    d_o = normal(x["v"], 7, 1.0, dtype)
+    got = Call(x, offs, delta, dtype).backward(d_o, None)
+    check_gradients(got, backward64(x, offs, delta, d_o, None), dtype)
