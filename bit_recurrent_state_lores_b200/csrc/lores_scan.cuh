@@ -314,10 +314,12 @@ __device__ __forceinline__ void split_tiles(const float (&c0)[4], const float (&
 }
 
 // Scales: the power of two c with m / c in [2^up, 2^(up+1)) for the magnitude m with the given
-// bits (1 for zero, limits at the ends of the range), and its inverse.
+// bits (limits at the ends of the range), and its inverse.  For zero: 1, or with LEAST the smallest, so that a
+// part that holds zeros alone does not count where parts are brought to their largest unit.
+template <bool LEAST = false>
 __device__ __forceinline__ float scale_of(unsigned bits, int up, float &inv) {
-  int e = (int)(bits >> 23) - up;
-  e = bits == 0u ? 127 : max(1, min(253, e));
+  int e = max(1, min(253, (int)(bits >> 23) - up));
+  if (!LEAST && bits == 0u) e = 127;
   inv = __uint_as_float((unsigned)(254 - e) << 23);
   return __uint_as_float((unsigned)e << 23);
 }
@@ -600,10 +602,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     float *gates = p.gates + ((long long)slot * p.H + head) * kGateFloats;
     float2 *G = gate_at((head - head0) & 1);
     float *bn = reinterpret_cast<float *>(G + kChunk);
-    // (b below 2^-60 everywhere counts with fewer digits: the scales of what it multiplies have to stay in range)
     float inv;
-    const float sb = scale_of(max(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(b[0]), fabsf(b[1])))), 0x21800000u),
-                              0, inv);
+    const float sb = scale_of(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(b[0]), fabsf(b[1])))), 0, inv);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (la[i] < -1000.0f) la[i] = -1000.0f;
@@ -1074,7 +1074,7 @@ __device__ __forceinline__ void fetch_rows(uint8_t *dst, const void *src, long l
   }
 }
 // ... turned in place into fp16 planes [64][16] (in tiles) over their scale; returns the bits of the largest magnitude.
-template <int NP>
+template <int NP, bool LEAST>
 __device__ __forceinline__ unsigned convert_rows(uint8_t *tile, int dtype, int lane) {
   float x[2][16];                          // rows lane and lane + 32
 #pragma unroll
@@ -1102,7 +1102,7 @@ __device__ __forceinline__ unsigned convert_rows(uint8_t *tile, int dtype, int l
   }
   const unsigned m = max_bits(x);          // (also: every lane has read its rows)
   float inv;
-  scale_of(m, 6, inv);
+  scale_of<LEAST>(m, 6, inv);
   __syncwarp();
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -1293,7 +1293,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
       cp_wait<0>();
       __syncwarp();
       if (live) {
-        const unsigned m = convert_rows<NP>(tile, p.dtype, lane);
+        const unsigned m = convert_rows<NP, !FWD>(tile, p.dtype, lane);
         if (lane == 0) tops[4 + (c & by)] = m;
       }
       // the stage's copies; a wait that runs out ends the walk for the whole CTA
@@ -1319,8 +1319,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
       // b too)
       const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), mV = tops[4 + (c & by)];
       float inv, invV;
-      const float scale = scale_of(mS, 6, inv);
-      float scaleV = scale_of(mV, 6, invV);
+      const float scale = scale_of<!FWD>(mS, 6, inv);
+      float scaleV = scale_of<!FWD>(mV, 6, invV);
       [[maybe_unused]] const float scaleO = scaleV;          // reverse: dO's own
       if (REV) scaleV *= qscale;
       if (!side) {
@@ -1727,7 +1727,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           if (lane == 0) tops[6 + h] = top;
           barrier_sync(sides, 32 * kSideWarps);
           float invE;
-          const float scaleE = scale_of(max(tops[6], tops[7]), 6, invE);
+          const float scaleE = scale_of<true>(max(tops[6], tops[7]), 6, invE);
           keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
           if (lane == 0 && h == 0) {
             p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
@@ -1901,7 +1901,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   // the group's two scales: of the left operand's planes and of the right one's
   const float *sl = group == KGROUP ? sE : group == 0 || !DELTA ? sO : sR,
               *sr2 = group == KGROUP ? sD : group == 3 ? sE : sS;
-  int topDS = 0, topRE = 0, topOE = 0, top = 0;
+  int topDS = 0, topRE = 0, topOE = 0, topOS = 0, topED = 0, topRS = 0;
 
   // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T (in halves: tiles NT .. NT + 3 dO E^T)
   constexpr int NA = HALF ? NT + 4 : NT > 16 ? NT : 16;
@@ -1915,6 +1915,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const Lane<DK> ld(lane);
   const Lane<kChunk> lc(lane);
 
+  int top = 0;
   for (int b = 0; b < blocks; ++b) {
     cp_wait<0>();
     if (tid == 0 && !mbar_wait_bounded(bars + (p.stages == 2 ? b & 1 : 0), (p.stages == 2 ? b >> 1 : b) & 1, kWaitNs)) {
@@ -1926,8 +1927,13 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     if (b == 0) {
       topDS = top_unit(sD, sS, blocks16, lane);
       topOE = top_unit(sO, sE, blocks16, lane);
-      if (DELTA) topRE = top_unit(sR, sE, blocks16, lane);
-      top = top_unit(sl, sr2, blocks16, lane);
+      topOS = top_unit(sO, sS, blocks16, lane);
+      topED = top_unit(sE, sD, blocks16, lane);
+      if (DELTA) {
+        topRE = top_unit(sR, sE, blocks16, lane);
+        topRS = top_unit(sR, sS, blocks16, lane);
+      }
+      top = group == KGROUP ? topED : group == 0 ? topOS : group == 1 ? topRS : DELTA ? topRE : topOE;
     }
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
     uint8_t *st = stage_of(b);
@@ -2063,16 +2069,19 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   if (lane == 0) red[warp] = ds;
   const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1], sb = gates[kGateScales + 2];
   const float isb = __uint_as_float((254u << 23) - __float_as_uint(sb));
-  const float ikappa = __uint_as_float((254u << 23) - __float_as_uint(kappa));
-  const float iqscale = __uint_as_float((254u << 23) - __float_as_uint(qscale));
   // The planes of dP' are held over the unit of dO E^T, dvp (rounded up to a power of two) and the scale of b, those of
   // dL' over that of R E^T likewise.  Entries of dO, E and R over their scales are below 2^7, so a sum over d_v of
   // products of two is below 2^14 dvp, and b over its scale below 2: the planes' entries are below 2^15.
   const int lg = 32 - __clz(p.dvp - 1);
-  const int topP = DELTA && (group & 1) ? topRE : topOE;                 // of the planes that the group multiplies
+  // A group's sums over value rows go on in the unit of its planes' products, 2^(topP + lg + eb) times the right operand's
+  // scale, or 2^-60 of their own unit where that is larger (the planes' part is then scaled down in turn).  E D is
+  // multiplied by w <= b, so its unit takes the scale of b.
+  const int topP = DELTA && (group & 1) ? topRE : topOE;
+  const int own = top + (group == KGROUP ? exponent(sb) : 0);
+  const int unitP = topP + lg + exponent(sb) + exponent(group == KGROUP ? qscale : kappa), unit = max(unitP, own - 60);
   const float F1 = pow2(top / 2), F2 = pow2(top - top / 2);              // unit of the group's sums, as two factors in range
-  const float to_unit = pow2(top - topP - lg);                           // from it to what the planes are held over
-  const float out1 = pow2(topP / 2) * pow2(lg), out2 = pow2(topP - topP / 2);
+  const float to_unit = pow2(own - unit);
+  const float out1 = pow2(unit / 2), out2 = pow2(unit - unit / 2);
 
   auto finish_rows = [&]() {
     // the row's dot with q or k, then the row in the planes' units
@@ -2082,7 +2091,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     for (int h = 0; h < 2; ++h) {
       const int t = m0 + g + 8 * h;
       float s = 0.0f;
-      const float to = (group == KGROUP ? w[t] * isb * iqscale : eG[t] * isb * (group == 1 ? -ikappa : ikappa)) * to_unit;
+      const float to = (group == KGROUP ? w[t] * isb : group == 1 ? -eG[t] : eG[t]) * to_unit;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int at = 2 * (tiled<DK>(m0 + 8 * h, 8 * i) + 2 * lane);
@@ -2205,6 +2214,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     // dP' K, dL' K: rows t, blocks s <= t; dP'^T Q, dL'^T K: rows s, blocks t >= s
     const bool rows_t = HALF ? group == 0 : group < 2;
     const uint32_t left = sx + (DELTA && (group & 1) ? 2 * SQ : 0), right = group == KGROUP ? sq : sk;
+    const __half2 down = __float2half2_rn(pow2(unitP - unit));
     if (DELTA || HALF || !(group & 1))
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -2214,6 +2224,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
           for (int c = 0; c < 2; ++c) {
             if (rows_t) lc.a_rows(a[c], left + c * SQ, m0, ks * 16);
             else lc.a_cols(a[c], left + c * SQ, ks * 16, m0);
+            if (unit != unitP) scale_frag(a[c], down);
           }
 #pragma unroll
           for (int np = 0; np < DK / 16; ++np) {
@@ -2228,13 +2239,12 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
         }
       }
   }
-  const float outs = out1 * (group == KGROUP ? qscale : kappa) * sb;
   float4 *hand = reinterpret_cast<float4 *>(smem + l.stage);             // [2][4 warps][NT][32]
   if (DELTA && (group & 1))
 #pragma unroll
     for (int i = 0; i < NT; ++i)
       hand[(((group >> 1) * 4 + w4) * NT + i) * 32 + lane] =
-          make_float4(acc[i][0] * outs * out2, acc[i][1] * outs * out2, acc[i][2] * outs * out2, acc[i][3] * outs * out2);
+          make_float4(acc[i][0] * out1 * out2, acc[i][1] * out1 * out2, acc[i][2] * out1 * out2, acc[i][3] * out1 * out2);
   if (DELTA) __syncthreads();
   if (group == 0 || group == KGROUP) {
     void *dst = group == 0 ? p.dq : p.dk;
@@ -2247,7 +2257,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[e][j] = acc[i + e][j] * outs * out2;
+        for (int j = 0; j < 4; ++j) x[e][j] = acc[i + e][j] * out1 * out2;
         if (DELTA && group == 2) {
           const float4 y = hand[(w4 * NT + i + e) * 32 + lane], z = hand[((4 + w4) * NT + i + e) * 32 + lane];
           x[e][0] += y.x + z.x; x[e][1] += y.y + z.y; x[e][2] += y.z + z.z; x[e][3] += y.w + z.w;

@@ -161,3 +161,33 @@ def test_the_first_states_gradient_behind_a_strong_decay(la, delta, dtype):
     d_o = normal(x["v"], 7, 1.0, dtype)
     got = Call(x, offs, delta, dtype).backward(d_o, None)
     check_gradients(got, backward64(x, offs, delta, d_o, None), dtype)
+
+
+@pytest.mark.parametrize("delta,dtype", [(1, F32), (0, F32), (0, BF16)])
+@pytest.mark.parametrize("rows", [16, 32])
+def test_zero_value_rows_beside_small_ones(rows, delta, dtype):
+    """A block of value rows that holds zeros everywhere says nothing about the others' size."""
+    x, offs = inputs([130], 2, 1, 64, 64, dtype, seed=235)
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8, 1e-9)
+    for t, by in ((x["v"], 1e-8), (d_o, 1e-9), (x["state"].transpose(2, 3), 1e-8), (d_S.transpose(2, 3), 1.0)):
+        t *= by
+        t[..., :rows] = 0.0
+    x["v"], d_o = x["v"].to(dtype).double(), d_o.to(dtype).double()
+    x["state"], d_S = x["state"].float().double(), d_S.float().double()
+    got = Call(x, offs, delta, dtype).backward(d_o, d_S)
+    check_gradients(got, backward64(x, offs, delta, d_o, d_S), dtype)
+
+
+@pytest.mark.parametrize("vs,ss,ks,b,delta", [(1e-20, 1e20, 1.0, 1.0, 0), (1e18, 1e-18, 1.0, 1.0, 0),
+                                              (1.0, 1.0, 1.0, 1e-25, 1), (1.0, 1.0, 1e-25, 1.0, 1),
+                                              (1.0, 1.0, 1e-17, 1e-17, 0)])
+def test_gradients_of_parts_of_extreme_sizes(vs, ss, ks, b, delta):
+    x, offs = inputs([130], 2, 2, 64, 48, F32, seed=236)
+    for n, by in (("v", vs), ("state", ss), ("k", ks), ("beta", b)):
+        x[n] = (x[n] * by).float().double()
+    c = Call(x, offs, delta, F32)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, delta)
+    assert rel(o, ro) <= FP32 and rel(S, rS) <= FP32
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    check_gradients(c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S), F32)
