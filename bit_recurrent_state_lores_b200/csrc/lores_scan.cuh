@@ -35,12 +35,11 @@
 //
 // Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
 // as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
-// 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi; 16-bit inputs are
-// exact as one plane.  fp16's range is met by powers of two that leave the result exactly:
-// K and Q are divided by one scale per chunk and head (largest entry in [1, 2)) and so are the betas in Z, Kb, dP' and
-// dL', P by one per row, the walks'
-// operands by one scale per 16 value rows and chunk (their largest entry in
-// [2^6, 2^7)).  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
+// 2^-25 where lo is subnormal.  A product is hi hi + hi lo + lo hi.  fp16's range is met by powers of two that leave the
+// result exactly: K and Q are divided by one scale per chunk and head and so are the betas in Z, Kb, dP' and
+// dL', P by one per row, the walks' operands by one per 16 value rows and chunk, so that the largest entries are near
+// fp16's end (kUp below).  16-bit inputs are exact as one plane down to 2^-31 of that largest entry (bf16; keys 2^-25),
+// fp32 ones keep 22 bits down to 2^-16 of it (keys 2^-10) and are off by at most 2^-39 of it (keys 2^-33) below.  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
 // (fp32 sums leave 2e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
 // they only reach a 16-bit o is not enough either: entries of o came out 1e-3 from the rounded exact value in bf16
 // (1.68e-3 from exact, where the rounding leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
@@ -56,6 +55,10 @@ namespace lores {
 namespace scan {
 
 constexpr int kChunk = 64;
+// Largest entries of the planes: 2^kUp .. 2^(kUp + 1) of S, D, V, dO, E and R and of Q, as large as fp16 allows, so that
+// smaller entries beside them keep their digits; less for K, whose planes' products with T (Kt, Kb: up to sqrt(d_k)
+// times as large) are planes too.  Products of K and Q come back into range by 2^kDownZ (d_k 2^15 2^9 2 = 2^32).
+constexpr int kUp = 14, kUpK = 8, kDownZ = -17;
 constexpr int kPrepThreads = 128;
 constexpr unsigned kFlagOffsets = 1u;  // a sequence's offsets were not 0 <= a <= b <= total
 constexpr unsigned kFlagWait = 2u;     // a wait for a kernel's own copies ran out
@@ -94,8 +97,8 @@ struct ScanParams {
   float *dlog_alpha, *dbeta;
 };
 
-// Record of a chunk and head, kChunk entries each: e^(G_C - G); e^G; w over the scale of K (that is, what multiplies a
-// row of khat); e^G likewise; what multiplies a row of P's planes (forward); w; b; G / ln 2 as a pair of floats.  Then
+// Record of a chunk and head, kChunk entries each: e^(G_C - G); e^G; w times 2^kUpK of the scale of K (that is, what
+// multiplies 2^-kUpK of a row of khat); e^G likewise; what multiplies a row of P's planes (forward); w; b; G / ln 2 as a pair of floats.  Then
 // the scales of K, Q and b.
 enum GateRow { kGateC, kGateE, kGateWk, kGateEk, kGateP, kGateW, kGateB, kGateG };   // kGateG: two rows' worth of pairs
 constexpr int kGateScales = (kGateG + 2) * kChunk;
@@ -572,21 +575,21 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
         red[4 + warp] = mq;
       }
       __syncthreads();
-      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), 0, inv);
+      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), kUpK, inv);
       put_rows<DK, NP, PASS>(xk, p.dtype, inv, K, ko, tid);
-      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), 0, inv);
+      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), kUp, inv);
       put_rows<DK, NP, PASS>(xq, p.dtype, inv, Q, qo, tid);
     } else {
       const unsigned mk = max_rows<NP, PASS>(xk, p.dtype);
       if (lane == 0) red[warp] = mk;
       __syncthreads();
-      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), 0, inv);
+      sk = scale_of(max(max(red[0], red[1]), max(red[2], red[3])), kUpK, inv);
       put_rows<DK, NP, PASS>(xk, p.dtype, inv, K, ko, tid);
       load_rows<DK, NP, PASS>(p, p.q, p.q_stride, token0, qh, n, xk, tid);
       const unsigned mq = max_rows<NP, PASS>(xk, p.dtype);
       if (lane == 0) red[4 + warp] = mq;
       __syncthreads();
-      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), 0, inv);
+      sq = scale_of(max(max(red[4], red[5]), max(red[6], red[7])), kUp, inv);
       put_rows<DK, NP, PASS>(xk, p.dtype, inv, Q, qo, tid);
     }
   }
@@ -602,6 +605,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     float *gates = p.gates + ((long long)slot * p.H + head) * kGateFloats;
     float2 *G = gate_at((head - head0) & 1);
     float *bn = reinterpret_cast<float *>(G + kChunk);
+    const float kn = sk * pow2(kUpK);
     float inv;
     const float sb = scale_of(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(b[0]), fabsf(b[1])))), 0, inv);
 #pragma unroll
@@ -624,8 +628,8 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
       G[t] = pair;
       bn[t] = b[i] * inv;
       gates[kGateE * kChunk + t] = e;
-      gates[kGateWk * kChunk + t] = w * sk;
-      gates[kGateEk * kChunk + t] = e * sk;
+      gates[kGateWk * kChunk + t] = w * kn;
+      gates[kGateEk * kChunk + t] = e * kn;
       gates[kGateW * kChunk + t] = w;
       gates[kGateB * kChunk + t] = b[i];
       gates[kGateC * kChunk + t] = c;
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
           const bool diagonal = i / 2 == warp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float p0 = P[i][2 * h] * bs.x, p1 = P[i][2 * h + 1] * bs.y;
+            float p0 = P[i][2 * h] * (BWD ? bs.x * pow2(kDownZ) : bs.x), p1 = P[i][2 * h + 1] * (BWD ? bs.y * pow2(kDownZ) : bs.y);
             if (KEEP) {
               p0 *= decay(gt[h], make_float2(gs.x, gs.y));
               p1 *= decay(gt[h], make_float2(gs.z, gs.w));
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
               if (i / 2 <= warp) m = fmaxf(m, fmaxf(fabsf(P[i][2 * h]), fabsf(P[i][2 * h + 1])));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            const float row = scale_of(__float_as_uint(m), 6, to[h]);
+            const float row = scale_of(__float_as_uint(m), kUp, to[h]);
             if ((lane & 3) == 0) p.gates[rec * kGateFloats + kGateP * kChunk + m0 + g + 8 * h] = row * sbk * sq;
           }
 #pragma unroll
@@ -1102,7 +1106,7 @@ __device__ __forceinline__ unsigned convert_rows(uint8_t *tile, int dtype, int l
   }
   const unsigned m = max_bits(x);          // (also: every lane has read its rows)
   float inv;
-  scale_of<LEAST>(m, 6, inv);
+  scale_of<LEAST>(m, kUp, inv);
   __syncwarp();
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -1246,7 +1250,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   float4 *last = reinterpret_cast<float4 *>(tail + l.last), *plus = reinterpret_cast<float4 *>(tail + l.plus);
   uint4 *planes = reinterpret_cast<uint4 *>(tail + l.planes);
   // bits of the largest magnitudes: [2 (i & 1) + h] of the state warps' columns at the start of the i-th chunk,
-  // [4 + stage] of the rows of V or dO, [6 + h] of the side warps' tokens of E or R
+  // [4 + stage] of the rows of V or dO, [6 + h] of E or R (forward: by the state warps, else of the side warps' tokens)
   unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
@@ -1310,17 +1314,16 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     // (forward: rows kGateE .. kGateP, else kGateC .. kGateEk)
     const float *eC = reinterpret_cast<const float *>(st + l.gates), *eG = FWD ? eC : eC + kChunk, *wk = eG + kChunk,
                 *ek = wk + kChunk, *rowP = ek + kChunk, *scalars = eC + 4 * kChunk;
-    const float kscale = scalars[0], qscale = scalars[1], bkscale = scalars[2] * kscale;
+    const float qscale = scalars[1], bkscale = scalars[2] * scalars[0];
     const long long rec = (long long)(base + c) * p.H + head;
     const int n = min(kChunk, len - c * kChunk);
     if (loader || !live) {
     } else {
       // scales: of the state, of V (or dO, which takes the scale of Q that the planes of Q and Z lack; Z those of K and
       // b too)
-      const unsigned mS = max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), mV = tops[4 + (c & by)];
-      float inv, invV;
-      const float scale = scale_of<!FWD>(mS, 6, inv);
-      float scaleV = scale_of<!FWD>(mV, 6, invV);
+            float inv, invV;
+      const float scale = scale_of<!FWD>(max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), kUp, inv);
+      float scaleV = scale_of<!FWD>(tops[4 + (c & by)], kUp, invV);
       [[maybe_unused]] const float scaleO = scaleV;          // reverse: dO's own
       if (REV) scaleV *= qscale;
       if (!side) {
@@ -1383,6 +1386,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) part[(h * 8 + i) * 32 + lane] = f4(E[i]);
           barrier_sync(X, PER);
+          const float s = scale * (REV && DELTA ? bkscale : pow2(-kUpK));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 u = sided[i * 32 + lane];
@@ -1391,9 +1395,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               E[i][0] += y.x; E[i][1] += y.y; E[i][2] += y.z; E[i][3] += y.w;
             }
             const float2 f = *reinterpret_cast<const float2 *>((!DELTA ? wk : REV ? eC : ek) + 8 * i + t2);
-            const float s = REV && DELTA ? scale * bkscale : scale, x = s * f.x, y = s * f.y;
-            E[i][0] = fmaf(E[i][0], x, u.x); E[i][1] = fmaf(E[i][1], y, u.y);
-            E[i][2] = fmaf(E[i][2], x, u.z); E[i][3] = fmaf(E[i][3], y, u.w);
+            // (not scale times f: that may leave fp32's range below)
+            E[i][0] = fmaf(E[i][0] * s, f.x, u.x); E[i][1] = fmaf(E[i][1] * s, f.y, u.y);
+            E[i][2] = fmaf(E[i][2] * s, f.x, u.z); E[i][3] = fmaf(E[i][3] * s, f.y, u.w);
           }
         } else {
           if (FWD) barrier_arrive(X, PER);
@@ -1403,6 +1407,11 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (NH == 1 || (i >> 2) == h) last[i * 32 + lane] = f4(E[i]);
+          if (FWD) {                     // (and the largest, for the scale of its planes)
+            const unsigned top = max_bits(E);
+            if (lane == 0) tops[6 + h] = top;
+            if (NH == 1 && lane == 0) tops[7] = top;
+          }
           barrier_arrive(Y, PER);
         }
         // S = e^{G_C} S0 + (diag(w) E)^T K, or D = e^{G_C} D + (diag(e^G) dO)^T Q - (diag(e^G) R)^T K: each tile's
@@ -1437,7 +1446,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
             E[i][0] *= f.x; E[i][1] *= f.y; E[i][2] *= f.x; E[i][3] *= f.y;
           }
           float invW;
-          scaleW = scale_of(max_bits(E), 6, invW);
+          scaleW = scale_of(max_bits(E), kUp, invW) * pow2(-kUpK);
           if (REV) invW = -invW;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) split_tiles(E[2 * ks], E[2 * ks + 1], invW, wh[ks], wl[ks]);
@@ -1528,7 +1537,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
               for (int i = 0; i < 2; ++i)
                 if (REV ? 2 * H + i <= ks : ks <= 2 * H + i) mma2(U[2 * i], U[2 * i + 1], v[ks][NP - 1], b[ks][0][i]);
           }
-          const float to = REV ? scaleV * bkscale : scaleV;
+          const float to = REV ? scaleV * (bkscale * pow2(-kDownZ)) : scaleV;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             sided[(4 * H + i) * 32 + lane] = make_float4(U[i][0] * to, U[i][1] * to, U[i][2] * to, U[i][3] * to);
@@ -1546,7 +1555,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           if (DK >= 32 || h == 0) {
             // (e^G over a scale of its own: behind a strong decay at the chunk's start all of it is small)
             float invG;
-            const float scaleG = scale_of(__float_as_uint(eG[0]), 0, invG), to = scaleV * scaleG;
+            const float scaleG = scale_of(__float_as_uint(eG[0]), -1, invG), to = scaleV * scaleG;
             uint32_t oh[4][4], ol[4][4];
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -1654,11 +1663,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           // + E^T P^T (E = V of a 16-bit type is exact in one plane)
           constexpr bool EL = JOIN || NP == 2;
           uint32_t eh[4][4], el[4][4];
-          // E = V - S k over a bound of it: |S k| of the chunk's start is below max |S| d_k 2 sk, and the delta rule's
-          // tokens together add at most 64 times max |V| (where |k|^2 b < 2); planes then stay below 2^14
           float scaleE = scaleV, invE;
-          if (JOIN)
-            scaleE = scale_of(max(mV, abs_bits(__uint_as_float(mS) * (2.0f * DK * kscale))), 6, invE);
+          if (JOIN) scaleE = scale_of(max(tops[6], tops[7]), kUp, invE);
 #pragma unroll
           for (int ks = 0; ks < 2 * H + 2; ++ks) {
             if (!JOIN) {
@@ -1727,7 +1733,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
           if (lane == 0) tops[6 + h] = top;
           barrier_sync(sides, 32 * kSideWarps);
           float invE;
-          const float scaleE = scale_of<true>(max(tops[6], tops[7]), 6, invE);
+          const float scaleE = scale_of<true>(max(tops[6], tops[7]), kUp, invE);
           keep_tiles((REV ? p.rt : p.et) + rec * (2ll * p.dvp * kChunk), (long long)p.dvp * kChunk, brow, 4 * h, O, invE, lane);
           if (lane == 0 && h == 0) {
             p.scales[REV ? kScaleR : kScaleE][rec * (p.dvp / 16) + brow / 16] = scaleE;
@@ -2070,9 +2076,10 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const float kappa = gates[kGateScales], qscale = gates[kGateScales + 1], sb = gates[kGateScales + 2];
   const float isb = __uint_as_float((254u << 23) - __float_as_uint(sb));
   // The planes of dP' are held over the unit of dO E^T, dvp (rounded up to a power of two) and the scale of b, those of
-  // dL' over that of R E^T likewise.  Entries of dO, E and R over their scales are below 2^7, so a sum over d_v of
-  // products of two is below 2^14 dvp, and b over its scale below 2: the planes' entries are below 2^15.
-  const int lg = 32 - __clz(p.dvp - 1);
+  // dL' over that of R E^T likewise.  Entries of dO, E and R over their scales are below 2^15, so a sum over d_v of
+  // products of two is below 2^30 dvp, and b over its scale below 2: the planes' entries are below
+  // 2^15.
+  const int lg = 2 + kUp + 32 - __clz(p.dvp - 1);
   // A group's sums over value rows go on in the unit of its planes' products, 2^(topP + lg + eb) times the right operand's
   // scale, or 2^-60 of their own unit where that is larger (the planes' part is then scaled down in turn).  E D is
   // multiplied by w <= b, so its unit takes the scale of b.

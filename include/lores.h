@@ -370,10 +370,15 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * on the GPU.
  *
  * Accuracy.  Products run on the tensor cores on operands of 22 bits of significand (two fp16
- * parts; 16-bit inputs are exact), sums and the state are fp32.  States, the gates'
- * gradients and everything fp32 are within a few 1e-6 (relative L2) of the recurrence in exact
- * arithmetic, 16-bit outputs within their own rounding, while |k_t|^2 beta_t < 2 holds with
- * delta = 1 (the domain of the recurrence).  An infinity or NaN in a token's
+ * parts), sums and the state are fp32.  States, the gates' gradients and everything fp32 are within
+ * a few 1e-6 (relative L2) of the recurrence in exact arithmetic, 16-bit outputs are the rounding of
+ * such results, while |k_t|^2 beta_t < 2 holds with delta = 1 (the domain of the recurrence).
+ * Operands are held over powers of two that fit their largest entry in a chunk (64 tokens of a
+ * sequence, counted from its start) and head; of v, d_o and states, in 16 value rows of it.
+ * 16-bit inputs are exact down to 2^-31 of that entry (k: 2^-25), fp32 ones have 22 bits down to 2^-16
+ * of it (k: 2^-10) and are off by at most 2^-39 of it (k: 2^-33) below.  A token's output is as exact
+ * for a small q as for a large one; a token's gradients carry the errors of their chunk's.
+ * An infinity or NaN in a token's
  * inputs may turn the outputs of the whole 64-token chunk that holds it (counted from the
  * sequence's start), and what follows (in the backward pass also what comes before), to NaN,
  * for the heads that read them; other heads and sequences are not touched. */

@@ -191,3 +191,50 @@ def test_gradients_of_parts_of_extreme_sizes(vs, ss, ks, b, delta):
     assert rel(o, ro) <= FP32 and rel(S, rS) <= FP32
     d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
     check_gradients(c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S), F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("delta", [0, 1])
+def test_queries_of_very_different_sizes(delta, dtype):
+    """o_t is linear in q_t: each token's output keeps its digits beside tokens with queries 1e6 times as large."""
+    x, offs = inputs([150], 2, 1, 64, 48, dtype, seed=241)
+    by = 2.0 ** -(torch.arange(150, device="cuda") * 7 % 21).double()[:, None, None]
+    if dtype == F16:
+        by = by.clamp(min=2.0 ** -6)                     # (fp16's own range)
+    x["q"] = (x["q"] * by).to(dtype).double()
+    o, _ = Call(x, offs, delta, dtype).forward()
+    ro, _ = forward64(x, offs, delta)
+    if dtype == F16:                                     # (outputs below fp16's normal range have its absolute step)
+        assert float(((o.double() - ro).abs() - ro.abs() * (2.0 ** -11 + 4 * FP32)).max()) <= 2.0 ** -25 + 8e-6
+        return
+    for t in range(150):
+        for h in range(2):
+            assert rel(o[t, h], ro[t, h]) <= tol(dtype), (t, h)
+
+
+@pytest.mark.parametrize("delta", [0, 1])
+def test_small_values_behind_a_dropped_state(delta):
+    """v (and d_o) of 1e-5 and 1e-6 of what stands before it in the chunk, and the state dropped between."""
+    for by in (1e-5, 1e-6):
+        x, offs = inputs([64], 2, 1, 64, 48, F32, seed=242)
+        x["v"][32:] *= by
+        x["v"] = x["v"].float().double()
+        x["log_alpha"][32] = -float("inf")
+        o, S = Call(x, offs, delta, F32).forward()
+        ro, rS = forward64(x, offs, delta)
+        assert rel(o[:32], ro[:32]) <= FP32 and rel(o[32:], ro[32:]) <= FP32 and rel(S, rS) <= FP32
+
+
+def test_16_bit_inputs_are_exact_far_below_the_chunks_largest():
+    """One large entry in each of q, k and v; the others, 2^-20 of it, still count with all their bits."""
+    x, offs = inputs([64], 1, 1, 64, 16, BF16, seed=243)
+    x["state"].zero_()
+    x["beta"].fill_(0.5)
+    x["log_alpha"].zero_()
+    for n in "qv":
+        x[n] = (x[n] * 2.0 ** -20).to(BF16).double()
+        x[n][0, 0, 0] = 1.0
+    o, _ = Call(x, offs, 0, BF16).forward()
+    ro, _ = forward64(x, offs, 0)
+    # token 1 on: columns other than the large one's
+    assert rel(o[1:, :, 1:], ro[1:, :, 1:]) <= tol(BF16)
