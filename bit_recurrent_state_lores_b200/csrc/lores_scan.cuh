@@ -336,6 +336,9 @@ __device__ __forceinline__ float decay(float2 gt, float2 gs) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(__fsub_rn(gt.x, gs.x), __fsub_rn(gt.y, gs.y))));
   return r;
 }
+// |x|, and NaN where x is not finite (fmaxf then passes it over).
+__device__ __forceinline__ float finite_abs(float x) { return fabsf(__fmaf_rn(x, 0.0f, x)); }
+constexpr unsigned kInf = 0x7F800000u;
 __device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // -------------------------------------------------------------------------------------
@@ -470,7 +473,8 @@ __device__ __forceinline__ void unpack_row(const uint4 (&raw)[NP], int dtype, fl
     }
   }
 }
-// Bits (of fp32) of the warp's largest magnitude; 16-bit types are compared as integers, two at a time.
+// Bits (of fp32) of the warp's largest finite magnitude; 16-bit types are compared as integers, two at a time.  (What is
+// not finite says nothing about a scale: under the scale of an infinity everything else would vanish.)
 template <int NP, int PASS>
 __device__ __forceinline__ unsigned max_rows(const uint4 (&raw)[PASS][NP], int dtype) {
   unsigned m = 0;
@@ -486,7 +490,19 @@ __device__ __forceinline__ unsigned max_rows(const uint4 (&raw)[PASS][NP], int d
     const uint32_t w = max(m & 0xFFFFu, m >> 16);
     m = dtype == 1 ? w << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)w)));
   }
-  return __reduce_max_sync(0xFFFFFFFFu, m);
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if (m >= kInf) {
+    float f = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      float x[8];
+      unpack_row<NP>(raw[i], dtype, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f = fmaxf(f, finite_abs(x[e]));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(f));
+  }
+  return m;
 }
 // The rows over their scale as planes, in shared memory and, where `out` is given, in the workspace.
 template <int DK, int NP, int PASS>
@@ -607,7 +623,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
     float *bn = reinterpret_cast<float *>(G + kChunk);
     const float kn = sk * pow2(kUpK);
     float inv;
-    const float sb = scale_of(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(b[0]), fabsf(b[1])))), 0, inv);
+    const float sb = scale_of(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(0.0f, fmaxf(finite_abs(b[0]), finite_abs(b[1]))))), 0, inv);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (la[i] < -1000.0f) la[i] = -1000.0f;
@@ -1044,6 +1060,7 @@ __device__ __forceinline__ void save_state(const float (&S)[NTH][4], float *dst,
         *reinterpret_cast<float2 *>(dst + (tile * d_v + r0 + 8 * h) * dk + c0 + 8 * i) =
             make_float2(S[i][2 * h], S[i][2 * h + 1]);
 }
+// Bits of the warp's largest finite magnitude.
 template <int N, int M>
 __device__ __forceinline__ unsigned max_bits(const float (&x)[N][M]) {
   float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};       // (a NaN is passed over: it is in the data all the same)
@@ -1051,7 +1068,16 @@ __device__ __forceinline__ unsigned max_bits(const float (&x)[N][M]) {
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int j = 0; j < M; ++j) m[j & 3] = fmaxf(m[j & 3], fabsf(x[i][j]));
-  return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))));
+  unsigned top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))));
+  if (top >= kInf) {                           // (an infinity would make zeros of the rest)
+    float f = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j) f = fmaxf(f, finite_abs(x[i][j]));
+    top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(f));
+  }
+  return top;
 }
 
 // A warp's 64 rows of 16 columns of the caller's tensor (columns >= have, a multiple of 4, and rows >= n are zeros).

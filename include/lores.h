@@ -378,10 +378,10 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * 16-bit inputs are exact down to 2^-31 of that entry (k: 2^-25), fp32 ones have 22 bits down to 2^-16
  * of it (k: 2^-10) and are off by at most 2^-39 of it (k: 2^-33) below.  A token's output is as exact
  * for a small q as for a large one; a token's gradients carry the errors of their chunk's.
- * An infinity or NaN in a token's
- * inputs may turn the outputs of the whole 64-token chunk that holds it (counted from the
- * sequence's start), and what follows (in the backward pass also what comes before), to NaN,
- * for the heads that read them; other heads and sequences are not touched. */
+ * An infinity or NaN in a token's inputs or in a state may turn the outputs of the whole 64-token
+ * chunk that holds it, and what follows (in the backward pass also what comes before), to NaN,
+ * for the heads that read them; an output that stays finite is the recurrence's.  Other heads and
+ * sequences are not touched. */
 typedef struct {
     int32_t n_seq;      /* sequences, >= 1                                                   */
     int64_t total;      /* tokens of all of them, 0 .. 2^31 - 1                              */

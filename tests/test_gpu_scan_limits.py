@@ -238,3 +238,57 @@ def test_16_bit_inputs_are_exact_far_below_the_chunks_largest():
     ro, _ = forward64(x, offs, 0)
     # token 1 on: columns other than the large one's
     assert rel(o[1:, :, 1:], ro[1:, :, 1:]) <= tol(BF16)
+
+
+def right_or_not_finite(got, want, t):
+    """Nothing is a finite number where the recurrence's result is not finite, or another than it."""
+    fine = torch.isfinite(want)
+    assert not torch.isfinite(got[~fine]).any()
+    both = fine & torch.isfinite(got)
+    if both.any():
+        assert rel(got[both], want[both]) <= t
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("delta", [0, 1])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "log_alpha", "state", "d_o", "d_state"])
+def test_a_value_that_is_not_finite(name, value, delta, dtype):
+    x, offs = inputs([150, 70], 4, 2, 64, 36, dtype, seed=251)
+    d_o, d_S = normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8)
+    clean, clean_S = forward64(x, offs, delta)
+    if name == "log_alpha":
+        value = float("nan")                                 # (infinities: -inf drops the state, +inf is outside the domain)
+    if name == "d_o":
+        d_o[90, 1, 5] = value
+    elif name == "d_state":
+        d_S[0, 1, 5, 7] = value
+    elif name == "state":
+        x["state"][0, 1, 5, 7] = value
+    else:
+        x[name][(90, 1) if name in ("beta", "log_alpha") else (90, 0 if name in "qk" else 1, 5)] = value
+    c = Call(x, offs, delta, dtype)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, delta)
+    right_or_not_finite(o, ro, tol(dtype, True))
+    right_or_not_finite(S, rS, FP32)
+    # chunks before it, other sequences and heads that do not read it are as they were; and so are the tokens of its
+    # chunk that it does not reach, where it is q
+    heads = [2, 3] if name in "qk" else [0, 2, 3]
+    assert rel(o[:, heads], clean[:, heads]) <= tol(dtype, True) and rel(S[:, heads], clean_S[:, heads]) <= FP32
+    assert rel(o[150:], clean[150:]) <= tol(dtype, True) and rel(S[1], clean_S[1]) <= FP32
+    if name != "state":
+        assert rel(o[:64], clean[:64]) <= tol(dtype, True)
+    if name in ("q", "d_o", "d_state"):
+        others = [t for t in range(220) if t != 90 or name != "q"]
+        assert rel(o[others], clean[others]) <= tol(dtype, True) and rel(S, clean_S) <= FP32
+    if name in ("v", "state"):
+        rows = [r for r in range(36) if r != 5]
+        assert rel(o[:, :, rows], clean[:, :, rows]) <= tol(dtype, True)
+    got, want = c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S)
+    for n in NAMES:
+        t = tol(dtype) if n in "qkv" else 4 * FP32 if n in ("log_alpha", "beta") else FP32
+        right_or_not_finite(got[n], want[n], t)
+        last = got[n][1:] if n == "state" else got[n][150:]
+        assert torch.isfinite(last).all() and rel(last, want[n][1:] if n == "state" else want[n][150:]) <= t, n
+    assert c.check() == c.L.LORES_OK
