@@ -119,6 +119,7 @@ unsigned long long layout(const Shape &s, bool backward, uint8_t *ws, ScanParams
   p.khat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
   p.qhat = w.take<__half>((unsigned long long)s.n_slots * c.heads_qk * s.np * kChunk * c.d_k);
   p.gates = w.take<float>(recs * kGateFloats);
+  p.seqs = w.take<longlong2>(s.c.n_seq);
   if (!backward || !c.delta) p.pp = w.take<__half>(recs * sq);
   if (c.delta) {
     p.tm = w.take<__half>(recs * sq);
@@ -283,10 +284,10 @@ cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t s
   const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
   p.rb = walk_blocks(s, kind);
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
-  p.stages = 2 * l.bytes + p.rb * l.tail + 32 <= kMaxShared ? 2 : 1;
+  p.stages = 2 * l.bytes + p.rb * l.tail + kWalkEnd <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],
                 dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * p.rb * (nh + kSideWarps + 1),
-                p.stages * l.bytes + p.rb * l.tail + 32, st, c.device, p, early_walk(s, kind),
+                p.stages * l.bytes + p.rb * l.tail + kWalkEnd, st, c.device, p, early_walk(s, kind),
                 raised[wi][s.np - 1][c.delta][kind]);
 }
 
@@ -413,7 +414,7 @@ lores_status lores_scan_backward(const lores_scan_config *cfg, const void *q, co
   if (e == cudaSuccess && p.parts && any) {
     p.dq = dq;
     p.dk = dk;
-    const long long n = c.total * c.heads_qk * (c.d_k / 4) * 2;
+    const long long n = (long long)s.n_slots * kChunk * c.heads_qk * (c.d_k / 4) * 2;
     const unsigned blocks = (unsigned)std::min<long long>((n + 255) / 256, 32ll * sm_count(c.device));
     const int dk = c.d_k;
     e = launch_early(reinterpret_cast<const void *>(&scan_shared_kernel), dim3(blocks), 256, 0, cs, early_grads(s), &p,

@@ -80,6 +80,7 @@ struct ScanParams {
   void *o;                             // forward: o; backward: d_o (read)
   unsigned *flag;
   // workspace
+  longlong2 *seqs;                     // [n_seq] first token, tokens (written by scan_prep)
   longlong2 *slot_tokens;              // [n_slots] first token, tokens (written by scan_prep for the backward pass)
   // records of one (slot, head); khat, qhat of one (slot, q/k head)
   float *gates;                        // kGateFloats
@@ -130,42 +131,82 @@ __device__ __forceinline__ bool seq_range(const ScanParams &p, int i, long long 
 // the sequences is needed.
 __device__ __forceinline__ int slot_base(long long start, int i) { return (int)(start / kChunk) + i; }
 
-// The first token of a slot's chunk and its number of tokens (0: the slot is not used).
-__device__ __forceinline__ int slot_tokens(const ScanParams &p, int slot, long long &token0) {
-  int lo = 0, hi = p.n_seq - 1;
+// Where some offsets do not fit, the sequences that do need not lie in order.  Whether sequence i starts behind the ends
+// of all earlier ones that fit (else it is taken as empty, since its slots could be another's).  All threads of a block.
+__device__ __forceinline__ bool in_order(const ScanParams &p, int i, long long start) {
+  int over = 0;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) {
+    long long s;
+    int n;
+    if (seq_range(p, j, s, n)) over |= s + n > start;
+  }
+  return !__syncthreads_or(over);
+}
+
+// The first token of a slot's chunk and its number of tokens (0: the slot is not used).  All threads of a block, which
+// looks every sequence over: a bisection would trust offsets that do not fit.  `bad`: some do not.  part: one word per warp.
+__device__ __forceinline__ int slot_tokens(const ScanParams &p, int slot, long long &token0, bool &bad, unsigned *part) {
+  bad = false;
   if (!p.offsets) {
     const long long each = p.total / p.n_seq;
+    int lo = 0, hi = p.n_seq - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (slot_base(each * mid, mid) <= slot) lo = mid; else hi = mid - 1;
     }
-  } else {
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (slot_base(__ldg(p.offsets + mid), mid) <= slot) lo = mid; else hi = mid - 1;
-    }
+    const long long first = (long long)(slot - slot_base(each * lo, lo)) * kChunk;
+    if (first < 0 || first >= each) return 0;
+    token0 = each * lo + first;
+    return (int)min((long long)kChunk, each - first);
   }
-  long long start;
-  int len;
-  seq_range(p, lo, start, len);
-  const long long first = (long long)(slot - slot_base(start, lo)) * kChunk;
-  if (first < 0 || first >= len) return 0;
-  token0 = start + first;
-  return (int)min((long long)kChunk, len - first);
+  constexpr unsigned NONE = 0xFFFFFFFFu;
+  for (int lo = 0;;) {
+    unsigned mine = NONE;
+    int wrong = 0;
+    for (int i = lo + (int)threadIdx.x; i < p.n_seq; i += blockDim.x) {
+      long long s;
+      int n;
+      wrong |= !seq_range(p, i, s, n);
+      const long long first = (long long)(slot - slot_base(s, i)) * kChunk;
+      if (first >= 0 && first < n) mine = min(mine, (unsigned)i);
+    }
+    mine = __reduce_min_sync(0xFFFFFFFFu, mine);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
+    bad |= __syncthreads_or(wrong) != 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) mine = min(mine, part[w]);
+    if (mine == NONE) return 0;
+    long long start;
+    int len;
+    seq_range(p, (int)mine, start, len);
+    if (bad && !in_order(p, (int)mine, start)) {
+      lo = (int)mine + 1;
+      continue;
+    }
+    const long long first = (long long)(slot - slot_base(start, (int)mine)) * kChunk;
+    token0 = start + first;
+    return (int)min((long long)kChunk, len - first);
+  }
 }
 
-// Whether a token belongs to a sequence (the others' rows are left as they were).
-__device__ __forceinline__ bool token_used(const ScanParams &p, long long tok) {
-  if (!p.offsets) return true;
-  int lo = 0, hi = p.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.offsets + mid) <= tok) lo = mid; else hi = mid - 1;
+// One block of scan_prep leaves the sequences as they are taken and the verdict in the workspace.
+__device__ __forceinline__ void keep_sequences(const ScanParams &p, bool bad) {
+  if (bad) {
+    for (int i = 0; i < p.n_seq; ++i) {
+      long long s;
+      int n;
+      seq_range(p, i, s, n);
+      if (!in_order(p, i, s)) n = 0;
+      if (threadIdx.x == 0) p.seqs[i] = make_longlong2(s, n);
+    }
+  } else {
+    for (int i = threadIdx.x; i < p.n_seq; i += blockDim.x) {
+      long long s;
+      int n;
+      seq_range(p, i, s, n);
+      p.seqs[i] = make_longlong2(s, n);
+    }
   }
-  long long start;
-  int len;
-  seq_range(p, lo, start, len);
-  return tok >= start && tok < start + len;
+  if (threadIdx.x == 0) *p.flag = bad ? kFlagOffsets : 0u;
 }
 
 // One block of a launch looks every sequence over and leaves the verdict in the workspace.
@@ -556,9 +597,10 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   const int slot = blockIdx.x, head0 = blockIdx.y * p.hpc;
   launch_next();
-  if (slot == 0 && head0 == 0) check_offsets(p);
   long long token0 = 0;
-  const int n = slot_tokens(p, slot, token0);
+  bool bad;
+  const int n = slot_tokens(p, slot, token0, bad, red + 12);
+  if (slot == 0 && head0 == 0) keep_sequences(p, bad);
   if (BWD && head0 == 0 && tid == 0) p.slot_tokens[slot] = make_longlong2(token0, n);
   if (n == 0) return;
   const int qh = head0 / p.share, hq = p.H / p.share;
@@ -1007,6 +1049,7 @@ struct WalkLayout {
   int kt, k, q, tm, pp, v, gates, bytes;         // byte offsets inside one stage
   int part, side, plus, last, planes, tops, tail;   // behind the stages, one record per block of rows
 };
+constexpr int kWalkEnd = 48;             // behind the blocks' records: two barriers, `stop`, the sequence
 // A block's 64 token rows of V (or dO): as they come, then as fp16 planes in tiles, then (output) again as
 // they go.
 __host__ __device__ constexpr int tile_bytes(int np) { return kChunk * 16 * 2 * np; }
@@ -1265,10 +1308,6 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   const int blk = loader ? warp - first_load : side ? (warp - first_side) / kSideWarps : warp / NH;
   const int h = loader ? 0 : side ? (warp - first_side) % kSideWarps : NH == 1 ? 0 : warp % NH;
   const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, KIND);
-  long long start;
-  int len;
-  seq_range(p, seq, start, len);
-  const int chunks = (len + kChunk - 1) / kChunk, base = slot_base(start, seq);
   const int brow = row0 + blk * 16, r0 = brow + g, c0 = h * DKH;
   const bool live = brow < p.dvp;
   uint8_t *tail = smem + p.stages * l.bytes + blk * l.tail;
@@ -1278,8 +1317,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   // bits of the largest magnitudes: [2 (i & 1) + h] of the state warps' columns at the start of the i-th chunk,
   // [4 + stage] of the rows of V or dO, [6 + h] of E or R (forward: by the state warps, else of the side warps' tokens)
   unsigned *tops = reinterpret_cast<unsigned *>(tail + l.tops);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * l.bytes + p.rb * l.tail);   // one per stage, `stop`, the sequence
   int *stop = reinterpret_cast<int *>(bars + 2);
+  volatile longlong2 *placed = reinterpret_cast<volatile longlong2 *>(bars + 4);
   const Lane<DK> ld(lane);
   const Lane<16> lv(lane);
   const int X = 1 + 3 * blk, Y = X + 1, Z = X + 2, sides = Z + 3 * kReverseBlocks;
@@ -1302,19 +1342,26 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   }
   const int by = p.stages == 2 ? 1 : 0;
   auto stage_of = [&](int c) { return smem + (c & by) * l.bytes; };
-  auto fetch = [&](int c) {
-    const long long token0 = start + (long long)c * kChunk;
-    if (blk == 0 && lane == 0) fetch_matrices<DK, NP, DELTA, KIND>(p, stage_of(c), bars + (c & by), l, base + c, head);
-    if (live)
-      fetch_rows<NP>(stage_of(c) + l.v + blk * tile_bytes(NP), REV ? p.o : p.v, REV ? p.o_stride : p.v_stride, token0,
-                     head * p.d_v + brow, min(kChunk, len - c * kChunk), p.d_v - brow, REV ? p.o16 : p.v16, lane);
-    cp_commit();
-  };
   // The reverse walk reads nothing of the recomputation, which has waited for scan_prep: it may run beside it, on the
   // SMs that it leaves free, and waits for it at its own end.
   if (!REV) wait_before();
   launch_next();
-  if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0);
+  const longlong2 range = __ldcg(p.seqs + seq);
+  const int chunks = ((int)range.y + kChunk - 1) / kChunk;
+  if (tid == 0) {                        // (kept there and not in registers, of which four blocks of rows have none left)
+    placed->x = range.x;
+    placed->y = range.y;
+  }
+  auto fetch = [&](int c, longlong2 of) {
+    const long long token0 = of.x + (long long)c * kChunk;
+    if (blk == 0 && lane == 0)
+      fetch_matrices<DK, NP, DELTA, KIND>(p, stage_of(c), bars + (c & by), l, slot_base(of.x, seq) + c, head);
+    if (live)
+      fetch_rows<NP>(stage_of(c) + l.v + blk * tile_bytes(NP), REV ? p.o : p.v, REV ? p.o_stride : p.v_stride, token0,
+                     head * p.d_v + brow, min(kChunk, (int)of.y - c * kChunk), p.d_v - brow, REV ? p.o16 : p.v16, lane);
+    cp_commit();
+  };
+  if (loader && chunks > 0) fetch(REV ? chunks - 1 : 0, range);
   for (int i0 = 0; i0 < chunks; ++i0) {
     const int c = REV ? chunks - 1 - i0 : i0, next = REV ? c - 1 : c + 1;
     uint8_t *st = stage_of(c);
@@ -1334,15 +1381,15 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     }
     __syncthreads();
     if (*stop) break;
-    if (by && loader && i0 + 1 < chunks) fetch(next);
+    if (by && loader && i0 + 1 < chunks) fetch(next, make_longlong2(placed->x, placed->y));
     const uint32_t kt = smem_addr(st + l.kt), sk = smem_addr(st + l.k), sq = smem_addr(st + l.q),
                    tm = smem_addr(st + l.tm), pp = smem_addr(st + l.pp), sv = smem_addr(tile);
     // (forward: rows kGateE .. kGateP, else kGateC .. kGateEk)
     const float *eC = reinterpret_cast<const float *>(st + l.gates), *eG = FWD ? eC : eC + kChunk, *wk = eG + kChunk,
                 *ek = wk + kChunk, *rowP = ek + kChunk, *scalars = eC + 4 * kChunk;
     const float qscale = scalars[1], bkscale = scalars[2] * scalars[0];
-    const long long rec = (long long)(base + c) * p.H + head;
-    const int n = min(kChunk, len - c * kChunk);
+    const long long start = placed->x, rec = (long long)(slot_base(start, seq) + c) * p.H + head;
+    const int n = min(kChunk, (int)placed->y - c * kChunk);
     if (loader || !live) {
     } else {
       // scales: of the state, of V (or dO, which takes the scale of Q that the planes of Q and Z lack; Z those of K and
@@ -1776,7 +1823,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     }
     if (!by) {
       __syncthreads();
-      if (loader && i0 + 1 < chunks) fetch(next);
+      if (loader && i0 + 1 < chunks) fetch(next, make_longlong2(placed->x, placed->y));
     }
   }
   if (live && !side && !loader && KIND != kRecompute && !*stop) {
@@ -2359,12 +2406,14 @@ static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParam
                                                                  const float *parts_k, int dk) {
   wait_before();
   const int hq = p.H / p.share, per = hq * (dk / 4);
-  const long long n = p.total * per, all = 2 * n;
+  const long long n = (long long)p.n_slots * kChunk * per, all = 2 * n;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const bool second = i >= n;
-    const long long j = second ? i - n : i, tok = j / per;
+    const long long j = second ? i - n : i, row = j / per;
     const int r = (int)(j % per), h = r / (dk / 4), c = (r % (dk / 4)) * 4;
-    if (!token_used(p, tok)) continue;
+    const longlong2 tokens = p.slot_tokens[row / kChunk];
+    if (row % kChunk >= tokens.y) continue;
+    const long long tok = tokens.x + row % kChunk;
     const float *src = (second ? parts_k : parts_q) + (tok * p.H + (long long)h * p.share) * dk + c;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int m = 0; m < p.share; ++m) {

@@ -412,7 +412,9 @@ lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward
  *   offsets    device int32 [n_seq + 1], or NULL: n_seq sequences of total / n_seq tokens.
  *              A sequence that does not satisfy 0 <= offsets[i] <= offsets[i+1] <= total with
  *              at most max_len tokens is taken as empty and reported by
- *              lores_scan_check_errors; sequences must not overlap.
+ *              lores_scan_check_errors; the others come out as if alone.  (Beside such offsets a
+ *              sequence that starts before the end of an earlier one may be taken as empty too.)
+ *              Sequences must not overlap.
  *   state_in   [n_seq, H, d_v, d_k] fp32, or NULL for zero states
  *   o          [total, H, d_v] of dtype; rows of tokens in no sequence are left as they were
  *   state_out  as state_in, may be the same buffer; NULL: not wanted.  An empty sequence's

@@ -292,3 +292,74 @@ def test_a_value_that_is_not_finite(name, value, delta, dtype):
         last = got[n][1:] if n == "state" else got[n][150:]
         assert torch.isfinite(last).all() and rel(last, want[n][1:] if n == "state" else want[n][150:]) <= t, n
     assert c.check() == c.L.LORES_OK
+
+
+def one_by_one(x, ranges, delta, d_o, d_S, dtype):
+    """Forward and backward of each sequence (begin, end; None: empty) by itself."""
+    out = []
+    for i, r in enumerate(ranges):
+        if r is None:
+            out.append(None)
+            continue
+        y = {n: (v[r[0]:r[1]] if n != "state" else v[i:i + 1]) for n, v in x.items()}
+        offs = [0, r[1] - r[0]]
+        c = Call(y, offs, delta, dtype)
+        o, S = (t.clone() for t in c.forward())
+        out.append((o, S, {n: t.clone() for n, t in c.backward(d_o[r[0]:r[1]], d_S[i:i + 1]).items()}))
+    return out
+
+
+SPIKES = [([0, 999, 170, 240], [None, None, (170, 240)]),
+          ([0, 80, 10 ** 6, 170, 240], [(0, 80), None, None, (170, 240)]),
+          ([0, -7, 100, 240], [None, None, (100, 240)]),
+          ([64, 10, 10, 200, 2 ** 31 - 1], [None, (10, 10), (10, 200), None]),
+          # sequences that start before the end of one that fits are taken as empty too
+          ([100, 240, 0, 100], [(100, 240), None, None]),
+          ([0, 80, 75, 240], [(0, 80), None, None])]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("delta,heads_qk", [(1, 1), (0, 2)])
+@pytest.mark.parametrize("bad,ranges", SPIKES, ids=[str(s[0]) for s in SPIKES])
+def test_sequences_beside_offsets_that_do_not_fit(bad, ranges, delta, heads_qk, dtype):
+    """Each sequence that fits comes out as if alone, and the others' rows and states stay."""
+    N = len(ranges)
+    x, _ = inputs([240 // N] * N, 2, heads_qk, 32, 16, dtype, seed=261, trail=240 - 240 // N * N)
+    d_o, d_S = normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8)
+    c = Call(x, None, delta, dtype, device_offsets=bad)
+    c.offs = bad
+    o, S = c.forward()
+    assert c.check() == c.L.LORES_ERR_INVALID_ARG
+    got = c.backward(d_o, d_S)
+    assert c.check() == c.L.LORES_ERR_INVALID_ARG
+    used = torch.zeros(240, dtype=torch.bool)
+    for i, (r, want) in enumerate(zip(ranges, one_by_one(x, ranges, delta, d_o, d_S, dtype))):
+        if r is None:
+            assert torch.equal(S[i], c.state[i]) and torch.equal(got["state"][i], d_S[i].float())
+            continue
+        used[r[0]:r[1]] = True
+        assert torch.equal(o[r[0]:r[1]], want[0]) and torch.equal(S[i], want[1][0])
+        for n in NAMES:
+            mine = got[n][i:i + 1] if n == "state" else got[n][r[0]:r[1]]
+            assert torch.equal(mine, want[2][n]), n
+    free = (~used).cuda()
+    assert (o[free] == 777).all()
+    for n in NAMES[:5]:
+        assert (got[n][free] == 777).all(), n
+
+
+def test_many_sequences_and_one_bad_offset():
+    N, each = 700, 3
+    x, offs = inputs([each] * N, 1, 1, 16, 4, F32, seed=262)
+    whole = Call(x, offs, 1, F32)                            # (max_len 0: the chunk kernels)
+    o, S = (t.clone() for t in whole.forward())
+    bad = list(offs)
+    bad[300] = 10 ** 9
+    c = Call(x, offs, 1, F32, device_offsets=bad)
+    c.work = whole.work
+    o2, S2 = c.forward()
+    assert c.check() == c.L.LORES_ERR_INVALID_ARG
+    keep = [i for i in range(N) if i not in (299, 300)]
+    assert torch.equal(S2[keep], S[keep]) and torch.equal(S2[299:301], c.state[299:301])
+    rows = [t for i in keep for t in range(offs[i], offs[i + 1])]
+    assert torch.equal(o2[rows], o[rows]) and (o2[offs[299]:offs[301]] == 777).all()
