@@ -163,7 +163,11 @@ __global__ void __launch_bounds__(kPoolThreads) write_states_kernel(const PoolPa
     const bool bad = requantize16<LPR>(x[r], bits == 32 ? 8 : bits, lpg, lane, tkey, n0, p.stochastic, words, s_new,
                                        f.store);
     if (row >= p.d_v) continue;
-    if (bad && lir == 0) atomicOr(p.flag, kFlagNonFinite);
+    // fp32 heads copy a row whatever its size: only what is not finite is reported (0 times it is NaN)
+    float zero = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero = __fmaf_rn(x[r][e], 0.0f, zero);
+    if (bits == 32 ? zero != 0.0f : bad && lir == 0) atomicOr(p.flag, kFlagNonFinite);
     uint8_t *rowp = codes + (size_t)row * f.rowb;
     if (!LORES_IN(p, kRgCodes, rowp, f.rowb)) continue;
     if (bits == 32) {

@@ -261,7 +261,8 @@ lores_status lores_load_state(lores_handle *h, const float *S, uint64_t step, vo
  * lores_write_states quantizes with the step's quantizer and the dither of `step` (the slot's
  * result is that of lores_load_state, bit for bit); where a slot is named twice the later
  * entry counts; a row that holds inf, NaN or a magnitude above 2^100 is stored as zero and
- * raises the sticky NONFINITE flag (fp32 heads copy it).  lores_read_states writes code * scale,
+ * raises the sticky NONFINITE flag (fp32 heads copy it, and inf and NaN alone raise the flag).
+ * lores_read_states writes code * scale,
  * rounded to dtype.  The other slots are untouched.  Asynchronous, allocation-free, capturable.
  * Errors: INVALID_ARG (NULL or misaligned pointers, n outside 0 .. B, dtype); UNSUPPORTED
  * (lores_write_states on a key-axis handle); CUDA. */

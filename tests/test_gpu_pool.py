@@ -222,3 +222,24 @@ def test_slots_beyond_32_bits():
         assert L.lores_check_errors(h) == L.LORES_OK
     finally:
         L.lores_destroy(h)
+
+
+def test_fp32_heads_report_what_is_not_finite_alone():
+    """An fp32 head copies a row whatever its size; only infinities and NaN are reported."""
+    L = lib()
+    wl = synth.Workload("p", B=2, H=2, d_k=32, d_v=24, steps=1)
+    g = GpuRun(wl, [32, 8], seed=1)
+    try:
+        S = states(2, 2, 24, 32)
+        S[1, 0, 3, 5] = 2.0 ** 110
+        L.lores_write_states(g.h, 2, None, S, 5)
+        assert torch.equal(g.dequant()[:, 0], S[:, 0]) and g.check() == L.LORES_OK
+        S[1, 0, 3, 5] = float("inf")
+        L.lores_write_states(g.h, 2, None, S, 5)
+        assert torch.equal(g.dequant()[:, 0], S[:, 0]) and g.check() == L.LORES_ERR_NONFINITE
+        S[1, 0, 3, 5] = 1.0
+        S[0, 1, 2, 2] = 2.0 ** 110                          # a quantized head stores such a row as zero
+        L.lores_write_states(g.h, 2, None, S, 5)
+        assert (g.dequant()[0, 1, 2] == 0).all() and g.check() == L.LORES_ERR_NONFINITE
+    finally:
+        g.close()
