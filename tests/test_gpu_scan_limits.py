@@ -363,3 +363,71 @@ def test_many_sequences_and_one_bad_offset():
     assert torch.equal(S2[keep], S[keep]) and torch.equal(S2[299:301], c.state[299:301])
     rows = [t for i in keep for t in range(offs[i], offs[i + 1])]
     assert torch.equal(o2[rows], o[rows]) and (o2[offs[299]:offs[301]] == 777).all()
+
+
+def test_several_heads_of_a_group_in_one_block_with_the_delta_rule():
+    """Enough chunks that the preparation takes two heads (and more) that share q and k."""
+    for H, Hq in ((32, 16), (32, 4)):
+        x, offs = inputs([1300, 33, 1290], H, Hq, 16, 4, BF16, seed=271)
+        c = Call(x, offs, 1, BF16)
+        o, S = c.forward()
+        ro, rS = forward64(x, offs, 1)
+        assert rel(o, ro) <= tol(BF16) and rel(S, rS) <= FP32
+
+
+def test_gradients_of_several_heads_of_a_group_with_the_delta_rule():
+    x, offs = inputs([330, 1, 300], 128, 2, 16, 4, F32, seed=272)
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    got = Call(x, offs, 1, F32).backward(d_o, d_S)
+    check_gradients(got, backward64(x, offs, 1, d_o, d_S), F32)
+
+
+GUARD = 4096                                                 # bytes before and behind each buffer
+
+
+class Guarded(Call):
+    """A call whose buffers lie between guard bands, the workspace of the exact size among them."""
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        self.bands = []
+        for n in ("q", "k", "v", "la", "be", "state", "o", "state_out"):
+            setattr(self, n, self.guard(getattr(self, n)))
+
+    def guard(self, t):
+        size = t.numel() * t.element_size()
+        buf = torch.full((GUARD + (size + 15) // 16 * 16 + GUARD,), 0xA5, dtype=torch.uint8, device="cuda")
+        inner = buf[GUARD:GUARD + size].view(t.dtype).view(t.shape)
+        inner.copy_(t)
+        self.bands.append((buf, size))
+        return inner
+
+    def workspace(self, backward):
+        n = self.L.lores_scan_workspace(self.cfg, backward)
+        self.work = self.guard(torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+        return self.work
+
+    def run_backward(self, d_o, d_S):
+        self.backward(d_o, d_S)                              # (makes the gradients' buffers)
+        names = ("d_o", "d_state_out", "dq", "dk_", "dv_", "dla", "dbe", "ds")
+        a = [self.guard(getattr(self, n)) for n in names]
+        self.L.lores_scan_backward(self.cfg, self.q, self.k, self.v, self.la, self.be, self.offsets, self.state,
+                                   *a, self.workspace(True))
+
+    def untouched(self):
+        for buf, size in self.bands:
+            assert (buf[:GUARD] == 0xA5).all() and (buf[GUARD + size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("lens,H,Hq,dk,dv,delta,dtype,pad,max_len", [
+    ([1], 1, 1, 16, 4, 1, F32, 0, 0), ([63, 1, 64, 0, 130], 3, 3, 64, 20, 1, F32, 0, 0),
+    ([17, 200, 5], 4, 2, 128, 100, 1, BF16, 0, 0), ([33, 128, 129], 4, 1, 32, 36, 1, F16, 8, 0),
+    ([70, 257], 4, 4, 128, 64, 0, BF16, 0, 0), ([320], 2, 2, 32, 260, 0, BF16, 8, 0),
+    ([100, 31], 8, 1, 128, 12, 0, F32, 4, 0), ([5, 0, 9], 4, 2, 128, 36, 1, BF16, 4, 9), ([40], 2, 1, 256, 20, 1, F32, 0, 0)])
+def test_nothing_is_written_outside_the_buffers(lens, H, Hq, dk, dv, delta, dtype, pad, max_len):
+    x, offs = inputs(lens, H, Hq, dk, dv, dtype, seed=281)
+    c = Guarded(x, offs, delta, dtype, pad, max_len=max_len)
+    c.forward()
+    if dk < 256:
+        c.run_backward(normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8))
+    c.untouched()
