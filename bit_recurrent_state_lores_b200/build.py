@@ -10,9 +10,9 @@ single/multi-token, and one key-axis family per key width) and of the state scan
 planes) build in parallel, one nvcc process per CPU core, then link.
 
 --checked builds liblores_checked.so instead: the same sources compiled with
-LORES_INDEX_CHECKS, so that every global access of the kernels is checked against the
-extent of its buffer first (include/lores.h, lores_index_checked); a debugging build, not
-the product.
+LORES_INDEX_CHECKS, so that every global access of the decode, loader, dequantizer and slot
+kernels is checked against the extent of its buffer first (include/lores.h,
+lores_index_checked); the state scan has no such checks.  A debugging build, not the product.
 
 No fast-math: the kernels' fp32 rounding is part of the state format, so every
 rounding-sensitive operation is written with explicit round-to-nearest intrinsics

@@ -146,8 +146,8 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, unsigned by
 }
 
 // -------------------------------------------------------------------------------------
-// index-checked build (LORES_INDEX_CHECKS): every global access of the decode, loader and
-// dequantizer kernels names the buffer it belongs to and its byte count; the access runs
+// index-checked build (LORES_INDEX_CHECKS): every global access of the decode, loader,
+// dequantizer and slot kernels names the buffer it belongs to and its byte count; the access runs
 // only if it lies inside that buffer's extent as the host declared it for the launch.
 // Otherwise the kernel raises kFlagIndex and the buffer's bit and skips the access (a
 // skipped bulk copy leaves its barrier short, so the wait runs out and TIMEOUT is raised

@@ -317,13 +317,14 @@ lores_status lores_set_fault_injection(lores_handle *h, int32_t seq, int32_t uni
 
 /* Index-checked build (no counterpart on the pages; a stand-in for a memory sanitizer).
  * liblores_checked.so is this library compiled with LORES_INDEX_CHECKS: every global
- * access of the decode, loader and dequantizer kernels (bulk copies, their shared-memory
- * destinations, loads, stores) is first checked against the extent of the buffer it
+ * access of the decode, loader, dequantizer and slot kernels (bulk copies, their shared-memory
+ * destinations, loads, stores; the state scan's kernels have no checks) is first checked against the extent of the buffer it
  * belongs to, as the host declares it for the launch:
  *   0 code pool (B * seq_code_bytes)   1 scales (scale_count floats)
  *   2 q, 3 k (T*B*H*d_k floats)        4 v (T*B*H*d_v)     5 alpha (T*B*H, d_k if diagonal)
  *   6 beta (T*B*H)                     7 o (T*B*H*d_v)     8 the fp32 state of
- *   lores_load_state / lores_dequant_state (B*H*d_v*d_k floats)
+ *   lores_load_state / lores_dequant_state (B*H*d_v*d_k floats), the caller's states of
+ *   lores_write_states / lores_read_states
  * An access outside its buffer is skipped and raises the handle's INDEX flag together
  * with bit 8 + the buffer's number (bit 17: a copy outside the launch's shared memory);
  * a skipped copy leaves its barrier short, so that warp's wait runs out as well.  Outputs
