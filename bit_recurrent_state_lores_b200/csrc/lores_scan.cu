@@ -251,6 +251,11 @@ cudaError_t run_prep(const Shape &s, bool backward, ScanParams p, cudaStream_t s
   const lores_scan_config &c = s.c;
   static std::atomic<unsigned long long> raised[4][2][2][2];
   const int wi = width_index(c.d_k);
+  if (c.n_seq > kFewSeqs) {
+    scan_sequences_kernel<<<1, kSeqThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   // as many of the heads that share q and k per CTA as leave every SM its four CTAs
   p.hpc = 1;
   for (int d = 2; d <= p.share; ++d)

@@ -80,7 +80,7 @@ struct ScanParams {
   void *o;                             // forward: o; backward: d_o (read)
   unsigned *flag;
   // workspace
-  longlong2 *seqs;                     // [n_seq] first token, tokens (written by scan_prep)
+  longlong2 *seqs;                     // [n_seq] first token, tokens (written by scan_prep or scan_sequences)
   longlong2 *slot_tokens;              // [n_slots] first token, tokens (written by scan_prep for the backward pass)
   // records of one (slot, head); khat, qhat of one (slot, q/k head)
   float *gates;                        // kGateFloats
@@ -131,8 +131,15 @@ __device__ __forceinline__ bool seq_range(const ScanParams &p, int i, long long 
 // the sequences is needed.
 __device__ __forceinline__ int slot_base(long long start, int i) { return (int)(start / kChunk) + i; }
 
-// Where some offsets do not fit, the sequences that do need not lie in order.  Whether sequence i starts behind the ends
-// of all earlier ones that fit (else it is taken as empty, since its slots could be another's).  All threads of a block.
+// Where some offsets do not fit, the sequences that do need not lie in order.  One that starts before the end of an
+// earlier one that fits is taken as empty, since its slots could be another's.
+//
+// Up to kFewSeqs sequences every block of scan_prep looks them all over for its slot (a bisection would trust offsets that
+// do not fit); more are put in order first, by scan_sequences, and scan_prep bisects what that leaves.  (16384 sequences of
+// 64 tokens, 2 heads of 32 x 32: looked over by every block 4345 us; 2048 of them, 4 heads: 476.)
+constexpr int kFewSeqs = 256, kSeqThreads = 1024;
+
+// Whether sequence i starts behind the ends of all earlier ones that fit.  All threads of a block.
 __device__ __forceinline__ bool in_order(const ScanParams &p, int i, long long start) {
   int over = 0;
   for (int j = threadIdx.x; j < i; j += blockDim.x) {
@@ -143,21 +150,22 @@ __device__ __forceinline__ bool in_order(const ScanParams &p, int i, long long s
   return !__syncthreads_or(over);
 }
 
-// The first token of a slot's chunk and its number of tokens (0: the slot is not used).  All threads of a block, which
-// looks every sequence over: a bisection would trust offsets that do not fit.  `bad`: some do not.  part: one word per warp.
+// The first token of a slot's chunk and its number of tokens (0: the slot is not used).  All threads of a block.
+// `bad`: some offsets do not fit (few sequences only).  part: one word per warp.
 __device__ __forceinline__ int slot_tokens(const ScanParams &p, int slot, long long &token0, bool &bad, unsigned *part) {
   bad = false;
-  if (!p.offsets) {
+  if (!p.offsets || p.n_seq > kFewSeqs) {
     const long long each = p.total / p.n_seq;
     int lo = 0, hi = p.n_seq - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (slot_base(each * mid, mid) <= slot) lo = mid; else hi = mid - 1;
+      if (slot_base(p.offsets ? __ldg(&p.seqs[mid].x) : each * mid, mid) <= slot) lo = mid; else hi = mid - 1;
     }
-    const long long first = (long long)(slot - slot_base(each * lo, lo)) * kChunk;
-    if (first < 0 || first >= each) return 0;
-    token0 = each * lo + first;
-    return (int)min((long long)kChunk, each - first);
+    const long long start = p.offsets ? __ldg(&p.seqs[lo].x) : each * lo, len = p.offsets ? __ldg(&p.seqs[lo].y) : each;
+    const long long first = (long long)(slot - slot_base(start, lo)) * kChunk;
+    if (first < 0 || first >= len) return 0;
+    token0 = start + first;
+    return (int)min((long long)kChunk, len - first);
   }
   constexpr unsigned NONE = 0xFFFFFFFFu;
   for (int lo = 0;;) {
@@ -188,7 +196,7 @@ __device__ __forceinline__ int slot_tokens(const ScanParams &p, int slot, long l
   }
 }
 
-// One block of scan_prep leaves the sequences as they are taken and the verdict in the workspace.
+// One block of scan_prep leaves few sequences as they are taken and the verdict in the workspace.
 __device__ __forceinline__ void keep_sequences(const ScanParams &p, bool bad) {
   if (bad) {
     for (int i = 0; i < p.n_seq; ++i) {
@@ -207,6 +215,41 @@ __device__ __forceinline__ void keep_sequences(const ScanParams &p, bool bad) {
     }
   }
   if (threadIdx.x == 0) *p.flag = bad ? kFlagOffsets : 0u;
+}
+
+// The same for many, by one block before scan_prep: a running maximum of the ends.  An empty sequence that does not fit
+// starts there, so that the slots of all begin in order.
+static __global__ void __launch_bounds__(kSeqThreads) scan_sequences_kernel(const ScanParams p) {
+  __shared__ long long tops[kSeqThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long before = 0;                  // the largest end of the sequences of the rounds before
+  int bad = 0;
+  for (int i0 = 0; i0 < p.n_seq; i0 += kSeqThreads) {
+    const int i = i0 + tid;
+    long long start = 0;
+    int len = 0;
+    const bool fits = i < p.n_seq && seq_range(p, i, start, len);
+    bad |= i < p.n_seq && !fits;
+    long long top = fits ? start + len : 0;      // of this warp's sequences up to this one
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long up = __shfl_up_sync(0xFFFFFFFFu, top, d);
+      if (lane >= d) top = max(top, up);
+    }
+    if (lane == 31) tops[warp] = top;
+    long long behind = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+    if (lane == 0) behind = 0;
+    __syncthreads();
+    long long all = before;
+    for (int w = 0; w < kSeqThreads / 32; ++w) {
+      if (w == warp) behind = max(behind, all);
+      all = max(all, tops[w]);
+    }
+    __syncthreads();
+    before = all;
+    if (i < p.n_seq) p.seqs[i] = fits && start >= behind ? make_longlong2(start, len) : make_longlong2(behind, 0);
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) *p.flag = bad ? kFlagOffsets : 0u;
 }
 
 // One block of a launch looks every sequence over and leaves the verdict in the workspace.
@@ -600,7 +643,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
   long long token0 = 0;
   bool bad;
   const int n = slot_tokens(p, slot, token0, bad, red + 12);
-  if (slot == 0 && head0 == 0) keep_sequences(p, bad);
+  if (p.n_seq <= kFewSeqs && slot == 0 && head0 == 0) keep_sequences(p, bad);
   if (BWD && head0 == 0 && tid == 0) p.slot_tokens[slot] = make_longlong2(token0, n);
   if (n == 0) return;
   const int qh = head0 / p.share, hq = p.H / p.share;

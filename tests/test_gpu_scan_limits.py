@@ -365,6 +365,37 @@ def test_many_sequences_and_one_bad_offset():
     assert torch.equal(o2[rows], o[rows]) and (o2[offs[299]:offs[301]] == 777).all()
 
 
+@pytest.mark.parametrize("N", [200, 700, 1500])
+def test_many_sequences_out_of_order(N):
+    """One offset that skips ahead to token 2 N (and so makes a long sequence), the next one back in line: what starts
+    before that long sequence's end is taken as empty, what starts behind it is right."""
+    each, at = 3, N // 3
+    x, offs = inputs([each] * N, 1, 1, 16, 4, F32, seed=263)
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    whole = Call(x, offs, 1, F32)
+    o, S = (t.clone() for t in whole.forward())
+    g = {n: t.clone() for n, t in whole.backward(d_o, d_S).items()}
+    wrong = list(offs)
+    wrong[at] = 2 * N
+    c = Call(x, offs, 1, F32, device_offsets=wrong)
+    c.work = whole.work
+    o2, S2 = c.forward()
+    assert c.check() == c.L.LORES_ERR_INVALID_ARG
+    g2 = c.backward(d_o, d_S)
+    good = [i for i in range(N) if i < at - 1 or (i > at and offs[i] >= 2 * N)]
+    empty = [i for i in range(N) if i == at or (i > at and offs[i] < 2 * N)]
+    assert torch.equal(S2[good], S[good]) and torch.equal(S2[empty], c.state[empty])
+    assert torch.equal(g2["state"][good], g["state"][good]) and torch.equal(g2["state"][empty], d_S[empty].float())
+    rows = [t for i in good for t in range(offs[i], offs[i + 1])]
+    assert torch.equal(o2[rows], o[rows])
+    for n in NAMES[:5]:
+        assert torch.equal(g2[n][rows], g[n][rows]), n
+    y = {n: (v[offs[at - 1]:2 * N] if n != "state" else v[at - 1:at]) for n, v in x.items()}
+    long = Call(y, [0, 2 * N - offs[at - 1]], 1, F32)
+    lo, lS = long.forward()
+    assert torch.equal(o2[offs[at - 1]:2 * N], lo) and torch.equal(S2[at - 1:at], lS)
+
+
 def test_several_heads_of_a_group_in_one_block_with_the_delta_rule():
     """Enough chunks that the preparation takes two heads (and more) that share q and k."""
     for H, Hq in ((32, 16), (32, 4)):
