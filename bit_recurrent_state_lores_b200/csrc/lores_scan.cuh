@@ -1416,10 +1416,12 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
         const unsigned m = convert_rows<NP, !FWD>(tile, p.dtype, lane);
         if (lane == 0) tops[4 + (c & by)] = m;
       }
-      // the stage's copies; a wait that runs out ends the walk for the whole CTA
+      // the stage's copies; a wait that runs out ends the walk for the whole CTA (after another wait: they write to its
+      // shared memory)
       if (blk == 0 && lane == 0 && !mbar_wait_bounded(bars + (c & by), (i0 >> by) & 1, kWaitNs)) {
         *stop = 1;
         atomicOr(p.flag, kFlagWait);
+        mbar_wait_bounded(bars + (c & by), (i0 >> by) & 1, kWaitNs);
       }
     }
     __syncthreads();
@@ -2043,6 +2045,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     if (tid == 0 && !mbar_wait_bounded(bars + (p.stages == 2 ? b & 1 : 0), (p.stages == 2 ? b >> 1 : b) & 1, kWaitNs)) {
       *stop = 1;
       atomicOr(p.flag, kFlagWait);
+      mbar_wait_bounded(bars + (p.stages == 2 ? b & 1 : 0), (p.stages == 2 ? b >> 1 : b) & 1, kWaitNs);
     }
     __syncthreads();
     if (*stop) return;
