@@ -229,9 +229,10 @@ lores_status device_ok(int device) {
 }
 
 // Blocks of 16 value rows per CTA of a walk: a CTA's blocks share one fetch of a chunk's tiles, but the CTAs
-// should fill the SMs.  Two blocks even where that leaves a quarter of the SMs idle (one block per CTA took 516 us
-// against 300 for one sequence of 8192 tokens and 32 heads of 128 x 128), four only for several rounds of CTAs
-// (322 us against 334 with 512 CTAs of four, 159 against 146 with 192).
+// should fill the SMs.  Two blocks even where that leaves a quarter of the SMs idle (one sequence of 8192 tokens and 32
+// heads of 128 x 128, when 16-bit outputs took one plane: one block per CTA 516 us, two 300), four, in the recomputation
+// without the delta rule, only for several rounds of CTAs (backward 6400 tokens, 64 heads of 64 x 128: 901 us a call
+// against 933 with two blocks; 159 against 146 us with 192 CTAs of four).
 int walk_blocks(const Shape &s, WalkKind kind) {
   const long long walks = (long long)s.c.n_seq * s.c.heads;
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);

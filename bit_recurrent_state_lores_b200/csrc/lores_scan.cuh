@@ -1066,7 +1066,9 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
-// Without the delta rule E = V and the state warps have no products before X; a CTA then takes four blocks.
+// Without the delta rule E = V and the state warps have no products before X; a CTA of the recomputation, which has no
+// output to form, then takes four blocks (20 warps of 96 registers; the forward walk, which spilled in them, took 491 us a
+// call where two blocks take 483).
 // A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit; one
 // took 465 us where two took 300): bulk copies, since 16-byte cp.async of the same 96 KB took longer
 // than the chunk's arithmetic (665 against 500 us); and it turns the block's rows of V into fp16 over
@@ -1084,7 +1086,7 @@ constexpr int kReverseBlocks = 2;        // at most, where E or R has a barrier 
 enum WalkKind { kForward, kRecompute, kReverse, kWalkKinds };
 // Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
 __host__ __device__ constexpr int max_blocks(int np, bool delta, int kind) {
-  return !delta && kind != kReverse && np == 1 ? 4 : 2;
+  return !delta && kind == kRecompute && np == 1 ? 4 : 2;
 }
 __host__ __device__ constexpr int walk_threads(int blocks) { return 32 * blocks * (2 + kSideWarps + 1); }
 
@@ -1391,7 +1393,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   launch_next();
   const longlong2 range = __ldcg(p.seqs + seq);
   const int chunks = ((int)range.y + kChunk - 1) / kChunk;
-  if (tid == 0) {                        // (kept there and not in registers, of which four blocks of rows have none left)
+  if (tid == 0) {                        // (kept there and not in registers, of which there are few)
     placed->x = range.x;
     placed->y = range.y;
   }

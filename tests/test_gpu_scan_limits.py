@@ -462,3 +462,31 @@ def test_nothing_is_written_outside_the_buffers(lens, H, Hq, dk, dv, delta, dtyp
     if dk < 256:
         c.run_backward(normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8))
     c.untouched()
+
+
+def test_many_sequences_of_one_length_and_a_captured_call():
+    x, offs = inputs([3] * 300, 2, 1, 32, 8, BF16, seed=291)
+    a, b = Call(x, offs, 1, BF16), Call(x, offs, 1, BF16, with_offsets=False)
+    d_o, d_S = normal(x["v"], 7, 1.0, BF16), normal(x["state"], 8)
+    for p, q in zip(a.forward(), b.forward()):
+        assert torch.equal(p, q)
+    g, h = a.backward(d_o, d_S), b.backward(d_o, d_S)
+    for n in NAMES:
+        assert torch.equal(g[n], h[n]), n
+    want = {n: t.clone() for n, t in g.items()}
+    o, S = a.o.clone(), a.state_out.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        a.L.lores_scan_forward(a.cfg, a.q, a.k, a.v, a.la, a.be, a.offsets, a.state, a.o, a.state_out, a.work)
+        a.L.lores_scan_backward(a.cfg, a.q, a.k, a.v, a.la, a.be, a.offsets, a.state, a.d_o, a.d_state_out, a.dq,
+                                a.dk_, a.dv_, a.dla, a.dbe, a.ds, a.work)
+    for t in (a.o, a.state_out, a.dq, a.dk_, a.dv_, a.dla, a.dbe, a.ds, a.work):
+        t.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a.o, o) and torch.equal(a.state_out, S)
+    for n in NAMES:
+        assert torch.equal(g[n], want[n]), n
+    assert a.check() == a.L.LORES_OK
