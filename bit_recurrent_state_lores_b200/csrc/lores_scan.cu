@@ -230,9 +230,10 @@ lores_status device_ok(int device) {
 
 // Blocks of 16 value rows per CTA of a walk: a CTA's blocks share one fetch of a chunk's tiles, but the CTAs
 // should fill the SMs.  Two blocks even where that leaves a quarter of the SMs idle (one sequence of 8192 tokens and 32
-// heads of 128 x 128, when 16-bit outputs took one plane: one block per CTA 516 us, two 300), four, in the recomputation
-// without the delta rule, only for several rounds of CTAs (backward 6400 tokens, 64 heads of 64 x 128: 901 us a call
-// against 933 with two blocks; 159 against 146 us with 192 CTAs of four).
+// heads of 128 x 128, when 16-bit outputs took one plane: one block per CTA 516 us, two 300), four, without the delta
+// rule, only for several rounds of CTAs (heads of 64 x 128: backward 6400 tokens, 64 heads 901 us a call against 933 with
+// two blocks; 64 sequences of 32 tokens, 128 heads 488 against 572, of 4 x 2000 tokens 491 against 483; 159 against 146 us
+// with 192 CTAs of four).
 int walk_blocks(const Shape &s, WalkKind kind) {
   const long long walks = (long long)s.c.n_seq * s.c.heads;
   const int blocks = s.dvp / 16, sms = sm_count(s.c.device);
@@ -289,11 +290,12 @@ cudaError_t run_walk(const Shape &s, WalkKind kind, ScanParams p, cudaStream_t s
   static std::atomic<unsigned long long> raised[4][2][2][kWalkKinds];
   const int wi = width_index(c.d_k), nh = state_warps(c.d_k);
   p.rb = walk_blocks(s, kind);
+  p.early = early_walk(s, kind);
   const WalkLayout l = walk_layout(c.d_k, s.np, p.rb, nh, c.delta, kind);
   p.stages = 2 * l.bytes + p.rb * l.tail + kWalkEnd <= kMaxShared ? 2 : 1;
   return launch(kernels().by_width[wi].walk[s.np - 1][c.delta][kind],
                 dim3(c.n_seq * c.heads, (s.dvp / 16 + p.rb - 1) / p.rb), 32 * p.rb * (nh + kSideWarps + 1),
-                p.stages * l.bytes + p.rb * l.tail + kWalkEnd, st, c.device, p, early_walk(s, kind),
+                p.stages * l.bytes + p.rb * l.tail + kWalkEnd, st, c.device, p, p.early != 0,
                 raised[wi][s.np - 1][c.delta][kind]);
 }
 

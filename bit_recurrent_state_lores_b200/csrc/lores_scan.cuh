@@ -68,6 +68,7 @@ enum ScaleOf { kScaleS, kScaleE, kScaleD, kScaleR, kScaleO, kScales };
 struct ScanParams {
   int n_seq, H, share, d_v, dvp, dtype, n_slots, max_len, stages;
   int rb;                              // walks: blocks of 16 value rows per CTA
+  int early;                           // walks: may start beside the kernel before
   int hpc;                             // scan_prep: heads per CTA (a divisor of share)
   int qk16, v16, o16;                  // 16-byte accesses to q and k, v (and dv), o (or d_o) rows
   long long total;
@@ -1066,9 +1067,7 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 //     chunk c + 1 waits for this alone, and NH = 2 halves it.
 //   2 side warps, 32 tokens each: Tm V before X; Q S0^T beside the state warps' second half, then
 //     (barrier Y, which the state warps only arrive at) P E and the output rows.
-// Without the delta rule E = V and the state warps have no products before X; a CTA of the recomputation, which has no
-// output to form, then takes four blocks (20 warps of 96 registers; the forward walk, which spilled in them, took 491 us a
-// call where two blocks take 483).
+// Without the delta rule E = V and the state warps have no products before X; a CTA then takes four blocks.
 // A loader warp per block fetches the next chunk's tiles meanwhile (two stages where they fit; one
 // took 465 us where two took 300): bulk copies, since 16-byte cp.async of the same 96 KB took longer
 // than the chunk's arithmetic (665 against 500 us); and it turns the block's rows of V into fp16 over
@@ -1086,7 +1085,7 @@ constexpr int kReverseBlocks = 2;        // at most, where E or R has a barrier 
 enum WalkKind { kForward, kRecompute, kReverse, kWalkKinds };
 // Blocks of value rows per CTA, at most: what registers and shared memory leave room for.
 __host__ __device__ constexpr int max_blocks(int np, bool delta, int kind) {
-  return !delta && kind == kRecompute && np == 1 ? 4 : 2;
+  return !delta && kind != kReverse && np == 1 ? 4 : 2;
 }
 __host__ __device__ constexpr int walk_threads(int blocks) { return 32 * blocks * (2 + kSideWarps + 1); }
 
@@ -1353,6 +1352,11 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   const int blk = loader ? warp - first_load : side ? (warp - first_side) / kSideWarps : warp / NH;
   const int h = loader ? 0 : side ? (warp - first_side) % kSideWarps : NH == 1 ? 0 : warp % NH;
   const WalkLayout l = walk_layout(DK, NP, p.rb, NH, DELTA, KIND);
+  // (a kernel that may start beside scan_prep, which writes it, waits first; without the delta rule all do, since the
+  // registers of 20 warps do not hold it over the loads of the state: 64 sequences of 32 tokens, 128 heads 488 us against 513)
+  const bool late = !DELTA || (!REV && p.early);
+  longlong2 range;
+  if (!late) range = __ldcg(p.seqs + seq);
   const int brow = row0 + blk * 16, r0 = brow + g, c0 = h * DKH;
   const bool live = brow < p.dvp;
   uint8_t *tail = smem + p.stages * l.bytes + blk * l.tail;
@@ -1391,7 +1395,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
   // SMs that it leaves free, and waits for it at its own end.
   if (!REV) wait_before();
   launch_next();
-  const longlong2 range = __ldcg(p.seqs + seq);
+  if (late) range = __ldcg(p.seqs + seq);
   const int chunks = ((int)range.y + kChunk - 1) / kChunk;
   if (tid == 0) {                        // (kept there and not in registers, of which there are few)
     placed->x = range.x;
