@@ -1897,8 +1897,9 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 //   dbeta_s = c_s + e^{G_C - G_s} k_s.(D^T E_s)
 //   dG_t = sum_s b_s dec_ts (...) - b_t dbeta_t + e^{G_t} (q_t.(S0^T dO_t) - d k_t.(S0^T R_t))
 //   dlog_alpha_r = sum_{t >= r} dG_t + sum_s w_s k_s.(D^T E_s) + e^{G_C} <D, S0>
-// (the pair (t, s) enters dG_t and, through dbeta_s, -dG_s with the same value, so the sums
-// over t >= r cancel exactly where they should).
+// (the pair (t, s) enters dG_t and, through dbeta_s, -dG_s with the same value: a token's own pair is left out of both,
+// and the terms of the last state are the same 64-bit number in both sums, since behind strong decays they are far larger
+// than what is left).
 // Scales: the planes of 16 value rows are held over their own powers of two, so a 16-row step
 // contributes in units that are the product of two of them; left operands are brought to
 // the largest unit F of the group's steps, and the group's sums are held over F.
@@ -1925,7 +1926,7 @@ __host__ __device__ inline GradLayout grad_layout(int dk, int np, int dvp, bool 
   l.k = at; at += np * kChunk * dk * 2;
   l.q = at; at += np * kChunk * dk * 2;
   l.x = at; at += (delta ? 4 : 2) * kChunk * kChunk * 2;  // dP' hi, lo, dL' hi, lo
-  l.f = at; at += (kGateFloats + 5 * kChunk + 4 * kChunk + 16 + 8) * 4;
+  l.f = at; at += (kGateFloats + 6 * kChunk + 4 * kChunk + 16 + 8) * 4;
   l.scales = at; at += kScales * (dvp / 16) * 4;
   l.stage = (at + 15) / 16 * 16;
   at = 0;
@@ -1983,8 +1984,8 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const float *eG = gates + kGateE * kChunk, *w = gates + kGateW * kChunk, *be = gates + kGateB * kChunk,
               *eC = gates + kGateC * kChunk;
   const float2 *G = reinterpret_cast<const float2 *>(gates + kGateG * kChunk);
-  float *rowv = gates + kGateFloats, *aq = rowv + 2 * kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *colp = kw + kChunk,
-        *red = colp + 4 * kChunk;
+  float *rowv = gates + kGateFloats, *aq = rowv + 2 * kChunk, *ak = aq + kChunk, *kw = ak + kChunk, *diagp = kw + kChunk,
+        *colp = diagp + kChunk, *red = colp + 4 * kChunk;
   uint64_t *bars = reinterpret_cast<uint64_t *>(red + 16);                // one per stage
   int *stop = reinterpret_cast<int *>(bars + 2);
   if (tid == 0) {
@@ -2305,6 +2306,11 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
               if (DELTA) m = fmaf(z[j], x[1][e][2 * h + j] * tok, m);
               // (a pair that the mask leaves out gives nothing, not 0 times a decay that overflowed)
               if (diagonal && s > t) m = 0.0f;
+              // (the pair (t, t) is dbeta's alone: in dG_t it cancels)
+              if (diagonal && s == t) {
+                diagp[t] = m * U1 * U2;
+                m = 0.0f;
+              }
               rs[h] = fmaf(b, m, rs[h]);
               cs[2 * step + e][j] += m;
               y[j] *= b * isb * to_planes;
@@ -2425,9 +2431,12 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
       const int t = 2 * lane + i;
       // (a token's columns are summed by the warps whose rows reach it)
       const float c = (colp[t] + colp[kChunk + t]) + (colp[2 * kChunk + t] + colp[3 * kChunk + t]);
-      db[i] = fmaf(eC[t], kw[t], c);
-      dG[i] = (double)rowv[t] + (HALF ? (double)rowv[kChunk + t] : 0.0) - (double)be[t] * db[i] + (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
-      tot += (double)w[t] * kw[t];
+      db[i] = fmaf(eC[t], kw[t], c + diagp[t]);
+      // (the last state's part of b_t dbeta_t, to be taken back by `tot` to the last bit)
+      const double x = (double)be[t] * ((double)eC[t] * (double)kw[t]);
+      dG[i] = (double)rowv[t] + (HALF ? (double)rowv[kChunk + t] : 0.0) - (double)be[t] * c - x +
+              (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
+      tot += x;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, d);

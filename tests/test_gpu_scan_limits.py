@@ -490,3 +490,19 @@ def test_many_sequences_of_one_length_and_a_captured_call():
     for n in NAMES:
         assert torch.equal(g[n], want[n]), n
     assert a.check() == a.L.LORES_OK
+
+
+@pytest.mark.parametrize("dtype,delta", [(F32, 0), (F32, 1), (BF16, 0), (BF16, 1)])
+def test_decay_gradients_that_are_small_beside_their_terms(dtype, delta):
+    """From zero states log_alpha of a sequence's first token has no gradient at all, and behind strong decays the others'
+    are far smaller than d_beta and than <d_state_out, state_out>, whose terms they are differences of."""
+    x, offs = inputs([1, 5, 40, 66], 4, 2, 64, 48, dtype, seed=301, decay=10.0)
+    x["state"].zero_()
+    d_o, d_S = normal(x["v"], 7, 1.0, dtype), normal(x["state"], 8, 1e3)
+    got = Call(x, offs, delta, dtype).backward(d_o, d_S)["log_alpha"]
+    want = backward64(x, offs, delta, d_o, d_S)["log_alpha"]
+    for a, b in zip(offs, offs[1:]):
+        # 64-bit sums of the terms of the state; what is left of d_o's is held to FP32 of d_o's terms
+        size = float(want[a:b].norm()) + float(x["beta"][a:b].norm())
+        assert float((got[a:b].double() - want[a:b]).norm()) <= 4 * FP32 * size, (a, b)
+    assert float(got[0].abs().max()) <= 1e-9
