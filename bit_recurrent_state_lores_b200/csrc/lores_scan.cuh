@@ -1898,8 +1898,8 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 //   dG_t = sum_s b_s dec_ts (...) - b_t dbeta_t + e^{G_t} (q_t.(S0^T dO_t) - d k_t.(S0^T R_t))
 //   dlog_alpha_r = sum_{t >= r} dG_t + sum_s w_s k_s.(D^T E_s) + e^{G_C} <D, S0>
 // (the pair (t, s) enters dG_t and, through dbeta_s, -dG_s with the same value: a token's own pair is left out of both,
-// and the terms of the last state are the same 64-bit number in both sums, since behind strong decays they are far larger
-// than what is left).
+// and of the terms of the last state those of the tokens before r are what is left, since behind strong decays the
+// others are far larger).
 // Scales: the planes of 16 value rows are held over their own powers of two, so a 16-row step
 // contributes in units that are the product of two of them; left operands are brought to
 // the largest unit F of the group's steps, and the group's sums are held over F.
@@ -2424,7 +2424,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     float dsum = 0.0f;
     for (int i = 0; i < kGradThreads / 32; ++i) dsum += red[i];
     dsum = dsum * pow2(topDS / 2) * pow2(topDS - topDS / 2);
-    double dG[2], tot = 0.0;
+    double dG[2], x[2];
     float db[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -2432,21 +2432,20 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
       // (a token's columns are summed by the warps whose rows reach it)
       const float c = (colp[t] + colp[kChunk + t]) + (colp[2 * kChunk + t] + colp[3 * kChunk + t]);
       db[i] = fmaf(eC[t], kw[t], c + diagp[t]);
-      // (the last state's part of b_t dbeta_t, to be taken back by `tot` to the last bit)
-      const double x = (double)be[t] * ((double)eC[t] * (double)kw[t]);
-      dG[i] = (double)rowv[t] + (HALF ? (double)rowv[kChunk + t] : 0.0) - (double)be[t] * c - x +
+      // (the last state's part: its sum over all tokens and, in dG, less that of t >= r leave the tokens before r)
+      x[i] = (double)be[t] * ((double)eC[t] * (double)kw[t]);
+      dG[i] = (double)rowv[t] + (HALF ? (double)rowv[kChunk + t] : 0.0) - (double)be[t] * c +
               (double)eG[t] * (aq[t] - (DELTA ? ak[t] : 0.0f));
-      tot += x;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, d);
-    tot += (double)eG[kChunk - 1] * dsum;
-    double run = dG[0] + dG[1];
+    double run = dG[0] + dG[1], past = x[0] + x[1];
     for (int d = 1; d < 32; d <<= 1) {
-      const double up = __shfl_down_sync(0xFFFFFFFFu, run, d);
+      const double up = __shfl_down_sync(0xFFFFFFFFu, run, d), down = __shfl_up_sync(0xFFFFFFFFu, past, d);
       if (lane + d < 32) run += up;
+      if (lane >= d) past += down;
     }
-    const double out[2] = {run + tot, run - dG[0] + tot};
+    past = __shfl_up_sync(0xFFFFFFFFu, past, 1);
+    if (lane == 0) past = 0.0;
+    const double end = (double)eG[kChunk - 1] * dsum, out[2] = {run + past + end, run - dG[0] + past + x[0] + end};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;

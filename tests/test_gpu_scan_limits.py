@@ -506,3 +506,20 @@ def test_decay_gradients_that_are_small_beside_their_terms(dtype, delta):
         size = float(want[a:b].norm()) + float(x["beta"][a:b].norm())
         assert float((got[a:b].double() - want[a:b]).norm()) <= 4 * FP32 * size, (a, b)
     assert float(got[0].abs().max()) <= 1e-9
+
+
+@pytest.mark.parametrize("delta", [0, 1])
+def test_decay_gradient_of_one_token_is_the_first_states(delta):
+    """One token of a sequence: d_log_alpha is a_t <dL/dS', S_0>, however large v, k and d_state_out are beside S_0."""
+    x, offs = inputs([1, 1], 2, 1, 64, 40, F32, seed=302)
+    x["v"] = (x["v"] * 1e6).float().double()
+    if not delta:
+        x["k"] = (x["k"] * 1e6).float().double()
+    x["state"] = (x["state"] * 1e-5).float().double()
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8, 1e3)
+    got = Call(x, offs, delta, F32).backward(d_o, d_S)["log_alpha"]
+    want = backward64(x, offs, delta, d_o, d_S)["log_alpha"]
+    # (sums of d_v d_k products of either sign: FP32 of a_t |dL/dS'| |S_0|)
+    size = (x["log_alpha"].exp() * (d_S.norm(dim=(2, 3)) + d_o.norm(dim=2) * x["q"].norm(dim=2))
+            * x["state"].norm(dim=(2, 3)))
+    assert ((got.double() - want).abs() <= 4 * FP32 * size).all()
