@@ -31,9 +31,10 @@ using namespace lores::scan;
 namespace {
 
 // Sequences up to this many tokens go token by token: the chunk kernels always pay for 64.  Measured, bf16, heads of
-// 128 x 128 with the delta rule, chunks / token by token: 64 sequences of 32 heads 338 / 281 us for 32 tokens and
-// 344 / 417 us for 48, one sequence 20.9 / 18.9 and 21.0 / 27.1 us; without it, 64 sequences of 128 heads of 64 x 128,
-// 365 / 345 us for 24 tokens and 370 / 446 us for 32.
+// 128 x 128 with the delta rule, chunks / token by token: 64 sequences of 32 heads 350 / 287 us for 32 tokens and
+// 360 / 425 us for 48, one sequence 20.5 / 18.9 and 20.7 / 27.0 us; without it, 64 sequences of 128 heads of 64 x 128 on 8
+// pairs of q and k, 414 / 364 us for 24 tokens and 420 / 467 us for 32.  (Narrower heads and fp32 would bear more: 32 heads
+// of 64 x 64, 48 tokens 176 / 111, fp32 heads of 128 x 128 446 / 402.)
 int recurrent_most(int delta) { return delta ? 32 : 24; }
 constexpr int kMaxDevices = 64;
 
@@ -274,7 +275,7 @@ long long walk_ctas(const Shape &s, WalkKind kind) {
 
 // Kernels that fill the GPU more than once start after the one before them: started early, their CTAs hold places on
 // SMs in an order that cost 2 to 9 % (backward 2 x 4096 tokens, 16 heads 777 -> 815 us; forward without the delta rule,
-// 7800 tokens, 128 heads 395 -> 431 us; 2 x 2048 tokens, 8 heads 56 -> 64 us).  Where each has an SM per CTA, early
+// 7897 tokens, 128 heads 395 -> 431 us; 2 x 2048 tokens, 8 heads 56 -> 64 us).  Where each has an SM per CTA, early
 // starts hide the launches (forward 1024 tokens, 4 heads of 64 x 64 in fp32 46 -> 42 us, backward 94 -> 64 us), and the
 // two walks of a backward call run side by side where both fit (4096 tokens, 16 heads of 128 x 128 546 -> 398 us, 2048
 // tokens, 8 heads 224 -> 174 us).

@@ -31,7 +31,9 @@
 // product's left operand within a few hundred cycles; tcgen05 wants 64 rows at least and keeps
 // accumulators in TMEM, so that every chunk would pay two trips through it on the critical path.
 // Nothing here is bound by the rate of the products: mma.sync measured 555 TFLOP/s on this card, and
-// the walk keeps the tensor cores busy for 1850 of a chunk's 4200 cycles.
+// the walk keeps the tensor cores busy for 2300 of a chunk's 5140 cycles.
+// (Comparisons below between variants of a walk were measured when 16-bit outputs had one plane of S0, P and E: 286 us
+// then for one sequence of 8192 tokens and 32 heads of 128 x 128, 335 with two.)
 //
 // Precision.  Sums and states are fp32; the tensor cores multiply fp16.  An fp32 operand x is given
 // as two fp16 planes, hi = fp16(x) and lo = fp16(x - hi): 22 bits of significand, or an absolute
@@ -39,8 +41,8 @@
 // result exactly: K and Q are divided by one scale per chunk and head and so are the betas in Z, Kb, dP' and
 // dL', P by one per row, the walks' operands by one per 16 value rows and chunk, so that the largest entries are near
 // fp16's end (kUp below).  16-bit inputs are exact as one plane down to 2^-31 of that largest entry (bf16; keys 2^-25),
-// fp32 ones keep 22 bits down to 2^-16 of it (keys 2^-10) and are off by at most 2^-39 of it (keys 2^-33) below.  States, gradients and outputs before their rounding are 6e-7 to 1.5e-6 from exact
-// (fp32 sums leave 2e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
+// fp32 ones keep 22 bits down to 2^-16 of it (keys 2^-10) and are off by at most 2^-39 of it (keys 2^-33) below.
+// States, gradients and outputs before their rounding are 3e-7 to 8e-7 from exact (fp32 sums leave 1e-7 to 3e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
 // they only reach a 16-bit o is not enough either: entries of o came out 1e-3 from the rounded exact value in bf16
 // (1.68e-3 from exact, where the rounding leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
 #pragma once
@@ -490,9 +492,9 @@ __device__ __forceinline__ void load4(const void *src, int dtype, long long i, f
 // Grid (slot, group of p.hpc heads that share K and Q), 4 warps; warp w owns rows 16w .. 16w+15 of every [64][.]
 // result, and only blocks on and below the diagonal are formed.  K and Q are fetched and converted
 // once for the group.  Bound by latency: a chain of short products with four CTAs per SM to hide it.
-// 8192 tokens, 32 heads, d_k = 128, bf16 (4096 items, 330 MB of matrices written): 147 us, 2.3 TB/s;
-// without the delta rule and with 16 heads on one pair of Q and K (7800 tokens, 128 heads): 76 us.
-// A CTA per head took 343 us there.  T = (I + A)^-1 by 16x16 blocks:
+// 8192 tokens, 32 heads, d_k = 128, bf16 (4096 items, 362 MB of matrices written): 154 us, 2.4 TB/s;
+// without the delta rule and with 16 heads on one pair of Q and K (7897 tokens, 128 heads): 96 us (76 with one plane of
+// P, when a CTA per head took 343).  T = (I + A)^-1 by 16x16 blocks:
 // the four diagonal blocks by forward substitution in fp32 (one lane per column); then warp j
 // forms block column j downwards, X_ij = -X_ii sum_{j <= k < i} A_ik X_kj, as
 // X_ij^T = -(sum_k X_kj^T A_ik^T) X_ii^T, so that every X_kj^T is an accumulator that becomes the next
@@ -1073,10 +1075,11 @@ __global__ void __launch_bounds__(kPrepThreads, NP == 1 ? 4 : 2) scan_prep_kerne
 // than the chunk's arithmetic (665 against 500 us); and it turns the block's rows of V into fp16 over
 // their scale.  In the backward pass's recomputation (kRecompute) the planes of S0 and E are kept
 // instead of o.
-// Bound by the latency of a chunk's chain, close behind it by shared memory (3000 of 4200 cycles:
-// fragments, exchanged parts, copies).  One sequence of 8192 tokens, 32 heads of 128 x 128, bf16: 128
-// chunks in 286 us, 2.2 us a chunk; the same recomputed for 2 x 4096 tokens and 16 heads: 136 us;
-// reverse: 172 us (200 to 220 with 67 KB of code in place of 60: the instruction cache).
+// Bound by the latency of a chunk's chain, close behind it by the side warps' products for o (two planes of S0, P and
+// E) and by shared memory (fragments, exchanged parts, copies).  One sequence of 8192 tokens, 32 heads of 128 x 128, bf16:
+// 128 chunks in 335 us, 2.6 us a chunk; the same recomputed for 2 x 4096 tokens and 16 heads: 144 us;
+// reverse: 186 us (before scales were taken from what E and R hold 172, and 200 to 220 with 67 KB of code in place of 60:
+// the instruction cache).
 // The reverse walk has the same roles: D for S, R for E, dO^T Z for Tm V; its side warps also
 // form D's sum over dO^T Q, which the state warps take last (barrier Z).
 constexpr int kSideWarps = 2;
@@ -1905,15 +1908,15 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
 // the largest unit F of the group's steps, and the group's sums are held over F.
 // Bound by latency and the tensor cores in turn: of an item's 35000 cycles 4300 wait for the first
 // copies, 17000 are the sums over value rows (10800 of products), 4200 the matrices dP' and dL', 3200
-// their products and 3600 the stores.  2 x 4096 tokens, 16 heads of 128 x 128, bf16 (2048 items): 280
-// us.  Items of a CTA one behind the other, the next one's copies under way: 357 us (registers).
+// their products and 3600 the stores.  2 x 4096 tokens, 16 heads of 128 x 128, bf16 (2048 items): 290
+// us (those cycles of 280).  Items of a CTA one behind the other, the next one's copies under way: 357 us (registers).
 // The tensor cores cut their sums off instead of rounding them: 768 products in a row (d_v = 4096) leave 1.6e-5, all
 // to one side.  So every kGradSum value rows (48 products, below 1.5e-6) the sums are added, rounded, to a copy in the
 // thread's local memory; narrower heads (the usual 64 to 256) never touch it.
 constexpr int kGradRows = 32, kGradSum = 256;
 // Without the delta rule and with one plane of K and Q an item fits half an SM: 8 warps in two groups (dO S0, E D), each
-// with every other 16 columns of dO E^T beside it, and two CTAs per SM cover each other's waits (7050
-// tokens, 64 heads of 64 x 128, bf16: 379 us where four groups in one CTA took 487).
+// with every other 16 columns of dO E^T beside it, and two CTAs per SM cover each other's waits (6400
+// tokens, 64 heads of 64 x 128, bf16: 366 us; 379 at first, where four groups in one CTA took 487).
 __host__ __device__ constexpr bool grad_halves(int np, bool delta) { return np == 1 && !delta; }
 __host__ __device__ constexpr int grad_threads(int np, bool delta) { return grad_halves(np, delta) ? 256 : 512; }
 
@@ -2460,7 +2463,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
 }
 
 // Sums the heads' parts of dq and dk where heads share q and k, in head order.  Memory bound: 8192
-// tokens, 16 heads on 8, d_k = 128, bf16: 40 us, 4.2 TB/s.  (scan_grads adding its part to the last
+// tokens, 16 heads on 8, d_k = 128, bf16: 38 us, 4.4 TB/s.  (scan_grads adding its part to the last
 // head's instead, heads of a group one behind the other: it took 497 us in place of 320.)
 static __global__ void __launch_bounds__(256) scan_shared_kernel(const ScanParams p, const float *parts_q,
                                                                  const float *parts_k, int dk) {

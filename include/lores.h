@@ -374,7 +374,8 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * Accuracy.  Products run on the tensor cores on operands of 22 bits of significand (two fp16
  * parts), sums and the state are fp32.  States, the gates' gradients and everything fp32 are within
  * a few 1e-6 (relative L2) of the recurrence in exact arithmetic, 16-bit outputs are the rounding of
- * such results, while |k_t|^2 beta_t < 2 holds with delta = 1 (the domain of the recurrence).
+ * such results, while |k_t|^2 beta_t < 2 holds with delta = 1 (the domain of the recurrence) and
+ * beta_s |k_t . k_s| stays below 65504 for the tokens of a chunk.
  * Operands are held over powers of two that fit their largest entry in a chunk (64 tokens of a
  * sequence, counted from its start) and head; of v, d_o and states, in 16 value rows of it.
  * 16-bit inputs are exact down to 2^-31 of that entry (k: 2^-25), fp32 ones have 22 bits down to 2^-16
@@ -404,7 +405,9 @@ typedef struct {
 } lores_scan_config;
 
 /* Bytes of workspace that a call with this configuration needs (backward: 0 or 1), at least
- * 256.  Host only.  Errors: INVALID_ARG, UNSUPPORTED (d_k = 256 with backward = 1). */
+ * 256.  It grows with tokens times heads: at d_k = d_v = 128 with the delta rule 1.4 KB a token and head
+ * forward, 5 KB backward (one prompt of 128k tokens and 32 heads: 6 and 21 GB).  Host only.
+ * Errors: INVALID_ARG, UNSUPPORTED (d_k = 256 with backward = 1). */
 lores_status lores_scan_workspace(const lores_scan_config *cfg, int32_t backward, uint64_t *bytes);
 
 /*   q, k       [total, heads_qk, d_k] of dtype, strides as in cfg, k of unit norm (not
