@@ -42,9 +42,10 @@
 // dL', P by one per row, the walks' operands by one per 16 value rows and chunk, so that the largest entries are near
 // fp16's end (kUp below).  16-bit inputs are exact as one plane down to 2^-31 of that largest entry (bf16; keys 2^-25),
 // fp32 ones keep 22 bits down to 2^-16 of it (keys 2^-10) and are off by at most 2^-39 of it (keys 2^-33) below.
-// States, gradients and outputs before their rounding are 3e-7 to 8e-7 from exact (fp32 sums leave 1e-7 to 3e-7); two bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where
-// they only reach a 16-bit o is not enough either: entries of o came out 1e-3 from the rounded exact value in bf16
-// (1.68e-3 from exact, where the rounding leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
+// States, gradients and outputs before their rounding are 3e-7 to 8e-7 from exact (fp32 sums leave 1e-7 to 3e-7); two
+// bf16 planes left 3e-6 to 1e-5, one fp16 plane 2e-4.  One plane of S0, P and E where they only reach a 16-bit o is not
+// enough either: entries of o came out 1e-3 from the rounded exact value in bf16 (1.68e-3 from exact, where the rounding
+// leaves 1.66e-3), and 1.6 times as far as the rounding in fp16.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

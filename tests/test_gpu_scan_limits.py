@@ -523,3 +523,22 @@ def test_decay_gradient_of_one_token_is_the_first_states(delta):
     size = (x["log_alpha"].exp() * (d_S.norm(dim=(2, 3)) + d_o.norm(dim=2) * x["q"].norm(dim=2))
             * x["state"].norm(dim=(2, 3)))
     assert ((got.double() - want).abs() <= 4 * FP32 * size).all()
+
+
+@pytest.mark.parametrize("lens,H,Hq,dk,dv,delta", [([300, 77], 4, 2, 128, 128, 1), ([300, 77], 4, 2, 128, 64, 0),
+                                                   ([130, 64], 2, 2, 64, 100, 1), ([200], 2, 1, 16, 36, 0)])
+def test_fp32_results_keep_their_bits(lens, H, Hq, dk, dv, delta):
+    """FP32 lets every rounding go the same way.  They go either way: an operand of 22 bits is off by 2^-23 / sqrt(3) (root
+    mean square), a product's two and the term it drops (2^-22 / 3) by less than 1.4 * 2^-23 together, a dozen one
+    behind the other by sqrt(12) times that, 5.8e-7; sums that the tensor cores cut off add at most 2^-23 for each of
+    some four in a row.  Twice all that."""
+    t = 2 * (12 ** 0.5 * 1.4 + 4) * 2.0 ** -23
+    x, offs = inputs(lens, H, Hq, dk, dv, F32, seed=311)
+    c = Call(x, offs, delta, F32)
+    o, S = c.forward()
+    ro, rS = forward64(x, offs, delta)
+    assert rel(o, ro) <= t and rel(S, rS) <= t
+    d_o, d_S = normal(x["v"], 7), normal(x["state"], 8)
+    got, want = c.backward(d_o, d_S), backward64(x, offs, delta, d_o, d_S)
+    for n in NAMES:
+        assert rel(got[n], want[n]) <= t * (4 if n in ("log_alpha", "beta") else 1), n
