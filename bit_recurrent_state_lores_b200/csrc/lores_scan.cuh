@@ -103,7 +103,8 @@ struct ScanParams {
 };
 
 // Record of a chunk and head, kChunk entries each: e^(G_C - G); e^G; w times 2^kUpK of the scale of K (that is, what
-// multiplies 2^-kUpK of a row of khat); e^G likewise; what multiplies a row of P's planes (forward); w; b; G / ln 2 as a pair of floats.  Then
+// multiplies 2^-kUpK of a row of khat); e^G likewise; what multiplies a row of P's planes (forward); w; b; G / ln 2 as a
+// pair of floats.  Then
 // the scales of K, Q and b.
 enum GateRow { kGateC, kGateE, kGateWk, kGateEk, kGateP, kGateW, kGateB, kGateG };   // kGateG: two rows' worth of pairs
 constexpr int kGateScales = (kGateG + 2) * kChunk;
@@ -1449,7 +1450,7 @@ __global__ void __launch_bounds__(walk_threads(max_blocks(NP, DELTA, KIND)), 1) 
     } else {
       // scales: of the state, of V (or dO, which takes the scale of Q that the planes of Q and Z lack; Z those of K and
       // b too)
-            float inv, invV;
+      float inv, invV;
       const float scale = scale_of<!FWD>(max(tops[2 * (i0 & 1)], tops[2 * (i0 & 1) + 1]), kUp, inv);
       float scaleV = scale_of<!FWD>(tops[4 + (c & by)], kUp, invV);
       [[maybe_unused]] const float scaleO = scaleV;          // reverse: dO's own
@@ -2036,7 +2037,7 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   // the group's two scales: of the left operand's planes and of the right one's
   const float *sl = group == KGROUP ? sE : group == 0 || !DELTA ? sO : sR,
               *sr2 = group == KGROUP ? sD : group == 3 ? sE : sS;
-  int topDS = 0, topRE = 0, topOE = 0, topOS = 0, topED = 0, topRS = 0;
+  int topDS = 0, topRE = 0, topOE = 0, top = 0;
 
   // groups 0 to 2: 16 rows x d_k; group 3: tiles 0-7 dO E^T, 8-15 R E^T (in halves: tiles NT .. NT + 3 dO E^T)
   constexpr int NA = HALF ? NT + 4 : NT > 16 ? NT : 16;
@@ -2050,7 +2051,6 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
   const Lane<DK> ld(lane);
   const Lane<kChunk> lc(lane);
 
-  int top = 0;
   for (int b = 0; b < blocks; ++b) {
     cp_wait<0>();
     if (tid == 0 && !mbar_wait_bounded(bars + (p.stages == 2 ? b & 1 : 0), (p.stages == 2 ? b >> 1 : b) & 1, kWaitNs)) {
@@ -2063,13 +2063,13 @@ __global__ void __launch_bounds__(grad_threads(NP, DELTA), grad_halves(NP, DELTA
     if (b == 0) {
       topDS = top_unit(sD, sS, blocks16, lane);
       topOE = top_unit(sO, sE, blocks16, lane);
-      topOS = top_unit(sO, sS, blocks16, lane);
-      topED = top_unit(sE, sD, blocks16, lane);
+      if (DELTA) topRE = top_unit(sR, sE, blocks16, lane);
       if (DELTA) {
-        topRE = top_unit(sR, sE, blocks16, lane);
-        topRS = top_unit(sR, sS, blocks16, lane);
+        top = top_unit(sl, sr2, blocks16, lane);
+      } else {                           // (both, and no addresses kept: 8 warps an item have no registers for them)
+        const int os = top_unit(sO, sS, blocks16, lane), ed = top_unit(sE, sD, blocks16, lane);
+        top = group == KGROUP ? ed : group == 0 ? os : topOE;
       }
-      top = group == KGROUP ? topED : group == 0 ? topOS : group == 1 ? topRS : DELTA ? topRE : topOE;
     }
     if (p.stages == 2 && b + 1 < blocks) fetch(b + 1);
     uint8_t *st = stage_of(b);
