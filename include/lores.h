@@ -379,8 +379,10 @@ lores_status lores_assign_bits_by_decay(const float *mean_decay, int32_t H, floa
  * Operands are held over powers of two that fit their largest entry in a chunk (64 tokens of a
  * sequence, counted from its start) and head; of v, d_o and states, in 16 value rows of it.
  * 16-bit inputs are exact down to 2^-31 of that entry (k: 2^-25), fp32 ones have 22 bits down to 2^-16
- * of it (k: 2^-10) and are off by at most 2^-39 of it (k: 2^-33) below.  A token's output is as exact
- * for a small q as for a large one; a token's gradients carry the errors of their chunk's.
+ * of it (k: 2^-10) and are off by at most 2^-39 of it (k: 2^-33) below; so is beta (2^-33 of the
+ * chunk's largest) where it multiplies k, beside tokens with a beta more than 2^10 times as large.
+ * A token's output is as exact for a small q as for a large one; a token's gradients carry the
+ * errors of their chunk's.
  * An infinity or NaN in a token's inputs or in a state may turn the outputs of the whole 64-token
  * chunk that holds it, and what follows (in the backward pass also what comes before), to NaN,
  * for the heads that read them; an output that stays finite is the recurrence's.  Other heads and
